@@ -14,7 +14,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(HERE, "libkda.so")
-SOURCES = ["kda_api.hip", "kda_fused.hip", "kda_decomp.hip", "kda_decode.hip"]
+SOURCES = ["kda_api.hip", "kda_fused.hip", "kda_decomp.hip", "kda_decode.hip", "kda_ssm_api.hip",
+           "kda_ssm.hip", "kda_ssm_step.hip", "kda_conv.hip", "kda_norm.hip"]
 ARCH = os.environ.get("KDA_OFFLOAD_ARCH", "gfx950")
 
 
@@ -49,7 +50,7 @@ def is_stale() -> bool:
     if not os.path.exists(LIB_PATH):
         return True
     t = os.path.getmtime(LIB_PATH)
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "kda.h")]
+    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, h) for h in ("kda.h", "kda_ssm.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

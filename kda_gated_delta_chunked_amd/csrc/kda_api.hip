@@ -9,34 +9,19 @@
 #include <mutex>
 
 #include "kda.h"
+#include "kda_checks.h"
 #include "kda_kernels.h"
 
 namespace {
 
 constexpr int kHeadDim = 128;
 constexpr int kMaxCkptPerSeq = 64;
-constexpr int64_t kInt32Max = 2147483647LL;
-
-struct Range {
-  uintptr_t lo = 0, hi = 0;  // [lo, hi); empty when lo == hi
-  bool empty() const { return lo == hi; }
-};
-
-Range range_of(const void* p, uint64_t bytes) {
-  Range r;
-  if (p && bytes) {
-    r.lo = reinterpret_cast<uintptr_t>(p);
-    r.hi = r.lo + bytes;
-  }
-  return r;
-}
-
-bool overlaps(const Range& a, const Range& b) {
-  return !a.empty() && !b.empty() && a.lo < b.hi && b.lo < a.hi;
-}
-bool exact(const Range& a, const Range& b) { return !a.empty() && a.lo == b.lo && a.hi == b.hi; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+using kda::aligned16;
+using kda::exact;
+using kda::kInt32Max;
+using kda::overlaps;
+using kda::Range;
+using kda::range_of;
 
 // checkpoint offsets per sequence (0 in the problem means 1)
 int ckpt_count(const kda_problem* p) { return p->ckpt_per_seq > 1 ? p->ckpt_per_seq : 1; }

@@ -1,0 +1,186 @@
+// kda_ssm_kernels.h -- launch interface between the C ABI layer of
+// include/kda_ssm.h and its HIP kernels, and what the kernels share (internal;
+// not installed).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kda_kernels.h"
+
+namespace kda {
+
+__device__ __forceinline__ float bf16_f32(uint32_t b) { return __uint_as_float(b << 16); }
+
+// two floats to two bf16 (round to nearest even), low half first
+__device__ __forceinline__ uint32_t bf16_pair(float x, float y) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  const b2 r = __builtin_convertvector((f2){x, y}, b2);
+  return __builtin_bit_cast(uint32_t, r);
+}
+
+// eight bf16 (16 bytes) to floats (exact) and back (round to nearest even)
+__device__ __forceinline__ void bf16x8_f32(const uint4& u, float* f) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 f32_bf16x8(const float* f) {
+  return make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+}
+
+// v sigmoid(v); for v -> -inf the exponential overflows to inf and the
+// quotient is -0
+__device__ __forceinline__ float silu(float v) { return v / (1.f + __expf(-v)); }
+
+// Token spans.  A packed batch is covered by spans of `len` tokens that start
+// at each sequence's first token.  Sequence n's spans take the slots from
+// floor(cu[n] / len) + n on: ceil(L / len) <= floor(cu[n + 1] / len) -
+// floor(cu[n] / len) + 1, so sequences never share a slot, each owns at least
+// one (also when it is empty), and floor(T / len) + N slots hold them all.  A
+// workgroup finds its sequence from its slot with a search over cu alone, so
+// no launch has to lay the spans out.  `len` is 1 << shift.
+struct Packing {
+  const void* cu;    // int32 or int64 [N + 1]; NULL: N sequences of T_fixed tokens
+  int cu64;
+  int N;
+  int64_t T_total;
+  int64_t T_fixed;
+};
+
+struct Span {
+  int seq;
+  int k;             // span of its sequence; negative: the slot holds none
+  int64_t begin;     // first token of the sequence
+  int64_t end;       // one past its last
+};
+
+inline int64_t span_slots(int64_t N, int64_t T_total, int shift) { return (T_total >> shift) + N; }
+
+__device__ __forceinline__ int64_t cu_at(const Packing& p, int i) {
+  int64_t v;
+  if (!p.cu) return (int64_t)i * p.T_fixed;
+  if (p.cu64)
+    v = reinterpret_cast<const int64_t*>(p.cu)[i];
+  else
+    v = reinterpret_cast<const int32_t*>(p.cu)[i];
+  return v < 0 ? 0 : (v > p.T_total ? p.T_total : v);
+}
+
+// the span of a slot (the same for all lanes of a wave): 64 probes a step
+__device__ __forceinline__ Span span_of(const Packing& p, int shift, int64_t slot) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, hi = p.N;
+  if (!p.cu) {
+    // sequence n's first slot: n T / len rounded down, plus n
+    while (hi - lo > 1) {
+      const int mid = lo + (hi - lo) / 2;
+      if ((((int64_t)mid * p.T_fixed) >> shift) + mid <= slot) lo = mid;
+      else hi = mid;
+    }
+  } else {
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 63) / 64;
+      const int64_t i = (int64_t)lo + (int64_t)step * (lane + 1);
+      const bool le = i < hi && (cu_at(p, (int)i) >> shift) + i <= slot;
+      // offsets that do not decrease give ones, then zeros
+      const unsigned long long m = __ballot(le);
+      const int c = ~m ? __ffsll((long long)~m) - 1 : 64;
+      lo += step * c;
+      const int64_t up = (int64_t)lo + step;
+      if (up < hi) hi = (int)up;
+    }
+  }
+  Span s;
+  s.seq = lo;
+  s.begin = cu_at(p, lo);
+  s.end = cu_at(p, lo + 1);
+  if (s.end < s.begin) s.end = s.begin;
+  const int64_t k = slot - ((s.begin >> shift) + lo);
+  s.k = k < 0 || (k > 0 && (k << shift) >= s.end - s.begin) ? -1 : (int)k;
+  return s;
+}
+
+struct ConvArgs {
+  Packing pk;
+  const uint16_t* x;
+  const uint16_t* weight;   // [D, W]
+  const uint16_t* bias;     // [D] or NULL
+  const uint16_t* initial;  // [N, W - 1, D] or NULL
+  uint16_t* out;
+  uint16_t* final_state;    // [N, W - 1, D] or NULL
+  int D, W, silu;
+  int64_t x_stride, out_stride;
+};
+hipError_t launch_conv(const ConvArgs& a, hipStream_t stream);
+
+struct ConvStepArgs {
+  const uint16_t* x;
+  const uint16_t* weight;
+  const uint16_t* bias;
+  uint16_t* pool;           // [pool_size, W - 1, D]
+  const int32_t* state_indices;
+  uint16_t* out;
+  int N, T, D, W, silu;
+  int64_t pool_size, x_stride, out_stride;
+};
+hipError_t launch_conv_step(const ConvStepArgs& a, hipStream_t stream);
+
+// The tokens of a scan, prefill and decode alike.
+struct SsmTokens {
+  const uint16_t* x;
+  const uint16_t* B;
+  const uint16_t* C;
+  const uint16_t* z;        // NULL: no gate
+  const float* dt;
+  const float* A;
+  const float* D;           // NULL: no skip term
+  const float* dt_bias;     // NULL: none
+  uint16_t* out;
+  int H, G, P, N;           // heads, groups, head_dim, d_state
+  int softplus;
+  int64_t x_stride, b_stride, c_stride, z_stride, out_stride;
+};
+
+struct SsmArgs {
+  SsmTokens t;
+  Packing pk;
+  const void* initial;      // [seqs, H, N, P] or NULL
+  void* final_state;        // or NULL
+  int state_bf16;
+};
+hipError_t launch_ssm(const SsmArgs& a, hipStream_t stream);
+
+struct SsmStepArgs {
+  SsmTokens t;
+  void* pool;
+  const int32_t* state_indices;
+  int seqs, T;
+  int64_t pool_size;
+  int state_bf16;
+};
+hipError_t launch_ssm_step(const SsmStepArgs& a, hipStream_t stream);
+
+struct NormArgs {
+  const uint16_t* x;
+  const uint16_t* residual;  // NULL: none
+  const uint16_t* weight;
+  void* out;                 // bf16, or e4m3 when scales is given
+  float* scales;
+  uint16_t* residual_out;    // or NULL
+  int64_t rows, x_stride;
+  int D, group;              // group 0: one scale per row
+  float eps;
+};
+hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
+
+// step of a token: dt (+ bias), softplus of it when asked
+__device__ __forceinline__ float ssm_step_of(float dt, float bias, int softplus) {
+  dt += bias;
+  return softplus ? fmaxf(dt, 0.f) + log1pf(expf(-fabsf(dt))) : dt;
+}
+
+}  // namespace kda
