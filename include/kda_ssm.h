@@ -63,7 +63,7 @@ typedef struct {
   int32_t width;             /* W, 2..4 */
   int32_t activation;        /* kda_activation */
   int32_t cu_seqlens_int64;  /* 0: int32 offsets, 1: int64 */
-  int64_t x_stride;          /* elements between rows, a multiple of 8 and >= D; 0 = D */
+  int64_t x_stride;          /* elements between rows, a multiple of 8, >= D and below 2^23; 0 = D */
   int64_t out_stride;        /* the same for out */
 } kda_conv_problem;
 
@@ -125,12 +125,13 @@ typedef struct {
   int32_t state_dtype;       /* kda_state_dtype of initial_state and final_state */
   int32_t cu_seqlens_int64;  /* 0: int32 offsets, 1: int64 */
   int32_t piece_tokens;      /* 0 = automatic.  Else sequences longer than this run in pieces of
-                                this many tokens (a multiple of 64), side by side: a first launch
-                                runs each sequence's first piece and the states that the pieces
-                                between add by themselves, a second runs the later pieces from
-                                their combined states.  Results equal the unsplit scan's up to
+                                this many tokens (a power of two from 64 on), side by side: a
+                                first launch runs each sequence's first piece and the states
+                                that the pieces between add by themselves, a second runs the
+                                later pieces from their combined states.  Results equal the unsplit scan's up to
                                 rounding */
-  int64_t x_stride;          /* elements between rows, a multiple of 8 and at least the row; 0 = the row */
+  int64_t x_stride;          /* elements between rows, a multiple of 8, at least the row and below
+                                2^23; 0 = the row */
   int64_t b_stride;
   int64_t c_stride;
   int64_t z_stride;
@@ -209,7 +210,7 @@ typedef struct {
   float eps;                 /* finite, >= 0 */
   int32_t out_dtype;         /* kda_out_dtype */
   int32_t scale_group;       /* KDA_OUT_E4M3: 0 (a scale per row) or 128; else 0 */
-  int64_t x_stride;          /* elements between x's rows, a multiple of 8 and >= D; 0 = D */
+  int64_t x_stride;          /* elements between x's rows, a multiple of 8, >= D and below 2^23; 0 = D */
 } kda_norm_problem;
 
 kda_status kda_add_rmsnorm_validate(const kda_norm_problem* p, const void* x, const void* residual,

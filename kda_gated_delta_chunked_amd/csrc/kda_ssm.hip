@@ -44,35 +44,35 @@ __device__ __forceinline__ f32x16 mfma(const bf16x8& a, const bf16x8& b, const f
 // within a row so that neither kind of operand read has bank conflicts: 16
 // consecutive rows' chunk c (an operand whose lanes are rows) land on 16
 // different bank groups, and so do the four chunks of four consecutive rows (a
-// transposed read).
+// transposed read).  The swizzle depends on row % 16 alone and is an exclusive
+// or, so tile_at(r + 16 i, c ^ d) = (tile_at(r, c) ^ 16 d) + 16 i rows: a lane
+// keeps one address per kind of read.
 template <int COLS>
 __device__ __forceinline__ int tile_at(int row, int chunk) {
   if constexpr (COLS == 128) return row * 256 + ((chunk ^ (((row & 3) << 2) | ((row >> 2) & 3))) << 4);
   return row * 128 + ((chunk ^ ((((row >> 1) & 1) << 2) | ((row >> 2) & 3))) << 4);
 }
 
-// Operand with lane = row, registers = 8 consecutive columns from 8 * chunk.
-template <int COLS>
-__device__ __forceinline__ bf16x8 rows_frag(const uint8_t* tile, int row, int chunk) {
-  return *reinterpret_cast<const bf16x8*>(tile + tile_at<COLS>(row, chunk));
+// Operand with lane = row, registers = 8 consecutive columns.
+__device__ __forceinline__ bf16x8 rows_frag(const uint8_t* tile, int at) {
+  return *reinterpret_cast<const bf16x8*>(tile + at);
 }
 
-// Operand with lane = column, registers = 8 consecutive rows from `row0` (+ 8
-// in the upper half of the wave): two transposed reads of four rows.  In a
-// group of 16 lanes, lane m supplies row m / 4 and four columns from its
-// `chunk` and `half`; lane i receives column i of the 16 that lanes 0..3 (of
-// each row) point to.
-template <int COLS>
-__device__ __forceinline__ bf16x8 cols_frag(const uint8_t* tile, int row0, int chunk, int half) {
+// Operand with lane = column, registers = 8 consecutive rows (the next 8 in
+// the upper half of the wave): two transposed reads of four rows.  In a group
+// of 16 lanes, lane m supplies four columns of row m / 4, and lane i receives
+// column i of the 16 that the four lanes of each row point to.
+__device__ __forceinline__ bf16x8 cols_frag(const uint8_t* tile, int at, int at4) {
   typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-  const int lane = threadIdx.x & 63;
-  const int row = row0 + 8 * (lane >> 5) + ((lane & 15) >> 2);
-  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(tile + tile_at<COLS>(row, chunk) + 8 * half));
-  const s16x4 hi =
-      __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(tile + tile_at<COLS>(row + 4, chunk) + 8 * half));
-  typedef short s16x8 __attribute__((ext_vector_type(8)));
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(tile + at));
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(tile + at4));
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
+
+// Keeps the compiler from holding everything derived from an address in
+// registers across the chunk loop.
+__device__ __forceinline__ void forget(int& v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void settle(float& v) { asm volatile("" : "+v"(v)); }
 
 __device__ __forceinline__ bf16x8 as_frag(const uint32_t (&u)[4]) {
   return __builtin_bit_cast(bf16x8, make_uint4(u[0], u[1], u[2], u[3]));
@@ -97,26 +97,50 @@ __device__ __forceinline__ void split3(float (&v)[8], bf16x8 (&part)[3]) {
   }
 }
 
-// 64 rows of COLS bf16 on their way from memory to a tile; rows past the end
-// are zeros
+// Memory as seen from one chunk's first row: rows from there on, bounded by
+// the hardware, so that rows past the sequence's end read as zeros and are not
+// written.  Row strides are below 2^23 elements: 64 rows stay below 2^31 bytes.
+struct Window {
+  __amdgpu_buffer_rsrc_t r;
+  __device__ __forceinline__ Window(const void* base, int64_t row_bytes, int64_t first, int rows, int width_bytes) {
+    char* p = const_cast<char*>(static_cast<const char*>(base)) + first * row_bytes;
+    r = __builtin_amdgcn_make_buffer_rsrc(p, 0, rows > 0 ? (int)((rows - 1) * row_bytes) + width_bytes : 0, 0x00020000);
+  }
+  __device__ __forceinline__ uint4 load16(int at) const {
+    return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
+  }
+  __device__ __forceinline__ uint2 load8(int at) const {
+    return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0));
+  }
+  __device__ __forceinline__ float load4(int at) const {
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
+  }
+  __device__ __forceinline__ void store8(int at, uint2 v) const {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    __builtin_amdgcn_raw_buffer_store_b64((u32x2){v.x, v.y}, r, at, 0, 0);
+  }
+};
+
+// 64 rows of COLS bf16 on their way from memory to a tile
 template <int COLS, int THREADS>
 struct Rows {
-  static constexpr int PER_ROW = COLS / 8, COUNT = L * PER_ROW / THREADS;
+  static constexpr int PER_ROW = COLS / 8, COUNT = L * PER_ROW / THREADS, STEP = THREADS / PER_ROW;
   uint4 v[COUNT];
-  __device__ __forceinline__ void load(const uint16_t* base, int64_t stride, int64_t tok, int64_t end) {
+  __device__ __forceinline__ void load(const uint16_t* base, int64_t stride, int64_t first, int rows) {
+    const Window w(base, stride * 2, first, rows, COLS * 2);
+    const int at = (threadIdx.x / PER_ROW) * (int)(stride * 2) + (threadIdx.x % PER_ROW) * 16;
 #pragma unroll
-    for (int i = 0; i < COUNT; ++i) {
-      const int id = i * THREADS + threadIdx.x;
-      const int64_t t = tok + id / PER_ROW;
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (t < end) v[i] = *reinterpret_cast<const uint4*>(base + t * stride + (id % PER_ROW) * 8);
-    }
+    for (int i = 0; i < COUNT; ++i) v[i] = w.load16(at + i * STEP * (int)(stride * 2));
   }
   __device__ __forceinline__ void store(uint8_t* tile) const {
+    const int at = tile_at<COLS>(threadIdx.x / PER_ROW, threadIdx.x % PER_ROW);
+    if constexpr (STEP % 16 == 0) {
 #pragma unroll
-    for (int i = 0; i < COUNT; ++i) {
-      const int id = i * THREADS + threadIdx.x;
-      *reinterpret_cast<uint4*>(tile + tile_at<COLS>(id / PER_ROW, id % PER_ROW)) = v[i];
+      for (int i = 0; i < COUNT; ++i) *reinterpret_cast<uint4*>(tile + at + i * STEP * COLS * 2) = v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i)
+        *reinterpret_cast<uint4*>(tile + tile_at<COLS>(threadIdx.x / PER_ROW + i * STEP, threadIdx.x % PER_ROW)) = v[i];
     }
   }
   // whether any value is an infinity or a NaN
@@ -132,6 +156,31 @@ struct Rows {
   }
 };
 
+// One step of a sum over the wave's lanes: adds what a data-parallel shift
+// brings (zero where it brings nothing).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double add_shifted(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+  return v + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+// sums of lanes 0..i in lane i: within rows of 16 lanes, then over the rows
+__device__ __forceinline__ double prefix_sum(double v) {
+  v = add_shifted<0x111, 0xf>(v);
+  v = add_shifted<0x112, 0xf>(v);
+  v = add_shifted<0x114, 0xf>(v);
+  v = add_shifted<0x118, 0xf>(v);
+  v = add_shifted<0x142, 0xa>(v);
+  return add_shifted<0x143, 0xc>(v);
+}
+__device__ __forceinline__ double last_lane(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, 63);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
 // a head's decays over a chunk
 struct Gates {
   float cum_hi[L], cum_lo[L];  // c_t log2(e) in two floats
@@ -141,242 +190,337 @@ struct Gates {
   float total;                 // exp(c_63)
 };
 
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)v >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
 template <int N, int P, int HPW>
-__global__ __launch_bounds__(HPW* P * 2, 2) void kda_ssm_kernel(SsmArgs a) {
+__global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 1 : 2) void kda_ssm_kernel(SsmArgs a) {
   constexpr int WPH = P / 32, WAVES = HPW * WPH, THREADS = WAVES * 64, XC = HPW * P, NB = N / 32;
   __shared__ __attribute__((aligned(16))) uint8_t tB[L * N * 2], tC[L * N * 2], tX[L * XC * 2], tM[HPW][L * L * 2];
-  __shared__ __attribute__((aligned(16))) Gates gates[HPW];
+  __shared__ __attribute__((aligned(16))) Gates gates[2][HPW];
   __shared__ int odd[2];  // whether the chunk's x holds infinities or NaNs
 
   const SsmTokens& k = a.t;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l32 = lane & 31, up = lane >> 5;
-  // blocks go to the 8 XCDs in turn: a sequence's heads, which read the same B
-  // and C, share one
+  // blocks go to the 8 XCDs in turn: the heads of a sequence (or of a piece),
+  // which read the same B and C, share one
   const int HG = k.H / HPW;
   const int64_t blk = blockIdx.x;
-  const int seq = (int)((blk / (8 * HG)) * 8 + (blk & 7));
-  if (seq >= a.pk.N) return;
+  const int64_t slot = (blk / (8 * HG)) * 8 + (blk & 7);
+  if (slot >= a.slots) return;
+  const Span sp = span_of(a.pk, a.shift, slot);
+  if (sp.k < 0) return;
+  const int seq = __builtin_amdgcn_readfirstlane(sp.seq), piece = __builtin_amdgcn_readfirstlane(sp.k);
+  const int64_t begin = uniform(sp.begin), end = uniform(sp.end);
+  const int64_t pieces = a.pass ? (end - begin + ((int64_t)1 << a.shift) - 1) >> a.shift : 1;
+  const bool last = piece + 1 >= pieces;
+  // first launch: first pieces whole, the states of those between; second
+  // launch: the later pieces whole
+  if (a.pass == 1 && piece > 0 && last) return;
+  if (a.pass == 2 && piece == 0) return;
+  const bool full = a.pass != 1 || piece == 0;
+  const int64_t from = begin + ((int64_t)piece << a.shift);
+  const int64_t to = a.pass && !last ? from + ((int64_t)1 << a.shift) : end;
+
   const int head0 = (int)((blk >> 3) % HG) * HPW;
   const int hh = wave / WPH, head = head0 + hh, pc = (wave % WPH) * 32;
   const int g = head0 / (k.H / k.G);
-  const int64_t from = cu_at(a.pk, seq);
-  int64_t to = cu_at(a.pk, seq + 1);
-  if (to < from) to = from;
+
+  // state rows 32 nb + 16 (r / 8) + 8 up + r % 8 of column pc + l32
+  const int64_t state0 = (int64_t)head * N * P + (int64_t)(8 * up) * P + pc + l32;
+  const int64_t per_seq = (int64_t)k.H * N * P;
+  auto row_of = [](int nb, int r) { return (32 * nb + 16 * (r >> 3) + (r & 7)) * P; };
+  f32x16 S[NB] = {};
+  if (a.pass == 2) {
+    // the state ahead of this piece: S <- d_q S + (what piece q adds)
+    for (int q = 0; q < piece; ++q) {
+      const int64_t sl = slot - piece + q;
+      const float* add = a.piece_state + sl * per_seq + state0;
+      const float d = q ? a.piece_decay[sl * k.H + head] : 0.f;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) S[nb][r] = (q ? d * S[nb][r] : 0.f) + add[row_of(nb, r)];
+    }
+  } else if (a.initial && full) {
+    if (a.state_bf16) {
+      const uint16_t* s0 = static_cast<const uint16_t*>(a.initial) + seq * per_seq + state0;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) S[nb][r] = bf16_f32(s0[row_of(nb, r)]);
+    } else {
+      const float* s0 = static_cast<const float*>(a.initial) + seq * per_seq + state0;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) S[nb][r] = s0[row_of(nb, r)];
+    }
+  }
 
   const uint16_t* Bp = k.B + g * N;
   const uint16_t* Cp = k.C + g * N;
   const uint16_t* Xp = k.x + (int64_t)head0 * P;
+  const uint16_t* Zp = k.z ? k.z + (int64_t)head0 * P : nullptr;
+  uint16_t* Op = k.out + (int64_t)head0 * P;
   const float Dh = k.D ? k.D[head] : 0.f;
 
-  // state rows 32 nb + 16 (r / 8) + 8 up + r % 8 of column pc + l32
-  auto state_at = [&](int nb, int r) {
-    return ((int64_t)seq * k.H + head) * N * P + (int64_t)(32 * nb + 16 * (r >> 3) + 8 * up + (r & 7)) * P + pc + l32;
-  };
-  f32x16 S[NB];
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-    for (int r = 0; r < 16; ++r)
-      S[nb][r] = !a.initial ? 0.f
-                 : a.state_bf16 ? bf16_f32(static_cast<const uint16_t*>(a.initial)[state_at(nb, r)])
-                                : static_cast<const float*>(a.initial)[state_at(nb, r)];
-
+  // rows left from a token on, at most a chunk
+  auto left = [&](int64_t tok) { return to - tok < L ? (int)(to - tok) : L; };
   Rows<N, THREADS> rB, rC;
   Rows<XC, THREADS> rX;
-  float rdt = 0.f;
   auto fetch = [&](int64_t tok) {
-    rB.load(Bp, k.b_stride, tok, to);
-    rC.load(Cp, k.c_stride, tok, to);
-    rX.load(Xp, k.x_stride, tok, to);
-    if (wave < HPW && tok + lane < to) rdt = k.dt[(tok + lane) * k.H + head0 + wave];
+    rB.load(Bp, k.b_stride, tok, left(tok));
+    if (full) rC.load(Cp, k.c_stride, tok, left(tok));
+    rX.load(Xp, k.x_stride, tok, left(tok));
   };
-  if (from < to) fetch(from);
-  if (tid < 2) odd[tid] = 0;
-  lds_barrier();
-
-  for (int64_t tok = from, c = 0; tok < to; tok += L, ++c) {
-    rB.store(tB);
-    rC.store(tC);
-    rX.store(tX);
-    if (rX.not_finite()) odd[c & 1] = 1;
-    if (wave < HPW) {
-      // one wave per head: steps, and the sums of a_t over the wave's 64 tokens
-      const int h = head0 + wave;
-      const float step =
-          tok + lane < to ? ssm_step_of(rdt, k.dt_bias ? k.dt_bias[h] : 0.f, k.softplus) : 0.f;
-      double cum = (double)step * (double)k.A[h];
+  // the steps and decays of a chunk, by the last wave, ahead of time
+  double log_decay[HPW] = {};  // of the whole piece so far
+  float rdt[HPW] = {};
+  auto fetch_steps = [&](int64_t tok) {
+    const Window w(k.dt, (int64_t)k.H * 4, tok, left(tok), k.H * 4);
 #pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const double other = __shfl_up(cum, o, 64);
-        if (lane >= o) cum += other;
-      }
-      const double end = __shfl(cum, 63, 64);
-      Gates& gt = gates[wave];
+    for (int q = 0; q < HPW; ++q) rdt[q] = w.load4((lane * k.H + head0 + q) * 4);
+  };
+  auto make_gates = [&](int64_t tok, int buf) {
+#pragma unroll
+    for (int q = 0; q < HPW; ++q) {
+      const int h = head0 + q;
+      const float step = lane < left(tok) ? ssm_step_of(rdt[q], k.dt_bias ? k.dt_bias[h] : 0.f, k.softplus) : 0.f;
+      const double cum = prefix_sum((double)step * (double)k.A[h]);
+      const double sum = last_lane(cum);
+      log_decay[q] += sum;
+      Gates& gt = gates[buf][q];
       const double c2 = cum * kLog2e;
       const float hi = (float)c2;
       gt.cum_hi[lane] = hi;
       gt.cum_lo[lane] = (float)(c2 - (double)hi);
       gt.step[lane] = step;
       gt.from_start[lane] = expf((float)cum);
-      gt.to_end[lane] = expf((float)(end - cum)) * step;
-      if (lane == 0) gt.total = expf((float)end);
+      gt.to_end[lane] = expf((float)(sum - cum)) * step;
+      if (lane == 0) gt.total = expf((float)sum);
     }
+  };
+  const bool gate_wave = wave == WAVES - 1;
+  if (from < to) {
+    fetch(from);
+    if (gate_wave) {
+      fetch_steps(from);
+      make_gates(from, 0);
+      if (from + L < to) fetch_steps(from + L);
+    }
+  }
+  if (tid < 2) odd[tid] = 0;
+  lds_barrier();
+
+  // a lane's addresses: operands whose lanes are rows (of B and C, and of M),
+  // and transposed reads of x and B (rows 0..3, then 4..7).  B's columns come
+  // in the order in which the accumulators hold the state's rows: bits 2 and 3
+  // of the row change places.
+  const int q1 = (lane >> 4) & 1, m = lane & 3, tr = 8 * up + ((lane & 15) >> 2);
+  const int xcol = (hh * P + pc) / 8;
+  int at_row = tile_at<N>(l32, up), at_m = tile_at<L>(l32, up);
+  int at_x = tile_at<XC>(tr, xcol + 2 * q1 + (m >> 1)) + 8 * (m & 1);
+  int at_x4 = tile_at<XC>(tr + 4, xcol + 2 * q1 + (m >> 1)) + 8 * (m & 1);
+  int at_b = tile_at<N>(tr, 2 * q1 + (m & 1)) + 8 * (m >> 1);
+  int at_b4 = tile_at<N>(tr + 4, 2 * q1 + (m & 1)) + 8 * (m >> 1);
+  int at_o = tile_at<XC>(l32, xcol) + 8 * up;
+
+  int c = 0;
+  for (int64_t tok = from; tok < to; tok += L, c ^= 1) {
+    forget(at_row); forget(at_m); forget(at_x); forget(at_x4); forget(at_b); forget(at_b4); forget(at_o);
+    rB.store(tB);
+    if (full) rC.store(tC);
+    rX.store(tX);
+    if (rX.not_finite()) odd[c] = 1;
     lds_barrier();
     if (tok + L < to) fetch(tok + L);
-    const bool slow = odd[c & 1] != 0;
-    if (tid == 0) odd[(c + 1) & 1] = 0;
+    const bool slow = odd[c] != 0;
+    if (tid == 0) odd[c ^ 1] = 0;
+    if (gate_wave && tok + L < to) {
+      make_gates(tok + L, c ^ 1);
+      if (tok + 2 * L < to) fetch_steps(tok + 2 * L);
+    }
 
-    // M: the lower triangle of C B^T in 32 x 32 tiles (transposed: lane = t,
-    // registers = j), decayed, to LDS
+    f32x16 Y[2] = {};
+    if (full) {
+      // M: the lower triangle of C B^T in 32 x 32 tiles (transposed: lane = t,
+      // registers = j), decayed, to LDS
+      for (int tile = wave; tile < 3; tile += WAVES) {
+        const int ti = tile ? 32 : 0, tj = tile == 2 ? 32 : 0;
+        f32x16 G = {};
 #pragma unroll
-    for (int tile = wave; tile < 3; tile += WAVES) {
-      const int ti = tile ? 32 : 0, tj = tile == 2 ? 32 : 0;
-      f32x16 G = {};
+        for (int s = 0; s < N / 16; ++s)
+          G = mfma(rows_frag(tB + tj * N * 2, at_row ^ (s << 5)), rows_frag(tC + ti * N * 2, at_row ^ (s << 5)), G);
 #pragma unroll
-      for (int s = 0; s < N / 16; ++s)
-        G = mfma(rows_frag<N>(tB, tj + l32, 2 * s + up), rows_frag<N>(tC, ti + l32, 2 * s + up), G);
-      const int t = ti + l32;
+        for (int q = 0; q < HPW; ++q) {
+          const Gates& gt = gates[c][q];
+          const float hi = gt.cum_hi[ti + l32], lo = gt.cum_lo[ti + l32];
 #pragma unroll
-      for (int q = 0; q < HPW; ++q) {
-        const Gates& gt = gates[q];
-        const float hi = gt.cum_hi[t], lo = gt.cum_lo[t];
+          for (int b = 0; b < 4; ++b) {
+            const int j = tj + 8 * b + 4 * up;
+            float mv[4];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int j = tj + 8 * b + 4 * up;
-          float m[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float e = (hi - gt.cum_hi[j + i]) + (lo - gt.cum_lo[j + i]);
-            m[i] = j + i <= t ? G[4 * b + i] * (__builtin_amdgcn_exp2f(e) * gt.step[j + i]) : 0.f;
+            for (int i = 0; i < 4; ++i) {
+              const float e = (hi - gt.cum_hi[j + i]) + (lo - gt.cum_lo[j + i]);
+              mv[i] = G[4 * b + i] * (__builtin_amdgcn_exp2f(e) * gt.step[j + i]);
+              settle(mv[i]);  // computed for every lane: a select, no branches
+              mv[i] = j + i <= ti + l32 ? mv[i] : 0.f;
+            }
+            *reinterpret_cast<uint2*>(tM[q] + ti * L * 2 + ((at_m ^ (up << 4) ^ (((tj >> 3) + b) << 4)) + 8 * up)) =
+                make_uint2(bf16_pair(mv[0], mv[1]), bf16_pair(mv[2], mv[3]));
           }
-          *reinterpret_cast<uint2*>(tM[q] + tile_at<L>(t, (tj >> 3) + b) + 8 * up) =
-              make_uint2(bf16_pair(m[0], m[1]), bf16_pair(m[2], m[3]));
         }
+      }
+
+      // y^T = S^T C^T, decayed from the chunk's start
+#pragma unroll
+      for (int s = 0; s < N / 16; ++s) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          u[i] = bf16_pair(S[s >> 1][8 * (s & 1) + 2 * i], S[s >> 1][8 * (s & 1) + 2 * i + 1]);
+        const bf16x8 sf = as_frag(u);
+        Y[0] = mfma(sf, rows_frag(tC, at_row ^ (s << 5)), Y[0]);
+        Y[1] = mfma(sf, rows_frag(tC + 32 * N * 2, at_row ^ (s << 5)), Y[1]);
+      }
+#pragma unroll
+      for (int tb = 0; tb < 2; ++tb) {
+        const float e = gates[c][hh].from_start[32 * tb + l32];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) Y[tb][r] *= e;
       }
     }
 
-    // y^T = S^T C^T, decayed from the chunk's start
-    f32x16 Y[2] = {};
-#pragma unroll
-    for (int s = 0; s < N / 16; ++s) {
-      uint32_t u[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        u[i] = bf16_pair(S[s >> 1][8 * (s & 1) + 2 * i], S[s >> 1][8 * (s & 1) + 2 * i + 1]);
-      const bf16x8 sf = as_frag(u);
-      Y[0] = mfma(sf, rows_frag<N>(tC, l32, 2 * s + up), Y[0]);
-      Y[1] = mfma(sf, rows_frag<N>(tC, 32 + l32, 2 * s + up), Y[1]);
-    }
-    const Gates& gt = gates[hh];
-#pragma unroll
-    for (int tb = 0; tb < 2; ++tb) {
-      const float e = gt.from_start[32 * tb + l32];
-#pragma unroll
-      for (int r = 0; r < 16; ++r) Y[tb][r] *= e;
-    }
-
     // S <- exp(c_63) S + B^T (w x)
-    const float total = gt.total;
+    const float total = gates[c][hh].total;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int r = 0; r < 16; ++r) S[nb][r] *= total;
-    const int q1 = (lane >> 4) & 1, m = lane & 3;
     bf16x8 xf[4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      xf[s] = cols_frag<XC>(tX, 16 * s, (hh * P + pc) / 8 + 2 * q1 + (m >> 1), m & 1);
+      xf[s] = cols_frag(tX + 16 * s * XC * 2, at_x, at_x4);
       float v[8];
       bf16x8_f32(__builtin_bit_cast(uint4, xf[s]), v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= gt.to_end[16 * s + 8 * up + i];
+      for (int i = 0; i < 8; ++i) v[i] *= gates[c][hh].to_end[16 * s + 8 * up + i];
       bf16x8 part[3];
       split3(v, part);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        // rows in the order in which the accumulators hold them: bits 2 and 3
-        // of the row change places
-        const bf16x8 bf = cols_frag<N>(tB, 16 * s, 4 * nb + 2 * q1 + (m & 1), m >> 1);
+        const bf16x8 bf = cols_frag(tB + 16 * s * N * 2, at_b ^ (nb << 6), at_b4 ^ (nb << 6));
 #pragma unroll
         for (int q = 0; q < 3; ++q) S[nb] = mfma(bf, part[q], S[nb]);
       }
     }
-    lds_barrier();
 
-    // y^T += x^T M^T
-    if (!slow) {
+    if (full) {
+      lds_barrier();
+      // y^T += x^T M^T
+      const uint8_t* M = tM[hh];
+      if (!slow) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        if (s < 2) Y[0] = mfma(xf[s], rows_frag<L>(tM[hh], l32, 2 * s + up), Y[0]);
-        Y[1] = mfma(xf[s], rows_frag<L>(tM[hh], 32 + l32, 2 * s + up), Y[1]);
+        for (int s = 0; s < 4; ++s) {
+          if (s < 2) Y[0] = mfma(xf[s], rows_frag(M, at_m ^ (s << 5)), Y[0]);
+          Y[1] = mfma(xf[s], rows_frag(M + 32 * L * 2, at_m ^ (s << 5)), Y[1]);
+        }
+      } else {
+        // a product with the zeros of M above the diagonal would carry a later
+        // token's infinity or NaN to an earlier one
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) {
+          const int t = 32 * tb + l32;
+          for (int j = 0; j <= t; ++j) {
+            const float w = bf16_f32(*reinterpret_cast<const uint16_t*>(M + tile_at<L>(t, j >> 3) + 2 * (j & 7)));
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const int p = hh * P + pc + 8 * (r >> 2) + 4 * up + (r & 3);
+              Y[tb][r] += w * bf16_f32(*reinterpret_cast<const uint16_t*>(tX + tile_at<XC>(j, p >> 3) + 2 * (p & 7)));
+            }
+          }
+        }
       }
-    } else {
-      // a product with the zeros of M above the diagonal would carry a later
-      // token's infinity or NaN to an earlier one
+
+      // out: lane = token, four columns at a time
+      const int width = HPW * P * 2, rows = left(tok);
+      const Window ow(Op, k.out_stride * 2, tok, rows, width), zw(Zp, k.z_stride * 2, tok, Zp ? rows : 0, width);
+      const int col = (hh * P + pc + 4 * up) * 2;
+#pragma unroll
       for (int tb = 0; tb < 2; ++tb) {
         const int t = 32 * tb + l32;
-        for (int j = 0; j <= t; ++j) {
-          const float w = bf16_f32(*reinterpret_cast<const uint16_t*>(tM[hh] + tile_at<L>(t, j >> 3) + 2 * (j & 7)));
+        const int oat = t * (int)(k.out_stride * 2) + col;
+        if (k.D) {
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int p = hh * P + pc + 8 * (r >> 2) + 4 * up + (r & 3);
-            const float x = bf16_f32(*reinterpret_cast<const uint16_t*>(tX + tile_at<XC>(j, p >> 3) + 2 * (p & 7)));
-            if (tb == 0) Y[0][r] += w * x;
-            else Y[1][r] += w * x;
+          for (int b = 0; b < 4; ++b) {
+            const uint2 xv = *reinterpret_cast<const uint2*>(tX + 32 * tb * XC * 2 + (at_o ^ (b << 4)));
+            const uint32_t xw[4] = {xv.x << 16, xv.x & 0xffff0000u, xv.y << 16, xv.y & 0xffff0000u};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) Y[tb][4 * b + i] += Dh * __uint_as_float(xw[i]);
           }
         }
-      }
-    }
-
-    // out: lane = token, four columns at a time
+        if (Zp) {
+          const int zat = t * (int)(k.z_stride * 2) + col;
+          uint2 zv[4];
 #pragma unroll
-    for (int tb = 0; tb < 2; ++tb) {
-      const int t = 32 * tb + l32;
-      if (tok + t < to) {
-        const int64_t col = (int64_t)head * P + pc + 4 * up;
-        uint16_t* out = k.out + (tok + t) * k.out_stride + col;
-        const uint16_t* z = k.z ? k.z + (tok + t) * k.z_stride + col : nullptr;
+          for (int b = 0; b < 4; ++b) zv[b] = zw.load8(zat + 16 * b);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const uint2 xv = *reinterpret_cast<const uint2*>(tX + tile_at<XC>(t, (hh * P + pc) / 8 + b) + 8 * up);
-          const uint32_t xw[4] = {xv.x << 16, xv.x & 0xffff0000u, xv.y << 16, xv.y & 0xffff0000u};
-          float o[4];
+          for (int b = 0; b < 4; ++b) {
+            const uint32_t zb[4] = {zv[b].x << 16, zv[b].x & 0xffff0000u, zv[b].y << 16, zv[b].y & 0xffff0000u};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = Y[tb][4 * b + i];
-          if (k.D)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] += Dh * __uint_as_float(xw[i]);
-          if (z) {
-            const uint2 zv = *reinterpret_cast<const uint2*>(z + 8 * b);
-            const uint32_t zw[4] = {zv.x << 16, zv.x & 0xffff0000u, zv.y << 16, zv.y & 0xffff0000u};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] *= silu(__uint_as_float(zw[i]));
+            for (int i = 0; i < 4; ++i) Y[tb][4 * b + i] *= silu(__uint_as_float(zb[i]));
           }
-          *reinterpret_cast<uint2*>(out + 8 * b) = make_uint2(bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3]));
         }
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          ow.store8(oat + 16 * b, make_uint2(bf16_pair(Y[tb][4 * b], Y[tb][4 * b + 1]),
+                                             bf16_pair(Y[tb][4 * b + 2], Y[tb][4 * b + 3])));
       }
     }
     lds_barrier();  // the tiles are rewritten next
   }
 
-  if (a.final_state) {
+  if (!last) {
+    float* out = a.piece_state + slot * per_seq + state0;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        if (a.state_bf16)
-          static_cast<uint16_t*>(a.final_state)[state_at(nb, r)] = (uint16_t)bf16_pair(S[nb][r], 0.f);
-        else
-          static_cast<float*>(a.final_state)[state_at(nb, r)] = S[nb][r];
-      }
+      for (int r = 0; r < 16; ++r) out[row_of(nb, r)] = S[nb][r];
+    if (gate_wave && lane == 0)
+#pragma unroll
+      for (int q = 0; q < HPW; ++q) a.piece_decay[slot * k.H + head0 + q] = expf((float)log_decay[q]);
+  } else if (a.final_state) {
+    if (a.state_bf16) {
+      uint16_t* out = static_cast<uint16_t*>(a.final_state) + seq * per_seq + state0;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) out[row_of(nb, r)] = (uint16_t)bf16_pair(S[nb][r], 0.f);
+    } else {
+      float* out = static_cast<float*>(a.final_state) + seq * per_seq + state0;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) out[row_of(nb, r)] = S[nb][r];
+    }
   }
 }
 
 template <int N, int P, int HPW>
-void launch(const SsmArgs& a, hipStream_t stream) {
-  const int64_t blocks = ((int64_t)a.pk.N + 7) / 8 * 8 * (a.t.H / HPW);
-  hipLaunchKernelGGL((kda_ssm_kernel<N, P, HPW>), dim3((unsigned)blocks), dim3(HPW * P * 2), 0, stream, a);
+void launch(SsmArgs a, hipStream_t stream) {
+  const int64_t blocks = (a.slots + 7) / 8 * 8 * (a.t.H / HPW);
+  const dim3 grid((unsigned)blocks), block(HPW * P * 2);
+  if (a.piece_state) {
+    a.pass = 1;
+    hipLaunchKernelGGL((kda_ssm_kernel<N, P, HPW>), grid, block, 0, stream, a);
+    a.pass = 2;
+  }
+  hipLaunchKernelGGL((kda_ssm_kernel<N, P, HPW>), grid, block, 0, stream, a);
 }
 
 // Heads of 64 columns run two to a workgroup where a group has an even number

@@ -21,8 +21,9 @@ using kda::range_of;
 bool flag(int32_t v) { return v == 0 || v == 1; }
 
 // a row stride: 0 stands for the packed row; else a multiple of 8 that holds it
+// (below 2^23, so that a kernel may address 64 rows with 32 bits)
 bool stride_ok(int64_t stride, int64_t row) {
-  return stride == 0 || (stride >= row && stride % 8 == 0 && stride <= kInt32Max);
+  return stride == 0 || (stride >= row && stride % 8 == 0 && stride < (1 << 23));
 }
 int64_t stride_of(int64_t stride, int64_t row) { return stride ? stride : row; }
 
@@ -83,7 +84,7 @@ kda_status check_heads(int32_t H, int32_t G, int32_t P, int32_t N, int32_t softp
   if ((P != 64 && P != 128) || (N != 64 && N != 128)) return KDA_ERR_UNSUPPORTED;
   if (H < 1 || G < 1 || H % G || !flag(softplus)) return KDA_ERR_INVALID_ARG;
   if (state_dtype != KDA_STATE_F32 && state_dtype != KDA_STATE_BF16) return KDA_ERR_UNSUPPORTED;
-  return (int64_t)H * P > kInt32Max / 8 ? KDA_ERR_TOO_LARGE : KDA_OK;
+  return (int64_t)H * P >= (1 << 23) ? KDA_ERR_TOO_LARGE : KDA_OK;
 }
 
 template <class Problem>
@@ -146,9 +147,25 @@ kda_status check_ssm(const kda_ssm_problem* p) {
   if (st != KDA_OK) return st;
   st = check_batch(p->num_seqs, p->total_tokens, p->cu_seqlens_int64);
   if (st != KDA_OK) return st;
-  if (p->piece_tokens < 0 || p->piece_tokens % 64 || !strides_ok(p)) return KDA_ERR_INVALID_ARG;
-  if ((int64_t)p->num_seqs * p->num_heads > kInt32Max / 8) return KDA_ERR_TOO_LARGE;
+  const int32_t piece = p->piece_tokens;
+  if (piece < 0 || (piece && (piece < 64 || (piece & (piece - 1)))) || !strides_ok(p)) return KDA_ERR_INVALID_ARG;
+  // workgroups: at most one per 64 tokens (plus one per sequence) and head
+  if ((p->total_tokens / 64 + p->num_seqs + 8) * p->num_heads > kInt32Max) return KDA_ERR_TOO_LARGE;
   return KDA_OK;
+}
+
+int log2_of(int32_t v) { return 31 - __builtin_clz((unsigned)v); }
+
+// the piece length of a scan, 0: no split
+int32_t ssm_pieces(const kda_ssm_problem* p) {
+  return p->piece_tokens && p->piece_tokens < p->total_tokens ? p->piece_tokens : 0;
+}
+
+// workspace of a split: a state and a decay per piece and head
+size_t ssm_bytes(const kda_ssm_problem* p, int32_t piece) {
+  if (!piece) return 0;
+  const size_t slots = (size_t)kda::span_slots(p->num_seqs, p->total_tokens, log2_of(piece));
+  return slots * p->num_heads * ((size_t)p->d_state * p->head_dim + 1) * 4;
 }
 
 }  // namespace
@@ -251,7 +268,7 @@ kda_status kda_ssm_plan(const kda_ssm_problem* p, int32_t* piece_tokens) {
   if (!piece_tokens) return KDA_ERR_INVALID_ARG;
   const kda_status st = check_ssm(p);
   if (st != KDA_OK) return st;
-  *piece_tokens = 0;
+  *piece_tokens = ssm_pieces(p);
   return KDA_OK;
 }
 
@@ -259,7 +276,7 @@ kda_status kda_ssm_prefill_workspace_size(const kda_ssm_problem* p, size_t* byte
   if (!bytes) return KDA_ERR_INVALID_ARG;
   const kda_status st = check_ssm(p);
   if (st != KDA_OK) return st;
-  *bytes = 0;
+  *bytes = ssm_bytes(p, ssm_pieces(p));
   return KDA_OK;
 }
 
@@ -285,6 +302,8 @@ kda_status kda_ssm_validate(const kda_ssm_problem* p, const void* x, const float
   if (any_overlap(rf, {r.x, r.B, r.C, r.z, r.dt, r.A, r.D, r.bias, rcu, rw})) return KDA_ERR_OVERLAP;
   if (any_overlap(rw, {r.x, r.B, r.C, r.z, r.dt, r.A, r.D, r.bias, rcu, ri})) return KDA_ERR_OVERLAP;
   if (overlaps(rf, ri) && !exact(rf, ri)) return KDA_ERR_OVERLAP;
+  if (p->piece_tokens && (workspace ? workspace_bytes : 0) < ssm_bytes(p, ssm_pieces(p)))
+    return KDA_ERR_WORKSPACE_TOO_SMALL;
   return KDA_OK;
 }
 
@@ -302,6 +321,13 @@ kda_status kda_ssm_prefill(const kda_ssm_problem* p, const uint16_t* x, const fl
   a.initial = initial_state;
   a.final_state = final_state;
   a.state_bf16 = p->state_dtype == KDA_STATE_BF16;
+  int32_t piece = ssm_pieces(p);
+  if ((workspace ? workspace_bytes : 0) < ssm_bytes(p, piece)) piece = 0;
+  a.shift = piece ? log2_of(piece) : kda::kUnsplit;
+  a.slots = kda::span_slots(p->num_seqs, p->total_tokens, a.shift);
+  a.piece_state = piece ? static_cast<float*>(workspace) : nullptr;
+  a.piece_decay = piece ? a.piece_state + a.slots * p->num_heads * p->d_state * p->head_dim : nullptr;
+  a.pass = 0;
   return done(kda::launch_ssm(a, static_cast<hipStream_t>(stream)));
 }
 

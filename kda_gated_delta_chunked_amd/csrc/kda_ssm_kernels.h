@@ -151,7 +151,13 @@ struct SsmArgs {
   const void* initial;      // [seqs, H, N, P] or NULL
   void* final_state;        // or NULL
   int state_bf16;
+  int shift;                // a piece is 1 << shift tokens (kUnsplit: a whole sequence)
+  int64_t slots;            // span_slots of the pieces
+  float* piece_state;       // [slots, H, N, P], or NULL: no split
+  float* piece_decay;       // [slots, H]
+  int pass;                 // 0: no split; 1, 2: the split's launches (set by launch_ssm)
 };
+constexpr int kUnsplit = 40;
 hipError_t launch_ssm(const SsmArgs& a, hipStream_t stream);
 
 struct SsmStepArgs {

@@ -123,15 +123,29 @@ def test_ssm_accepts():
 @pytest.mark.parametrize("want,kw", [
     (UNSUPPORTED, dict(P=32)), (UNSUPPORTED, dict(S_=256)), (INVALID, dict(H=0)), (INVALID, dict(G=0)),
     (INVALID, dict(G=3)), (INVALID, dict(soft=2)), (UNSUPPORTED, dict(sd=2)), (INVALID, dict(N=0)),
-    (INVALID, dict(T=-1)), (INVALID, dict(piece=-64)), (INVALID, dict(piece=32)), (INVALID, dict(xs=248)),
+    (INVALID, dict(T=-1)), (INVALID, dict(piece=-64)), (INVALID, dict(piece=32)), (INVALID, dict(piece=192)), (WS, dict(piece=64)), (INVALID, dict(xs=248)), (INVALID, dict(xs=1 << 23)),
     (INVALID, dict(bs=250)), (INVALID, dict(zs=260)), (INVALID, dict(A=0)), (INVALID, dict(x=0)),
     (INVALID, dict(dt=0)), (INVALID, dict(C=0)), (INVALID, dict(out=0)), (INVALID, dict(cu=0, T=129)),
     (ALIGN, dict(dt=at(1) + 4)), (ALIGN, dict(B=at(3) + 2)), (OVERLAP, dict(out=at(0))),
     (OVERLAP, dict(out=at(1))), (OVERLAP, dict(out=at(9))), (OVERLAP, dict(fin=at(9) + 16)),
     (OVERLAP, dict(fin=at(6))), (TOO_LARGE, dict(T=1 << 31)), (TOO_LARGE, dict(H=1 << 24)),
-    (TOO_LARGE, dict(N=1 << 28, H=2))])
+    (TOO_LARGE, dict(N=1 << 30, H=2, G=2))])
 def test_ssm_refuses(want, kw):
     assert ssm(**kw) == want
+
+
+def test_ssm_workspace_of_a_split():
+    p = ssm_problem(N=3, T=1000, H=4, G=1, P=64, S_=128, piece=256)
+    # floor(1000 / 256) + 3 pieces, a state and a decay per head
+    want = (3 + 3) * 4 * (64 * 128 + 1) * 4
+    assert K.ssm_workspace_size(p) == want and K.ssm_plan(p) == 256
+    ws = dict(ws=at(12), p=p)
+    assert ssm(want, **ws) == OK
+    assert ssm(want - 1, **ws) == WS
+    assert ssm(want, ws=0, p=p) == WS
+    assert ssm(want, ws=at(10), p=p) == OVERLAP
+    # no sequence is longer than the piece: nothing to split
+    assert K.ssm_workspace_size(ssm_problem(N=1, T=256, piece=256)) == 0
 
 
 STEP = ["x", "dt", "A", "B", "C", "D", "z", "bias", "pool", "idx", "out"]
