@@ -126,9 +126,9 @@ typedef struct {
   int32_t cu_seqlens_int64;  /* 0: int32 offsets, 1: int64 */
   int32_t piece_tokens;      /* 0 = automatic.  Else sequences longer than this run in pieces of
                                 this many tokens (a power of two from 64 on), side by side: a
-                                first launch runs each sequence's first piece and the states
-                                that the pieces between add by themselves, a second runs the
-                                later pieces from their combined states.  Results equal the unsplit scan's up to
+                                first launch computes the state that each piece adds, a second
+                                joins them into the states ahead of the pieces, a third runs
+                                the pieces from those.  Results equal the unsplit scan's up to
                                 rounding */
   int64_t x_stride;          /* elements between rows, a multiple of 8, at least the row and below
                                 2^23; 0 = the row */

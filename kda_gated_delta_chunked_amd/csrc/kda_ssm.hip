@@ -20,6 +20,12 @@
 // leave M in LDS as bf16.  The next chunk's rows are in flight to registers
 // meanwhile.  Sums of logarithms are taken in 64 bits (a chunk's sum can be
 // large where the difference of two tokens' sums is small).
+//
+// Few (sequence, head) pairs leave the device idle behind their chains of
+// chunks.  A split cuts sequences into pieces: a first launch computes the state
+// that each piece's own tokens add (the first piece's from the initial state),
+// a second joins these into the states ahead of each piece, and a third runs
+// all pieces side by side from them.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -145,14 +151,16 @@ struct Rows {
   }
   // whether any value is an infinity or a NaN
   __device__ __forceinline__ bool not_finite() const {
-    bool bad = false;
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 top = {0, 0};  // the largest magnitudes, as 16-bit numbers
 #pragma unroll
     for (int i = 0; i < COUNT; ++i) {
       const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) bad |= (w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u;
+      for (int j = 0; j < 4; ++j)
+        top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, w[j] & 0x7fff7fffu));
     }
-    return bad;
+    return top[0] >= 0x7f80 || top[1] >= 0x7f80;
   }
 };
 
@@ -174,20 +182,23 @@ __device__ __forceinline__ double prefix_sum(double v) {
   v = add_shifted<0x142, 0xa>(v);
   return add_shifted<0x143, 0xc>(v);
 }
-__device__ __forceinline__ double last_lane(double v) {
+__device__ __forceinline__ double lane_of(double v, int lane) {
   const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, 63);
-  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
   return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
-// a head's decays over a chunk
-struct Gates {
-  float cum_hi[L], cum_lo[L];  // c_t log2(e) in two floats
+// A head's decays over a chunk.  M's tiles take their differences of c_t from
+// sums that start at their own 32 tokens, in fp32: an error of 2^-24 of such a
+// sum matters least where the decays, and so the sums, are large.
+struct __attribute__((aligned(16))) Gates {
+  float cum[L];         // log2(e) (c_t - c_31 for t >= 32, c_t before)
   float step[L];
-  float from_start[L];         // exp(c_t)
-  float to_end[L];             // w_t
-  float total;                 // exp(c_63)
+  float mid[L];         // exp(c_31 - c_j) s_j for j < 32, exp(c_t - c_31) from 32 on
+  float from_start[L];  // exp(c_t)
+  float to_end[L];      // w_t
+  float total;          // exp(c_63)
 };
 
 __device__ __forceinline__ int64_t uniform(int64_t v) {
@@ -197,11 +208,20 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 }
 
 template <int N, int P, int HPW>
+struct __attribute__((aligned(16))) Tiles {
+  uint8_t B[L * N * 2], C[L * N * 2], X[L * HPW * P * 2], M[HPW][L * L * 2];
+  Gates gates[2][HPW];
+  int odd[2];  // whether the chunk's x holds infinities or NaNs
+};
+
+// One piece (or a whole sequence) and HPW heads of a group per workgroup.
+// FULL: with outputs; else the state that a piece's own tokens add.  The chunk
+// loop's memory accesses are the same on every path, so that waiting for the
+// next chunk's rows never waits for this one's stores.
+template <int N, int P, int HPW, bool FULL>
 __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 1 : 2) void kda_ssm_kernel(SsmArgs a) {
   constexpr int WPH = P / 32, WAVES = HPW * WPH, THREADS = WAVES * 64, XC = HPW * P, NB = N / 32;
-  __shared__ __attribute__((aligned(16))) uint8_t tB[L * N * 2], tC[L * N * 2], tX[L * XC * 2], tM[HPW][L * L * 2];
-  __shared__ __attribute__((aligned(16))) Gates gates[2][HPW];
-  __shared__ int odd[2];  // whether the chunk's x holds infinities or NaNs
+  __shared__ Tiles<N, P, HPW> lds;
 
   const SsmTokens& k = a.t;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -215,72 +235,68 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 1 : 2) void kda_ssm_kern
   const Span sp = span_of(a.pk, a.shift, slot);
   if (sp.k < 0) return;
   const int seq = __builtin_amdgcn_readfirstlane(sp.seq), piece = __builtin_amdgcn_readfirstlane(sp.k);
-  const int64_t begin = uniform(sp.begin), end = uniform(sp.end);
-  const int64_t pieces = a.pass ? (end - begin + ((int64_t)1 << a.shift) - 1) >> a.shift : 1;
-  const bool last = piece + 1 >= pieces;
-  // first launch: first pieces whole, the states of those between; second
-  // launch: the later pieces whole
-  if (a.pass == 1 && piece > 0 && last) return;
-  if (a.pass == 2 && piece == 0) return;
-  const bool full = a.pass != 1 || piece == 0;
-  const int64_t from = begin + ((int64_t)piece << a.shift);
-  const int64_t to = a.pass && !last ? from + ((int64_t)1 << a.shift) : end;
-
-  const int head0 = (int)((blk >> 3) % HG) * HPW;
-  const int hh = wave / WPH, head = head0 + hh, pc = (wave % WPH) * 32;
-  const int g = head0 / (k.H / k.G);
+  const int64_t end = uniform(sp.end), from = uniform(sp.begin) + ((int64_t)piece << a.shift);
+  const bool last = !a.piece_state || end - from <= (int64_t)1 << a.shift;
+  int64_t to = last ? end : from + ((int64_t)1 << a.shift);
+  const int head0 = (int)((blk >> 3) % HG) * HPW, hh = wave / WPH, head = head0 + hh, pc = (wave % WPH) * 32;
 
   // state rows 32 nb + 16 (r / 8) + 8 up + r % 8 of column pc + l32
   const int64_t state0 = (int64_t)head * N * P + (int64_t)(8 * up) * P + pc + l32;
   const int64_t per_seq = (int64_t)k.H * N * P;
   auto row_of = [](int nb, int r) { return (32 * nb + 16 * (r >> 3) + (r & 7)) * P; };
   f32x16 S[NB] = {};
-  if (a.pass == 2) {
-    // the state ahead of this piece: S <- d_q S + (what piece q adds)
-    for (int q = 0; q < piece; ++q) {
-      const int64_t sl = slot - piece + q;
-      const float* add = a.piece_state + sl * per_seq + state0;
-      const float d = q ? a.piece_decay[sl * k.H + head] : 0.f;
+  // A piece starts from the state ahead of it; the first launch of a split
+  // starts first pieces from the initial state and the others from zero.
+  const float* s0 = FULL && a.piece_state ? a.piece_state + slot * per_seq + state0
+                    : a.initial && piece == 0 && !a.state_bf16
+                        ? static_cast<const float*>(a.initial) + seq * per_seq + state0
+                        : nullptr;
+  if (s0) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) S[nb][r] = s0[row_of(nb, r)];
+  } else if (a.initial && piece == 0) {
+    const uint16_t* s16 = static_cast<const uint16_t*>(a.initial) + seq * per_seq + state0;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) S[nb][r] = bf16_f32(s16[row_of(nb, r)]);
+  }
+  if (!FULL) {
+    // the second launch takes every piece's state from here, so that the
+    // final state may overwrite the initial one
+    if (piece == 0) {
+      float* out = a.piece_state + slot * per_seq + state0;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) S[nb][r] = (q ? d * S[nb][r] : 0.f) + add[row_of(nb, r)];
+        for (int r = 0; r < 16; ++r) out[row_of(nb, r)] = S[nb][r];
     }
-  } else if (a.initial && full) {
-    if (a.state_bf16) {
-      const uint16_t* s0 = static_cast<const uint16_t*>(a.initial) + seq * per_seq + state0;
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) S[nb][r] = bf16_f32(s0[row_of(nb, r)]);
-    } else {
-      const float* s0 = static_cast<const float*>(a.initial) + seq * per_seq + state0;
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) S[nb][r] = s0[row_of(nb, r)];
-    }
+    if (last) return;
   }
 
+  double log_decay[HPW] = {};  // of the whole piece, in the last wave
+  const int g = head0 / (k.H / k.G);
   const uint16_t* Bp = k.B + g * N;
   const uint16_t* Cp = k.C + g * N;
   const uint16_t* Xp = k.x + (int64_t)head0 * P;
   const uint16_t* Zp = k.z ? k.z + (int64_t)head0 * P : nullptr;
   uint16_t* Op = k.out + (int64_t)head0 * P;
   const float Dh = k.D ? k.D[head] : 0.f;
+  const bool gate_wave = wave == WAVES - 1;
 
-  // rows left from a token on, at most a chunk
-  auto left = [&](int64_t tok) { return to - tok < L ? (int)(to - tok) : L; };
+  // rows left from a token on, at most a chunk, none past the end
+  auto left = [&](int64_t tok) { return to - tok >= L ? L : (to > tok ? (int)(to - tok) : 0); };
   Rows<N, THREADS> rB, rC;
   Rows<XC, THREADS> rX;
+  float rdt[HPW];
   auto fetch = [&](int64_t tok) {
     rB.load(Bp, k.b_stride, tok, left(tok));
-    if (full) rC.load(Cp, k.c_stride, tok, left(tok));
+    if constexpr (FULL) rC.load(Cp, k.c_stride, tok, left(tok));
     rX.load(Xp, k.x_stride, tok, left(tok));
   };
-  // the steps and decays of a chunk, by the last wave, ahead of time
-  double log_decay[HPW] = {};  // of the whole piece so far
-  float rdt[HPW] = {};
+  // a chunk's steps, and its decays by the last wave, one chunk ahead
   auto fetch_steps = [&](int64_t tok) {
     const Window w(k.dt, (int64_t)k.H * 4, tok, left(tok), k.H * 4);
 #pragma unroll
@@ -291,30 +307,23 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 1 : 2) void kda_ssm_kern
     for (int q = 0; q < HPW; ++q) {
       const int h = head0 + q;
       const float step = lane < left(tok) ? ssm_step_of(rdt[q], k.dt_bias ? k.dt_bias[h] : 0.f, k.softplus) : 0.f;
-      const double cum = prefix_sum((double)step * (double)k.A[h]);
-      const double sum = last_lane(cum);
+      const double cum = prefix_sum((double)step * (double)k.A[h] * kLog2e);
+      const double sum = lane_of(cum, 63), mid = lane_of(cum, 31);
       log_decay[q] += sum;
-      Gates& gt = gates[buf][q];
-      const double c2 = cum * kLog2e;
-      const float hi = (float)c2;
-      gt.cum_hi[lane] = hi;
-      gt.cum_lo[lane] = (float)(c2 - (double)hi);
+      Gates& gt = lds.gates[buf][q];
+      gt.cum[lane] = (float)(lane < 32 ? cum : cum - mid);
       gt.step[lane] = step;
-      gt.from_start[lane] = expf((float)cum);
-      gt.to_end[lane] = expf((float)(sum - cum)) * step;
-      if (lane == 0) gt.total = expf((float)sum);
+      gt.mid[lane] = __builtin_amdgcn_exp2f((float)(lane < 32 ? mid - cum : cum - mid)) * (lane < 32 ? step : 1.f);
+      gt.from_start[lane] = __builtin_amdgcn_exp2f((float)cum);
+      gt.to_end[lane] = __builtin_amdgcn_exp2f((float)(sum - cum)) * step;
+      if (lane == 0) gt.total = __builtin_amdgcn_exp2f((float)sum);
     }
   };
-  const bool gate_wave = wave == WAVES - 1;
-  if (from < to) {
-    fetch(from);
-    if (gate_wave) {
-      fetch_steps(from);
-      make_gates(from, 0);
-      if (from + L < to) fetch_steps(from + L);
-    }
-  }
-  if (tid < 2) odd[tid] = 0;
+  fetch_steps(from);
+  fetch(from);
+  if (gate_wave) make_gates(from, 0);
+  fetch_steps(from + L);
+  if (tid < 2) lds.odd[tid] = 0;
   lds_barrier();
 
   // a lane's addresses: operands whose lanes are rows (of B and C, and of M),
@@ -333,21 +342,20 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 1 : 2) void kda_ssm_kern
   int c = 0;
   for (int64_t tok = from; tok < to; tok += L, c ^= 1) {
     forget(at_row); forget(at_m); forget(at_x); forget(at_x4); forget(at_b); forget(at_b4); forget(at_o);
-    rB.store(tB);
-    if (full) rC.store(tC);
-    rX.store(tX);
-    if (rX.not_finite()) odd[c] = 1;
+    rB.store(lds.B);
+    if constexpr (FULL) rC.store(lds.C);
+    rX.store(lds.X);
+    if (FULL && rX.not_finite()) lds.odd[c] = 1;
     lds_barrier();
-    if (tok + L < to) fetch(tok + L);
-    const bool slow = odd[c] != 0;
-    if (tid == 0) odd[c ^ 1] = 0;
-    if (gate_wave && tok + L < to) {
-      make_gates(tok + L, c ^ 1);
-      if (tok + 2 * L < to) fetch_steps(tok + 2 * L);
-    }
+    fetch(tok + L);
+    const bool slow = FULL && lds.odd[c] != 0;
+    if (tid == 0) lds.odd[c ^ 1] = 0;
+    if (gate_wave) make_gates(tok + L, c ^ 1);
+    fetch_steps(tok + 2 * L);
+    const Gates& gt = lds.gates[c][hh];
 
     f32x16 Y[2] = {};
-    if (full) {
+    if constexpr (FULL) {
       // M: the lower triangle of C B^T in 32 x 32 tiles (transposed: lane = t,
       // registers = j), decayed, to LDS
       for (int tile = wave; tile < 3; tile += WAVES) {
@@ -355,23 +363,27 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 1 : 2) void kda_ssm_kern
         f32x16 G = {};
 #pragma unroll
         for (int s = 0; s < N / 16; ++s)
-          G = mfma(rows_frag(tB + tj * N * 2, at_row ^ (s << 5)), rows_frag(tC + ti * N * 2, at_row ^ (s << 5)), G);
+          G = mfma(rows_frag(lds.B + tj * N * 2, at_row ^ (s << 5)), rows_frag(lds.C + ti * N * 2, at_row ^ (s << 5)), G);
 #pragma unroll
         for (int q = 0; q < HPW; ++q) {
-          const Gates& gt = gates[c][q];
-          const float hi = gt.cum_hi[ti + l32], lo = gt.cum_lo[ti + l32];
+          const Gates& gq = lds.gates[c][q];
+          const float ct = gq.cum[ti + l32], ft = gq.mid[32 + l32];
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
             const int j = tj + 8 * b + 4 * up;
             float mv[4];
+            if (tile == 1) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float e = (hi - gt.cum_hi[j + i]) + (lo - gt.cum_lo[j + i]);
-              mv[i] = G[4 * b + i] * (__builtin_amdgcn_exp2f(e) * gt.step[j + i]);
-              settle(mv[i]);  // computed for every lane: a select, no branches
-              mv[i] = j + i <= ti + l32 ? mv[i] : 0.f;
+              for (int i = 0; i < 4; ++i) mv[i] = G[4 * b + i] * (ft * gq.mid[j + i]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                mv[i] = G[4 * b + i] * (__builtin_amdgcn_exp2f(ct - gq.cum[j + i]) * gq.step[j + i]);
+                settle(mv[i]);  // computed for every lane: a select, no branches
+                mv[i] = j + i <= ti + l32 ? mv[i] : 0.f;
+              }
             }
-            *reinterpret_cast<uint2*>(tM[q] + ti * L * 2 + ((at_m ^ (up << 4) ^ (((tj >> 3) + b) << 4)) + 8 * up)) =
+            *reinterpret_cast<uint2*>(lds.M[q] + ti * L * 2 + ((at_m ^ (up << 4) ^ (((tj >> 3) + b) << 4)) + 8 * up)) =
                 make_uint2(bf16_pair(mv[0], mv[1]), bf16_pair(mv[2], mv[3]));
           }
         }
@@ -385,19 +397,19 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 1 : 2) void kda_ssm_kern
         for (int i = 0; i < 4; ++i)
           u[i] = bf16_pair(S[s >> 1][8 * (s & 1) + 2 * i], S[s >> 1][8 * (s & 1) + 2 * i + 1]);
         const bf16x8 sf = as_frag(u);
-        Y[0] = mfma(sf, rows_frag(tC, at_row ^ (s << 5)), Y[0]);
-        Y[1] = mfma(sf, rows_frag(tC + 32 * N * 2, at_row ^ (s << 5)), Y[1]);
+        Y[0] = mfma(sf, rows_frag(lds.C, at_row ^ (s << 5)), Y[0]);
+        Y[1] = mfma(sf, rows_frag(lds.C + 32 * N * 2, at_row ^ (s << 5)), Y[1]);
       }
 #pragma unroll
       for (int tb = 0; tb < 2; ++tb) {
-        const float e = gates[c][hh].from_start[32 * tb + l32];
+        const float e = gt.from_start[32 * tb + l32];
 #pragma unroll
         for (int r = 0; r < 16; ++r) Y[tb][r] *= e;
       }
     }
 
     // S <- exp(c_63) S + B^T (w x)
-    const float total = gates[c][hh].total;
+    const float total = gt.total;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -405,25 +417,32 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 1 : 2) void kda_ssm_kern
     bf16x8 xf[4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      xf[s] = cols_frag(tX + 16 * s * XC * 2, at_x, at_x4);
+      xf[s] = cols_frag(lds.X + 16 * s * XC * 2, at_x, at_x4);
+      bf16x8 bf[NB];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) bf[nb] = cols_frag(lds.B + 16 * s * N * 2, at_b ^ (nb << 6), at_b4 ^ (nb << 6));
+      const float4 w0 = *reinterpret_cast<const float4*>(gt.to_end + 16 * s + 8 * up);
+      const float4 w1 = *reinterpret_cast<const float4*>(gt.to_end + 16 * s + 8 * up + 4);
+      const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
       float v[8];
       bf16x8_f32(__builtin_bit_cast(uint4, xf[s]), v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= gates[c][hh].to_end[16 * s + 8 * up + i];
+      for (int i = 0; i < 8; ++i) v[i] *= w[i];
       bf16x8 part[3];
       split3(v, part);
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const bf16x8 bf = cols_frag(tB + 16 * s * N * 2, at_b ^ (nb << 6), at_b4 ^ (nb << 6));
+      for (int q = 0; q < 3; ++q)
 #pragma unroll
-        for (int q = 0; q < 3; ++q) S[nb] = mfma(bf, part[q], S[nb]);
-      }
+        for (int nb = 0; nb < NB; ++nb) S[nb] = mfma(bf[nb], part[q], S[nb]);
     }
 
-    if (full) {
+    if constexpr (FULL) {
+      const int width = HPW * P * 2, rows = left(tok);
+      const Window ow(Op, k.out_stride * 2, tok, rows, width), zw(Zp, k.z_stride * 2, tok, Zp ? rows : 0, width);
+      const int col = (hh * P + pc + 4 * up) * 2;
       lds_barrier();
       // y^T += x^T M^T
-      const uint8_t* M = tM[hh];
+      const uint8_t* M = lds.M[hh];
       if (!slow) {
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
@@ -441,34 +460,30 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 1 : 2) void kda_ssm_kern
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
               const int p = hh * P + pc + 8 * (r >> 2) + 4 * up + (r & 3);
-              Y[tb][r] += w * bf16_f32(*reinterpret_cast<const uint16_t*>(tX + tile_at<XC>(j, p >> 3) + 2 * (p & 7)));
+              Y[tb][r] += w * bf16_f32(*reinterpret_cast<const uint16_t*>(lds.X + tile_at<XC>(j, p >> 3) + 2 * (p & 7)));
             }
           }
         }
       }
 
       // out: lane = token, four columns at a time
-      const int width = HPW * P * 2, rows = left(tok);
-      const Window ow(Op, k.out_stride * 2, tok, rows, width), zw(Zp, k.z_stride * 2, tok, Zp ? rows : 0, width);
-      const int col = (hh * P + pc + 4 * up) * 2;
 #pragma unroll
       for (int tb = 0; tb < 2; ++tb) {
         const int t = 32 * tb + l32;
-        const int oat = t * (int)(k.out_stride * 2) + col;
+        const int oat = t * (int)(k.out_stride * 2) + col, zat = t * (int)(k.z_stride * 2) + col;
+        uint2 zv[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) zv[b] = zw.load8(zat + 16 * b);
         if (k.D) {
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
-            const uint2 xv = *reinterpret_cast<const uint2*>(tX + 32 * tb * XC * 2 + (at_o ^ (b << 4)));
+            const uint2 xv = *reinterpret_cast<const uint2*>(lds.X + 32 * tb * XC * 2 + (at_o ^ (b << 4)));
             const uint32_t xw[4] = {xv.x << 16, xv.x & 0xffff0000u, xv.y << 16, xv.y & 0xffff0000u};
 #pragma unroll
             for (int i = 0; i < 4; ++i) Y[tb][4 * b + i] += Dh * __uint_as_float(xw[i]);
           }
         }
         if (Zp) {
-          const int zat = t * (int)(k.z_stride * 2) + col;
-          uint2 zv[4];
-#pragma unroll
-          for (int b = 0; b < 4; ++b) zv[b] = zw.load8(zat + 16 * b);
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
             const uint32_t zb[4] = {zv[b].x << 16, zv[b].x & 0xffff0000u, zv[b].y << 16, zv[b].y & 0xffff0000u};
@@ -485,16 +500,17 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 1 : 2) void kda_ssm_kern
     lds_barrier();  // the tiles are rewritten next
   }
 
-  if (!last) {
-    float* out = a.piece_state + slot * per_seq + state0;
+  if (!FULL) {
+    // the state ahead of the next piece, if nothing came into this one
+    float* out = a.piece_state + (slot + 1) * per_seq + state0;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int r = 0; r < 16; ++r) out[row_of(nb, r)] = S[nb][r];
     if (gate_wave && lane == 0)
 #pragma unroll
-      for (int q = 0; q < HPW; ++q) a.piece_decay[slot * k.H + head0 + q] = expf((float)log_decay[q]);
-  } else if (a.final_state) {
+      for (int q = 0; q < HPW; ++q) a.piece_decay[slot * k.H + head0 + q] = __builtin_amdgcn_exp2f((float)log_decay[q]);
+  } else if (last && a.final_state) {
     if (a.state_bf16) {
       uint16_t* out = static_cast<uint16_t*>(a.final_state) + seq * per_seq + state0;
 #pragma unroll
@@ -511,16 +527,55 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 1 : 2) void kda_ssm_kern
   }
 }
 
+// Between a split's launches: the state ahead of piece q + 1 is what piece q
+// adds plus the state ahead of q, decayed over q; four elements per thread.
+// The reads do not depend on the sums, eight of them are in flight.
+__global__ __launch_bounds__(256) void kda_ssm_join_kernel(SsmArgs a, int blocks_per_head) {
+  const int64_t per_head = (int64_t)a.t.N * a.t.P, per_seq = a.t.H * per_head;
+  const int seq = (int)(blockIdx.x / ((int64_t)blocks_per_head * a.t.H));
+  const int in = (int)(blockIdx.x % ((int64_t)blocks_per_head * a.t.H));
+  const int h = in / blocks_per_head;
+  const int64_t begin = cu_at(a.pk, seq);
+  int64_t end = cu_at(a.pk, seq + 1);
+  if (end < begin) end = begin;
+  const int64_t pieces = (end - begin + ((int64_t)1 << a.shift) - 1) >> a.shift;
+  if (pieces < 3) return;  // the first piece started from the initial state
+  const int64_t slot = (begin >> a.shift) + seq;
+  float* at = a.piece_state + slot * per_seq + h * per_head + ((in % blocks_per_head) * 256 + threadIdx.x) * 4;
+  const float* decay = a.piece_decay + slot * a.t.H + h;
+  float4 S = *reinterpret_cast<const float4*>(at + per_seq);
+  for (int64_t q = 1; q + 1 < pieces; q += 8) {
+    float4 add[8];
+    float d[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (q + i + 1 < pieces) {
+        add[i] = *reinterpret_cast<const float4*>(at + (q + i + 1) * per_seq);
+        d[i] = decay[(q + i) * a.t.H];
+      }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (q + i + 1 < pieces) {
+        S.x = d[i] * S.x + add[i].x;
+        S.y = d[i] * S.y + add[i].y;
+        S.z = d[i] * S.z + add[i].z;
+        S.w = d[i] * S.w + add[i].w;
+        *reinterpret_cast<float4*>(at + (q + i + 1) * per_seq) = S;
+      }
+  }
+}
+
 template <int N, int P, int HPW>
-void launch(SsmArgs a, hipStream_t stream) {
+void launch(const SsmArgs& a, hipStream_t stream) {
   const int64_t blocks = (a.slots + 7) / 8 * 8 * (a.t.H / HPW);
   const dim3 grid((unsigned)blocks), block(HPW * P * 2);
   if (a.piece_state) {
-    a.pass = 1;
-    hipLaunchKernelGGL((kda_ssm_kernel<N, P, HPW>), grid, block, 0, stream, a);
-    a.pass = 2;
+    const int blocks_per_head = N * P / 1024;
+    const int64_t join = (int64_t)a.pk.N * a.t.H * blocks_per_head;
+    hipLaunchKernelGGL((kda_ssm_kernel<N, P, HPW, false>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL(kda_ssm_join_kernel, dim3((unsigned)join), dim3(256), 0, stream, a, blocks_per_head);
   }
-  hipLaunchKernelGGL((kda_ssm_kernel<N, P, HPW>), grid, block, 0, stream, a);
+  hipLaunchKernelGGL((kda_ssm_kernel<N, P, HPW, true>), grid, block, 0, stream, a);
 }
 
 // Heads of 64 columns run two to a workgroup where a group has an even number

@@ -327,7 +327,6 @@ kda_status kda_ssm_prefill(const kda_ssm_problem* p, const uint16_t* x, const fl
   a.slots = kda::span_slots(p->num_seqs, p->total_tokens, a.shift);
   a.piece_state = piece ? static_cast<float*>(workspace) : nullptr;
   a.piece_decay = piece ? a.piece_state + a.slots * p->num_heads * p->d_state * p->head_dim : nullptr;
-  a.pass = 0;
   return done(kda::launch_ssm(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -32,9 +32,9 @@ __device__ __forceinline__ uint4 f32_bf16x8(const float* f) {
   return make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
 }
 
-// v sigmoid(v); for v -> -inf the exponential overflows to inf and the
-// quotient is -0
-__device__ __forceinline__ float silu(float v) { return v / (1.f + __expf(-v)); }
+// v sigmoid(v); far below zero the exponential overflows to inf and its
+// reciprocal (one unit in the last place off at most) is zero
+__device__ __forceinline__ float silu(float v) { return v * __builtin_amdgcn_rcpf(1.f + __expf(-v)); }
 
 // Token spans.  A packed batch is covered by spans of `len` tokens that start
 // at each sequence's first token.  Sequence n's spans take the slots from
@@ -153,9 +153,8 @@ struct SsmArgs {
   int state_bf16;
   int shift;                // a piece is 1 << shift tokens (kUnsplit: a whole sequence)
   int64_t slots;            // span_slots of the pieces
-  float* piece_state;       // [slots, H, N, P], or NULL: no split
+  float* piece_state;       // [slots, H, N, P], the state ahead of each piece; NULL: no split
   float* piece_decay;       // [slots, H]
-  int pass;                 // 0: no split; 1, 2: the split's launches (set by launch_ssm)
 };
 constexpr int kUnsplit = 40;
 hipError_t launch_ssm(const SsmArgs& a, hipStream_t stream);
