@@ -1,12 +1,12 @@
 // kda_ssm.hip -- the selective state space scan for prompts, for gfx950
-// (MI355X), in chunks of 64 tokens on the matrix cores.
+// (MI355X), in chunks of 32 tokens on the matrix cores.
 //
 // Per head, with the step s_t, the logarithm of the decay a_t = s_t A, its sum
 // c_t over a chunk's tokens up to t, and S the state ahead of the chunk, the
 // recurrence S <- exp(a_t) S + s_t B_t x_t^T, y_t = S^T C_t gives
 //   y_t = exp(c_t) S^T C_t + sum_{j <= t} M[t, j] x_j,
 //                       M[t, j] = (C_t . B_j) exp(c_t - c_j) s_j
-//   S  <- exp(c_63) S + sum_j w_j B_j x_j^T,  w_j = exp(c_63 - c_j) s_j
+//   S  <- exp(c_31) S + sum_j w_j B_j x_j^T,  w_j = exp(c_31 - c_j) s_j
 // A workgroup runs one sequence (or a piece of one) and HPW heads of one
 // group, chunk after chunk.  Each wave owns 32 columns of one head's state,
 // all d_state rows in fp32 accumulators, so both products of the state stay
@@ -39,14 +39,19 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int L = 64;  // tokens per chunk
+constexpr int L = 32;  // tokens per chunk
 constexpr double kLog2e = 1.4426950408889634;
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ f32x4 mfma16(const bf16x8& a, const bf16x8& b, const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
 __device__ __forceinline__ f32x16 mfma(const bf16x8& a, const bf16x8& b, const f32x16& c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// A tile of 64 rows of COLS bf16 in LDS, rows packed, 16-byte chunks swizzled
+// A tile of L rows of COLS bf16 in LDS, rows packed, 16-byte chunks swizzled
 // within a row so that neither kind of operand read has bank conflicts: 16
 // consecutive rows' chunk c (an operand whose lanes are rows) land on 16
 // different bank groups, and so do the four chunks of four consecutive rows (a
@@ -127,7 +132,7 @@ struct Window {
   }
 };
 
-// 64 rows of COLS bf16 on their way from memory to a tile
+// L rows of COLS bf16 on their way from memory to a tile
 template <int COLS, int THREADS>
 struct Rows {
   static constexpr int PER_ROW = COLS / 8, COUNT = L * PER_ROW / THREADS, STEP = THREADS / PER_ROW;
@@ -149,19 +154,6 @@ struct Rows {
         *reinterpret_cast<uint4*>(tile + tile_at<COLS>(threadIdx.x / PER_ROW + i * STEP, threadIdx.x % PER_ROW)) = v[i];
     }
   }
-  // whether any value is an infinity or a NaN
-  __device__ __forceinline__ bool not_finite() const {
-    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-    u16x2 top = {0, 0};  // the largest magnitudes, as 16-bit numbers
-#pragma unroll
-    for (int i = 0; i < COUNT; ++i) {
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, w[j] & 0x7fff7fffu));
-    }
-    return top[0] >= 0x7f80 || top[1] >= 0x7f80;
-  }
 };
 
 // One step of a sum over the wave's lanes: adds what a data-parallel shift
@@ -173,14 +165,14 @@ __device__ __forceinline__ double add_shifted(double v) {
   const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
   return v + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
-// sums of lanes 0..i in lane i: within rows of 16 lanes, then over the rows
-__device__ __forceinline__ double prefix_sum(double v) {
+// sums of lanes 0..i in lane i and of lanes 32..i in lane i >= 32: within rows
+// of 16 lanes, then from a row to the next
+__device__ __forceinline__ double prefix_sums(double v) {
   v = add_shifted<0x111, 0xf>(v);
   v = add_shifted<0x112, 0xf>(v);
   v = add_shifted<0x114, 0xf>(v);
   v = add_shifted<0x118, 0xf>(v);
-  v = add_shifted<0x142, 0xa>(v);
-  return add_shifted<0x143, 0xc>(v);
+  return add_shifted<0x142, 0xa>(v);
 }
 __device__ __forceinline__ double lane_of(double v, int lane) {
   const uint64_t u = __builtin_bit_cast(uint64_t, v);
@@ -189,16 +181,43 @@ __device__ __forceinline__ double lane_of(double v, int lane) {
   return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
-// A head's decays over a chunk.  M's tiles take their differences of c_t from
-// sums that start at their own 32 tokens, in fp32: an error of 2^-24 of such a
-// sum matters least where the decays, and so the sums, are large.
+// Whether any lane's fragments hold an infinity or a NaN.
+__device__ __forceinline__ bool any_not_finite(const bf16x8 (&f)[2]) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 top = {0, 0};  // the largest magnitudes, as 16-bit numbers
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const uint4 u = __builtin_bit_cast(uint4, f[s]);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, w[j] & 0x7fff7fffu));
+  }
+  return __any(top[0] >= 0x7f80 || top[1] >= 0x7f80);
+}
+
+// The decays of 64 (token, head) pairs: two chunks of one head, or a chunk of
+// two heads.  c_t is taken from the chunk's first token, in fp32: its error,
+// 2^-24 of the sum, matters least where the decays, and so the sums, are large.
 struct __attribute__((aligned(16))) Gates {
-  float cum[L];         // log2(e) (c_t - c_31 for t >= 32, c_t before)
-  float step[L];
-  float mid[L];         // exp(c_31 - c_j) s_j for j < 32, exp(c_t - c_31) from 32 on
-  float from_start[L];  // exp(c_t)
-  float to_end[L];      // w_t
-  float total;          // exp(c_63)
+  float cum[64];     // log2(e) c_t
+  float step[64];    // s_t
+  float to_end[64];  // w_t
+  float total[2];    // exp(c_31)
+};
+
+// M's lower triangle as 16 x 16 blocks of rows t and columns j, (0, 0), (1, 0),
+// (1, 1); a row's two 16-byte chunks change places from row 8 on (no bank
+// conflicts between 16 lanes' rows)
+constexpr int M_BLOCK = 16 * 16 * 2;
+__device__ __forceinline__ int m_at(int t, int chunk) { return t * 32 + ((chunk ^ ((t >> 3) & 1)) << 4); }
+
+template <int N, int P, int HPW, bool FULL>
+struct __attribute__((aligned(16))) Tiles {
+  uint8_t B[2][L * N * 2], X[2][L * HPW * P * 2];
+  uint8_t C[FULL ? 2 : 1][FULL ? L * N * 2 : 16], M[HPW][FULL ? 3 * M_BLOCK : 16];
+  uint4 zeros;
+  Gates gates[FULL ? 1 : 2];
 };
 
 __device__ __forceinline__ int64_t uniform(int64_t v) {
@@ -207,21 +226,15 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
   return (int64_t)(((uint64_t)hi << 32) | lo);
 }
 
-template <int N, int P, int HPW>
-struct __attribute__((aligned(16))) Tiles {
-  uint8_t B[L * N * 2], C[L * N * 2], X[L * HPW * P * 2], M[HPW][L * L * 2];
-  Gates gates[2][HPW];
-  int odd[2];  // whether the chunk's x holds infinities or NaNs
-};
-
 // One piece (or a whole sequence) and HPW heads of a group per workgroup.
 // FULL: with outputs; else the state that a piece's own tokens add.  The chunk
 // loop's memory accesses are the same on every path, so that waiting for the
-// next chunk's rows never waits for this one's stores.
+// next chunk's rows never waits for this one's stores.  Chunks of 32 tokens in
+// two LDS buffers and 168 registers let three workgroups share a CU.
 template <int N, int P, int HPW, bool FULL>
-__global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 1 : 2) void kda_ssm_kernel(SsmArgs a) {
+__global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : (N == 128 && FULL ? 2 : 3)) void kda_ssm_kernel(SsmArgs a) {
   constexpr int WPH = P / 32, WAVES = HPW * WPH, THREADS = WAVES * 64, XC = HPW * P, NB = N / 32;
-  __shared__ Tiles<N, P, HPW> lds;
+  __shared__ Tiles<N, P, HPW, FULL> lds;
 
   const SsmTokens& k = a.t;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -276,7 +289,6 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 1 : 2) void kda_ssm_kern
     if (last) return;
   }
 
-  double log_decay[HPW] = {};  // of the whole piece, in the last wave
   const int g = head0 / (k.H / k.G);
   const uint16_t* Bp = k.B + g * N;
   const uint16_t* Cp = k.C + g * N;
@@ -286,106 +298,125 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 1 : 2) void kda_ssm_kern
   const float Dh = k.D ? k.D[head] : 0.f;
   const bool gate_wave = wave == WAVES - 1;
 
-  // rows left from a token on, at most a chunk, none past the end
-  auto left = [&](int64_t tok) { return to - tok >= L ? L : (to > tok ? (int)(to - tok) : 0); };
+  // rows left from a token on, at most `most`, none past the end
+  auto left = [&](int64_t tok, int most) { return to - tok >= most ? most : (to > tok ? (int)(to - tok) : 0); };
   Rows<N, THREADS> rB, rC;
   Rows<XC, THREADS> rX;
-  float rdt[HPW];
   auto fetch = [&](int64_t tok) {
-    rB.load(Bp, k.b_stride, tok, left(tok));
-    if constexpr (FULL) rC.load(Cp, k.c_stride, tok, left(tok));
-    rX.load(Xp, k.x_stride, tok, left(tok));
+    const int rows = left(tok, L);
+    rB.load(Bp, k.b_stride, tok, rows);
+    if constexpr (FULL) rC.load(Cp, k.c_stride, tok, rows);
+    rX.load(Xp, k.x_stride, tok, rows);
   };
-  // a chunk's steps, and its decays by the last wave, one chunk ahead
+  auto put = [&](int buf) {
+    rB.store(lds.B[buf]);
+    if constexpr (FULL) rC.store(lds.C[buf]);
+    rX.store(lds.X[buf]);
+  };
+  // Decays, by the last wave: lane = token, the upper half of the wave the
+  // second head (HPW 2) or the second chunk of a block of two.
+  constexpr int BLOCK = HPW == 2 ? L : 2 * L;  // tokens
+  const int gate_head = head0 + (HPW == 2 ? up : 0), gate_tok = HPW == 2 ? l32 : lane;
+  const float gate_A = k.A[gate_head], gate_bias = k.dt_bias ? k.dt_bias[gate_head] : 0.f;
+  double log_decay[2] = {};  // of the whole piece, per half of the wave
+  float rdt, g_cum, g_step, g_end, g_total;
   auto fetch_steps = [&](int64_t tok) {
-    const Window w(k.dt, (int64_t)k.H * 4, tok, left(tok), k.H * 4);
-#pragma unroll
-    for (int q = 0; q < HPW; ++q) rdt[q] = w.load4((lane * k.H + head0 + q) * 4);
+    const Window w(k.dt, (int64_t)k.H * 4, tok, left(tok, BLOCK), k.H * 4);
+    rdt = w.load4((gate_tok * k.H + gate_head) * 4);
   };
-  auto make_gates = [&](int64_t tok, int buf) {
-#pragma unroll
-    for (int q = 0; q < HPW; ++q) {
-      const int h = head0 + q;
-      const float step = lane < left(tok) ? ssm_step_of(rdt[q], k.dt_bias ? k.dt_bias[h] : 0.f, k.softplus) : 0.f;
-      const double cum = prefix_sum((double)step * (double)k.A[h] * kLog2e);
-      const double sum = lane_of(cum, 63), mid = lane_of(cum, 31);
-      log_decay[q] += sum;
-      Gates& gt = lds.gates[buf][q];
-      gt.cum[lane] = (float)(lane < 32 ? cum : cum - mid);
-      gt.step[lane] = step;
-      gt.mid[lane] = __builtin_amdgcn_exp2f((float)(lane < 32 ? mid - cum : cum - mid)) * (lane < 32 ? step : 1.f);
-      gt.from_start[lane] = __builtin_amdgcn_exp2f((float)cum);
-      gt.to_end[lane] = __builtin_amdgcn_exp2f((float)(sum - cum)) * step;
-      if (lane == 0) gt.total = __builtin_amdgcn_exp2f((float)sum);
-    }
+  auto make_gates = [&](int64_t tok) {
+    g_step = gate_tok < left(tok, BLOCK) ? ssm_step_of(rdt, gate_bias, k.softplus) : 0.f;
+    const double cum = prefix_sums((double)g_step * (double)gate_A * kLog2e);
+    const double sum0 = lane_of(cum, 31), sum1 = lane_of(cum, 63), sum = up ? sum1 : sum0;
+    log_decay[0] += sum0;
+    log_decay[1] += sum1;
+    g_cum = (float)cum;
+    g_end = __builtin_amdgcn_exp2f((float)(sum - cum)) * g_step;
+    g_total = __builtin_amdgcn_exp2f((float)sum);
+  };
+  auto put_gates = [&](Gates& gt) {
+    gt.cum[lane] = g_cum;
+    gt.step[lane] = g_step;
+    gt.to_end[lane] = g_end;
+    if (l32 == 0) gt.total[up] = g_total;
   };
   fetch_steps(from);
   fetch(from);
-  if (gate_wave) make_gates(from, 0);
-  fetch_steps(from + L);
-  if (tid < 2) lds.odd[tid] = 0;
-  lds_barrier();
+  if (gate_wave) {
+    make_gates(from);
+    put_gates(lds.gates[0]);
+  }
+  fetch_steps(from + BLOCK);
+  if (tid == 0) lds.zeros = make_uint4(0, 0, 0, 0);
+  put(0);
+  fetch(from + L);
 
-  // a lane's addresses: operands whose lanes are rows (of B and C, and of M),
-  // and transposed reads of x and B (rows 0..3, then 4..7).  B's columns come
-  // in the order in which the accumulators hold the state's rows: bits 2 and 3
-  // of the row change places.
+  // a lane's addresses: operands whose lanes are rows (of C, and of M with its
+  // zeros above the diagonal), and transposed reads of x and B (rows 0..3, then
+  // 4..7).  B's columns come in the order in which the accumulators hold the
+  // state's rows: bits 2 and 3 of the row change places.
   const int q1 = (lane >> 4) & 1, m = lane & 3, tr = 8 * up + ((lane & 15) >> 2);
-  const int xcol = (hh * P + pc) / 8;
-  int at_row = tile_at<N>(l32, up), at_m = tile_at<L>(l32, up);
+  const int xcol = (hh * P + pc) / 8, l16 = lane & 15, q4 = lane >> 4;
+  int at_row = tile_at<N>(l32, up), at_row16 = tile_at<N>(l16, q4);
   int at_x = tile_at<XC>(tr, xcol + 2 * q1 + (m >> 1)) + 8 * (m & 1);
   int at_x4 = tile_at<XC>(tr + 4, xcol + 2 * q1 + (m >> 1)) + 8 * (m & 1);
   int at_b = tile_at<N>(tr, 2 * q1 + (m & 1)) + 8 * (m >> 1);
   int at_b4 = tile_at<N>(tr + 4, 2 * q1 + (m & 1)) + 8 * (m >> 1);
   int at_o = tile_at<XC>(l32, xcol) + 8 * up;
+  uint8_t* const base = reinterpret_cast<uint8_t*>(&lds);
+  const int m_base = (int)(reinterpret_cast<uint8_t*>(lds.M[hh]) - base) + m_at(l16, up);
+  int at_m0 = m_base + (l32 < 16 ? 0 : M_BLOCK);
+  int at_m1 = l32 < 16 ? (int)(reinterpret_cast<uint8_t*>(&lds.zeros) - base) : m_base + 2 * M_BLOCK;
 
   int c = 0;
-  for (int64_t tok = from; tok < to; tok += L, c ^= 1) {
-    forget(at_row); forget(at_m); forget(at_x); forget(at_x4); forget(at_b); forget(at_b4); forget(at_o);
-    rB.store(lds.B);
-    if constexpr (FULL) rC.store(lds.C);
-    rX.store(lds.X);
-    if (FULL && rX.not_finite()) lds.odd[c] = 1;
+  for (int64_t tok = from; tok < to; tok += L, ++c) {
+    const int buf = c & 1;
+    const uint8_t *tB = lds.B[buf], *tC = lds.C[FULL ? buf : 0], *tX = lds.X[buf];
+    const Gates& gt = lds.gates[FULL ? 0 : (HPW == 2 ? buf : (c >> 1) & 1)];
+    const int gh = HPW == 2 ? hh : buf, g0 = 32 * gh;  // this head's and chunk's half of the gates
     lds_barrier();
-    fetch(tok + L);
-    const bool slow = FULL && lds.odd[c] != 0;
-    if (tid == 0) lds.odd[c ^ 1] = 0;
-    if (gate_wave) make_gates(tok + L, c ^ 1);
-    fetch_steps(tok + 2 * L);
-    const Gates& gt = lds.gates[c][hh];
-
-    f32x16 Y[2] = {};
+    forget(at_row); forget(at_row16); forget(at_x); forget(at_x4); forget(at_b); forget(at_b4); forget(at_o); forget(at_m0); forget(at_m1);
+    const int rows = left(tok, L), zcol = (hh * P + pc + 4 * up) * 2;
+    uint2 zv[4];
     if constexpr (FULL) {
-      // M: the lower triangle of C B^T in 32 x 32 tiles (transposed: lane = t,
-      // registers = j), decayed, to LDS
-      for (int tile = wave; tile < 3; tile += WAVES) {
-        const int ti = tile ? 32 : 0, tj = tile == 2 ? 32 : 0;
-        f32x16 G = {};
+      const Window zw(Zp, k.z_stride * 2, tok, Zp ? rows : 0, HPW * P * 2);
 #pragma unroll
-        for (int s = 0; s < N / 16; ++s)
-          G = mfma(rows_frag(lds.B + tj * N * 2, at_row ^ (s << 5)), rows_frag(lds.C + ti * N * 2, at_row ^ (s << 5)), G);
+      for (int b = 0; b < 4; ++b) zv[b] = zw.load8(l32 * (int)(k.z_stride * 2) + zcol + 16 * b);
+    }
+
+    // the decays of the next chunk, or block of two
+    const bool gates_due = gate_wave && (HPW == 2 || buf);
+    if (gates_due) {
+      make_gates(tok + L);
+      if (!FULL) put_gates(lds.gates[HPW == 2 ? buf ^ 1 : ((c >> 1) & 1) ^ 1]);
+    }
+    fetch_steps(HPW == 2 ? tok + 2 * L : tok + (buf ? L : 2 * L));
+
+    f32x16 Y = {};
+    if constexpr (FULL) {
+      // M: the lower triangle of C B^T in 16 x 16 blocks (transposed: lane = t,
+      // registers = j), decayed, to LDS
+      for (int blk16 = wave; blk16 < 3; blk16 += WAVES) {
+        const int ti = blk16 ? 16 : 0, tj = blk16 == 2 ? 16 : 0;
+        f32x4 G = {};
+#pragma unroll
+        for (int s = 0; s < N / 32; ++s)
+          G = mfma16(rows_frag(tB + tj * N * 2, at_row16 ^ (s << 6)), rows_frag(tC + ti * N * 2, at_row16 ^ (s << 6)), G);
 #pragma unroll
         for (int q = 0; q < HPW; ++q) {
-          const Gates& gq = lds.gates[c][q];
-          const float ct = gq.cum[ti + l32], ft = gq.mid[32 + l32];
+          const int q0 = HPW == 2 ? 32 * q : g0, j = tj + 4 * q4, t = ti + l16;
+          const float ct = gt.cum[q0 + t];
+          const float4 cj = *reinterpret_cast<const float4*>(gt.cum + q0 + j);
+          const float4 sj = *reinterpret_cast<const float4*>(gt.step + q0 + j);
+          float mv[4] = {G[0] * (__builtin_amdgcn_exp2f(ct - cj.x) * sj.x), G[1] * (__builtin_amdgcn_exp2f(ct - cj.y) * sj.y),
+                         G[2] * (__builtin_amdgcn_exp2f(ct - cj.z) * sj.z), G[3] * (__builtin_amdgcn_exp2f(ct - cj.w) * sj.w)};
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const int j = tj + 8 * b + 4 * up;
-            float mv[4];
-            if (tile == 1) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) mv[i] = G[4 * b + i] * (ft * gq.mid[j + i]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                mv[i] = G[4 * b + i] * (__builtin_amdgcn_exp2f(ct - gq.cum[j + i]) * gq.step[j + i]);
-                settle(mv[i]);  // computed for every lane: a select, no branches
-                mv[i] = j + i <= ti + l32 ? mv[i] : 0.f;
-              }
-            }
-            *reinterpret_cast<uint2*>(lds.M[q] + ti * L * 2 + ((at_m ^ (up << 4) ^ (((tj >> 3) + b) << 4)) + 8 * up)) =
-                make_uint2(bf16_pair(mv[0], mv[1]), bf16_pair(mv[2], mv[3]));
+          for (int i = 0; i < 4; ++i) {
+            settle(mv[i]);  // computed for every lane: a select, no branches
+            mv[i] = j + i <= t ? mv[i] : 0.f;
           }
+          *reinterpret_cast<uint2*>(lds.M[q] + blk16 * M_BLOCK + m_at(l16, q4 >> 1) + 8 * (q4 & 1)) =
+              make_uint2(bf16_pair(mv[0], mv[1]), bf16_pair(mv[2], mv[3]));
         }
       }
 
@@ -396,33 +427,25 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 1 : 2) void kda_ssm_kern
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           u[i] = bf16_pair(S[s >> 1][8 * (s & 1) + 2 * i], S[s >> 1][8 * (s & 1) + 2 * i + 1]);
-        const bf16x8 sf = as_frag(u);
-        Y[0] = mfma(sf, rows_frag(lds.C, at_row ^ (s << 5)), Y[0]);
-        Y[1] = mfma(sf, rows_frag(lds.C + 32 * N * 2, at_row ^ (s << 5)), Y[1]);
+        Y = mfma(as_frag(u), rows_frag(tC, at_row ^ (s << 5)), Y);
       }
+      const float e = __builtin_amdgcn_exp2f(gt.cum[g0 + l32]);
 #pragma unroll
-      for (int tb = 0; tb < 2; ++tb) {
-        const float e = gt.from_start[32 * tb + l32];
-#pragma unroll
-        for (int r = 0; r < 16; ++r) Y[tb][r] *= e;
-      }
+      for (int r = 0; r < 16; ++r) Y[r] *= e;
     }
 
-    // S <- exp(c_63) S + B^T (w x)
-    const float total = gt.total;
+    // S <- exp(c_31) S + B^T (w x)
+    const float total = gt.total[gh];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int r = 0; r < 16; ++r) S[nb][r] *= total;
-    bf16x8 xf[4];
+    bf16x8 xf[2];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      xf[s] = cols_frag(lds.X + 16 * s * XC * 2, at_x, at_x4);
-      bf16x8 bf[NB];
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) bf[nb] = cols_frag(lds.B + 16 * s * N * 2, at_b ^ (nb << 6), at_b4 ^ (nb << 6));
-      const float4 w0 = *reinterpret_cast<const float4*>(gt.to_end + 16 * s + 8 * up);
-      const float4 w1 = *reinterpret_cast<const float4*>(gt.to_end + 16 * s + 8 * up + 4);
+    for (int s = 0; s < 2; ++s) {
+      xf[s] = cols_frag(tX + 16 * s * XC * 2, at_x, at_x4);
+      const float4 w0 = *reinterpret_cast<const float4*>(gt.to_end + g0 + 16 * s + 8 * up);
+      const float4 w1 = *reinterpret_cast<const float4*>(gt.to_end + g0 + 16 * s + 8 * up + 4);
       const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
       float v[8];
       bf16x8_f32(__builtin_bit_cast(uint4, xf[s]), v);
@@ -431,73 +454,62 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 1 : 2) void kda_ssm_kern
       bf16x8 part[3];
       split3(v, part);
 #pragma unroll
-      for (int q = 0; q < 3; ++q)
+      for (int nb = 0; nb < NB; ++nb) {
+        const bf16x8 bf = cols_frag(tB + 16 * s * N * 2, at_b ^ (nb << 6), at_b4 ^ (nb << 6));
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) S[nb] = mfma(bf[nb], part[q], S[nb]);
+        for (int q = 0; q < 3; ++q) S[nb] = mfma(bf, part[q], S[nb]);
+      }
     }
 
+    // the next chunk's rows; nobody reads the other buffer any more
+    put(buf ^ 1);
+    fetch(tok + 2 * L);
+
     if constexpr (FULL) {
-      const int width = HPW * P * 2, rows = left(tok);
-      const Window ow(Op, k.out_stride * 2, tok, rows, width), zw(Zp, k.z_stride * 2, tok, Zp ? rows : 0, width);
-      const int col = (hh * P + pc + 4 * up) * 2;
       lds_barrier();
+      if (gates_due) put_gates(lds.gates[0]);
       // y^T += x^T M^T
-      const uint8_t* M = lds.M[hh];
-      if (!slow) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          if (s < 2) Y[0] = mfma(xf[s], rows_frag(M, at_m ^ (s << 5)), Y[0]);
-          Y[1] = mfma(xf[s], rows_frag(M + 32 * L * 2, at_m ^ (s << 5)), Y[1]);
-        }
+      if (!any_not_finite(xf)) {
+        Y = mfma(xf[0], rows_frag(base, at_m0), Y);
+        Y = mfma(xf[1], rows_frag(base, at_m1), Y);
       } else {
         // a product with the zeros of M above the diagonal would carry a later
         // token's infinity or NaN to an earlier one
+        for (int j = 0; j <= l32; ++j) {
+          const uint8_t* at = lds.M[hh] + (l32 < 16 ? 0 : j < 16 ? M_BLOCK : 2 * M_BLOCK) + m_at(l16, (j & 15) >> 3);
+          const float w = bf16_f32(*reinterpret_cast<const uint16_t*>(at + 2 * (j & 7)));
 #pragma unroll
-        for (int tb = 0; tb < 2; ++tb) {
-          const int t = 32 * tb + l32;
-          for (int j = 0; j <= t; ++j) {
-            const float w = bf16_f32(*reinterpret_cast<const uint16_t*>(M + tile_at<L>(t, j >> 3) + 2 * (j & 7)));
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-              const int p = hh * P + pc + 8 * (r >> 2) + 4 * up + (r & 3);
-              Y[tb][r] += w * bf16_f32(*reinterpret_cast<const uint16_t*>(lds.X + tile_at<XC>(j, p >> 3) + 2 * (p & 7)));
-            }
+          for (int r = 0; r < 16; ++r) {
+            const int p = hh * P + pc + 8 * (r >> 2) + 4 * up + (r & 3);
+            Y[r] += w * bf16_f32(*reinterpret_cast<const uint16_t*>(tX + tile_at<XC>(j, p >> 3) + 2 * (p & 7)));
           }
         }
       }
 
       // out: lane = token, four columns at a time
+      if (k.D) {
 #pragma unroll
-      for (int tb = 0; tb < 2; ++tb) {
-        const int t = 32 * tb + l32;
-        const int oat = t * (int)(k.out_stride * 2) + col, zat = t * (int)(k.z_stride * 2) + col;
-        uint2 zv[4];
+        for (int b = 0; b < 4; ++b) {
+          const uint2 xv = *reinterpret_cast<const uint2*>(tX + (at_o ^ (b << 4)));
+          const uint32_t xw[4] = {xv.x << 16, xv.x & 0xffff0000u, xv.y << 16, xv.y & 0xffff0000u};
 #pragma unroll
-        for (int b = 0; b < 4; ++b) zv[b] = zw.load8(zat + 16 * b);
-        if (k.D) {
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const uint2 xv = *reinterpret_cast<const uint2*>(lds.X + 32 * tb * XC * 2 + (at_o ^ (b << 4)));
-            const uint32_t xw[4] = {xv.x << 16, xv.x & 0xffff0000u, xv.y << 16, xv.y & 0xffff0000u};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) Y[tb][4 * b + i] += Dh * __uint_as_float(xw[i]);
-          }
+          for (int i = 0; i < 4; ++i) Y[4 * b + i] += Dh * __uint_as_float(xw[i]);
         }
-        if (Zp) {
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const uint32_t zb[4] = {zv[b].x << 16, zv[b].x & 0xffff0000u, zv[b].y << 16, zv[b].y & 0xffff0000u};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) Y[tb][4 * b + i] *= silu(__uint_as_float(zb[i]));
-          }
-        }
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          ow.store8(oat + 16 * b, make_uint2(bf16_pair(Y[tb][4 * b], Y[tb][4 * b + 1]),
-                                             bf16_pair(Y[tb][4 * b + 2], Y[tb][4 * b + 3])));
       }
+      if (Zp) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t zb[4] = {zv[b].x << 16, zv[b].x & 0xffff0000u, zv[b].y << 16, zv[b].y & 0xffff0000u};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) Y[4 * b + i] *= silu(__uint_as_float(zb[i]));
+        }
+      }
+      const Window ow(Op, k.out_stride * 2, tok, rows, HPW * P * 2);
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        ow.store8(l32 * (int)(k.out_stride * 2) + zcol + 16 * b,
+                  make_uint2(bf16_pair(Y[4 * b], Y[4 * b + 1]), bf16_pair(Y[4 * b + 2], Y[4 * b + 3])));
     }
-    lds_barrier();  // the tiles are rewritten next
   }
 
   if (!FULL) {
@@ -507,9 +519,15 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 1 : 2) void kda_ssm_kern
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int r = 0; r < 16; ++r) out[row_of(nb, r)] = S[nb][r];
-    if (gate_wave && lane == 0)
-#pragma unroll
-      for (int q = 0; q < HPW; ++q) a.piece_decay[slot * k.H + head0 + q] = __builtin_amdgcn_exp2f((float)log_decay[q]);
+    if (gate_wave && lane == 0) {
+      float* decay = a.piece_decay + slot * k.H + head0;
+      if (HPW == 2) {
+        decay[0] = __builtin_amdgcn_exp2f((float)log_decay[0]);
+        decay[1] = __builtin_amdgcn_exp2f((float)log_decay[1]);
+      } else {
+        decay[0] = __builtin_amdgcn_exp2f((float)(log_decay[0] + log_decay[1]));
+      }
+    }
   } else if (last && a.final_state) {
     if (a.state_bf16) {
       uint16_t* out = static_cast<uint16_t*>(a.final_state) + seq * per_seq + state0;
