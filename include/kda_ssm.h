@@ -125,7 +125,7 @@ typedef struct {
   int32_t state_dtype;       /* kda_state_dtype of initial_state and final_state */
   int32_t cu_seqlens_int64;  /* 0: int32 offsets, 1: int64 */
   int32_t piece_tokens;      /* 0 = automatic.  Else sequences longer than this run in pieces of
-                                this many tokens (a power of two from 64 on), side by side: a
+                                this many tokens (a multiple of 64), side by side: a
                                 first launch computes the state that each piece adds, a second
                                 joins them into the states ahead of the pieces, a third runs
                                 the pieces from those.  Results equal the unsplit scan's up to

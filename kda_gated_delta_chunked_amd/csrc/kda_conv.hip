@@ -69,7 +69,7 @@ template <int W>
 __global__ __launch_bounds__(256) void kda_conv_kernel(ConvArgs a, int shift, int64_t waves, int blocks) {
   const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (id >= waves) return;
-  const Span sp = span_of(a.pk, shift, id / blocks);
+  const Span sp = span_of(a.pk, 1u << shift, id / blocks);
   const int col = (int)(id % blocks) * 512 + (threadIdx.x & 63) * 8;
   if (sp.k < 0 || col >= a.D) return;
   const int64_t len = sp.end - sp.begin;
@@ -159,7 +159,7 @@ __global__ __launch_bounds__(256) void kda_conv_step_kernel(ConvStepArgs a, int6
 hipError_t launch_conv(const ConvArgs& a, hipStream_t stream) {
   constexpr int shift = 5;
   const int blocks = (a.D + 511) / 512;
-  const int64_t waves = span_slots(a.pk.N, a.pk.T_total, shift) * blocks;
+  const int64_t waves = span_slots(a.pk.N, a.pk.T_total, 1 << shift) * blocks;
   const dim3 grid((unsigned)((waves + 3) / 4)), block(256);
   switch (a.W) {
     case 2: hipLaunchKernelGGL(kda_conv_kernel<2>, grid, block, 0, stream, a, shift, waves, blocks); break;

@@ -80,6 +80,15 @@ __device__ __forceinline__ bf16x8 cols_frag(const uint8_t* tile, int at, int at4
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
+// A barrier for data that the waves' own LDS writes hold: lds_barrier would
+// also wait for the copies in flight to LDS.
+__device__ __forceinline__ void lds_only_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // Keeps the compiler from holding everything derived from an address in
 // registers across the chunk loop.
 __device__ __forceinline__ void forget(int& v) { asm volatile("" : "+v"(v)); }
@@ -108,51 +117,47 @@ __device__ __forceinline__ void split3(float (&v)[8], bf16x8 (&part)[3]) {
   }
 }
 
-// Memory as seen from one chunk's first row: rows from there on, bounded by
-// the hardware, so that rows past the sequence's end read as zeros and are not
-// written.  Row strides are below 2^23 elements: 64 rows stay below 2^31 bytes.
-struct Window {
-  __amdgpu_buffer_rsrc_t r;
-  __device__ __forceinline__ Window(const void* base, int64_t row_bytes, int64_t first, int rows, int width_bytes) {
-    char* p = const_cast<char*>(static_cast<const char*>(base)) + first * row_bytes;
-    r = __builtin_amdgcn_make_buffer_rsrc(p, 0, rows > 0 ? (int)((rows - 1) * row_bytes) + width_bytes : 0, 0x00020000);
-  }
-  __device__ __forceinline__ uint4 load16(int at) const {
-    return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
-  }
-  __device__ __forceinline__ uint2 load8(int at) const {
-    return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0));
-  }
-  __device__ __forceinline__ float load4(int at) const {
-    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
-  }
-  __device__ __forceinline__ void store8(int at, uint2 v) const {
-    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    __builtin_amdgcn_raw_buffer_store_b64((u32x2){v.x, v.y}, r, at, 0, 0);
+// A buffer's rows from one chunk's first on, bounded by the hardware: rows past
+// the end read as zeros and are not written.  Row strides are below 2^23
+// elements, so a chunk's offsets stay below 2^31 bytes.
+struct Cursor {
+  uint64_t base;
+  int row_bytes, width;  // of a row: its distance to the next, and what of it is ours
+  __device__ __forceinline__ Cursor(const void* p, int64_t tok, int64_t row_bytes_, int width_)
+      : base(reinterpret_cast<uint64_t>(p) + tok * row_bytes_), row_bytes((int)row_bytes_), width(width_) {}
+  __device__ __forceinline__ void advance(int rows) { base += (int64_t)rows * row_bytes; }
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t window(int rows) const {
+    const int bytes = (rows - 1) * row_bytes + width;
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), 0, rows > 0 ? bytes : 0, 0x00020000);
   }
 };
 
-// L rows of COLS bf16 on their way from memory to a tile
+// L rows of COLS bf16 from memory to a tile, asynchronously: each wave copies
+// 1 KiB at a time, its lanes' 16-byte chunks in LDS order, so that the swizzle
+// is in the addresses they read.
 template <int COLS, int THREADS>
-struct Rows {
+struct RowCopy {
   static constexpr int PER_ROW = COLS / 8, COUNT = L * PER_ROW / THREADS, STEP = THREADS / PER_ROW;
-  uint4 v[COUNT];
-  __device__ __forceinline__ void load(const uint16_t* base, int64_t stride, int64_t first, int rows) {
-    const Window w(base, stride * 2, first, rows, COLS * 2);
-    const int at = (threadIdx.x / PER_ROW) * (int)(stride * 2) + (threadIdx.x % PER_ROW) * 16;
+  static constexpr int KINDS = STEP % 16 ? 16 / STEP : 1;  // the swizzle repeats every 16 rows
+  int at[KINDS];
+  __device__ __forceinline__ RowCopy(int row_bytes) {
 #pragma unroll
-    for (int i = 0; i < COUNT; ++i) v[i] = w.load16(at + i * STEP * (int)(stride * 2));
-  }
-  __device__ __forceinline__ void store(uint8_t* tile) const {
-    const int at = tile_at<COLS>(threadIdx.x / PER_ROW, threadIdx.x % PER_ROW);
-    if constexpr (STEP % 16 == 0) {
-#pragma unroll
-      for (int i = 0; i < COUNT; ++i) *reinterpret_cast<uint4*>(tile + at + i * STEP * COLS * 2) = v[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < COUNT; ++i)
-        *reinterpret_cast<uint4*>(tile + tile_at<COLS>(threadIdx.x / PER_ROW + i * STEP, threadIdx.x % PER_ROW)) = v[i];
+    for (int v = 0; v < KINDS; ++v) {
+      const int row = v * STEP + threadIdx.x / PER_ROW, chunk = threadIdx.x % PER_ROW;
+      at[v] = row * row_bytes + ((tile_at<COLS>(row, chunk) >> 4) & (PER_ROW - 1)) * 16;
     }
+  }
+  __device__ __forceinline__ void start(const Cursor& c, int rows, uint8_t* tile, int wave) const {
+#if defined(__HIP_DEVICE_COMPILE__)  // the host pass has no 16-byte form of the builtin
+    typedef __attribute__((address_space(3))) void* lds_ptr;
+    const __amdgpu_buffer_rsrc_t w = c.window(rows);
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(w, (lds_ptr)(tile + (i * THREADS + wave * 64) * 16), 16,
+                                               at[i % KINDS] + i / KINDS * (KINDS * STEP) * c.row_bytes, 0, 0, 0);
+#else
+    (void)c, (void)rows, (void)tile, (void)wave;
+#endif
   }
 };
 
@@ -203,7 +208,6 @@ struct __attribute__((aligned(16))) Gates {
   float cum[64];     // log2(e) c_t
   float step[64];    // s_t
   float to_end[64];  // w_t
-  float total[2];    // exp(c_31)
 };
 
 // M's lower triangle as 16 x 16 blocks of rows t and columns j, (0, 0), (1, 0),
@@ -211,14 +215,6 @@ struct __attribute__((aligned(16))) Gates {
 // conflicts between 16 lanes' rows)
 constexpr int M_BLOCK = 16 * 16 * 2;
 __device__ __forceinline__ int m_at(int t, int chunk) { return t * 32 + ((chunk ^ ((t >> 3) & 1)) << 4); }
-
-template <int N, int P, int HPW, bool FULL>
-struct __attribute__((aligned(16))) Tiles {
-  uint8_t B[2][L * N * 2], X[2][L * HPW * P * 2];
-  uint8_t C[FULL ? 2 : 1][FULL ? L * N * 2 : 16], M[HPW][FULL ? 3 * M_BLOCK : 16];
-  uint4 zeros;
-  Gates gates[FULL ? 1 : 2];
-};
 
 __device__ __forceinline__ int64_t uniform(int64_t v) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
@@ -229,12 +225,15 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 // One piece (or a whole sequence) and HPW heads of a group per workgroup.
 // FULL: with outputs; else the state that a piece's own tokens add.  The chunk
 // loop's memory accesses are the same on every path, so that waiting for the
-// next chunk's rows never waits for this one's stores.  Chunks of 32 tokens in
-// two LDS buffers and 168 registers let three workgroups share a CU.
+// next chunk's rows never waits for this one's stores.
 template <int N, int P, int HPW, bool FULL>
-__global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : (N == 128 && FULL ? 2 : 3)) void kda_ssm_kernel(SsmArgs a) {
+__global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kernel(SsmArgs a) {
   constexpr int WPH = P / 32, WAVES = HPW * WPH, THREADS = WAVES * 64, XC = HPW * P, NB = N / 32;
-  __shared__ Tiles<N, P, HPW, FULL> lds;
+  // two buffers per tile, objects of their own: the copies in flight to one are
+  // then known not to touch what is read from the other
+  constexpr int TB = L * N * 2, TX = L * XC * 2, TC = FULL ? TB : 16, TM = FULL ? HPW * 3 * M_BLOCK : 16;
+  __shared__ __attribute__((aligned(16))) uint8_t b0[TB], b1[TB], x0[TX], x1[TX], c0[TC], c1[TC], tM[TM];
+  __shared__ Gates gates[2];
 
   const SsmTokens& k = a.t;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -245,12 +244,12 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : (N == 128 && FULL ? 
   const int64_t blk = blockIdx.x;
   const int64_t slot = (blk / (8 * HG)) * 8 + (blk & 7);
   if (slot >= a.slots) return;
-  const Span sp = span_of(a.pk, a.shift, slot);
+  const Span sp = span_of(a.pk, a.piece, slot);
   if (sp.k < 0) return;
   const int seq = __builtin_amdgcn_readfirstlane(sp.seq), piece = __builtin_amdgcn_readfirstlane(sp.k);
-  const int64_t end = uniform(sp.end), from = uniform(sp.begin) + ((int64_t)piece << a.shift);
-  const bool last = !a.piece_state || end - from <= (int64_t)1 << a.shift;
-  int64_t to = last ? end : from + ((int64_t)1 << a.shift);
+  const int64_t end = uniform(sp.end), from = uniform(sp.begin) + (int64_t)piece * a.piece;
+  const bool last = !a.piece_state || end - from <= a.piece;
+  const int64_t to = last ? end : from + a.piece;
   const int head0 = (int)((blk >> 3) % HG) * HPW, hh = wave / WPH, head = head0 + hh, pc = (wave % WPH) * 32;
 
   // state rows 32 nb + 16 (r / 8) + 8 up + r % 8 of column pc + l32
@@ -298,58 +297,43 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : (N == 128 && FULL ? 
   const float Dh = k.D ? k.D[head] : 0.f;
   const bool gate_wave = wave == WAVES - 1;
 
-  // rows left from a token on, at most `most`, none past the end
-  auto left = [&](int64_t tok, int most) { return to - tok >= most ? most : (to > tok ? (int)(to - tok) : 0); };
-  Rows<N, THREADS> rB, rC;
-  Rows<XC, THREADS> rX;
-  auto fetch = [&](int64_t tok) {
-    const int rows = left(tok, L);
-    rB.load(Bp, k.b_stride, tok, rows);
-    if constexpr (FULL) rC.load(Cp, k.c_stride, tok, rows);
-    rX.load(Xp, k.x_stride, tok, rows);
-  };
-  auto put = [&](int buf) {
-    rB.store(lds.B[buf]);
-    if constexpr (FULL) rC.store(lds.C[buf]);
-    rX.store(lds.X[buf]);
-  };
+  // rows left in the piece (a long one counts down from 2^30)
+  int rem = to - from < (1 << 30) ? (int)(to - from) : 1 << 30;
+  Cursor cB(Bp, from, k.b_stride * 2, N * 2), cC(Cp, from, k.c_stride * 2, N * 2), cX(Xp, from, k.x_stride * 2, XC * 2);
+  Cursor cO(Op, from, k.out_stride * 2, XC * 2), cZ(Zp, from, k.z_stride * 2, XC * 2);
+  Cursor cT(k.dt + head0, from, (int64_t)k.H * 4, HPW * 4);
+  const RowCopy<N, THREADS> copyB(cB.row_bytes), copyC(cC.row_bytes);
+  const RowCopy<XC, THREADS> copyX(cX.row_bytes);
   // Decays, by the last wave: lane = token, the upper half of the wave the
   // second head (HPW 2) or the second chunk of a block of two.
   constexpr int BLOCK = HPW == 2 ? L : 2 * L;  // tokens
   const int gate_head = head0 + (HPW == 2 ? up : 0), gate_tok = HPW == 2 ? l32 : lane;
   const float gate_A = k.A[gate_head], gate_bias = k.dt_bias ? k.dt_bias[gate_head] : 0.f;
   double log_decay[2] = {};  // of the whole piece, per half of the wave
-  float rdt, g_cum, g_step, g_end, g_total;
-  auto fetch_steps = [&](int64_t tok) {
-    const Window w(k.dt, (int64_t)k.H * 4, tok, left(tok, BLOCK), k.H * 4);
-    rdt = w.load4((gate_tok * k.H + gate_head) * 4);
+  int gbuf = 0;
+  float rdt;
+  auto fetch_steps = [&](int rows) {
+    rdt = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+        cT.window(rows), gate_tok * cT.row_bytes + (HPW == 2 ? up * 4 : 0), 0, 0));
   };
-  auto make_gates = [&](int64_t tok) {
-    g_step = gate_tok < left(tok, BLOCK) ? ssm_step_of(rdt, gate_bias, k.softplus) : 0.f;
-    const double cum = prefix_sums((double)g_step * (double)gate_A * kLog2e);
-    const double sum0 = lane_of(cum, 31), sum1 = lane_of(cum, 63), sum = up ? sum1 : sum0;
+  auto make_gates = [&](int rows, Gates& gt) {
+    const float step = gate_tok < rows ? ssm_step_of(rdt, gate_bias, k.softplus) : 0.f;
+    const double cum = prefix_sums((double)step * (double)gate_A * kLog2e);
+    const double sum0 = lane_of(cum, 31), sum1 = lane_of(cum, 63);
     log_decay[0] += sum0;
     log_decay[1] += sum1;
-    g_cum = (float)cum;
-    g_end = __builtin_amdgcn_exp2f((float)(sum - cum)) * g_step;
-    g_total = __builtin_amdgcn_exp2f((float)sum);
+    gt.cum[lane] = (float)cum;
+    gt.step[lane] = step;
+    gt.to_end[lane] = __builtin_amdgcn_exp2f((float)((up ? sum1 : sum0) - cum)) * step;
   };
-  auto put_gates = [&](Gates& gt) {
-    gt.cum[lane] = g_cum;
-    gt.step[lane] = g_step;
-    gt.to_end[lane] = g_end;
-    if (l32 == 0) gt.total[up] = g_total;
-  };
-  fetch_steps(from);
-  fetch(from);
-  if (gate_wave) {
-    make_gates(from);
-    put_gates(lds.gates[0]);
-  }
-  fetch_steps(from + BLOCK);
-  if (tid == 0) lds.zeros = make_uint4(0, 0, 0, 0);
-  put(0);
-  fetch(from + L);
+  fetch_steps(rem);
+  copyB.start(cB, min(rem, L), b0, wave);
+  if constexpr (FULL) copyC.start(cC, min(rem, L), c0, wave);
+  copyX.start(cX, min(rem, L), x0, wave);
+  if (gate_wave) make_gates(rem, gates[0]);
+  cT.advance(BLOCK);
+  fetch_steps(rem - BLOCK);
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): the first chunk's rows are in
 
   // a lane's addresses: operands whose lanes are rows (of C, and of M with its
   // zeros above the diagonal), and transposed reads of x and B (rows 0..3, then
@@ -363,34 +347,45 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : (N == 128 && FULL ? 
   int at_b = tile_at<N>(tr, 2 * q1 + (m & 1)) + 8 * (m >> 1);
   int at_b4 = tile_at<N>(tr + 4, 2 * q1 + (m & 1)) + 8 * (m >> 1);
   int at_o = tile_at<XC>(l32, xcol) + 8 * up;
-  uint8_t* const base = reinterpret_cast<uint8_t*>(&lds);
-  const int m_base = (int)(reinterpret_cast<uint8_t*>(lds.M[hh]) - base) + m_at(l16, up);
-  int at_m0 = m_base + (l32 < 16 ? 0 : M_BLOCK);
-  int at_m1 = l32 < 16 ? (int)(reinterpret_cast<uint8_t*>(&lds.zeros) - base) : m_base + 2 * M_BLOCK;
+  const int m_base = hh * 3 * M_BLOCK + m_at(l16, up);
+  // above the diagonal: the zeros behind row 0 of block (0, 0)
+  int at_m0 = m_base + (l32 < 16 ? 0 : M_BLOCK), at_m1 = l32 < 16 ? hh * 3 * M_BLOCK + m_at(0, 1) : m_base + 2 * M_BLOCK;
+  const int zcol = (hh * P + pc + 4 * up) * 2;
 
-  int c = 0;
-  for (int64_t tok = from; tok < to; tok += L, ++c) {
-    const int buf = c & 1;
-    const uint8_t *tB = lds.B[buf], *tC = lds.C[FULL ? buf : 0], *tX = lds.X[buf];
-    const Gates& gt = lds.gates[FULL ? 0 : (HPW == 2 ? buf : (c >> 1) & 1)];
+  while (rem > 0) {
+#pragma unroll
+   for (int buf = 0; buf < 2; ++buf) {
+    if (buf && rem <= 0) break;
+    const uint8_t *tB = buf ? b1 : b0, *tC = buf ? c1 : c0, *tX = buf ? x1 : x0;
+    const Gates& gt = gates[HPW == 2 ? buf : gbuf];
     const int gh = HPW == 2 ? hh : buf, g0 = 32 * gh;  // this head's and chunk's half of the gates
+    // the rows copied in the last round are in once at most its four stores,
+    // which came after, are left (vmcnt 4)
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (FULL ? 4 : 0));
     lds_barrier();
-    forget(at_row); forget(at_row16); forget(at_x); forget(at_x4); forget(at_b); forget(at_b4); forget(at_o); forget(at_m0); forget(at_m1);
-    const int rows = left(tok, L), zcol = (hh * P + pc + 4 * up) * 2;
+    forget(at_row); forget(at_row16); forget(at_x); forget(at_x4); forget(at_b); forget(at_b4); forget(at_o);
+    forget(at_m0); forget(at_m1);
     uint2 zv[4];
     if constexpr (FULL) {
-      const Window zw(Zp, k.z_stride * 2, tok, Zp ? rows : 0, HPW * P * 2);
+      const __amdgpu_buffer_rsrc_t zw = cZ.window(Zp ? min(rem, L) : 0);
 #pragma unroll
-      for (int b = 0; b < 4; ++b) zv[b] = zw.load8(l32 * (int)(k.z_stride * 2) + zcol + 16 * b);
+      for (int b = 0; b < 4; ++b)
+        zv[b] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(zw, l32 * cZ.row_bytes + zcol, 16 * b, 0));
     }
+    // the next chunk's rows; nobody reads the other buffer any more
+    cB.advance(L);
+    cC.advance(L);
+    cX.advance(L);
+    copyB.start(cB, min(rem - L, L), buf ? b0 : b1, wave);
+    if constexpr (FULL) copyC.start(cC, min(rem - L, L), buf ? c0 : c1, wave);
+    copyX.start(cX, min(rem - L, L), buf ? x0 : x1, wave);
 
     // the decays of the next chunk, or block of two
-    const bool gates_due = gate_wave && (HPW == 2 || buf);
-    if (gates_due) {
-      make_gates(tok + L);
-      if (!FULL) put_gates(lds.gates[HPW == 2 ? buf ^ 1 : ((c >> 1) & 1) ^ 1]);
+    if (gate_wave && (HPW == 2 || buf)) make_gates(rem - L, gates[HPW == 2 ? buf ^ 1 : gbuf ^ 1]);
+    if (HPW == 2 || buf) {
+      cT.advance(BLOCK);
+      fetch_steps(rem - L - BLOCK);
     }
-    fetch_steps(HPW == 2 ? tok + 2 * L : tok + (buf ? L : 2 * L));
 
     f32x16 Y = {};
     if constexpr (FULL) {
@@ -415,7 +410,7 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : (N == 128 && FULL ? 
             settle(mv[i]);  // computed for every lane: a select, no branches
             mv[i] = j + i <= t ? mv[i] : 0.f;
           }
-          *reinterpret_cast<uint2*>(lds.M[q] + blk16 * M_BLOCK + m_at(l16, q4 >> 1) + 8 * (q4 & 1)) =
+          *reinterpret_cast<uint2*>(tM + (q * 3 + blk16) * M_BLOCK + m_at(l16, q4 >> 1) + 8 * (q4 & 1)) =
               make_uint2(bf16_pair(mv[0], mv[1]), bf16_pair(mv[2], mv[3]));
         }
       }
@@ -435,7 +430,7 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : (N == 128 && FULL ? 
     }
 
     // S <- exp(c_31) S + B^T (w x)
-    const float total = gt.total[gh];
+    const float total = __builtin_amdgcn_exp2f(gt.cum[g0 + 31]);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -461,22 +456,17 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : (N == 128 && FULL ? 
       }
     }
 
-    // the next chunk's rows; nobody reads the other buffer any more
-    put(buf ^ 1);
-    fetch(tok + 2 * L);
-
     if constexpr (FULL) {
-      lds_barrier();
-      if (gates_due) put_gates(lds.gates[0]);
+      lds_only_barrier();
       // y^T += x^T M^T
       if (!any_not_finite(xf)) {
-        Y = mfma(xf[0], rows_frag(base, at_m0), Y);
-        Y = mfma(xf[1], rows_frag(base, at_m1), Y);
+        Y = mfma(xf[0], rows_frag(tM, at_m0), Y);
+        Y = mfma(xf[1], rows_frag(tM, at_m1), Y);
       } else {
         // a product with the zeros of M above the diagonal would carry a later
         // token's infinity or NaN to an earlier one
         for (int j = 0; j <= l32; ++j) {
-          const uint8_t* at = lds.M[hh] + (l32 < 16 ? 0 : j < 16 ? M_BLOCK : 2 * M_BLOCK) + m_at(l16, (j & 15) >> 3);
+          const uint8_t* at = tM + (hh * 3 + (l32 < 16 ? 0 : j < 16 ? 1 : 2)) * M_BLOCK + m_at(l16, (j & 15) >> 3);
           const float w = bf16_f32(*reinterpret_cast<const uint16_t*>(at + 2 * (j & 7)));
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
@@ -504,12 +494,19 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : (N == 128 && FULL ? 
           for (int i = 0; i < 4; ++i) Y[4 * b + i] *= silu(__uint_as_float(zb[i]));
         }
       }
-      const Window ow(Op, k.out_stride * 2, tok, rows, HPW * P * 2);
+      const __amdgpu_buffer_rsrc_t ow = cO.window(min(rem, L));
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        ow.store8(l32 * (int)(k.out_stride * 2) + zcol + 16 * b,
-                  make_uint2(bf16_pair(Y[4 * b], Y[4 * b + 1]), bf16_pair(Y[4 * b + 2], Y[4 * b + 3])));
+      for (int b = 0; b < 4; ++b) {
+        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+        const u32x2 o = {bf16_pair(Y[4 * b], Y[4 * b + 1]), bf16_pair(Y[4 * b + 2], Y[4 * b + 3])};
+        __builtin_amdgcn_raw_buffer_store_b64(o, ow, l32 * cO.row_bytes + zcol, 16 * b, 0);
+      }
+      cO.advance(L);
+      cZ.advance(L);
     }
+    rem -= L;
+    if (buf) gbuf ^= 1;
+   }
   }
 
   if (!FULL) {
@@ -556,9 +553,9 @@ __global__ __launch_bounds__(256) void kda_ssm_join_kernel(SsmArgs a, int blocks
   const int64_t begin = cu_at(a.pk, seq);
   int64_t end = cu_at(a.pk, seq + 1);
   if (end < begin) end = begin;
-  const int64_t pieces = (end - begin + ((int64_t)1 << a.shift) - 1) >> a.shift;
+  const int64_t pieces = (end - begin + a.piece - 1) / a.piece;
   if (pieces < 3) return;  // the first piece started from the initial state
-  const int64_t slot = (begin >> a.shift) + seq;
+  const int64_t slot = begin / a.piece + seq;
   float* at = a.piece_state + slot * per_seq + h * per_head + ((in % blocks_per_head) * 256 + threadIdx.x) * 4;
   const float* decay = a.piece_decay + slot * a.t.H + h;
   float4 S = *reinterpret_cast<const float4*>(at + per_seq);

@@ -148,13 +148,11 @@ kda_status check_ssm(const kda_ssm_problem* p) {
   st = check_batch(p->num_seqs, p->total_tokens, p->cu_seqlens_int64);
   if (st != KDA_OK) return st;
   const int32_t piece = p->piece_tokens;
-  if (piece < 0 || (piece && (piece < 64 || (piece & (piece - 1)))) || !strides_ok(p)) return KDA_ERR_INVALID_ARG;
+  if (piece < 0 || piece % 64 || !strides_ok(p)) return KDA_ERR_INVALID_ARG;
   // workgroups: at most one per 64 tokens (plus one per sequence) and head
   if ((p->total_tokens / 64 + p->num_seqs + 8) * p->num_heads > kInt32Max) return KDA_ERR_TOO_LARGE;
   return KDA_OK;
 }
-
-int log2_of(int32_t v) { return 31 - __builtin_clz((unsigned)v); }
 
 // the piece length of a scan, 0: no split
 int32_t ssm_pieces(const kda_ssm_problem* p) {
@@ -164,7 +162,7 @@ int32_t ssm_pieces(const kda_ssm_problem* p) {
 // workspace of a split: a state and a decay per piece and head
 size_t ssm_bytes(const kda_ssm_problem* p, int32_t piece) {
   if (!piece) return 0;
-  const size_t slots = (size_t)kda::span_slots(p->num_seqs, p->total_tokens, log2_of(piece));
+  const size_t slots = (size_t)kda::span_slots(p->num_seqs, p->total_tokens, piece);
   return slots * p->num_heads * ((size_t)p->d_state * p->head_dim + 1) * 4;
 }
 
@@ -323,8 +321,8 @@ kda_status kda_ssm_prefill(const kda_ssm_problem* p, const uint16_t* x, const fl
   a.state_bf16 = p->state_dtype == KDA_STATE_BF16;
   int32_t piece = ssm_pieces(p);
   if ((workspace ? workspace_bytes : 0) < ssm_bytes(p, piece)) piece = 0;
-  a.shift = piece ? log2_of(piece) : kda::kUnsplit;
-  a.slots = kda::span_slots(p->num_seqs, p->total_tokens, a.shift);
+  a.piece = piece ? (uint32_t)piece : kda::kUnsplit;
+  a.slots = kda::span_slots(p->num_seqs, p->total_tokens, a.piece);
   a.piece_state = piece ? static_cast<float*>(workspace) : nullptr;
   a.piece_decay = piece ? a.piece_state + a.slots * p->num_heads * p->d_state * p->head_dim : nullptr;
   return done(kda::launch_ssm(a, static_cast<hipStream_t>(stream)));

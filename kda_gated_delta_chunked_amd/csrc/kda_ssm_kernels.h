@@ -42,7 +42,7 @@ __device__ __forceinline__ float silu(float v) { return v * __builtin_amdgcn_rcp
 // floor(cu[n] / len) + 1, so sequences never share a slot, each owns at least
 // one (also when it is empty), and floor(T / len) + N slots hold them all.  A
 // workgroup finds its sequence from its slot with a search over cu alone, so
-// no launch has to lay the spans out.  `len` is 1 << shift.
+// no launch has to lay the spans out.  Offsets are below 2^31.
 struct Packing {
   const void* cu;    // int32 or int64 [N + 1]; NULL: N sequences of T_fixed tokens
   int cu64;
@@ -58,7 +58,7 @@ struct Span {
   int64_t end;       // one past its last
 };
 
-inline int64_t span_slots(int64_t N, int64_t T_total, int shift) { return (T_total >> shift) + N; }
+inline int64_t span_slots(int64_t N, int64_t T_total, int64_t len) { return T_total / len + N; }
 
 __device__ __forceinline__ int64_t cu_at(const Packing& p, int i) {
   int64_t v;
@@ -71,21 +71,21 @@ __device__ __forceinline__ int64_t cu_at(const Packing& p, int i) {
 }
 
 // the span of a slot (the same for all lanes of a wave): 64 probes a step
-__device__ __forceinline__ Span span_of(const Packing& p, int shift, int64_t slot) {
+__device__ __forceinline__ Span span_of(const Packing& p, uint32_t len, int64_t slot) {
   const int lane = threadIdx.x & 63;
   int lo = 0, hi = p.N;
   if (!p.cu) {
     // sequence n's first slot: n T / len rounded down, plus n
     while (hi - lo > 1) {
       const int mid = lo + (hi - lo) / 2;
-      if ((((int64_t)mid * p.T_fixed) >> shift) + mid <= slot) lo = mid;
+      if ((int64_t)((uint32_t)(mid * p.T_fixed) / len) + mid <= slot) lo = mid;
       else hi = mid;
     }
   } else {
     while (hi - lo > 1) {
       const int step = (hi - lo + 63) / 64;
       const int64_t i = (int64_t)lo + (int64_t)step * (lane + 1);
-      const bool le = i < hi && (cu_at(p, (int)i) >> shift) + i <= slot;
+      const bool le = i < hi && (int64_t)((uint32_t)cu_at(p, (int)i) / len) + i <= slot;
       // offsets that do not decrease give ones, then zeros
       const unsigned long long m = __ballot(le);
       const int c = ~m ? __ffsll((long long)~m) - 1 : 64;
@@ -99,8 +99,8 @@ __device__ __forceinline__ Span span_of(const Packing& p, int shift, int64_t slo
   s.begin = cu_at(p, lo);
   s.end = cu_at(p, lo + 1);
   if (s.end < s.begin) s.end = s.begin;
-  const int64_t k = slot - ((s.begin >> shift) + lo);
-  s.k = k < 0 || (k > 0 && (k << shift) >= s.end - s.begin) ? -1 : (int)k;
+  const int64_t k = slot - ((int64_t)((uint32_t)s.begin / len) + lo);
+  s.k = k < 0 || (k > 0 && k * len >= s.end - s.begin) ? -1 : (int)k;
   return s;
 }
 
@@ -151,12 +151,12 @@ struct SsmArgs {
   const void* initial;      // [seqs, H, N, P] or NULL
   void* final_state;        // or NULL
   int state_bf16;
-  int shift;                // a piece is 1 << shift tokens (kUnsplit: a whole sequence)
+  uint32_t piece;           // tokens of a piece (kUnsplit: whole sequences)
   int64_t slots;            // span_slots of the pieces
   float* piece_state;       // [slots, H, N, P], the state ahead of each piece; NULL: no split
   float* piece_decay;       // [slots, H]
 };
-constexpr int kUnsplit = 40;
+constexpr uint32_t kUnsplit = 1u << 31;
 hipError_t launch_ssm(const SsmArgs& a, hipStream_t stream);
 
 struct SsmStepArgs {

@@ -123,7 +123,7 @@ def test_ssm_accepts():
 @pytest.mark.parametrize("want,kw", [
     (UNSUPPORTED, dict(P=32)), (UNSUPPORTED, dict(S_=256)), (INVALID, dict(H=0)), (INVALID, dict(G=0)),
     (INVALID, dict(G=3)), (INVALID, dict(soft=2)), (UNSUPPORTED, dict(sd=2)), (INVALID, dict(N=0)),
-    (INVALID, dict(T=-1)), (INVALID, dict(piece=-64)), (INVALID, dict(piece=32)), (INVALID, dict(piece=192)), (WS, dict(piece=64)), (INVALID, dict(xs=248)), (INVALID, dict(xs=1 << 23)),
+    (INVALID, dict(T=-1)), (INVALID, dict(piece=-64)), (INVALID, dict(piece=32)), (INVALID, dict(piece=96)), (WS, dict(piece=64)), (INVALID, dict(xs=248)), (INVALID, dict(xs=1 << 23)),
     (INVALID, dict(bs=250)), (INVALID, dict(zs=260)), (INVALID, dict(A=0)), (INVALID, dict(x=0)),
     (INVALID, dict(dt=0)), (INVALID, dict(C=0)), (INVALID, dict(out=0)), (INVALID, dict(cu=0, T=129)),
     (ALIGN, dict(dt=at(1) + 4)), (ALIGN, dict(B=at(3) + 2)), (OVERLAP, dict(out=at(0))),

@@ -209,7 +209,7 @@ def test_ssm_prefill(lens, dims, H, G, z, softplus, skip, init, strided, slow):
 
 
 @pytest.mark.parametrize("dims", DIMS, ids=str)
-@pytest.mark.parametrize("piece", [64, 128, 256])
+@pytest.mark.parametrize("piece", [64, 128, 192, 256])
 def test_ssm_prefill_in_pieces(dims, piece):
     P, N = dims
     lens, H, G = [piece * 3 + 7, 0, piece, 1, piece + 1, piece * 4], 2, 1
