@@ -89,6 +89,26 @@ __device__ __forceinline__ void lds_only_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// An 8-byte write to LDS that does not wait for the copies in flight to other
+// tiles (the compiler cannot tell them apart and would).  A wave's LDS accesses
+// execute in order; a barrier behind it has to wait for it (lds_only_barrier).
+__device__ __forceinline__ void lds_write8(uint8_t* at, uint32_t lo, uint32_t hi) {
+  const uint64_t v = ((uint64_t)hi << 32) | lo;
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef __attribute__((address_space(3))) uint8_t* lds_ptr;
+  asm volatile("ds_write_b64 %0, %1" ::"v"((uint32_t)(uintptr_t)(lds_ptr)at), "v"(v) : "memory");
+#else
+  (void)at, (void)v;
+#endif
+}
+
+// Waits until at most `left` of the wave's memory accesses are under way.
+template <int LEFT>
+__device__ __forceinline__ void memory_left() {
+  static_assert(LEFT < 64, "six bits");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (LEFT & 15) | (LEFT >> 4) << 14);
+}
+
 // Keeps the compiler from holding everything derived from an address in
 // registers across the chunk loop.
 __device__ __forceinline__ void forget(int& v) { asm volatile("" : "+v"(v)); }
@@ -98,24 +118,30 @@ __device__ __forceinline__ bf16x8 as_frag(const uint32_t (&u)[4]) {
   return __builtin_bit_cast(bf16x8, make_uint4(u[0], u[1], u[2], u[3]));
 }
 
-// v as a sum of three bf16 fragments, exactly: each part takes the upper 16
-// bits of what is left, 8 significant bits at a time
-__device__ __forceinline__ void split3(float (&v)[8], bf16x8 (&part)[3]) {
-#pragma unroll
-  for (int q = 0; q < 3; ++q) {
-    uint32_t u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t a = __float_as_uint(v[2 * i]), b = __float_as_uint(v[2 * i + 1]);
-      u[i] = __builtin_amdgcn_perm(b, a, 0x07060302u);  // upper halves of a, then b
-      if (q < 2) {
-        v[2 * i] -= __uint_as_float(a & 0xffff0000u);
-        v[2 * i + 1] -= __uint_as_float(b & 0xffff0000u);
-      }
-    }
-    part[q] = as_frag(u);
+// x w as a sum of three bf16 fragments: each part takes the upper 16 bits of
+// what is left, 8 significant bits at a time.
+struct Split {
+  uint32_t part[3][4];
+  __device__ __forceinline__ void pair(int i, const bf16x8& x, float w0, float w1) {
+    const uint32_t u = reinterpret_cast<const uint32_t*>(&x)[i];
+    const float x0 = __uint_as_float(u << 16), x1 = __uint_as_float(u & 0xffff0000u);
+    float v0 = x0 * w0, v1 = x1 * w1;
+    part[0][i] = upper(v0, v1);
+    v0 = __builtin_fmaf(x0, w0, -top(v0));
+    v1 = __builtin_fmaf(x1, w1, -top(v1));
+    part[1][i] = upper(v0, v1);
+    v0 -= top(v0);
+    v1 -= top(v1);
+    part[2][i] = upper(v0, v1);
   }
-}
+  __device__ __forceinline__ bf16x8 frag(int q) const { return as_frag(part[q]); }
+
+ private:
+  static __device__ __forceinline__ float top(float v) { return __uint_as_float(__float_as_uint(v) & 0xffff0000u); }
+  static __device__ __forceinline__ uint32_t upper(float a, float b) {
+    return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+  }
+};
 
 // A buffer's rows from one chunk's first on, bounded by the hardware: rows past
 // the end read as zeros and are not written.  Row strides are below 2^23
@@ -204,11 +230,16 @@ __device__ __forceinline__ bool any_not_finite(const bf16x8 (&f)[2]) {
 // The decays of 64 (token, head) pairs: two chunks of one head, or a chunk of
 // two heads.  c_t is taken from the chunk's first token, in fp32: its error,
 // 2^-24 of the sum, matters least where the decays, and so the sums, are large.
+// The state is held scaled: it is the accumulators times 2^lf, lf <= 0 going
+// down with the chunks' decays, until 2^lf would fall below 2^kLeast: then the
+// accumulators take the factor in and lf is zero again.  Most chunks then need
+// no pass over the accumulators.
 struct __attribute__((aligned(16))) Gates {
-  float cum[64];     // log2(e) c_t
+  float cum[64];     // lf + log2(e) c_t
   float step[64];    // s_t
-  float to_end[64];  // w_t
+  float to_end[64];  // w_t over the accumulators' scale behind the chunk
 };
+constexpr float kLeast = -20.f;
 
 // M's lower triangle as 16 x 16 blocks of rows t and columns j, (0, 0), (1, 0),
 // (1, 1); a row's two 16-byte chunks change places from row 8 on (no bank
@@ -227,12 +258,12 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 // loop's memory accesses are the same on every path, so that waiting for the
 // next chunk's rows never waits for this one's stores.
 template <int N, int P, int HPW, bool FULL>
-__global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kernel(SsmArgs a) {
+__global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 || (N == 128 && FULL) ? 2 : 3) void kda_ssm_kernel(SsmArgs a) {
   constexpr int WPH = P / 32, WAVES = HPW * WPH, THREADS = WAVES * 64, XC = HPW * P, NB = N / 32;
   // two buffers per tile, objects of their own: the copies in flight to one are
   // then known not to touch what is read from the other
   constexpr int TB = L * N * 2, TX = L * XC * 2, TC = FULL ? TB : 16, TM = FULL ? HPW * 3 * M_BLOCK : 16;
-  __shared__ __attribute__((aligned(16))) uint8_t b0[TB], b1[TB], x0[TX], x1[TX], c0[TC], c1[TC], tM[TM];
+  __shared__ __attribute__((aligned(16))) uint8_t b0[TB], b1[TB], x0[TX], x1[TX], c0[TC], c1[TC], tM[TM], tZ[FULL ? TX : 16];
   __shared__ Gates gates[2];
 
   const SsmTokens& k = a.t;
@@ -303,13 +334,16 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
   Cursor cO(Op, from, k.out_stride * 2, XC * 2), cZ(Zp, from, k.z_stride * 2, XC * 2);
   Cursor cT(k.dt + head0, from, (int64_t)k.H * 4, HPW * 4);
   const RowCopy<N, THREADS> copyB(cB.row_bytes), copyC(cC.row_bytes);
-  const RowCopy<XC, THREADS> copyX(cX.row_bytes);
+  const RowCopy<XC, THREADS> copyX(cX.row_bytes), copyZ(cZ.row_bytes);
+  constexpr int NEXT_COPIES = (FULL ? 2 : 1) * RowCopy<N, THREADS>::COUNT + RowCopy<XC, THREADS>::COUNT;
   // Decays, by the last wave: lane = token, the upper half of the wave the
   // second head (HPW 2) or the second chunk of a block of two.
   constexpr int BLOCK = HPW == 2 ? L : 2 * L;  // tokens
   const int gate_head = head0 + (HPW == 2 ? up : 0), gate_tok = HPW == 2 ? l32 : lane;
   const float gate_A = k.A[gate_head], gate_bias = k.dt_bias ? k.dt_bias[gate_head] : 0.f;
   double log_decay[2] = {};  // of the whole piece, per half of the wave
+  double lf[2] = {};         // its head's or heads' scale
+  float scale_left = 0.f;    // the accumulators' scale behind the last chunk
   int gbuf = 0;
   float rdt;
   auto fetch_steps = [&](int rows) {
@@ -322,9 +356,21 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
     const double sum0 = lane_of(cum, 31), sum1 = lane_of(cum, 63);
     log_decay[0] += sum0;
     log_decay[1] += sum1;
-    gt.cum[lane] = (float)cum;
+    // the scale ahead of each half's chunk and behind it: of two heads, or of
+    // one head's chunks one after the other
+    double lf1 = lf[1];
+    const double next0 = lf[0] + sum0;
+    const bool fold0 = (float)next0 < kLeast;
+    if (HPW == 1) lf1 = fold0 ? 0.0 : next0;
+    const double next1 = lf1 + sum1;
+    const bool fold1 = (float)next1 < kLeast;
+    gt.cum[lane] = (float)(cum + (up ? lf1 : lf[0]));
     gt.step[lane] = step;
-    gt.to_end[lane] = __builtin_amdgcn_exp2f((float)((up ? sum1 : sum0) - cum)) * step;
+    const double off = up ? (fold1 ? sum1 : -lf1) : (fold0 ? sum0 : -lf[0]);
+    gt.to_end[lane] = __builtin_amdgcn_exp2f((float)(off - cum)) * step;
+    lf[0] = fold0 ? 0.0 : next0;
+    lf[1] = fold1 ? 0.0 : next1;
+    if (HPW == 1) lf[0] = lf[1];
   };
   fetch_steps(rem);
   copyB.start(cB, min(rem, L), b0, wave);
@@ -350,7 +396,8 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
   const int m_base = hh * 3 * M_BLOCK + m_at(l16, up);
   // above the diagonal: the zeros behind row 0 of block (0, 0)
   int at_m0 = m_base + (l32 < 16 ? 0 : M_BLOCK), at_m1 = l32 < 16 ? hh * 3 * M_BLOCK + m_at(0, 1) : m_base + 2 * M_BLOCK;
-  const int zcol = (hh * P + pc + 4 * up) * 2;
+  int at_s = tile_at<XC>(lane >> 2, xcol + (lane & 3));
+  const int scol = (xcol + (lane & 3)) * 16;
 
   while (rem > 0) {
 #pragma unroll
@@ -359,33 +406,27 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
     const uint8_t *tB = buf ? b1 : b0, *tC = buf ? c1 : c0, *tX = buf ? x1 : x0;
     const Gates& gt = gates[HPW == 2 ? buf : gbuf];
     const int gh = HPW == 2 ? hh : buf, g0 = 32 * gh;  // this head's and chunk's half of the gates
-    // the rows copied in the last round are in once at most its four stores,
-    // which came after, are left (vmcnt 4)
-    __builtin_amdgcn_s_waitcnt(0x0F70 | (FULL ? 4 : 0));
+    // the rows copied in the last round are in once at most its two stores,
+    // which came after, are left
+    memory_left<FULL ? 2 : 0>();
     lds_barrier();
     forget(at_row); forget(at_row16); forget(at_x); forget(at_x4); forget(at_b); forget(at_b4); forget(at_o);
-    forget(at_m0); forget(at_m1);
-    uint2 zv[4];
-    if constexpr (FULL) {
-      const __amdgpu_buffer_rsrc_t zw = cZ.window(Zp ? min(rem, L) : 0);
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-        zv[b] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(zw, l32 * cZ.row_bytes + zcol, 16 * b, 0));
-    }
-    // the next chunk's rows; nobody reads the other buffer any more
-    cB.advance(L);
-    cC.advance(L);
-    cX.advance(L);
-    copyB.start(cB, min(rem - L, L), buf ? b0 : b1, wave);
-    if constexpr (FULL) copyC.start(cC, min(rem - L, L), buf ? c0 : c1, wave);
-    copyX.start(cX, min(rem - L, L), buf ? x0 : x1, wave);
-
+    forget(at_m0); forget(at_m1); forget(at_s);
     // the decays of the next chunk, or block of two
     if (gate_wave && (HPW == 2 || buf)) make_gates(rem - L, gates[HPW == 2 ? buf ^ 1 : gbuf ^ 1]);
     if (HPW == 2 || buf) {
       cT.advance(BLOCK);
       fetch_steps(rem - L - BLOCK);
     }
+    // this chunk's gate, then the next chunk's rows; nobody reads the other
+    // buffer any more
+    if constexpr (FULL) copyZ.start(cZ, Zp ? min(rem, L) : 0, tZ, wave);
+    cB.advance(L);
+    cC.advance(L);
+    cX.advance(L);
+    copyB.start(cB, min(rem - L, L), buf ? b0 : b1, wave);
+    if constexpr (FULL) copyC.start(cC, min(rem - L, L), buf ? c0 : c1, wave);
+    copyX.start(cX, min(rem - L, L), buf ? x0 : x1, wave);
 
     f32x16 Y = {};
     if constexpr (FULL) {
@@ -410,53 +451,90 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
             settle(mv[i]);  // computed for every lane: a select, no branches
             mv[i] = j + i <= t ? mv[i] : 0.f;
           }
-          *reinterpret_cast<uint2*>(tM + (q * 3 + blk16) * M_BLOCK + m_at(l16, q4 >> 1) + 8 * (q4 & 1)) =
-              make_uint2(bf16_pair(mv[0], mv[1]), bf16_pair(mv[2], mv[3]));
+          lds_write8(tM + (q * 3 + blk16) * M_BLOCK + m_at(l16, q4 >> 1) + 8 * (q4 & 1), bf16_pair(mv[0], mv[1]),
+                     bf16_pair(mv[2], mv[3]));
         }
       }
 
-      // y^T = S^T C^T, decayed from the chunk's start
+    }
+
+    // Two products per chunk, y^T = S^T C^T and S += B^T (w x).  The order is
+    // written out: operands are read from LDS ahead of their use, and x w is
+    // split behind the other products.
+    const float* wp = gt.to_end + g0 + 8 * up;
+    float w[2][8];
+    bf16x8 xf[2];
+    Split xs[2];
+    auto read_w = [&](int s) {
+      *reinterpret_cast<float4*>(w[s]) = *reinterpret_cast<const float4*>(wp + 16 * s);
+      *reinterpret_cast<float4*>(w[s] + 4) = *reinterpret_cast<const float4*>(wp + 16 * s + 4);
+    };
+    auto read_b = [&](int s, int nb) { return cols_frag(tB + 16 * s * N * 2, at_b ^ (nb << 6), at_b4 ^ (nb << 6)); };
+    const float next = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(gt.cum[g0 + 31])));
+    xf[0] = cols_frag(tX, at_x, at_x4);
+    read_w(0);
+    bf16x8 bf[NB];
+    if constexpr (FULL) {
+      constexpr int KS = N / 16, AHEAD = 3;
+      bf16x8 cf[KS];
 #pragma unroll
-      for (int s = 0; s < N / 16; ++s) {
+      for (int s = 0; s < AHEAD; ++s) cf[s] = rows_frag(tC, at_row ^ (s << 5));
+      const float e = __builtin_amdgcn_exp2f(gt.cum[g0 + l32]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
         uint32_t u[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           u[i] = bf16_pair(S[s >> 1][8 * (s & 1) + 2 * i], S[s >> 1][8 * (s & 1) + 2 * i + 1]);
-        Y = mfma(as_frag(u), rows_frag(tC, at_row ^ (s << 5)), Y);
+        Y = mfma(as_frag(u), cf[s], Y);
+        if (s + AHEAD < KS) cf[s + AHEAD] = rows_frag(tC, at_row ^ ((s + AHEAD) << 5));
+        if (s == KS - 4) xf[1] = cols_frag(tX + 16 * XC * 2, at_x, at_x4);
+        if (s == KS - 3) bf[0] = read_b(0, 0);
+        if (s == KS - 2) bf[1] = read_b(0, 1);
+        if (s >= KS - 4) xs[0].pair(s - (KS - 4), xf[0], w[0][2 * (s - (KS - 4))], w[0][2 * (s - (KS - 4)) + 1]);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      const float e = __builtin_amdgcn_exp2f(gt.cum[g0 + l32]);
+      read_w(1);
+#pragma unroll
+      for (int nb = 2; nb < NB; ++nb) bf[nb] = read_b(0, nb);
 #pragma unroll
       for (int r = 0; r < 16; ++r) Y[r] *= e;
+    } else {
+      bf[0] = read_b(0, 0);
+      bf[1] = read_b(0, 1);
+      xf[1] = cols_frag(tX + 16 * XC * 2, at_x, at_x4);
+      read_w(1);
+#pragma unroll
+      for (int nb = 2; nb < NB; ++nb) bf[nb] = read_b(0, nb);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xs[0].pair(i, xf[0], w[0][2 * i], w[0][2 * i + 1]);
     }
-
-    // S <- exp(c_31) S + B^T (w x)
-    const float total = __builtin_amdgcn_exp2f(gt.cum[g0 + 31]);
+    scale_left = next;
+    if (next < kLeast) {
+      const float f = __builtin_amdgcn_exp2f(next);
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) S[nb][r] *= total;
-    bf16x8 xf[2];
+        for (int r = 0; r < 16; ++r) S[nb][r] *= f;
+      scale_left = 0.f;
+    }
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      xf[s] = cols_frag(tX + 16 * s * XC * 2, at_x, at_x4);
-      const float4 w0 = *reinterpret_cast<const float4*>(gt.to_end + g0 + 16 * s + 8 * up);
-      const float4 w1 = *reinterpret_cast<const float4*>(gt.to_end + g0 + 16 * s + 8 * up + 4);
-      const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-      float v[8];
-      bf16x8_f32(__builtin_bit_cast(uint4, xf[s]), v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= w[i];
-      bf16x8 part[3];
-      split3(v, part);
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const bf16x8 bf = cols_frag(tB + 16 * s * N * 2, at_b ^ (nb << 6), at_b4 ^ (nb << 6));
 #pragma unroll
-        for (int q = 0; q < 3; ++q) S[nb] = mfma(bf, part[q], S[nb]);
+        for (int q = 0; q < 3; ++q) S[nb] = mfma(bf[nb], xs[s].frag(q), S[nb]);
+        if (s == 0) {
+          bf[nb] = read_b(1, nb);
+#pragma unroll
+          for (int i = nb * 4 / NB; i < (nb + 1) * 4 / NB; ++i) xs[1].pair(i, xf[1], w[1][2 * i], w[1][2 * i + 1]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-    }
 
     if constexpr (FULL) {
+      memory_left<NEXT_COPIES>();  // the gate's rows are in
       lds_only_barrier();
       // y^T += x^T M^T
       if (!any_not_finite(xf)) {
@@ -476,7 +554,8 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
         }
       }
 
-      // out: lane = token, four columns at a time
+      // lane = token, four columns at a time; the rounded values take x's place
+      // in the tile, for stores of whole 64-byte runs
       if (k.D) {
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
@@ -489,17 +568,22 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
       if (Zp) {
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          const uint32_t zb[4] = {zv[b].x << 16, zv[b].x & 0xffff0000u, zv[b].y << 16, zv[b].y & 0xffff0000u};
+          const uint2 zv = *reinterpret_cast<const uint2*>(tZ + (at_o ^ (b << 4)));
+          const uint32_t zw[4] = {zv.x << 16, zv.x & 0xffff0000u, zv.y << 16, zv.y & 0xffff0000u};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) Y[4 * b + i] *= silu(__uint_as_float(zb[i]));
+          for (int i = 0; i < 4; ++i) Y[4 * b + i] *= silu(__uint_as_float(zw[i]));
         }
       }
+      uint8_t* yt = buf ? x1 : x0;
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        lds_write8(yt + (at_o ^ (b << 4)), bf16_pair(Y[4 * b], Y[4 * b + 1]), bf16_pair(Y[4 * b + 2], Y[4 * b + 3]));
       const __amdgpu_buffer_rsrc_t ow = cO.window(min(rem, L));
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-        const u32x2 o = {bf16_pair(Y[4 * b], Y[4 * b + 1]), bf16_pair(Y[4 * b + 2], Y[4 * b + 3])};
-        __builtin_amdgcn_raw_buffer_store_b64(o, ow, l32 * cO.row_bytes + zcol, 16 * b, 0);
+      for (int i = 0; i < 2; ++i) {
+        typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+        const u32x4 o = *reinterpret_cast<const u32x4*>(yt + at_s + i * 16 * XC * 2);
+        __builtin_amdgcn_raw_buffer_store_b128(o, ow, (16 * i + (lane >> 2)) * cO.row_bytes + scol, 0, 0);
       }
       cO.advance(L);
       cZ.advance(L);
@@ -509,6 +593,13 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
    }
   }
 
+  {
+    const float f = __builtin_amdgcn_exp2f(scale_left);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) S[nb][r] *= f;
+  }
   if (!FULL) {
     // the state ahead of the next piece, if nothing came into this one
     float* out = a.piece_state + (slot + 1) * per_seq + state0;

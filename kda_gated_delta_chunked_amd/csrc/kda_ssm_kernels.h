@@ -182,10 +182,30 @@ struct NormArgs {
 };
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
 
+// softplus: max(v, 0) + log(1 + e), e = exp(-|v|), to a few units in the last
+// place.  log(1 + e) = 2 artanh(u) with u = e / (2 + e) <= 1/3, by its series
+// (the first term left out is below u 2^-27); the exponential's argument is
+// carried in two parts, so that e keeps its accuracy where it is all there is.
+__device__ __forceinline__ float softplus(float v) {
+  const float a = -fabsf(v), hi = a * 1.44269502f;  // log2(e) = 1.44269502 + 1.92596e-8
+  const float lo = __builtin_fmaf(a, 1.44269502f, -hi) + a * 1.92596e-8f;
+  const float e0 = __builtin_amdgcn_exp2f(hi), e = __builtin_fmaf(e0, lo * 0.693147182f, e0);
+  const float u = e * __builtin_amdgcn_rcpf(2.f + e), q = u * u;
+  float p = 2.f / 15.f;
+  p = __builtin_fmaf(p, q, 2.f / 13.f);
+  p = __builtin_fmaf(p, q, 2.f / 11.f);
+  p = __builtin_fmaf(p, q, 2.f / 9.f);
+  p = __builtin_fmaf(p, q, 2.f / 7.f);
+  p = __builtin_fmaf(p, q, 2.f / 5.f);
+  p = __builtin_fmaf(p, q, 2.f / 3.f);
+  p = __builtin_fmaf(p, q, 2.f);
+  return __builtin_fmaf(u, p, v != v ? v : fmaxf(v, 0.f));
+}
+
 // step of a token: dt (+ bias), softplus of it when asked
-__device__ __forceinline__ float ssm_step_of(float dt, float bias, int softplus) {
+__device__ __forceinline__ float ssm_step_of(float dt, float bias, int with_softplus) {
   dt += bias;
-  return softplus ? fmaxf(dt, 0.f) + log1pf(expf(-fabsf(dt))) : dt;
+  return with_softplus ? softplus(dt) : dt;
 }
 
 }  // namespace kda
