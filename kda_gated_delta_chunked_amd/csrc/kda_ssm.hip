@@ -73,10 +73,12 @@ __device__ __forceinline__ bf16x8 rows_frag(const uint8_t* tile, int at) {
 // the upper half of the wave): two transposed reads of four rows.  In a group
 // of 16 lanes, lane m supplies four columns of row m / 4, and lane i receives
 // column i of the 16 that the four lanes of each row point to.
-__device__ __forceinline__ bf16x8 cols_frag(const uint8_t* tile, int at, int at4) {
+// The swizzle of row r + 4 (r % 8 < 4) differs in the lowest bit of the chunk.
+template <int COLS>
+__device__ __forceinline__ bf16x8 cols_frag(const uint8_t* tile, int at) {
   typedef __attribute__((address_space(3))) s16x4* lds_ptr;
   const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(tile + at));
-  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(tile + at4));
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(tile + 4 * COLS * 2 + (at ^ 16)));
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
@@ -178,9 +180,12 @@ struct RowCopy {
     typedef __attribute__((address_space(3))) void* lds_ptr;
     const __amdgpu_buffer_rsrc_t w = c.window(rows);
 #pragma unroll
-    for (int i = 0; i < COUNT; ++i)
+    for (int i = 0; i < COUNT; ++i) {
+      int from = at[i % KINDS];
+      forget(from);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(w, (lds_ptr)(tile + (i * THREADS + wave * 64) * 16), 16,
-                                               at[i % KINDS] + i / KINDS * (KINDS * STEP) * c.row_bytes, 0, 0, 0);
+                                               from + i / KINDS * (KINDS * STEP) * c.row_bytes, 0, 0, 0);
+    }
 #else
     (void)c, (void)rows, (void)tile, (void)wave;
 #endif
@@ -258,12 +263,14 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 // loop's memory accesses are the same on every path, so that waiting for the
 // next chunk's rows never waits for this one's stores.
 template <int N, int P, int HPW, bool FULL>
-__global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 || (N == 128 && FULL) ? 2 : 3) void kda_ssm_kernel(SsmArgs a) {
+__global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kernel(SsmArgs a) {
   constexpr int WPH = P / 32, WAVES = HPW * WPH, THREADS = WAVES * 64, XC = HPW * P, NB = N / 32;
-  // two buffers per tile, objects of their own: the copies in flight to one are
-  // then known not to touch what is read from the other
+  // Two buffers for B and x, objects of their own: the copies in flight to one
+  // are then known not to touch what is read from the other.  C is last read
+  // ahead of the chunk's second barrier and copied behind it, to one buffer, so
+  // that three workgroups fit a CU.
   constexpr int TB = L * N * 2, TX = L * XC * 2, TC = FULL ? TB : 16, TM = FULL ? HPW * 3 * M_BLOCK : 16;
-  __shared__ __attribute__((aligned(16))) uint8_t b0[TB], b1[TB], x0[TX], x1[TX], c0[TC], c1[TC], tM[TM], tZ[FULL ? TX : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t b0[TB], b1[TB], x0[TX], x1[TX], tC[TC], tM[TM], tZ[FULL ? TX : 16];
   __shared__ Gates gates[2];
 
   const SsmTokens& k = a.t;
@@ -335,7 +342,7 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 || (N == 128 && FULL) ? 2 
   Cursor cT(k.dt + head0, from, (int64_t)k.H * 4, HPW * 4);
   const RowCopy<N, THREADS> copyB(cB.row_bytes), copyC(cC.row_bytes);
   const RowCopy<XC, THREADS> copyX(cX.row_bytes), copyZ(cZ.row_bytes);
-  constexpr int NEXT_COPIES = (FULL ? 2 : 1) * RowCopy<N, THREADS>::COUNT + RowCopy<XC, THREADS>::COUNT;
+  constexpr int NEXT_COPIES = RowCopy<N, THREADS>::COUNT + RowCopy<XC, THREADS>::COUNT;
   // Decays, by the last wave: lane = token, the upper half of the wave the
   // second head (HPW 2) or the second chunk of a block of two.
   constexpr int BLOCK = HPW == 2 ? L : 2 * L;  // tokens
@@ -347,15 +354,19 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 || (N == 128 && FULL) ? 2 
   int gbuf = 0;
   float rdt;
   auto fetch_steps = [&](int rows) {
-    rdt = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-        cT.window(rows), gate_tok * cT.row_bytes + (HPW == 2 ? up * 4 : 0), 0, 0));
+    int tok = gate_tok;
+    forget(tok);
+    rdt = __uint_as_float(
+        __builtin_amdgcn_raw_buffer_load_b32(cT.window(rows), tok * cT.row_bytes + (HPW == 2 ? up * 4 : 0), 0, 0));
   };
   auto make_gates = [&](int rows, Gates& gt) {
     const float step = gate_tok < rows ? ssm_step_of(rdt, gate_bias, k.softplus) : 0.f;
     const double cum = prefix_sums((double)step * (double)gate_A * kLog2e);
     const double sum0 = lane_of(cum, 31), sum1 = lane_of(cum, 63);
-    log_decay[0] += sum0;
-    log_decay[1] += sum1;
+    if (!FULL) {
+      log_decay[0] += sum0;
+      log_decay[1] += sum1;
+    }
     // the scale ahead of each half's chunk and behind it: of two heads, or of
     // one head's chunks one after the other
     double lf1 = lf[1];
@@ -368,13 +379,13 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 || (N == 128 && FULL) ? 2 
     gt.step[lane] = step;
     const double off = up ? (fold1 ? sum1 : -lf1) : (fold0 ? sum0 : -lf[0]);
     gt.to_end[lane] = __builtin_amdgcn_exp2f((float)(off - cum)) * step;
-    lf[0] = fold0 ? 0.0 : next0;
-    lf[1] = fold1 ? 0.0 : next1;
-    if (HPW == 1) lf[0] = lf[1];
+    // (uniform values, kept in scalar registers)
+    lf[1] = lane_of(fold1 ? 0.0 : next1, 0);
+    lf[0] = HPW == 1 ? lf[1] : lane_of(fold0 ? 0.0 : next0, 0);
   };
   fetch_steps(rem);
   copyB.start(cB, min(rem, L), b0, wave);
-  if constexpr (FULL) copyC.start(cC, min(rem, L), c0, wave);
+  if constexpr (FULL) copyC.start(cC, min(rem, L), tC, wave);
   copyX.start(cX, min(rem, L), x0, wave);
   if (gate_wave) make_gates(rem, gates[0]);
   cT.advance(BLOCK);
@@ -389,9 +400,7 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 || (N == 128 && FULL) ? 2 
   const int xcol = (hh * P + pc) / 8, l16 = lane & 15, q4 = lane >> 4;
   int at_row = tile_at<N>(l32, up), at_row16 = tile_at<N>(l16, q4);
   int at_x = tile_at<XC>(tr, xcol + 2 * q1 + (m >> 1)) + 8 * (m & 1);
-  int at_x4 = tile_at<XC>(tr + 4, xcol + 2 * q1 + (m >> 1)) + 8 * (m & 1);
   int at_b = tile_at<N>(tr, 2 * q1 + (m & 1)) + 8 * (m >> 1);
-  int at_b4 = tile_at<N>(tr + 4, 2 * q1 + (m & 1)) + 8 * (m >> 1);
   int at_o = tile_at<XC>(l32, xcol) + 8 * up;
   const int m_base = hh * 3 * M_BLOCK + m_at(l16, up);
   // above the diagonal: the zeros behind row 0 of block (0, 0)
@@ -403,14 +412,14 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 || (N == 128 && FULL) ? 2 
 #pragma unroll
    for (int buf = 0; buf < 2; ++buf) {
     if (buf && rem <= 0) break;
-    const uint8_t *tB = buf ? b1 : b0, *tC = buf ? c1 : c0, *tX = buf ? x1 : x0;
+    const uint8_t *tB = buf ? b1 : b0, *tX = buf ? x1 : x0;
     const Gates& gt = gates[HPW == 2 ? buf : gbuf];
     const int gh = HPW == 2 ? hh : buf, g0 = 32 * gh;  // this head's and chunk's half of the gates
     // the rows copied in the last round are in once at most its two stores,
     // which came after, are left
     memory_left<FULL ? 2 : 0>();
     lds_barrier();
-    forget(at_row); forget(at_row16); forget(at_x); forget(at_x4); forget(at_b); forget(at_b4); forget(at_o);
+    forget(at_row); forget(at_row16); forget(at_x); forget(at_b); forget(at_o);
     forget(at_m0); forget(at_m1); forget(at_s);
     // the decays of the next chunk, or block of two
     if (gate_wave && (HPW == 2 || buf)) make_gates(rem - L, gates[HPW == 2 ? buf ^ 1 : gbuf ^ 1]);
@@ -422,10 +431,8 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 || (N == 128 && FULL) ? 2 
     // buffer any more
     if constexpr (FULL) copyZ.start(cZ, Zp ? min(rem, L) : 0, tZ, wave);
     cB.advance(L);
-    cC.advance(L);
     cX.advance(L);
     copyB.start(cB, min(rem - L, L), buf ? b0 : b1, wave);
-    if constexpr (FULL) copyC.start(cC, min(rem - L, L), buf ? c0 : c1, wave);
     copyX.start(cX, min(rem - L, L), buf ? x0 : x1, wave);
 
     f32x16 Y = {};
@@ -469,13 +476,13 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 || (N == 128 && FULL) ? 2 
       *reinterpret_cast<float4*>(w[s]) = *reinterpret_cast<const float4*>(wp + 16 * s);
       *reinterpret_cast<float4*>(w[s] + 4) = *reinterpret_cast<const float4*>(wp + 16 * s + 4);
     };
-    auto read_b = [&](int s, int nb) { return cols_frag(tB + 16 * s * N * 2, at_b ^ (nb << 6), at_b4 ^ (nb << 6)); };
+    auto read_b = [&](int s, int nb) { return cols_frag<N>(tB + 16 * s * N * 2, at_b ^ (nb << 6)); };
     const float next = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(gt.cum[g0 + 31])));
-    xf[0] = cols_frag(tX, at_x, at_x4);
+    xf[0] = cols_frag<XC>(tX, at_x);
     read_w(0);
     bf16x8 bf[NB];
     if constexpr (FULL) {
-      constexpr int KS = N / 16, AHEAD = 3;
+      constexpr int KS = N / 16, AHEAD = 2;
       bf16x8 cf[KS];
 #pragma unroll
       for (int s = 0; s < AHEAD; ++s) cf[s] = rows_frag(tC, at_row ^ (s << 5));
@@ -489,13 +496,11 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 || (N == 128 && FULL) ? 2 
           u[i] = bf16_pair(S[s >> 1][8 * (s & 1) + 2 * i], S[s >> 1][8 * (s & 1) + 2 * i + 1]);
         Y = mfma(as_frag(u), cf[s], Y);
         if (s + AHEAD < KS) cf[s + AHEAD] = rows_frag(tC, at_row ^ ((s + AHEAD) << 5));
-        if (s == KS - 4) xf[1] = cols_frag(tX + 16 * XC * 2, at_x, at_x4);
         if (s == KS - 3) bf[0] = read_b(0, 0);
         if (s == KS - 2) bf[1] = read_b(0, 1);
         if (s >= KS - 4) xs[0].pair(s - (KS - 4), xf[0], w[0][2 * (s - (KS - 4))], w[0][2 * (s - (KS - 4)) + 1]);
         __builtin_amdgcn_sched_barrier(0);
       }
-      read_w(1);
 #pragma unroll
       for (int nb = 2; nb < NB; ++nb) bf[nb] = read_b(0, nb);
 #pragma unroll
@@ -503,8 +508,6 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 || (N == 128 && FULL) ? 2 
     } else {
       bf[0] = read_b(0, 0);
       bf[1] = read_b(0, 1);
-      xf[1] = cols_frag(tX + 16 * XC * 2, at_x, at_x4);
-      read_w(1);
 #pragma unroll
       for (int nb = 2; nb < NB; ++nb) bf[nb] = read_b(0, nb);
 #pragma unroll
@@ -519,23 +522,33 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 || (N == 128 && FULL) ? 2 
         for (int r = 0; r < 16; ++r) S[nb][r] *= f;
       scale_left = 0.f;
     }
+    // neighbouring products go to different accumulators
+    forget(at_b);
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int q = 0; q < 3; ++q)
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-        for (int q = 0; q < 3; ++q) S[nb] = mfma(bf[nb], xs[s].frag(q), S[nb]);
-        if (s == 0) {
-          bf[nb] = read_b(1, nb);
-#pragma unroll
-          for (int i = nb * 4 / NB; i < (nb + 1) * 4 / NB; ++i) xs[1].pair(i, xf[1], w[1][2 * i], w[1][2 * i + 1]);
+        S[nb] = mfma(bf[nb], xs[0].frag(q), S[nb]);
+        if (q == 2) bf[nb] = read_b(1, nb);
+        if (q == 0 && nb == NB / 2 - 1) xf[1] = cols_frag<XC>(tX + 16 * XC * 2, at_x);
+        if (q == 0 && nb == NB / 2) read_w(1);
+        if (nb % (NB / 2) == NB / 2 - 1 && q > 0) {
+          const int i = 2 * (q - 1) + nb / (NB / 2);
+          xs[1].pair(i, xf[1], w[1][2 * i], w[1][2 * i + 1]);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) S[nb] = mfma(bf[nb], xs[1].frag(q), S[nb]);
 
     if constexpr (FULL) {
       memory_left<NEXT_COPIES>();  // the gate's rows are in
       lds_only_barrier();
+      // C has been read
+      cC.advance(L);
+      copyC.start(cC, min(rem - L, L), tC, wave);
       // y^T += x^T M^T
       if (!any_not_finite(xf)) {
         Y = mfma(xf[0], rows_frag(tM, at_m0), Y);
@@ -543,12 +556,15 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 || (N == 128 && FULL) ? 2 
       } else {
         // a product with the zeros of M above the diagonal would carry a later
         // token's infinity or NaN to an earlier one
-        for (int j = 0; j <= l32; ++j) {
-          const uint8_t* at = tM + (hh * 3 + (l32 < 16 ? 0 : j < 16 ? 1 : 2)) * M_BLOCK + m_at(l16, (j & 15) >> 3);
+        int t = l32, half = up;
+        forget(t);
+        forget(half);
+        for (int j = 0; j <= t; ++j) {
+          const uint8_t* at = tM + (hh * 3 + (t < 16 ? 0 : j < 16 ? 1 : 2)) * M_BLOCK + m_at(t & 15, (j & 15) >> 3);
           const float w = bf16_f32(*reinterpret_cast<const uint16_t*>(at + 2 * (j & 7)));
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
-            const int p = hh * P + pc + 8 * (r >> 2) + 4 * up + (r & 3);
+            const int p = hh * P + pc + 8 * (r >> 2) + 4 * half + (r & 3);
             Y[r] += w * bf16_f32(*reinterpret_cast<const uint16_t*>(tX + tile_at<XC>(j, p >> 3) + 2 * (p & 7)));
           }
         }
@@ -578,12 +594,14 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 || (N == 128 && FULL) ? 2 
 #pragma unroll
       for (int b = 0; b < 4; ++b)
         lds_write8(yt + (at_o ^ (b << 4)), bf16_pair(Y[4 * b], Y[4 * b + 1]), bf16_pair(Y[4 * b + 2], Y[4 * b + 3]));
+      int srow = lane >> 2;
+      forget(srow);
       const __amdgpu_buffer_rsrc_t ow = cO.window(min(rem, L));
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
         const u32x4 o = *reinterpret_cast<const u32x4*>(yt + at_s + i * 16 * XC * 2);
-        __builtin_amdgcn_raw_buffer_store_b128(o, ow, (16 * i + (lane >> 2)) * cO.row_bytes + scol, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(o, ow, (16 * i + srow) * cO.row_bytes + scol, 0, 0);
       }
       cO.advance(L);
       cZ.advance(L);
