@@ -130,6 +130,8 @@ typedef struct {
                                 joins them into the states ahead of the pieces, a third runs
                                 the pieces from those.  Results equal the unsplit scan's up to
                                 rounding */
+  int32_t packed;            /* 1 when the call passes cu_seqlens, 0 when not (the automatic piece
+                                length takes a packed batch to be ragged) */
   int64_t x_stride;          /* elements between rows, a multiple of 8, at least the row and below
                                 2^23; 0 = the row */
   int64_t b_stride;

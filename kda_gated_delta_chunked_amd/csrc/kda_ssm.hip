@@ -210,6 +210,13 @@ __device__ __forceinline__ double prefix_sums(double v) {
   v = add_shifted<0x118, 0xf>(v);
   return add_shifted<0x142, 0xa>(v);
 }
+// 2^v to fp32 accuracy: the whole part apart, so that a large argument costs the
+// fraction no bits
+__device__ __forceinline__ float exp2_of(double v) {
+  const double whole = __builtin_rint(v);
+  return ldexpf(__builtin_amdgcn_exp2f((float)(v - whole)), (int)fmin(fmax(whole, -1000.0), 1000.0));
+}
+
 __device__ __forceinline__ double lane_of(double v, int lane) {
   const uint64_t u = __builtin_bit_cast(uint64_t, v);
   const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane);
@@ -230,6 +237,18 @@ __device__ __forceinline__ bool any_not_finite(const bf16x8 (&f)[2]) {
       top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, w[j] & 0x7fff7fffu));
   }
   return __any(top[0] >= 0x7f80 || top[1] >= 0x7f80);
+}
+
+// The fragment with zeros in the place of infinities and NaNs.
+__device__ __forceinline__ bf16x8 finite_only(const bf16x8& f) {
+  const uint4 u = __builtin_bit_cast(uint4, f);
+  uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
+    if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu;
+  }
+  return as_frag(w);
 }
 
 // The decays of 64 (token, head) pairs: two chunks of one head, or a chunk of
@@ -361,7 +380,9 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
   };
   auto make_gates = [&](int rows, Gates& gt) {
     const float step = gate_tok < rows ? ssm_step_of(rdt, gate_bias, k.softplus) : 0.f;
-    const double cum = prefix_sums((double)step * (double)gate_A * kLog2e);
+    float A = gate_A;
+    settle(A);
+    const double cum = prefix_sums((double)step * (double)A * kLog2e);
     const double sum0 = lane_of(cum, 31), sum1 = lane_of(cum, 63);
     if (!FULL) {
       log_decay[0] += sum0;
@@ -378,7 +399,7 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
     gt.cum[lane] = (float)(cum + (up ? lf1 : lf[0]));
     gt.step[lane] = step;
     const double off = up ? (fold1 ? sum1 : -lf1) : (fold0 ? sum0 : -lf[0]);
-    gt.to_end[lane] = __builtin_amdgcn_exp2f((float)(off - cum)) * step;
+    gt.to_end[lane] = exp2_of(off - cum) * step;
     // (uniform values, kept in scalar registers)
     lf[1] = lane_of(fold1 ? 0.0 : next1, 0);
     lf[0] = HPW == 1 ? lf[1] : lane_of(fold0 ? 0.0 : next0, 0);
@@ -549,13 +570,17 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
       // C has been read
       cC.advance(L);
       copyC.start(cC, min(rem - L, L), tC, wave);
-      // y^T += x^T M^T
-      if (!any_not_finite(xf)) {
-        Y = mfma(xf[0], rows_frag(tM, at_m0), Y);
-        Y = mfma(xf[1], rows_frag(tM, at_m1), Y);
-      } else {
-        // a product with the zeros of M above the diagonal would carry a later
-        // token's infinity or NaN to an earlier one
+      // y^T += x^T M^T.  A product with the zeros of M above the diagonal would
+      // carry a later token's infinity or NaN to an earlier one: those elements
+      // of x are left out of it and added to the tokens behind them alone.
+      const bool odd = any_not_finite(xf);
+      if (odd) {
+        xf[0] = finite_only(xf[0]);
+        xf[1] = finite_only(xf[1]);
+      }
+      Y = mfma(xf[0], rows_frag(tM, at_m0), Y);
+      Y = mfma(xf[1], rows_frag(tM, at_m1), Y);
+      if (odd) {
         int t = l32, half = up;
         forget(t);
         forget(half);
@@ -565,7 +590,8 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             const int p = hh * P + pc + 8 * (r >> 2) + 4 * half + (r & 3);
-            Y[r] += w * bf16_f32(*reinterpret_cast<const uint16_t*>(tX + tile_at<XC>(j, p >> 3) + 2 * (p & 7)));
+            const uint32_t x = *reinterpret_cast<const uint16_t*>(tX + tile_at<XC>(j, p >> 3) + 2 * (p & 7));
+            if ((x & 0x7f80) == 0x7f80) Y[r] += w * bf16_f32(x);
           }
         }
       }

@@ -2,6 +2,7 @@
 // argument validation and launch.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -147,6 +148,7 @@ kda_status check_ssm(const kda_ssm_problem* p) {
   if (st != KDA_OK) return st;
   st = check_batch(p->num_seqs, p->total_tokens, p->cu_seqlens_int64);
   if (st != KDA_OK) return st;
+  if (!flag(p->packed)) return KDA_ERR_INVALID_ARG;
   const int32_t piece = p->piece_tokens;
   if (piece < 0 || piece % 64 || !strides_ok(p)) return KDA_ERR_INVALID_ARG;
   // workgroups: at most one per 64 tokens (plus one per sequence) and head
@@ -154,9 +156,69 @@ kda_status check_ssm(const kda_ssm_problem* p) {
   return KDA_OK;
 }
 
-// the piece length of a scan, 0: no split
+// The piece length of a scan, 0: no split.  A workgroup runs its chunks of 32
+// tokens one after the other, so few (sequence, head) pairs leave most of the
+// device idle; a split pays a second pass over the tokens for the states and a
+// join.  The model is in us on MI355X (256 CUs in 8 XCDs, to which the sequences
+// or pieces go in turn with all their heads; three workgroups on a CU).  A chunk
+// takes 1.8 alone on its CU (2.6 in a workgroup of two waves), and a CU finishes
+// one of four waves every 1.5; a workgroup costs 2.5 chunks besides its own; the
+// states' pass takes 0.55 of the full one; the join moves each piece's state
+// twice.  A packed batch of several sequences is taken to be ragged: its longest
+// sequence is twice the mean, half a piece per sequence comes on top, and the
+// last pieces to run leave half of the device idle.  Measured, unsplit / split
+// where the rule splits: B1 T8192 H12 581 / 66, B1 T1024 H12 79 / 32, B8 T8192
+// H12 460 / 241, 32 ragged prompts of 24 heads 420 / 360; and where it does not:
+// B32 T512 H12 65 / 87.
+struct SsmModel {
+  double groups, alone, rate = 1.5, state;
+  explicit SsmModel(const kda_ssm_problem* p) {
+    const bool four = p->head_dim == 128 || (p->num_heads / p->num_groups) % 2 == 0;
+    groups = p->head_dim == 128 ? p->num_heads : (double)p->num_heads / 2;  // of four waves
+    alone = four ? 1.8 : 2.6;
+    state = (double)p->num_heads * p->d_state * p->head_dim;
+  }
+  // spans of `chunks` chunks each
+  double equal(double spans, double chunks) const {
+    const double per_cu = std::ceil(spans / 8) * groups / 32;
+    return (chunks + 2.5) * std::max(alone, rate * (per_cu <= 3 ? std::ceil(per_cu) : per_cu + 1));
+  }
+  // `total` chunks in spans of at most `chunks`
+  double ragged(double spans, double chunks, double total) const {
+    const double per_cu = spans * groups / 256;
+    return std::max(alone * (chunks + 2.5),
+                    rate * groups / 256 * (total + 2.5 * spans) + 0.5 * rate * chunks * std::min(per_cu, 3.0));
+  }
+  double split(double pass, double spans) const { return 1.55 * pass + spans * state * 8 / 7.5e6 + 12; }
+};
+
 int32_t ssm_pieces(const kda_ssm_problem* p) {
-  return p->piece_tokens && p->piece_tokens < p->total_tokens ? p->piece_tokens : 0;
+  if (p->piece_tokens) return p->piece_tokens < p->total_tokens ? p->piece_tokens : 0;
+  const SsmModel model(p);
+  const double N = p->num_seqs, T = (double)p->total_tokens, mean = T / N;
+  const bool ragged = p->packed && p->num_seqs > 1;
+  double best = model.equal(N, (ragged ? std::min(T, 2 * mean) : mean) / 32);
+  int32_t piece = 0;
+  auto consider = [&](double len, double spans, double pass) {
+    const double us = model.split(pass, spans);
+    if (us < best) {
+      best = us;
+      piece = (int32_t)len;
+    }
+  };
+  if (ragged) {
+    // lengths that whole prompts tend to be multiples of
+    for (int64_t len = 128; (double)len < mean; len = len & (len - 1) ? len / 3 * 4 : len / 2 * 3) {
+      const double spans = T / (double)len + N / 2;
+      consider((double)len, spans, model.ragged(spans, (double)len / 32, T / 32));
+    }
+  } else {
+    for (int n = 2; n <= 256 && mean / n > 64; ++n) {
+      const double len = std::ceil(mean / n / 64) * 64, spans = N * std::ceil(mean / len);
+      if (len < mean) consider(len, spans, model.equal(spans, len / 32));
+    }
+  }
+  return piece;
 }
 
 // workspace of a split: a state and a decay per piece and head
@@ -286,7 +348,7 @@ kda_status kda_ssm_validate(const kda_ssm_problem* p, const void* x, const float
   const kda_status st = check_ssm(p);
   if (st != KDA_OK) return st;
   const int64_t T = p->total_tokens, N = p->num_seqs, H = p->num_heads;
-  if (!cu_seqlens && T % N) return KDA_ERR_INVALID_ARG;
+  if ((cu_seqlens != nullptr) != (p->packed != 0) || (!cu_seqlens && T % N)) return KDA_ERR_INVALID_ARG;
   if (!A || (T > 0 && (!x || !dt || !B || !C || !out))) return KDA_ERR_INVALID_ARG;
   if (!all_aligned({x, dt, A, B, C, D, z, dt_bias, cu_seqlens, initial_state, out, final_state, workspace}))
     return KDA_ERR_ALIGNMENT;

@@ -38,7 +38,7 @@ class SsmProblem(ctypes.Structure):
 
     _fields_ = [("num_seqs", _i32), ("total_tokens", _i64), ("num_heads", _i32), ("num_groups", _i32),
                 ("head_dim", _i32), ("d_state", _i32), ("dt_softplus", _i32), ("state_dtype", _i32),
-                ("cu_seqlens_int64", _i32), ("piece_tokens", _i32), ("x_stride", _i64), ("b_stride", _i64),
+                ("cu_seqlens_int64", _i32), ("piece_tokens", _i32), ("packed", _i32), ("x_stride", _i64), ("b_stride", _i64),
                 ("c_stride", _i64), ("z_stride", _i64), ("out_stride", _i64)]
 
 
@@ -333,7 +333,8 @@ def ssm_prefill(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, dt_softplus: bo
     if final_state is None and output_final_state:
         final_state = torch.empty(shape, dtype=state_dtype, device=dev)
         mine.append(final_state)
-    p = SsmProblem(N, T, H, G, P, S, int(dt_softplus), kind, cu64, int(piece_tokens), _row_stride("x", x, lead),
+    p = SsmProblem(N, T, H, G, P, S, int(dt_softplus), kind, cu64, int(piece_tokens),
+                   int(cu_seqlens is not None), _row_stride("x", x, lead),
                    _row_stride("B", B, lead), _row_stride("C", C, lead),
                    0 if z is None else _row_stride("z", z, lead), _row_stride("out", out, lead))
     if workspace is None:

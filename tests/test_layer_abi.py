@@ -97,8 +97,9 @@ def test_conv_decode_checks(want, kw):
     assert conv_step(**kw) == want
 
 
-def ssm_problem(N=2, T=128, H=4, G=2, P=64, S_=128, soft=1, sd=0, cu64=0, piece=0, xs=0, bs=0, cs=0, zs=0, os_=0):
-    return S.SsmProblem(N, T, H, G, P, S_, soft, sd, cu64, piece, xs, bs, cs, zs, os_)
+def ssm_problem(N=2, T=128, H=4, G=2, P=64, S_=128, soft=1, sd=0, cu64=0, piece=0, packed=1, xs=0, bs=0, cs=0, zs=0,
+                os_=0):
+    return S.SsmProblem(N, T, H, G, P, S_, soft, sd, cu64, piece, packed, xs, bs, cs, zs, os_)
 
 
 NAMES = ["x", "dt", "A", "B", "C", "D", "z", "bias", "cu", "s0", "out", "fin", "ws"]
@@ -113,7 +114,7 @@ def ssm(ws_bytes=0, p=None, **kw):
 def test_ssm_accepts():
     assert ssm() == OK
     assert ssm(D=0, z=0, bias=0, s0=0, fin=0) == OK
-    assert ssm(cu=0) == OK
+    assert ssm(cu=0, packed=0) == OK
     assert ssm(T=0, x=0, dt=0, B=0, C=0, out=0) == OK
     assert ssm(fin=at(NAMES.index("s0"))) == OK
     # x, B and C as columns of one row
@@ -125,8 +126,8 @@ def test_ssm_accepts():
     (INVALID, dict(G=3)), (INVALID, dict(soft=2)), (UNSUPPORTED, dict(sd=2)), (INVALID, dict(N=0)),
     (INVALID, dict(T=-1)), (INVALID, dict(piece=-64)), (INVALID, dict(piece=32)), (INVALID, dict(piece=96)), (WS, dict(piece=64)), (INVALID, dict(xs=248)), (INVALID, dict(xs=1 << 23)),
     (INVALID, dict(bs=250)), (INVALID, dict(zs=260)), (INVALID, dict(A=0)), (INVALID, dict(x=0)),
-    (INVALID, dict(dt=0)), (INVALID, dict(C=0)), (INVALID, dict(out=0)), (INVALID, dict(cu=0, T=129)),
-    (ALIGN, dict(dt=at(1) + 4)), (ALIGN, dict(B=at(3) + 2)), (OVERLAP, dict(out=at(0))),
+    (INVALID, dict(dt=0)), (INVALID, dict(C=0)), (INVALID, dict(out=0)), (INVALID, dict(cu=0, packed=0, T=129)),
+    (INVALID, dict(cu=0)), (INVALID, dict(packed=0)), (INVALID, dict(packed=2)), (ALIGN, dict(dt=at(1) + 4)), (ALIGN, dict(B=at(3) + 2)), (OVERLAP, dict(out=at(0))),
     (OVERLAP, dict(out=at(1))), (OVERLAP, dict(out=at(9))), (OVERLAP, dict(fin=at(9) + 16)),
     (OVERLAP, dict(fin=at(6))), (TOO_LARGE, dict(T=1 << 31)), (TOO_LARGE, dict(H=1 << 24)),
     (TOO_LARGE, dict(N=1 << 30, H=2, G=2))])
@@ -146,6 +147,17 @@ def test_ssm_workspace_of_a_split():
     assert ssm(want, ws=at(10), p=p) == OVERLAP
     # no sequence is longer than the piece: nothing to split
     assert K.ssm_workspace_size(ssm_problem(N=1, T=256, piece=256)) == 0
+
+
+@pytest.mark.parametrize("want,kw", [
+    (1024, dict(N=8, T=65536, H=12, G=1, P=128, packed=0)), (0, dict(N=32, T=16384, H=12, G=1, P=128, packed=0)),
+    (0, dict(N=1, T=37, H=4, P=64)), (0, dict(N=1, T=0)), (0, dict(N=256, T=4096, H=64))])
+def test_ssm_automatic_pieces(want, kw):
+    p = ssm_problem(**kw)
+    assert K.ssm_plan(p) == want
+    assert (K.ssm_workspace_size(p) > 0) == (want > 0)
+    # without the workspace the scan runs unsplit
+    assert ssm(0, p=p, **({} if kw.get("packed", 1) else dict(cu=0))) == OK
 
 
 STEP = ["x", "dt", "A", "B", "C", "D", "z", "bias", "pool", "idx", "out"]
