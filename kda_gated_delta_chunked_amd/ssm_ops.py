@@ -8,7 +8,6 @@ the library, and there is no fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional
 
@@ -134,29 +133,25 @@ def _row_stride(name: str, t, lead: int) -> int:
     return step
 
 
-def _tensors(dev, **named):
-    """Checks (tensor or None, dtype, shape) per name: dtype, device, shape."""
-    for name, (t, dtype, shape) in named.items():
-        if t is None:
-            continue
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-
-
-def _contiguous(**named):
-    for name, t in named.items():
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+def _check_tensor(name: str, t, dtype, shape, dev, contiguous: bool = True):
+    """dtype, device, shape and packing of a tensor (None passes)."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
 def _gpu(t):
-    if t.device.type != "cuda":
+    dev = t.device
+    if dev.type != "cuda":
         raise ValueError("libkda runs on the GPU: tensors must be on a cuda (HIP) device")
-    return t.device
+    return dev
 
 
 def _launch(name: str, dev, stream, problem, args, mine=()):
@@ -165,17 +160,18 @@ def _launch(name: str, dev, stream, problem, args, mine=()):
     one the allocator is told, so that it does not hand them out early."""
     import torch
 
-    current = torch.cuda.current_stream(dev)
-    if stream is None:
-        stream = current
-    other = torch.cuda.current_device() != dev.index
-    with torch.cuda.device(dev) if other else contextlib.nullcontext():
-        status = call_raw(name, problem, *args, stream.cuda_stream)
-    if stream != current:
+    current = torch._C._cuda_getCurrentRawStream(dev.index)
+    raw = current if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev.index:
+        status = call_raw(name, problem, *args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = call_raw(name, problem, *args, raw)
+    if raw != current:
         for t in mine:
-            if t is not None:
-                t.record_stream(stream)
-    _check(status, name)
+            t.record_stream(stream)
+    if status:
+        _check(status, name)
 
 
 def _offsets(cu_seqlens, dev):
@@ -197,10 +193,10 @@ def _batch(x, inner: int, cu_seqlens, what: str):
     if x.dim() == inner + 2:
         if cu_seqlens is not None:
             raise ValueError("cu_seqlens is for packed inputs")
-        return 2, int(x.shape[0]), int(x.shape[0] * x.shape[1])
+        return 2, x.shape[0], x.shape[0] * x.shape[1]
     if x.dim() != inner + 1:
         raise ValueError(f"x must be {what}")
-    return 1, 1 if cu_seqlens is None else int(cu_seqlens.numel()) - 1, int(x.shape[0])
+    return 1, 1 if cu_seqlens is None else cu_seqlens.numel() - 1, x.shape[0]
 
 
 def conv_prefill(x, weight, bias=None, *, cu_seqlens=None, initial_state=None, final_state=None,
@@ -220,12 +216,15 @@ def conv_prefill(x, weight, bias=None, *, cu_seqlens=None, initial_state=None, f
     dev = _gpu(x)
     bf = torch.bfloat16
     lead, N, T = _batch(x, 1, cu_seqlens, "[T, D] or [B, T, D]")
-    D, W = int(x.shape[-1]), int(weight.shape[-1])
+    shape = x.shape
+    D, W = shape[-1], weight.shape[-1]
     state = (N, W - 1, D)
-    _tensors(dev, x=(x, bf, tuple(x.shape)), weight=(weight, bf, (D, W)), bias=(bias, bf, (D,)),
-             initial_state=(initial_state, bf, state), final_state=(final_state, bf, state),
-             out=(out, bf, tuple(x.shape)))
-    _contiguous(weight=weight, bias=bias, initial_state=initial_state, final_state=final_state)
+    _check_tensor("x", x, bf, shape, dev, False)
+    _check_tensor("weight", weight, bf, (D, W), dev)
+    _check_tensor("bias", bias, bf, (D,), dev)
+    _check_tensor("initial_state", initial_state, bf, state, dev)
+    _check_tensor("final_state", final_state, bf, state, dev)
+    _check_tensor("out", out, bf, shape, dev, False)
     cu64 = _offsets(cu_seqlens, dev)
     mine = []
     if out is None:
@@ -255,17 +254,20 @@ def conv_decode(x, weight, bias, state_pool, state_indices, *, activation: str =
     bf = torch.bfloat16
     if x.dim() != 3 or state_pool.dim() != 3:
         raise ValueError("x must be [N, T, D] and state_pool [P, W - 1, D]")
-    N, T, D = (int(v) for v in x.shape)
-    W = int(weight.shape[-1])
-    _tensors(dev, x=(x, bf, (N, T, D)), weight=(weight, bf, (D, W)), bias=(bias, bf, (D,)),
-             state_pool=(state_pool, bf, (int(state_pool.shape[0]), W - 1, D)),
-             state_indices=(state_indices, torch.int32, (N,)), out=(out, bf, (N, T, D)))
-    _contiguous(weight=weight, bias=bias, state_pool=state_pool, state_indices=state_indices)
+    shape, size = x.shape, state_pool.shape[0]
+    N, T, D = shape
+    W = weight.shape[-1]
+    _check_tensor("x", x, bf, shape, dev, False)
+    _check_tensor("weight", weight, bf, (D, W), dev)
+    _check_tensor("bias", bias, bf, (D,), dev)
+    _check_tensor("state_pool", state_pool, bf, (size, W - 1, D), dev)
+    _check_tensor("state_indices", state_indices, torch.int32, (N,), dev)
+    _check_tensor("out", out, bf, shape, dev, False)
     mine = []
     if out is None:
-        out = torch.empty((N, T, D), dtype=bf, device=dev)
+        out = torch.empty(shape, dtype=bf, device=dev)
         mine.append(out)
-    p = ConvDecodeProblem(N, T, D, W, ACTIVATIONS[activation], int(state_pool.shape[0]),
+    p = ConvDecodeProblem(N, T, D, W, ACTIVATIONS[activation], size,
                           _row_stride("x", x, 2), _row_stride("out", out, 2))
     _launch("kda_conv_decode", dev, stream, p,
             [_ptr(x), _ptr(weight), _ptr(bias), _ptr(state_pool), _ptr(state_indices), _ptr(out)], mine)
@@ -278,15 +280,20 @@ def _ssm_tokens(x, dt, A, B, C, D, z, dt_bias, out, lead):
 
     dev = _gpu(x)
     bf, f32 = torch.bfloat16, torch.float32
-    tok = tuple(int(v) for v in x.shape[:lead])
-    H, P = int(x.shape[-2]), int(x.shape[-1])
+    shape = x.shape
+    tok, (H, P) = shape[:lead], shape[lead:]
     if B.dim() != lead + 2:
         raise ValueError("B and C must be x.shape[:-2] + (G, N)")
-    G, N = int(B.shape[-2]), int(B.shape[-1])
-    _tensors(dev, x=(x, bf, tok + (H, P)), dt=(dt, f32, tok + (H,)), A=(A, f32, (H,)), B=(B, bf, tok + (G, N)),
-             C=(C, bf, tok + (G, N)), D=(D, f32, (H,)), z=(z, bf, tok + (H, P)), dt_bias=(dt_bias, f32, (H,)),
-             out=(out, bf, tok + (H, P)))
-    _contiguous(dt=dt, A=A, D=D, dt_bias=dt_bias)
+    G, N = B.shape[lead:]
+    _check_tensor("x", x, bf, shape, dev, False)
+    _check_tensor("dt", dt, f32, tok + (H,), dev)
+    _check_tensor("A", A, f32, (H,), dev)
+    _check_tensor("B", B, bf, tok + (G, N), dev, False)
+    _check_tensor("C", C, bf, B.shape, dev, False)
+    _check_tensor("D", D, f32, (H,), dev)
+    _check_tensor("z", z, bf, shape, dev, False)
+    _check_tensor("dt_bias", dt_bias, f32, (H,), dev)
+    _check_tensor("out", out, bf, shape, dev, False)
     return H, G, P, N
 
 
@@ -323,8 +330,8 @@ def ssm_prefill(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, dt_softplus: bo
         state_dtype = torch.float32 if given is None else given.dtype
     kind = _state_dtype(state_dtype)
     shape = (N, H, S, P)
-    _tensors(dev, initial_state=(initial_state, state_dtype, shape), final_state=(final_state, state_dtype, shape))
-    _contiguous(initial_state=initial_state, final_state=final_state, workspace=workspace)
+    _check_tensor("initial_state", initial_state, state_dtype, shape, dev)
+    _check_tensor("final_state", final_state, state_dtype, shape, dev)
     cu64 = _offsets(cu_seqlens, dev)
     mine = []
     if out is None:
@@ -342,8 +349,8 @@ def ssm_prefill(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, dt_softplus: bo
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
             mine.append(workspace)
-    elif workspace.device != dev:
-        raise ValueError(f"workspace is on {workspace.device}, expected {dev}")
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {dev}")
     size = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _launch("kda_ssm_prefill", dev, stream, p,
             [_ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(cu_seqlens),
@@ -366,18 +373,18 @@ def ssm_decode(x, dt, A, B, C, state_pool, state_indices, *, D=None, z=None, dt_
         raise ValueError("x must be [N, T, H, P]")
     H, G, P, S = _ssm_tokens(x, dt, A, B, C, D, z, dt_bias, out, 2)
     dev = x.device
-    N, T = int(x.shape[0]), int(x.shape[1])
+    N, T = x.shape[:2]
     kind = _state_dtype(state_pool.dtype)
     if state_pool.dim() != 4:
         raise ValueError(f"state_pool must be [pool, {H}, {S}, {P}]")
-    _tensors(dev, state_pool=(state_pool, state_pool.dtype, (int(state_pool.shape[0]), H, S, P)),
-             state_indices=(state_indices, torch.int32, (N,)))
-    _contiguous(state_pool=state_pool, state_indices=state_indices)
+    size = state_pool.shape[0]
+    _check_tensor("state_pool", state_pool, state_pool.dtype, (size, H, S, P), dev)
+    _check_tensor("state_indices", state_indices, torch.int32, (N,), dev)
     mine = []
     if out is None:
         out = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
         mine.append(out)
-    p = SsmDecodeProblem(N, T, H, G, P, S, int(dt_softplus), kind, int(state_pool.shape[0]),
+    p = SsmDecodeProblem(N, T, H, G, P, S, int(dt_softplus), kind, size,
                          _row_stride("x", x, 2), _row_stride("B", B, 2), _row_stride("C", C, 2),
                          0 if z is None else _row_stride("z", z, 2), _row_stride("out", out, 2))
     _launch("kda_ssm_decode", dev, stream, p,
@@ -401,7 +408,7 @@ def add_rmsnorm(x, weight, *, residual=None, eps: float = 1e-6, out_dtype=None, 
 
     dev = _gpu(x)
     bf = torch.bfloat16
-    shape = tuple(int(v) for v in x.shape)
+    shape = x.shape
     D = shape[-1]
     if out_dtype is None:
         out_dtype = bf if out is None else out.dtype
@@ -412,7 +419,7 @@ def add_rmsnorm(x, weight, *, residual=None, eps: float = 1e-6, out_dtype=None, 
         raise ValueError("residual_out needs a residual")
     if not fp8 and (scales is not None or scale_group):
         raise ValueError("scales are for a float8_e4m3fn output")
-    groups = shape[:-1] + ((D + 127) // 128 if scale_group else 1,)
+    groups = shape[:-1] + ((D + 127) // 128 if scale_group else 1,) if fp8 else None
     mine = []
     if residual is None or residual_out is False:
         residual_out = None
@@ -425,10 +432,12 @@ def add_rmsnorm(x, weight, *, residual=None, eps: float = 1e-6, out_dtype=None, 
     if fp8 and scales is None:
         scales = torch.empty(groups, dtype=torch.float32, device=dev)
         mine.append(scales)
-    _tensors(dev, x=(x, bf, shape), residual=(residual, bf, shape), weight=(weight, bf, (D,)),
-             out=(out, out_dtype, shape), scales=(scales, torch.float32, groups),
-             residual_out=(residual_out, bf, shape))
-    _contiguous(residual=residual, weight=weight, out=out, scales=scales, residual_out=residual_out)
+    _check_tensor("x", x, bf, shape, dev, False)
+    _check_tensor("residual", residual, bf, shape, dev)
+    _check_tensor("weight", weight, bf, (D,), dev)
+    _check_tensor("out", out, out_dtype, shape, dev)
+    _check_tensor("scales", scales, torch.float32, groups, dev)
+    _check_tensor("residual_out", residual_out, bf, shape, dev)
     p = NormProblem(x.numel() // D if D else 0, D, float(eps), int(fp8), int(scale_group),
                     _row_stride("x", x, x.dim() - 1))
     _launch("kda_add_rmsnorm", dev, stream, p,
