@@ -108,11 +108,19 @@ __global__ __launch_bounds__(256) void kda_conv_kernel(ConvArgs a, int shift, in
     }
   }
   const Taps<W> taps(a.weight, a.bias, col);
-  for (int64_t t = from; t < to; ++t) {
-    float cur[8];
-    bf16x8_f32(load8(x + t * a.x_stride), cur);
-    store8(a.out + t * a.out_stride + col, taps(past, cur, a.silu));
-    shift_in<W>(past, cur);
+  // eight rows are in flight at a time; behind the span the last one again
+  for (int64_t t = from; t < to; t += 8) {
+    uint4 row[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) row[i] = load8(x + (t + i < to ? t + i : to - 1) * a.x_stride);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float cur[8];
+      bf16x8_f32(row[i], cur);
+      const uint4 y = taps(past, cur, a.silu);
+      if (t + i < to) store8(a.out + (t + i) * a.out_stride + col, y);
+      shift_in<W>(past, cur);
+    }
   }
 }
 
@@ -157,8 +165,14 @@ __global__ __launch_bounds__(256) void kda_conv_step_kernel(ConvStepArgs a, int6
 }  // namespace
 
 hipError_t launch_conv(const ConvArgs& a, hipStream_t stream) {
-  constexpr int shift = 5;
+  // Spans of 16 tokens, of 8 where that leaves few waves: the W - 1 rows ahead
+  // of each span are read twice, mostly from a cache, and short spans keep more
+  // rows in flight.  us on MI355X at spans of 8 / 16 / 32 / 64 tokens: B8 T8192
+  // D4608 245 / 227 / 234 / 250 (5.3 TB/s of its bytes at 16), six ragged
+  // prompts D1792 15.7 / 16.3 / 19.4 / 22.2, T2048 D4608 11.3 / 12.4 / 13.6 /
+  // 21.4, T300 D1536 5.4 / 7.3 / 11.0 / 18.6.
   const int blocks = (a.D + 511) / 512;
+  const int shift = (a.pk.T_total >> 4) * blocks < 6144 ? 3 : 4;
   const int64_t waves = span_slots(a.pk.N, a.pk.T_total, 1 << shift) * blocks;
   const dim3 grid((unsigned)((waves + 3) / 4)), block(256);
   switch (a.W) {

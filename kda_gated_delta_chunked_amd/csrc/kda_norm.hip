@@ -4,9 +4,11 @@
 //   s = x + residual,  y = s / sqrt(mean(s^2) + eps) w,  residual_out = bf16(s)
 //   out = bf16(y), or e4m3(y / scale) with scale = max(max |y| / 448, 2^-126)
 //
-// One workgroup per row: each thread keeps its columns, eight at a time, in
+// LANES lanes per row, each with C pieces of eight columns that stay in
 // registers as fp32 between the sum of squares and the output, so the row is
-// read once.  Sums and maxima are fp32.
+// read once; sums and maxima are fp32.  Bound by memory.  Rows up to 2048
+// columns take 16 to 64 lanes of one wave, several rows per workgroup, and need
+// no barrier; longer ones take a workgroup.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -32,18 +34,32 @@ __device__ __forceinline__ uint2 e4m3x8(const float* f) {
   return make_uint2((uint32_t)lo, (uint32_t)hi);
 }
 
-// C pieces of eight columns per thread
-template <int C>
+// sum or max over the LANES lanes of a row; over a whole workgroup through
+// `red`, a slot per wave
+template <int LANES, class Op>
+__device__ __forceinline__ float over_row(float v, float* red, Op op) {
+#pragma unroll
+  for (int o = (LANES < 64 ? LANES : 64) / 2; o >= 1; o >>= 1) v = op(v, __shfl_xor(v, o, 64));
+  if constexpr (LANES > 64) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    lds_barrier();
+    v = op(op(red[0], red[1]), op(red[2], red[3]));
+  }
+  return v;
+}
+
+template <int LANES, int C>
 __global__ __launch_bounds__(THREADS) void kda_norm_kernel(NormArgs a) {
   __shared__ float red[2][THREADS / 64];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int64_t row = blockIdx.x;
+  const int in = threadIdx.x % LANES;
+  const int64_t row = (int64_t)blockIdx.x * (THREADS / LANES) + threadIdx.x / LANES;
+  if (row >= a.rows) return;  // whole rows' lanes (LANES 256: none)
   const int D = a.D;
   float v[C][8];
   float sum = 0.f;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int col = (c * THREADS + tid) * 8;
+    const int col = (c * LANES + in) * 8;
     if (col < D) {
       bf16x8_f32(*reinterpret_cast<const uint4*>(a.x + row * a.x_stride + col), v[c]);
       if (a.residual) {
@@ -60,17 +76,13 @@ __global__ __launch_bounds__(THREADS) void kda_norm_kernel(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum += v[c][i] * v[c][i];
   }
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
-  if (lane == 0) red[0][w] = sum;
-  lds_barrier();
-  sum = (red[0][0] + red[0][1]) + (red[0][2] + red[0][3]);
+  sum = over_row<LANES>(sum, red[0], [](float x, float y) { return x + y; });
   const float inv = 1.f / sqrtf(sum / (float)D + a.eps);
 
   float top = 0.f;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int col = (c * THREADS + tid) * 8;
+    const int col = (c * LANES + in) * 8;
     if (col < D) {
       float wt[8];
       bf16x8_f32(*reinterpret_cast<const uint4*>(a.weight + col), wt);
@@ -84,11 +96,8 @@ __global__ __launch_bounds__(THREADS) void kda_norm_kernel(NormArgs a) {
       }
     }
     if (a.scales && a.group) {
-      // 128 columns: 16 neighbouring threads
-      float m = top;
-#pragma unroll
-      for (int o = 8; o >= 1; o >>= 1) m = max_nan(m, __shfl_xor(m, o, 64));
-      m /= kE4m3Max;
+      // 128 columns: 16 neighbouring lanes
+      const float m = over_row<16>(top, nullptr, max_nan) / kE4m3Max;
       const float scale = m < kMinScale ? kMinScale : m;
       if (col < D) {
         const float is = 1.f / scale;
@@ -96,41 +105,54 @@ __global__ __launch_bounds__(THREADS) void kda_norm_kernel(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = v[c][i] * is;
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + row * D + col) = e4m3x8(f);
-        if ((lane & 15) == 0) a.scales[row * ((D + 127) / 128) + col / 128] = scale;
+        if ((in & 15) == 0) a.scales[row * ((D + 127) / 128) + col / 128] = scale;
       }
       top = 0.f;
     }
   }
   if (a.scales && !a.group) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) top = max_nan(top, __shfl_xor(top, o, 64));
-    if (lane == 0) red[1][w] = top;
-    lds_barrier();
-    top = max_nan(max_nan(red[1][0], red[1][1]), max_nan(red[1][2], red[1][3])) / kE4m3Max;
+    top = over_row<LANES>(top, red[1], max_nan) / kE4m3Max;
     const float scale = top < kMinScale ? kMinScale : top;
     const float is = 1.f / scale;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int col = (c * THREADS + tid) * 8;
+      const int col = (c * LANES + in) * 8;
       if (col < D) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[c][i] *= is;
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + row * D + col) = e4m3x8(v[c]);
       }
     }
-    if (tid == 0) a.scales[row] = scale;
+    if (in == 0) a.scales[row] = scale;
   }
+}
+
+template <int LANES, int C>
+void launch(const NormArgs& a, hipStream_t stream) {
+  constexpr int rows = THREADS / LANES;
+  hipLaunchKernelGGL((kda_norm_kernel<LANES, C>), dim3((unsigned)((a.rows + rows - 1) / rows)), dim3(THREADS), 0,
+                     stream, a);
 }
 
 }  // namespace
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
   if (a.rows == 0) return hipSuccess;
-  const dim3 grid((unsigned)a.rows), block(THREADS);
-  if (a.D <= 2048) hipLaunchKernelGGL(kda_norm_kernel<1>, grid, block, 0, stream, a);
-  else if (a.D <= 4096) hipLaunchKernelGGL(kda_norm_kernel<2>, grid, block, 0, stream, a);
-  else if (a.D <= 8192) hipLaunchKernelGGL(kda_norm_kernel<4>, grid, block, 0, stream, a);
-  else hipLaunchKernelGGL(kda_norm_kernel<8>, grid, block, 0, stream, a);
+  // The fewest lanes that hold a row with one piece each, then more pieces on a
+  // wave, then a workgroup; few rows take a workgroup from 512 columns on, whose
+  // lanes each have less to do one after the other.  us on MI355X: 98304 x 128
+  // 10.0 (5.05 TB/s; 49 with a workgroup per row), 65536 x 1536 to e4m3 131
+  // (5.4 TB/s), 65536 x 4096 to e4m3 318 (5.9 TB/s), 1 x 1536 2.3 with a
+  // workgroup and 3.7 with a wave.
+  if (a.D <= 128) launch<16, 1>(a, stream);
+  else if (a.D <= 256) launch<32, 1>(a, stream);
+  else if (a.D <= 512) launch<64, 1>(a, stream);
+  else if (a.D <= 2048 && a.rows < 1024) launch<256, 1>(a, stream);
+  else if (a.D <= 1024) launch<64, 2>(a, stream);
+  else if (a.D <= 2048) launch<64, 4>(a, stream);
+  else if (a.D <= 4096) launch<256, 2>(a, stream);
+  else if (a.D <= 8192) launch<256, 4>(a, stream);
+  else launch<256, 8>(a, stream);
   return hipGetLastError();
 }
 

@@ -7,8 +7,12 @@
 // state's columns, CPT = 4 with an fp32 pool and 8 with a bf16 one; columns
 // are independent.  Thread (rr = tid / 8, cg = tid % 8) holds rows rr + 32 i
 // of CPT consecutive columns in registers, read once from the pool, kept
-// across the call's tokens and written back in place.  Bound by the state's
-// bytes in and out.
+// across the call's tokens and written back in place.  The tokens' vectors are
+// staged in LDS up to four at a time, and each token's partial sums over the
+// rows are left there, so a group of tokens takes two barriers.  Bound by the
+// state's bytes in and out where they are many (1024 requests x 12 heads of
+// 128 x 128, one token: 312 us, 5.1 TB/s), else by the tokens' latency (9 requests x 4
+// tokens x 24 heads of 64 x 128, bf16: 6.6 us).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -38,10 +42,10 @@ __device__ __forceinline__ void store_state(void* base, int64_t e, const float* 
 
 template <int N, int P, bool BF>
 __global__ __launch_bounds__(256) void kda_ssm_step_kernel(SsmStepArgs a) {
-  constexpr int CPT = BF ? 8 : 4, WC = 8 * CPT, PARTS = P / WC, ROWS = N / 32;
+  constexpr int CPT = BF ? 8 : 4, WC = 8 * CPT, PARTS = P / WC, ROWS = N / 32, GROUP = 4;
   static_assert(N + WC < 256, "one thread per staged value");
-  __shared__ float sB[N], sC[N], sx[WC], sz[WC], sstep;
-  __shared__ float red[4][WC];
+  __shared__ float sB[GROUP][N], sC[GROUP][N], sx[GROUP][WC], sz[GROUP][WC], sstep[GROUP];
+  __shared__ float red[GROUP][4][WC];
 
   const SsmTokens& k = a.t;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
@@ -73,74 +77,71 @@ __global__ __launch_bounds__(256) void kda_ssm_step_kernel(SsmStepArgs a) {
   for (int i = 0; i < ROWS; ++i) load_state<CPT, BF>(a.pool, se + (int64_t)(32 * i) * P, S[i]);
   const float A = k.A[h], Dh = k.D ? k.D[h] : 0.f, bias = k.dt_bias ? k.dt_bias[h] : 0.f;
 
-  // the token's vectors, fetched one token ahead
-  uint16_t v0 = 0, v1 = 0;
-  float vdt = 0.f;
-  auto fetch = [&](int64_t tok) {
+  // a group's vectors: a thread's place in B and C, in x and z, or the step
+  auto stage = [&](int64_t tok, int j) {
     if (tid < N) {
-      v0 = k.B[tok * k.b_stride + g * N + tid];
-      v1 = k.C[tok * k.c_stride + g * N + tid];
+      sB[j][tid] = bf16_f32(k.B[tok * k.b_stride + g * N + tid]);
+      sC[j][tid] = bf16_f32(k.C[tok * k.c_stride + g * N + tid]);
     } else if (tid < N + WC) {
-      const int c = (h * P) + part * WC + tid - N;
-      v0 = k.x[tok * k.x_stride + c];
-      if (k.z) v1 = k.z[tok * k.z_stride + c];
+      const int c = h * P + part * WC + tid - N;
+      sx[j][tid - N] = bf16_f32(k.x[tok * k.x_stride + c]);
+      if (k.z) sz[j][tid - N] = bf16_f32(k.z[tok * k.z_stride + c]);
     } else if (tid == N + WC) {
-      vdt = k.dt[tok * k.H + h];
+      sstep[j] = ssm_step_of(k.dt[tok * k.H + h], bias, k.softplus);
     }
   };
-  fetch(tok0);
 
-  for (int t = 0; t < a.T; ++t) {
-    if (tid < N) {
-      sB[tid] = bf16_f32(v0);
-      sC[tid] = bf16_f32(v1);
-    } else if (tid < N + WC) {
-      sx[tid - N] = bf16_f32(v0);
-      sz[tid - N] = bf16_f32(v1);
-    } else if (tid == N + WC) {
-      sstep = ssm_step_of(vdt, bias, k.softplus);
-    }
+  for (int t0 = 0; t0 < a.T; t0 += GROUP) {
+    const int tokens = a.T - t0 < GROUP ? a.T - t0 : GROUP;
+#pragma unroll
+    for (int j = 0; j < GROUP; ++j)
+      if (j < tokens) stage(tok0 + t0 + j, j);
     lds_barrier();
-    if (t + 1 < a.T) fetch(tok0 + t + 1);
-    const float step = sstep, decay = expf(step * A);
-    float x[CPT], y[CPT];
 #pragma unroll
-    for (int j = 0; j < CPT; ++j) {
-      x[j] = sx[CPT * cg + j];
-      y[j] = 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      const float b = step * sB[rr + 32 * i], c = sC[rr + 32 * i];
+    for (int t = 0; t < GROUP; ++t) {
+      if (t >= tokens) break;
+      const float step = sstep[t], decay = expf(step * A);
+      float x[CPT], y[CPT];
 #pragma unroll
       for (int j = 0; j < CPT; ++j) {
-        S[i][j] = decay * S[i][j] + b * x[j];
-        y[j] += c * S[i][j];
+        x[j] = sx[t][CPT * cg + j];
+        y[j] = 0.f;
       }
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) {
+        const float b = step * sB[t][rr + 32 * i], c = sC[t][rr + 32 * i];
+#pragma unroll
+        for (int j = 0; j < CPT; ++j) {
+          S[i][j] = decay * S[i][j] + b * x[j];
+          y[j] += c * S[i][j];
+        }
+      }
+      // over the wave's 8 row positions
+#pragma unroll
+      for (int j = 0; j < CPT; ++j)
+#pragma unroll
+        for (int o = 8; o < 64; o <<= 1) y[j] += __shfl_xor(y[j], o, 64);
+      if (lane < 8)
+#pragma unroll
+        for (int j = 0; j < CPT; ++j) red[t][w][CPT * cg + j] = y[j];
     }
-    // over the wave's 8 row positions, then over the 4 waves
-#pragma unroll
-    for (int j = 0; j < CPT; ++j)
-#pragma unroll
-      for (int o = 8; o < 64; o <<= 1) y[j] += __shfl_xor(y[j], o, 64);
-    if (lane < 8)
-#pragma unroll
-      for (int j = 0; j < CPT; ++j) red[w][CPT * cg + j] = y[j];
     lds_barrier();
-    if (rr == 0) {
+    // over the 4 waves: eight threads a token
+    if (rr < tokens) {
+      const int t = rr;
       float o[CPT];
 #pragma unroll
       for (int j = 0; j < CPT; ++j) {
         const int c = CPT * cg + j;
-        o[j] = (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]) + Dh * x[j];
-        if (k.z) o[j] *= silu(sz[c]);
+        o[j] = (red[t][0][c] + red[t][1][c]) + (red[t][2][c] + red[t][3][c]) + Dh * sx[t][c];
+        if (k.z) o[j] *= silu(sz[t][c]);
       }
 #pragma unroll
       for (int c = 0; c < CPT; c += 4)
-        *reinterpret_cast<uint2*>(out + t * k.out_stride + c) =
+        *reinterpret_cast<uint2*>(out + (t0 + t) * k.out_stride + c) =
             make_uint2(bf16_pair(o[c], o[c + 1]), bf16_pair(o[c + 2], o[c + 3]));
     }
-    lds_barrier();  // the staged vectors and partial sums are rewritten next token
+    if (t0 + GROUP < a.T) lds_barrier();  // the staged vectors are rewritten next
   }
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) store_state<CPT, BF>(a.pool, se + (int64_t)(32 * i) * P, S[i]);
