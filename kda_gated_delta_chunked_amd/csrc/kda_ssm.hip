@@ -253,7 +253,8 @@ __device__ __forceinline__ bf16x8 finite_only(const bf16x8& f) {
 
 // The decays of 64 (token, head) pairs: two chunks of one head, or a chunk of
 // two heads.  c_t is taken from the chunk's first token, in fp32: its error,
-// 2^-24 of the sum, matters least where the decays, and so the sums, are large.
+// 2^-24 of the sum, is 2^-12 at most (32 logarithms of -256) and matters least
+// where the decays, and so the sums, are large.
 // The state is held scaled: it is the accumulators times 2^lf, lf <= 0 going
 // down with the chunks' decays, until 2^lf would fall below 2^kLeast: then the
 // accumulators take the factor in and lf is zero again.  Most chunks then need
@@ -382,7 +383,11 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
     const float step = gate_tok < rows ? ssm_step_of(rdt, gate_bias, k.softplus) : 0.f;
     float A = gate_A;
     settle(A);
-    const double cum = prefix_sums((double)step * (double)A * kLog2e);
+    // A token that keeps less than 2^-256 keeps nothing in fp32: without the bound
+    // its logarithm would take the bits of the small ones behind it from the sums.
+    double log = (double)step * (double)A * kLog2e;
+    log = log < -256.0 ? -256.0 : log;
+    const double cum = prefix_sums(log);
     const double sum0 = lane_of(cum, 31), sum1 = lane_of(cum, 63);
     if (!FULL) {
       log_decay[0] += sum0;
@@ -636,6 +641,7 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
     if (buf) gbuf ^= 1;
    }
   }
+  memory_left<0>();  // no copy to LDS outlives the workgroup
 
   {
     const float f = __builtin_amdgcn_exp2f(scale_left);

@@ -174,6 +174,13 @@ def _launch(name: str, dev, stream, problem, args, mine=()):
         _check(status, name)
 
 
+def _activation(name) -> int:
+    kind = ACTIVATIONS.get(name)
+    if kind is None:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {name!r}")
+    return kind
+
+
 def _offsets(cu_seqlens, dev):
     import torch
 
@@ -233,7 +240,7 @@ def conv_prefill(x, weight, bias=None, *, cu_seqlens=None, initial_state=None, f
     if final_state is None and output_final_state:
         final_state = torch.empty(state, dtype=bf, device=dev)
         mine.append(final_state)
-    p = ConvProblem(N, T, D, W, ACTIVATIONS[activation], cu64, _row_stride("x", x, lead),
+    p = ConvProblem(N, T, D, W, _activation(activation), cu64, _row_stride("x", x, lead),
                     _row_stride("out", out, lead))
     _launch("kda_conv_prefill", dev, stream, p,
             [_ptr(x), _ptr(weight), _ptr(bias), _ptr(cu_seqlens), _ptr(initial_state), _ptr(out),
@@ -267,7 +274,7 @@ def conv_decode(x, weight, bias, state_pool, state_indices, *, activation: str =
     if out is None:
         out = torch.empty(shape, dtype=bf, device=dev)
         mine.append(out)
-    p = ConvDecodeProblem(N, T, D, W, ACTIVATIONS[activation], size,
+    p = ConvDecodeProblem(N, T, D, W, _activation(activation), size,
                           _row_stride("x", x, 2), _row_stride("out", out, 2))
     _launch("kda_conv_decode", dev, stream, p,
             [_ptr(x), _ptr(weight), _ptr(bias), _ptr(state_pool), _ptr(state_indices), _ptr(out)], mine)
