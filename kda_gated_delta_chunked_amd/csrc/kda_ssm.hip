@@ -29,6 +29,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "kda_ssm_kernels.h"
 
@@ -120,10 +121,12 @@ __device__ __forceinline__ bf16x8 as_frag(const uint32_t (&u)[4]) {
   return __builtin_bit_cast(bf16x8, make_uint4(u[0], u[1], u[2], u[3]));
 }
 
-// x w as a sum of three bf16 fragments: each part takes the upper 16 bits of
-// what is left, 8 significant bits at a time.
+// x w as a sum of bf16 fragments: each part takes the upper 16 bits of what is
+// left, 8 significant bits at a time.  Three parts are the fp32 product; two
+// leave out 2^-15 of it at most.
 struct Split {
   uint32_t part[3][4];
+  template <int PARTS>
   __device__ __forceinline__ void pair(int i, const bf16x8& x, float w0, float w1) {
     const uint32_t u = reinterpret_cast<const uint32_t*>(&x)[i];
     const float x0 = __uint_as_float(u << 16), x1 = __uint_as_float(u & 0xffff0000u);
@@ -132,9 +135,11 @@ struct Split {
     v0 = __builtin_fmaf(x0, w0, -top(v0));
     v1 = __builtin_fmaf(x1, w1, -top(v1));
     part[1][i] = upper(v0, v1);
-    v0 -= top(v0);
-    v1 -= top(v1);
-    part[2][i] = upper(v0, v1);
+    if (PARTS == 3) {
+      v0 -= top(v0);
+      v1 -= top(v1);
+      part[2][i] = upper(v0, v1);
+    }
   }
   __device__ __forceinline__ bf16x8 frag(int q) const { return as_frag(part[q]); }
 
@@ -278,37 +283,27 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
   return (int64_t)(((uint64_t)hi << 32) | lo);
 }
 
-// One piece (or a whole sequence) and HPW heads of a group per workgroup.
-// FULL: with outputs; else the state that a piece's own tokens add.  The chunk
-// loop's memory accesses are the same on every path, so that waiting for the
-// next chunk's rows never waits for this one's stores.
-template <int N, int P, int HPW, bool FULL>
-__global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kernel(SsmArgs a) {
+// One piece (or a whole sequence) and HPW heads of a group.  FULL: with
+// outputs; else the state that a piece's own tokens add.  PARTS: of x w.  The
+// chunk loop's memory accesses are the same on every path, so that waiting for
+// the next chunk's rows never waits for this one's stores.  Two buffers for B
+// and x, objects of their own: the copies in flight to one are then known not to
+// touch what is read from the other.  C is last read ahead of the chunk's second
+// barrier and copied behind it, to one buffer, so that three workgroups fit a CU.
+template <int N, int P, int HPW, bool FULL, bool GATE, int PARTS>
+__device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int64_t slot, int head0, uint8_t* b0,
+                                          uint8_t* b1, uint8_t* x0, uint8_t* x1, uint8_t* tC, uint8_t* tM, uint8_t* tZ,
+                                          Gates* gates) {
   constexpr int WPH = P / 32, WAVES = HPW * WPH, THREADS = WAVES * 64, XC = HPW * P, NB = N / 32;
-  // Two buffers for B and x, objects of their own: the copies in flight to one
-  // are then known not to touch what is read from the other.  C is last read
-  // ahead of the chunk's second barrier and copied behind it, to one buffer, so
-  // that three workgroups fit a CU.
-  constexpr int TB = L * N * 2, TX = L * XC * 2, TC = FULL ? TB : 16, TM = FULL ? HPW * 3 * M_BLOCK : 16;
-  __shared__ __attribute__((aligned(16))) uint8_t b0[TB], b1[TB], x0[TX], x1[TX], tC[TC], tM[TM], tZ[FULL ? TX : 16];
-  __shared__ Gates gates[2];
 
   const SsmTokens& k = a.t;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l32 = lane & 31, up = lane >> 5;
-  // blocks go to the 8 XCDs in turn: the heads of a sequence (or of a piece),
-  // which read the same B and C, share one
-  const int HG = k.H / HPW;
-  const int64_t blk = blockIdx.x;
-  const int64_t slot = (blk / (8 * HG)) * 8 + (blk & 7);
-  if (slot >= a.slots) return;
-  const Span sp = span_of(a.pk, a.piece, slot);
-  if (sp.k < 0) return;
   const int seq = __builtin_amdgcn_readfirstlane(sp.seq), piece = __builtin_amdgcn_readfirstlane(sp.k);
   const int64_t end = uniform(sp.end), from = uniform(sp.begin) + (int64_t)piece * a.piece;
   const bool last = !a.piece_state || end - from <= a.piece;
   const int64_t to = last ? end : from + a.piece;
-  const int head0 = (int)((blk >> 3) % HG) * HPW, hh = wave / WPH, head = head0 + hh, pc = (wave % WPH) * 32;
+  const int hh = wave / WPH, head = head0 + hh, pc = (wave % WPH) * 32;
 
   // state rows 32 nb + 16 (r / 8) + 8 up + r % 8 of column pc + l32
   const int64_t state0 = (int64_t)head * N * P + (int64_t)(8 * up) * P + pc + l32;
@@ -350,9 +345,10 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
   const uint16_t* Bp = k.B + g * N;
   const uint16_t* Cp = k.C + g * N;
   const uint16_t* Xp = k.x + (int64_t)head0 * P;
-  const uint16_t* Zp = k.z ? k.z + (int64_t)head0 * P : nullptr;
+  const uint16_t* Zp = GATE ? k.z + (int64_t)head0 * P : nullptr;
   uint16_t* Op = k.out + (int64_t)head0 * P;
   const float Dh = k.D ? k.D[head] : 0.f;
+  const uint32_t skip = k.D ? ~0u : 0u;  // without a skip term, x's infinities stay out of it
   const bool gate_wave = wave == WAVES - 1;
 
   // rows left in the piece (a long one counts down from 2^30)
@@ -455,7 +451,7 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
     }
     // this chunk's gate, then the next chunk's rows; nobody reads the other
     // buffer any more
-    if constexpr (FULL) copyZ.start(cZ, Zp ? min(rem, L) : 0, tZ, wave);
+    if constexpr (GATE) copyZ.start(cZ, min(rem, L), tZ, wave);
     cB.advance(L);
     cX.advance(L);
     copyB.start(cB, min(rem - L, L), buf ? b0 : b1, wave);
@@ -507,6 +503,7 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
     xf[0] = cols_frag<XC>(tX, at_x);
     read_w(0);
     bf16x8 bf[NB];
+    float decay_y = 0.f;
     if constexpr (FULL) {
       constexpr int KS = N / 16, AHEAD = 2;
       bf16x8 cf[KS];
@@ -524,20 +521,19 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
         if (s + AHEAD < KS) cf[s + AHEAD] = rows_frag(tC, at_row ^ ((s + AHEAD) << 5));
         if (s == KS - 3) bf[0] = read_b(0, 0);
         if (s == KS - 2) bf[1] = read_b(0, 1);
-        if (s >= KS - 4) xs[0].pair(s - (KS - 4), xf[0], w[0][2 * (s - (KS - 4))], w[0][2 * (s - (KS - 4)) + 1]);
+        if (s >= KS - 4) xs[0].template pair<PARTS>(s - (KS - 4), xf[0], w[0][2 * (s - (KS - 4))], w[0][2 * (s - (KS - 4)) + 1]);
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int nb = 2; nb < NB; ++nb) bf[nb] = read_b(0, nb);
-#pragma unroll
-      for (int r = 0; r < 16; ++r) Y[r] *= e;
+      decay_y = e;
     } else {
       bf[0] = read_b(0, 0);
       bf[1] = read_b(0, 1);
 #pragma unroll
       for (int nb = 2; nb < NB; ++nb) bf[nb] = read_b(0, nb);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) xs[0].pair(i, xf[0], w[0][2 * i], w[0][2 * i + 1]);
+      for (int i = 0; i < 4; ++i) xs[0].template pair<PARTS>(i, xf[0], w[0][2 * i], w[0][2 * i + 1]);
     }
     scale_left = next;
     if (next < kLeast) {
@@ -551,25 +547,35 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
     // neighbouring products go to different accumulators
     forget(at_b);
 #pragma unroll
-    for (int q = 0; q < 3; ++q)
+    for (int q = 0; q < PARTS; ++q)
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         S[nb] = mfma(bf[nb], xs[0].frag(q), S[nb]);
-        if (q == 2) bf[nb] = read_b(1, nb);
+        if constexpr (FULL) {
+          if (q == PARTS - 1) {
+#pragma unroll
+            for (int r = nb * 16 / NB; r < (nb + 1) * 16 / NB; ++r) Y[r] *= decay_y;
+          }
+        }
+        if (q == PARTS - 1) bf[nb] = read_b(1, nb);
         if (q == 0 && nb == NB / 2 - 1) xf[1] = cols_frag<XC>(tX + 16 * XC * 2, at_x);
         if (q == 0 && nb == NB / 2) read_w(1);
         if (nb % (NB / 2) == NB / 2 - 1 && q > 0) {
-          const int i = 2 * (q - 1) + nb / (NB / 2);
-          xs[1].pair(i, xf[1], w[1][2 * i], w[1][2 * i + 1]);
+          constexpr int PAIRS = 4 / (PARTS - 1) / 2;
+#pragma unroll
+          for (int j = 0; j < PAIRS; ++j) {
+            const int i = PAIRS * (2 * (q - 1) + nb / (NB / 2)) + j;
+            xs[1].template pair<PARTS>(i, xf[1], w[1][2 * i], w[1][2 * i + 1]);
+          }
         }
         __builtin_amdgcn_sched_barrier(0);
       }
+    if constexpr (!FULL) {
 #pragma unroll
-    for (int q = 0; q < 3; ++q)
+      for (int q = 0; q < PARTS; ++q)
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) S[nb] = mfma(bf[nb], xs[1].frag(q), S[nb]);
-
-    if constexpr (FULL) {
+        for (int nb = 0; nb < NB; ++nb) S[nb] = mfma(bf[nb], xs[1].frag(q), S[nb]);
+    } else {
       memory_left<NEXT_COPIES>();  // the gate's rows are in
       lds_only_barrier();
       // C has been read
@@ -601,30 +607,36 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
         }
       }
 
-      // lane = token, four columns at a time; the rounded values take x's place
-      // in the tile, for stores of whole 64-byte runs
-      if (k.D) {
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const uint2 xv = *reinterpret_cast<const uint2*>(tX + (at_o ^ (b << 4)));
-          const uint32_t xw[4] = {xv.x << 16, xv.x & 0xffff0000u, xv.y << 16, xv.y & 0xffff0000u};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) Y[4 * b + i] += Dh * __uint_as_float(xw[i]);
-        }
-      }
-      if (Zp) {
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const uint2 zv = *reinterpret_cast<const uint2*>(tZ + (at_o ^ (b << 4)));
-          const uint32_t zw[4] = {zv.x << 16, zv.x & 0xffff0000u, zv.y << 16, zv.y & 0xffff0000u};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) Y[4 * b + i] *= silu(__uint_as_float(zw[i]));
-        }
-      }
+      // The state's products of the chunk's second half, and in their shadow the
+      // outputs: lane = token, four columns at a time; the rounded values take
+      // x's place in the tile, for stores of whole 64-byte runs.
       uint8_t* yt = buf ? x1 : x0;
+      constexpr int PRODUCTS = PARTS * NB;
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        lds_write8(yt + (at_o ^ (b << 4)), bf16_pair(Y[4 * b], Y[4 * b + 1]), bf16_pair(Y[4 * b + 2], Y[4 * b + 3]));
+      for (int i = 0; i < PRODUCTS; ++i) {
+        S[i % NB] = mfma(bf[i % NB], xs[1].frag(i / NB), S[i % NB]);
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (b * PRODUCTS / 4 == i) {
+            float gate[4];
+            if constexpr (GATE) {
+              const uint2 zv = *reinterpret_cast<const uint2*>(tZ + (at_o ^ (b << 4)));
+              const uint32_t zw[4] = {zv.x << 16, zv.x & 0xffff0000u, zv.y << 16, zv.y & 0xffff0000u};
+#pragma unroll
+              for (int c = 0; c < 4; ++c) gate[c] = silu(__uint_as_float(zw[c]));
+            }
+            const uint2 xv = *reinterpret_cast<const uint2*>(tX + (at_o ^ (b << 4)));
+            const uint32_t x01 = xv.x & skip, x23 = xv.y & skip;
+            const uint32_t xw[4] = {x01 << 16, x01 & 0xffff0000u, x23 << 16, x23 & 0xffff0000u};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              Y[4 * b + c] += Dh * __uint_as_float(xw[c]);
+              if constexpr (GATE) Y[4 * b + c] *= gate[c];
+            }
+            lds_write8(yt + (at_o ^ (b << 4)), bf16_pair(Y[4 * b], Y[4 * b + 1]), bf16_pair(Y[4 * b + 2], Y[4 * b + 3]));
+          }
+        __builtin_amdgcn_sched_barrier(0);
+      }
       int srow = lane >> 2;
       forget(srow);
       const __amdgpu_buffer_rsrc_t ow = cO.window(min(rem, L));
@@ -666,7 +678,7 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
         decay[0] = __builtin_amdgcn_exp2f((float)(log_decay[0] + log_decay[1]));
       }
     }
-  } else if (last && a.final_state) {
+  } else if (PARTS == 3) {  // the last piece, and a final state is wanted
     if (a.state_bf16) {
       uint16_t* out = static_cast<uint16_t*>(a.final_state) + seq * per_seq + state0;
 #pragma unroll
@@ -681,6 +693,33 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
         for (int r = 0; r < 16; ++r) out[row_of(nb, r)] = S[nb][r];
     }
   }
+}
+
+// Where no final state comes from a launch, the state is read for the outputs
+// alone, rounded to bf16: two parts of x w are enough.
+template <int N, int P, int HPW, bool FULL, bool GATE>
+__global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kernel(SsmArgs a) {
+  constexpr int XC = HPW * P, TB = L * N * 2, TX = L * XC * 2, TC = FULL ? TB : 16, TM = FULL ? HPW * 3 * M_BLOCK : 16;
+  __shared__ __attribute__((aligned(16))) uint8_t b0[TB], b1[TB], x0[TX], x1[TX], tC[TC], tM[TM], tZ[GATE ? TX : 16];
+  __shared__ Gates gates[2];
+  // blocks go to the 8 XCDs in turn: the heads of a sequence (or of a piece),
+  // which read the same B and C, share one
+  const int HG = a.t.H / HPW;
+  const int64_t blk = blockIdx.x;
+  int64_t slot = (blk / (8 * HG)) * 8 + (blk & 7);
+  if (slot >= a.slots) return;
+  if (FULL && a.piece_state) slot = a.slots - 1 - slot;
+  const Span sp = span_of(a.pk, a.piece, slot);
+  if (sp.k < 0) return;
+  const int head0 = (int)((blk >> 3) % HG) * HPW;
+  if constexpr (FULL) {
+    const bool last = uniform(sp.end - sp.begin - (int64_t)sp.k * a.piece) <= (int64_t)a.piece;
+    if (!last || !a.final_state) {
+      run_piece<N, P, HPW, FULL, GATE, 2>(a, sp, slot, head0, b0, b1, x0, x1, tC, tM, tZ, gates);
+      return;
+    }
+  }
+  run_piece<N, P, HPW, FULL, GATE, 3>(a, sp, slot, head0, b0, b1, x0, x1, tC, tM, tZ, gates);
 }
 
 // Between a split's launches: the state ahead of piece q + 1 is what piece q
@@ -728,10 +767,11 @@ void launch(const SsmArgs& a, hipStream_t stream) {
   if (a.piece_state) {
     const int blocks_per_head = N * P / 1024;
     const int64_t join = (int64_t)a.pk.N * a.t.H * blocks_per_head;
-    hipLaunchKernelGGL((kda_ssm_kernel<N, P, HPW, false>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((kda_ssm_kernel<N, P, HPW, false, false>), grid, block, 0, stream, a);
     hipLaunchKernelGGL(kda_ssm_join_kernel, dim3((unsigned)join), dim3(256), 0, stream, a, blocks_per_head);
   }
-  hipLaunchKernelGGL((kda_ssm_kernel<N, P, HPW, true>), grid, block, 0, stream, a);
+  if (a.t.z) hipLaunchKernelGGL((kda_ssm_kernel<N, P, HPW, true, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((kda_ssm_kernel<N, P, HPW, true, false>), grid, block, 0, stream, a);
 }
 
 // Heads of 64 columns run two to a workgroup where a group has an even number
