@@ -105,6 +105,15 @@ __device__ __forceinline__ void lds_write8(uint8_t* at, uint32_t lo, uint32_t hi
 #endif
 }
 
+__device__ __forceinline__ void lds_write4(uint8_t* at, float v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef __attribute__((address_space(3))) uint8_t* lds_ptr;
+  asm volatile("ds_write_b32 %0, %1" ::"v"((uint32_t)(uintptr_t)(lds_ptr)at), "v"(v) : "memory");
+#else
+  (void)at, (void)v;
+#endif
+}
+
 // Waits until at most `left` of the wave's memory accesses are under way.
 template <int LEFT>
 __device__ __forceinline__ void memory_left() {
@@ -276,6 +285,9 @@ constexpr float kLeast = -20.f;
 // conflicts between 16 lanes' rows)
 constexpr int M_BLOCK = 16 * 16 * 2;
 __device__ __forceinline__ int m_at(int t, int chunk) { return t * 32 + ((chunk ^ ((t >> 3) & 1)) << 4); }
+// The diagonal blocks' rows 0..7 are zero in their second chunk: row 0's stands
+// for all, rows 1..4's hold what the 16 diagonal elements lost to bf16.
+__device__ __forceinline__ int lost_at(int t) { return m_at(1 + (t >> 2), 1) + 4 * (t & 3); }
 
 __device__ __forceinline__ int64_t uniform(int64_t v) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
@@ -348,7 +360,6 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
   const uint16_t* Zp = GATE ? k.z + (int64_t)head0 * P : nullptr;
   uint16_t* Op = k.out + (int64_t)head0 * P;
   const float Dh = k.D ? k.D[head] : 0.f;
-  const uint32_t skip = k.D ? ~0u : 0u;  // without a skip term, x's infinities stay out of it
   const bool gate_wave = wave == WAVES - 1;
 
   // rows left in the piece (a long one counts down from 2^30)
@@ -424,9 +435,10 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
   int at_x = tile_at<XC>(tr, xcol + 2 * q1 + (m >> 1)) + 8 * (m & 1);
   int at_b = tile_at<N>(tr, 2 * q1 + (m & 1)) + 8 * (m >> 1);
   int at_o = tile_at<XC>(l32, xcol) + 8 * up;
-  const int m_base = hh * 3 * M_BLOCK + m_at(l16, up);
-  // above the diagonal: the zeros behind row 0 of block (0, 0)
-  int at_m0 = m_base + (l32 < 16 ? 0 : M_BLOCK), at_m1 = l32 < 16 ? hh * 3 * M_BLOCK + m_at(0, 1) : m_base + 2 * M_BLOCK;
+  const int m_block = hh * 3 * M_BLOCK, m_row = m_block + m_at(l16, up), m_zeros = m_block + m_at(0, 1);
+  const int m_diag = l16 < 8 && up ? m_zeros : m_row + (l32 < 16 ? 0 : 2 * M_BLOCK);
+  int at_m0 = l32 < 16 ? m_diag : m_row + M_BLOCK, at_m1 = l32 < 16 ? m_zeros : m_diag;
+  const int at_lost = m_block + (l32 < 16 ? 0 : 2 * M_BLOCK) + lost_at(l16);
   int at_s = tile_at<XC>(lane >> 2, xcol + (lane & 3));
   const int scol = (xcol + (lane & 3)) * 16;
 
@@ -482,6 +494,10 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
           }
           lds_write8(tM + (q * 3 + blk16) * M_BLOCK + m_at(l16, q4 >> 1) + 8 * (q4 & 1), bf16_pair(mv[0], mv[1]),
                      bf16_pair(mv[2], mv[3]));
+          if (PARTS == 3 && blk16 != 1 && l16 >> 2 == q4) {
+            const float v = l16 & 2 ? (l16 & 1 ? mv[3] : mv[2]) : (l16 & 1 ? mv[1] : mv[0]);
+            lds_write4(tM + (q * 3 + blk16) * M_BLOCK + lost_at(l16), v - bf16_f32(bf16_pair(v, 0.f) & 0xffff));
+          }
         }
       }
 
@@ -610,6 +626,9 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
       // The state's products of the chunk's second half, and in their shadow the
       // outputs: lane = token, four columns at a time; the rounded values take
       // x's place in the tile, for stores of whole 64-byte runs.
+      // x_t's coefficient is the skip term and what M's diagonal lost when it was
+      // rounded, which a short sequence has little else to even out.
+      const float own = PARTS == 3 ? Dh + *reinterpret_cast<const float*>(tM + at_lost) : Dh;
       uint8_t* yt = buf ? x1 : x0;
       constexpr int PRODUCTS = PARTS * NB;
 #pragma unroll
@@ -626,11 +645,10 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
               for (int c = 0; c < 4; ++c) gate[c] = silu(__uint_as_float(zw[c]));
             }
             const uint2 xv = *reinterpret_cast<const uint2*>(tX + (at_o ^ (b << 4)));
-            const uint32_t x01 = xv.x & skip, x23 = xv.y & skip;
-            const uint32_t xw[4] = {x01 << 16, x01 & 0xffff0000u, x23 << 16, x23 & 0xffff0000u};
+            const uint32_t xw[4] = {xv.x << 16, xv.x & 0xffff0000u, xv.y << 16, xv.y & 0xffff0000u};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              Y[4 * b + c] += Dh * __uint_as_float(xw[c]);
+              Y[4 * b + c] += own * __uint_as_float(xw[c]);
               if constexpr (GATE) Y[4 * b + c] *= gate[c];
             }
             lds_write8(yt + (at_o ^ (b << 4)), bf16_pair(Y[4 * b], Y[4 * b + 1]), bf16_pair(Y[4 * b + 2], Y[4 * b + 3]));
