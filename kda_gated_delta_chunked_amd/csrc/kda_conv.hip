@@ -173,7 +173,7 @@ hipError_t launch_conv(const ConvArgs& a, hipStream_t stream) {
   // 21.4, T300 D1536 5.4 / 7.3 / 11.0 / 18.6.
   const int blocks = (a.D + 511) / 512;
   const int shift = (a.pk.T_total >> 4) * blocks < 6144 ? 3 : 4;
-  const int64_t waves = span_slots(a.pk.N, a.pk.T_total, 1 << shift) * blocks;
+  const int64_t waves = span_slots(a.pk.cu, a.pk.N, a.pk.T_total, 1 << shift) * blocks;
   const dim3 grid((unsigned)((waves + 3) / 4)), block(256);
   switch (a.W) {
     case 2: hipLaunchKernelGGL(kda_conv_kernel<2>, grid, block, 0, stream, a, shift, waves, blocks); break;

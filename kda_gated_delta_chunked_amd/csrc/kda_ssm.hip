@@ -726,6 +726,8 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
   const int64_t blk = blockIdx.x;
   int64_t slot = (blk / (8 * HG)) * 8 + (blk & 7);
   if (slot >= a.slots) return;
+  // last pieces first: the first launch has just read them, and the device's
+  // last cache may still hold them (B8 T8192 H12 in pieces of 512: 286 -> 272 us)
   if (FULL && a.piece_state) slot = a.slots - 1 - slot;
   const Span sp = span_of(a.pk, a.piece, slot);
   if (sp.k < 0) return;
@@ -753,7 +755,7 @@ __global__ __launch_bounds__(256) void kda_ssm_join_kernel(SsmArgs a, int blocks
   if (end < begin) end = begin;
   const int64_t pieces = (end - begin + a.piece - 1) / a.piece;
   if (pieces < 3) return;  // the first piece started from the initial state
-  const int64_t slot = begin / a.piece + seq;
+  const int64_t slot = first_slot(a.pk, a.piece, seq, begin);
   float* at = a.piece_state + slot * per_seq + h * per_head + ((in % blocks_per_head) * 256 + threadIdx.x) * 4;
   const float* decay = a.piece_decay + slot * a.t.H + h;
   float4 S = *reinterpret_cast<const float4*>(at + per_seq);

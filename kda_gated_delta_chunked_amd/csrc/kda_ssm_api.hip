@@ -161,21 +161,21 @@ kda_status check_ssm(const kda_ssm_problem* p) {
 // device idle; a split pays a second pass over the tokens for the states and a
 // join.  The model is in us on MI355X (256 CUs in 8 XCDs, to which the sequences
 // or pieces go in turn with all their heads; three workgroups on a CU).  A chunk
-// takes 1.8 alone on its CU (2.6 in a workgroup of two waves), and a CU finishes
-// one of four waves every 1.5; a workgroup costs 2.5 chunks besides its own; the
+// takes 1.95 alone on its CU (2.6 in a workgroup of two waves), and a CU finishes
+// one of four waves every 1.4; a workgroup costs 2.5 chunks besides its own; the
 // states' pass takes 0.55 of the full one; the join moves each piece's state
 // twice.  A packed batch of several sequences is taken to be ragged: its longest
 // sequence is twice the mean, half a piece per sequence comes on top, and the
-// last pieces to run leave half of the device idle.  Measured, unsplit / split
-// where the rule splits: B1 T8192 H12 581 / 66, B1 T1024 H12 79 / 32, B8 T8192
-// H12 460 / 241, 32 ragged prompts of 24 heads 420 / 360; and where it does not:
-// B32 T512 H12 65 / 87.
+// last pieces to run leave half of the device idle.  Measured with a gate,
+// unsplit / split where the rule splits: B1 T8192 H12 609 / 65, B1 T1024 H12
+// 83 / 34, B8 T1024 H12 84 / 68, B8 T8192 H12 679 / 288, 32 ragged prompts of 24
+// heads 470 / 360; and where it does not: B32 T512 H12 65 / 87.
 struct SsmModel {
-  double groups, alone, rate = 1.5, state;
+  double groups, alone, rate = 1.4, state;
   explicit SsmModel(const kda_ssm_problem* p) {
     const bool four = p->head_dim == 128 || (p->num_heads / p->num_groups) % 2 == 0;
     groups = p->head_dim == 128 ? p->num_heads : (double)p->num_heads / 2;  // of four waves
-    alone = four ? 1.8 : 2.6;
+    alone = four ? 1.95 : 2.6;
     state = (double)p->num_heads * p->d_state * p->head_dim;
   }
   // spans of `chunks` chunks each
@@ -224,7 +224,7 @@ int32_t ssm_pieces(const kda_ssm_problem* p) {
 // workspace of a split: a state and a decay per piece and head
 size_t ssm_bytes(const kda_ssm_problem* p, int32_t piece) {
   if (!piece) return 0;
-  const size_t slots = (size_t)kda::span_slots(p->num_seqs, p->total_tokens, piece);
+  const size_t slots = (size_t)kda::span_slots(p->packed, p->num_seqs, p->total_tokens, piece);
   return slots * p->num_heads * ((size_t)p->d_state * p->head_dim + 1) * 4;
 }
 
@@ -384,7 +384,7 @@ kda_status kda_ssm_prefill(const kda_ssm_problem* p, const uint16_t* x, const fl
   int32_t piece = ssm_pieces(p);
   if ((workspace ? workspace_bytes : 0) < ssm_bytes(p, piece)) piece = 0;
   a.piece = piece ? (uint32_t)piece : kda::kUnsplit;
-  a.slots = kda::span_slots(p->num_seqs, p->total_tokens, a.piece);
+  a.slots = kda::span_slots(p->packed, p->num_seqs, p->total_tokens, a.piece);
   a.piece_state = piece ? static_cast<float*>(workspace) : nullptr;
   a.piece_decay = piece ? a.piece_state + a.slots * p->num_heads * p->d_state * p->head_dim : nullptr;
   return done(kda::launch_ssm(a, static_cast<hipStream_t>(stream)));

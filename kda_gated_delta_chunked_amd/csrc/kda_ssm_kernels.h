@@ -36,8 +36,9 @@ __device__ __forceinline__ uint4 f32_bf16x8(const float* f) {
 // reciprocal (one unit in the last place off at most) is zero
 __device__ __forceinline__ float silu(float v) { return v * __builtin_amdgcn_rcpf(1.f + __expf(-v)); }
 
-// Token spans.  A packed batch is covered by spans of `len` tokens that start
-// at each sequence's first token.  Sequence n's spans take the slots from
+// Token spans.  A batch is covered by spans of `len` tokens that start at each
+// sequence's first token.  Where all sequences are equally long, their spans
+// follow one another (an empty sequence has one).  Of a packed batch, sequence n's spans take the slots from
 // floor(cu[n] / len) + n on: ceil(L / len) <= floor(cu[n + 1] / len) -
 // floor(cu[n] / len) + 1, so sequences never share a slot, each owns at least
 // one (also when it is empty), and floor(T / len) + N slots hold them all.  A
@@ -58,7 +59,11 @@ struct Span {
   int64_t end;       // one past its last
 };
 
-inline int64_t span_slots(int64_t N, int64_t T_total, int64_t len) { return T_total / len + N; }
+inline int64_t span_slots(bool packed, int64_t N, int64_t T_total, int64_t len) {
+  if (packed) return T_total / len + N;
+  const int64_t T = T_total / N;
+  return N * (T ? (T + len - 1) / len : 1);
+}
 
 __device__ __forceinline__ int64_t cu_at(const Packing& p, int i) {
   int64_t v;
@@ -70,17 +75,21 @@ __device__ __forceinline__ int64_t cu_at(const Packing& p, int i) {
   return v < 0 ? 0 : (v > p.T_total ? p.T_total : v);
 }
 
+// slots of a sequence where all are equally long (len is at most 2^31)
+__device__ __forceinline__ uint32_t fixed_slots(const Packing& p, uint32_t len) {
+  return p.T_fixed ? ((uint32_t)p.T_fixed + (len - 1)) / len : 1;
+}
+// the first slot of a sequence that begins at token `begin`
+__device__ __forceinline__ int64_t first_slot(const Packing& p, uint32_t len, int seq, int64_t begin) {
+  return p.cu ? (int64_t)((uint32_t)begin / len) + seq : (int64_t)seq * fixed_slots(p, len);
+}
+
 // the span of a slot (the same for all lanes of a wave): 64 probes a step
 __device__ __forceinline__ Span span_of(const Packing& p, uint32_t len, int64_t slot) {
   const int lane = threadIdx.x & 63;
   int lo = 0, hi = p.N;
   if (!p.cu) {
-    // sequence n's first slot: n T / len rounded down, plus n
-    while (hi - lo > 1) {
-      const int mid = lo + (hi - lo) / 2;
-      if ((int64_t)((uint32_t)(mid * p.T_fixed) / len) + mid <= slot) lo = mid;
-      else hi = mid;
-    }
+    lo = (int)((uint32_t)slot / fixed_slots(p, len));
   } else {
     while (hi - lo > 1) {
       const int step = (hi - lo + 63) / 64;
@@ -99,7 +108,7 @@ __device__ __forceinline__ Span span_of(const Packing& p, uint32_t len, int64_t 
   s.begin = cu_at(p, lo);
   s.end = cu_at(p, lo + 1);
   if (s.end < s.begin) s.end = s.begin;
-  const int64_t k = slot - ((int64_t)((uint32_t)s.begin / len) + lo);
+  const int64_t k = slot - first_slot(p, len, lo, s.begin);
   s.k = k < 0 || (k > 0 && k * len >= s.end - s.begin) ? -1 : (int)k;
   return s;
 }
