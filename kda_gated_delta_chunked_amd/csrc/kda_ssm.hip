@@ -238,19 +238,21 @@ __device__ __forceinline__ double lane_of(double v, int lane) {
   return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
-// Whether any lane's fragments hold an infinity or a NaN.
+// Whether any lane's fragments hold an infinity or a NaN, or a value of 2^121 or
+// more: read as halves, all of these are NaNs, which a maximum keeps.
 __device__ __forceinline__ bool any_not_finite(const bf16x8 (&f)[2]) {
-  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-  u16x2 top = {0, 0};  // the largest magnitudes, as 16-bit numbers
+  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+  f16x2 v[8];
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     const uint4 u = __builtin_bit_cast(uint4, f[s]);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, w[j] & 0x7fff7fffu));
+    for (int j = 0; j < 4; ++j) v[4 * s + j] = __builtin_bit_cast(f16x2, w[j]);
   }
-  return __any(top[0] >= 0x7f80 || top[1] >= 0x7f80);
+  auto most = [](f16x2 a, f16x2 b) { return __builtin_elementwise_maximum(a, b); };
+  const f16x2 t = most(most(most(most(v[0], v[1]), most(v[2], v[3])), most(v[4], v[5])), most(v[6], v[7]));
+  return __any(t[0] != t[0] || t[1] != t[1]);
 }
 
 // The fragment with zeros in the place of infinities and NaNs.

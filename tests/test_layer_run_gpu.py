@@ -516,3 +516,55 @@ def test_single_tokens_are_rounded_once(dims, H, skip, z):
     out, _ = K().ssm_prefill(*a, **kw, cu_seqlens=offsets(lens).cuda())
     err = (out.cpu().to(R.F64) - ref).abs()
     assert (err <= R.BF16 * ref.abs() + 2e-5 * mag).all(), (err - R.BF16 * ref.abs() - 2e-5 * mag).max()
+
+
+@pytest.mark.parametrize("dims", [(128, 128), (64, 64)], ids=str)
+@pytest.mark.parametrize("piece", [0, 64])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), NAN, 3e38])
+def test_special_inputs_reach_their_column_and_later_tokens_alone(dims, piece, value):
+    # x feeds one column of one head's state: everything else, and that column
+    # ahead of the token, is as if it were not there (a huge value is finite but
+    # overflows what follows it)
+    P, N = dims
+    T, H = 200, 2
+    g = torch.Generator().manual_seed(92)
+    c = scan_case(g, T, H, 1, P, N, z=False, softplus=False, skip=True, slow=True)
+    s0 = rand(g, 1, H, N, P, dtype=torch.float32)
+    ref, final, mag, smag = scan_ref(c, s0, [T])
+    hit = [(70, 0, 5), (17, 1, P - 1), (95, 1, 33)]
+    for t, h, p in hit:
+        c["x"][t, h, p] = value
+    a, kw = scan_args(on_gpu(c))
+    out, fin = K().ssm_prefill(*a, **kw, cu_seqlens=offsets([T]).cuda(), initial_state=s0.cuda(), piece_tokens=piece)
+    out, fin = out.cpu(), fin.cpu()
+    clean, kept = torch.ones(T, H, P, dtype=torch.bool), torch.ones(H, N, P, dtype=torch.bool)
+    for t, h, p in hit:
+        clean[t:, h, p] = False
+        kept[h, :, p] = False
+        if value != 3e38:
+            assert not torch.isfinite(out[t:, h, p].float()).any() and not torch.isfinite(fin[0, h, :, p]).any()
+    R.assert_scan_out(out[clean], ref[clean], mag[clean])
+    R.assert_state(fin[0][kept], final[0][kept], smag[0][kept])
+
+
+@pytest.mark.parametrize("dims", [(128, 128), (64, 128)], ids=str)
+@pytest.mark.parametrize("piece", [0, 64])
+def test_a_bad_step_stays_in_its_head_and_a_bad_read_in_its_token(dims, piece):
+    P, N = dims
+    T, H = 150, 4
+    g = torch.Generator().manual_seed(93)
+    c = scan_case(g, T, H, 2, P, N, z=True, softplus=True, skip=True)
+    s0 = rand(g, 1, H, N, P, dtype=torch.float32)
+    ref, final, mag, smag = scan_ref(c, s0, [T])
+    c["dt"][70, 0] = NAN
+    c["C"][33, 1, 3] = NAN
+    c["z"][100, 1, 7] = NAN
+    a, kw = scan_args(on_gpu(c))
+    out, fin = K().ssm_prefill(*a, **kw, cu_seqlens=offsets([T]).cuda(), initial_state=s0.cuda(), piece_tokens=piece)
+    out, fin = out.cpu(), fin.cpu()
+    bad = torch.zeros(T, H, P, dtype=torch.bool)
+    bad[70:, 0] = bad[33, 2:] = True
+    bad[100, 1, 7] = True
+    assert torch.isnan(out[bad].float()).all() and torch.isnan(fin[0, 0]).all()
+    R.assert_scan_out(out[~bad], ref[~bad], mag[~bad])
+    R.assert_state(fin[0, 1:], final[0, 1:], smag[0, 1:])
