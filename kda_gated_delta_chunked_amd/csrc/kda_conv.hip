@@ -6,7 +6,8 @@
 // A thread owns eight channels (16 bytes of a row) and walks a run of tokens
 // with the last W - 1 rows in registers, so each row is read once plus W - 1
 // rows ahead of every run.  Both kernels are bound by memory: 4 bytes per
-// token and channel against 2 W flops.
+// token and channel against 2 W flops.  The step reads and writes the state's
+// rows besides: 1024 requests of 4608 channels, one token, take 14 us.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -167,10 +168,10 @@ __global__ __launch_bounds__(256) void kda_conv_step_kernel(ConvStepArgs a, int6
 hipError_t launch_conv(const ConvArgs& a, hipStream_t stream) {
   // Spans of 16 tokens, of 8 where that leaves few waves: the W - 1 rows ahead
   // of each span are read twice, mostly from a cache, and short spans keep more
-  // rows in flight.  us on MI355X at spans of 8 / 16 / 32 / 64 tokens: B8 T8192
-  // D4608 245 / 227 / 234 / 250 (5.3 TB/s of its bytes at 16), six ragged
-  // prompts D1792 15.7 / 16.3 / 19.4 / 22.2, T2048 D4608 11.3 / 12.4 / 13.6 /
-  // 21.4, T300 D1536 5.4 / 7.3 / 11.0 / 18.6.
+  // rows in flight.  us on one MI355X at spans of 8 / 16 / 32 / 64 tokens: B8
+  // T8192 D4608 261 / 242 / 237 / 253 (at 16 from 216 to 242 on different cards:
+  // 5.6 to 5.0 TB/s of its bytes), six ragged prompts D1792 16.0 / 16.9 / 20.1 /
+  // 22.3, T2048 D4608 10.8 / 12.0 / 12.9 / 20.6, T300 D1536 4.6 / 6.5 / 10.2 / 17.8.
   const int blocks = (a.D + 511) / 512;
   const int shift = (a.pk.T_total >> 4) * blocks < 6144 ? 3 : 4;
   const int64_t waves = span_slots(a.pk.cu, a.pk.N, a.pk.T_total, 1 << shift) * blocks;

@@ -9,7 +9,6 @@ the library, and there is no fallback.
 from __future__ import annotations
 
 import ctypes
-from typing import Optional
 
 from .ops import STATE_DTYPES, _check, _ptr, load_library
 
@@ -154,6 +153,13 @@ def _gpu(t):
     return dev
 
 
+def _like(x, dtype=None):
+    """A packed tensor of x's shape (about 1 us cheaper than one from a shape)."""
+    import torch
+
+    return torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
+
+
 def _launch(name: str, dev, stream, problem, args, mine=()):
     """Enqueue on `stream` (None: the current one).  Buffers the binding took
     from torch's allocator (`mine`) belong to the current stream; on another
@@ -235,10 +241,10 @@ def conv_prefill(x, weight, bias=None, *, cu_seqlens=None, initial_state=None, f
     cu64 = _offsets(cu_seqlens, dev)
     mine = []
     if out is None:
-        out = torch.empty(x.shape, dtype=bf, device=dev)
+        out = _like(x)
         mine.append(out)
     if final_state is None and output_final_state:
-        final_state = torch.empty(state, dtype=bf, device=dev)
+        final_state = x.new_empty(state)
         mine.append(final_state)
     p = ConvProblem(N, T, D, W, _activation(activation), cu64, _row_stride("x", x, lead),
                     _row_stride("out", out, lead))
@@ -272,7 +278,7 @@ def conv_decode(x, weight, bias, state_pool, state_indices, *, activation: str =
     _check_tensor("out", out, bf, shape, dev, False)
     mine = []
     if out is None:
-        out = torch.empty(shape, dtype=bf, device=dev)
+        out = _like(x)
         mine.append(out)
     p = ConvDecodeProblem(N, T, D, W, _activation(activation), size,
                           _row_stride("x", x, 2), _row_stride("out", out, 2))
@@ -342,10 +348,10 @@ def ssm_prefill(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, dt_softplus: bo
     cu64 = _offsets(cu_seqlens, dev)
     mine = []
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+        out = _like(x)
         mine.append(out)
     if final_state is None and output_final_state:
-        final_state = torch.empty(shape, dtype=state_dtype, device=dev)
+        final_state = x.new_empty(shape, dtype=state_dtype)
         mine.append(final_state)
     p = SsmProblem(N, T, H, G, P, S, int(dt_softplus), kind, cu64, int(piece_tokens),
                    int(cu_seqlens is not None), _row_stride("x", x, lead),
@@ -354,7 +360,7 @@ def ssm_prefill(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, dt_softplus: bo
     if workspace is None:
         need = ssm_workspace_size(p)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = x.new_empty((need,), dtype=torch.uint8)
             mine.append(workspace)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on {dev}")
@@ -389,7 +395,7 @@ def ssm_decode(x, dt, A, B, C, state_pool, state_indices, *, D=None, z=None, dt_
     _check_tensor("state_indices", state_indices, torch.int32, (N,), dev)
     mine = []
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+        out = _like(x)
         mine.append(out)
     p = SsmDecodeProblem(N, T, H, G, P, S, int(dt_softplus), kind, size,
                          _row_stride("x", x, 2), _row_stride("B", B, 2), _row_stride("C", C, 2),
@@ -431,13 +437,13 @@ def add_rmsnorm(x, weight, *, residual=None, eps: float = 1e-6, out_dtype=None, 
     if residual is None or residual_out is False:
         residual_out = None
     elif residual_out is None:
-        residual_out = torch.empty(shape, dtype=bf, device=dev)
+        residual_out = _like(x)
         mine.append(residual_out)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=dev)
+        out = _like(x, out_dtype)
         mine.append(out)
     if fp8 and scales is None:
-        scales = torch.empty(groups, dtype=torch.float32, device=dev)
+        scales = x.new_empty(groups, dtype=torch.float32)
         mine.append(scales)
     _check_tensor("x", x, bf, shape, dev, False)
     _check_tensor("residual", residual, bf, shape, dev)
