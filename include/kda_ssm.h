@@ -14,6 +14,8 @@
  * compared, never dereferenced); base pointers are 16-byte aligned; buffers a
  * call writes overlap no other buffer except where an exact alias is named.
  * A buffer with a row stride counts as its whole span, first element to last.
+ * KDA_ERR_TOO_LARGE: 2^31 tokens or rows or more, or so much work that a launch
+ * would have 2^32 threads (2^32 / 16 rows of the norm, say).
  *
  * Sequences.  A batch is N sequences of T_total tokens in all: fixed
  * (cu_seqlens NULL, T_total / N tokens each) or packed, with cu_seqlens int32

@@ -166,15 +166,8 @@ __global__ __launch_bounds__(256) void kda_conv_step_kernel(ConvStepArgs a, int6
 }  // namespace
 
 hipError_t launch_conv(const ConvArgs& a, hipStream_t stream) {
-  // Spans of 16 tokens, of 8 where that leaves few waves: the W - 1 rows ahead
-  // of each span are read twice, mostly from a cache, and short spans keep more
-  // rows in flight.  us on one MI355X at spans of 8 / 16 / 32 / 64 tokens: B8
-  // T8192 D4608 261 / 242 / 237 / 253 (at 16 from 216 to 242 on different cards:
-  // 5.6 to 5.0 TB/s of its bytes), six ragged prompts D1792 16.0 / 16.9 / 20.1 /
-  // 22.3, T2048 D4608 10.8 / 12.0 / 12.9 / 20.6, T300 D1536 4.6 / 6.5 / 10.2 / 17.8.
-  const int blocks = (a.D + 511) / 512;
-  const int shift = (a.pk.T_total >> 4) * blocks < 6144 ? 3 : 4;
-  const int64_t waves = span_slots(a.pk.cu, a.pk.N, a.pk.T_total, 1 << shift) * blocks;
+  const int blocks = (int)conv_blocks(a.D), shift = conv_shift(a.pk.T_total, a.D);
+  const int64_t waves = conv_waves(a.pk.cu, a.pk.N, a.pk.T_total, a.D);
   const dim3 grid((unsigned)((waves + 3) / 4)), block(256);
   switch (a.W) {
     case 2: hipLaunchKernelGGL(kda_conv_kernel<2>, grid, block, 0, stream, a, shift, waves, blocks); break;
@@ -186,7 +179,7 @@ hipError_t launch_conv(const ConvArgs& a, hipStream_t stream) {
 
 hipError_t launch_conv_step(const ConvStepArgs& a, hipStream_t stream) {
   if (a.N == 0) return hipSuccess;
-  const int blocks = (a.D + 511) / 512;
+  const int blocks = (int)conv_blocks(a.D);
   const int64_t waves = (int64_t)a.N * blocks;
   const dim3 grid((unsigned)((waves + 3) / 4)), block(256);
   switch (a.W) {

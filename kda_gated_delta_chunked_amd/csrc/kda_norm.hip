@@ -138,18 +138,19 @@ void launch(const NormArgs& a, hipStream_t stream) {
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
   if (a.rows == 0) return hipSuccess;
-  // The fewest lanes that hold a row with one piece each, then more pieces on a
-  // wave, then a workgroup; few rows take a workgroup from 512 columns on, whose
+  // (norm_lanes.)  The fewest lanes that hold a row with one piece each, then more
+  // pieces on a wave, then a workgroup; few rows take a workgroup from 512 columns on, whose
   // lanes each have less to do one after the other.  us on MI355X: 98304 x 128
   // 10.0 (5.05 TB/s; 49 with a workgroup per row), 65536 x 1536 to e4m3 131
   // (5.4 TB/s), 65536 x 4096 to e4m3 318 (5.9 TB/s), 1 x 1536 2.3 with a
   // workgroup and 3.7 with a wave.
-  if (a.D <= 128) launch<16, 1>(a, stream);
-  else if (a.D <= 256) launch<32, 1>(a, stream);
-  else if (a.D <= 512) launch<64, 1>(a, stream);
-  else if (a.D <= 2048 && a.rows < 1024) launch<256, 1>(a, stream);
-  else if (a.D <= 1024) launch<64, 2>(a, stream);
-  else if (a.D <= 2048) launch<64, 4>(a, stream);
+  const int lanes = norm_lanes(a.rows, a.D);
+  if (lanes == 16) launch<16, 1>(a, stream);
+  else if (lanes == 32) launch<32, 1>(a, stream);
+  else if (lanes == 64 && a.D <= 512) launch<64, 1>(a, stream);
+  else if (lanes == 64 && a.D <= 1024) launch<64, 2>(a, stream);
+  else if (lanes == 64) launch<64, 4>(a, stream);
+  else if (a.D <= 2048) launch<256, 1>(a, stream);
   else if (a.D <= 4096) launch<256, 2>(a, stream);
   else if (a.D <= 8192) launch<256, 4>(a, stream);
   else launch<256, 8>(a, stream);

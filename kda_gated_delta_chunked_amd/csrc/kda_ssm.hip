@@ -717,7 +717,7 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
         decay[0] = __builtin_amdgcn_exp2f((float)(log_decay[0] + log_decay[1]));
       }
     }
-  } else if (PARTS == 3) {  // the last piece, and a final state is wanted
+  } else if (PARTS == 3 && a.final_state) {
     if (a.state_bf16) {
       uint16_t* out = static_cast<uint16_t*>(a.final_state) + seq * per_seq + state0;
 #pragma unroll
@@ -734,8 +734,8 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
   }
 }
 
-// Where no final state comes from a launch, the state is read for the outputs
-// alone, rounded to bf16: two parts of x w are enough.
+// Ahead of a sequence's last piece, the state is read for the outputs alone,
+// rounded to bf16: two parts of x w are enough.
 template <int N, int P, int HPW, bool FULL, bool GATE>
 __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kernel(SsmArgs a) {
   constexpr int XC = HPW * P, TB = L * N * 2, TX = L * XC * 2, TC = FULL ? TB : 16, TM = FULL ? HPW * 3 * M_BLOCK : 16;
@@ -755,7 +755,7 @@ __global__ __launch_bounds__(HPW* P * 2, HPW* P == 64 ? 2 : 3) void kda_ssm_kern
   const int head0 = (int)((blk >> 3) % HG) * HPW;
   if constexpr (FULL) {
     const bool last = uniform(sp.end - sp.begin - (int64_t)sp.k * a.piece) <= (int64_t)a.piece;
-    if (!last || !a.final_state) {
+    if (!last) {
       run_piece<N, P, HPW, FULL, GATE, 2>(a, sp, slot, head0, b0, b1, x0, x1, tC, tM, tZ, gates);
       return;
     }
@@ -803,11 +803,10 @@ __global__ __launch_bounds__(256) void kda_ssm_join_kernel(SsmArgs a, int blocks
 
 template <int N, int P, int HPW>
 void launch(const SsmArgs& a, hipStream_t stream) {
-  const int64_t blocks = (a.slots + 7) / 8 * 8 * (a.t.H / HPW);
-  const dim3 grid((unsigned)blocks), block(HPW * P * 2);
+  const dim3 block(HPW * P * 2), grid((unsigned)(ssm_threads(a.slots, a.t.H, P) / block.x));
   if (a.piece_state) {
     const int blocks_per_head = N * P / 1024;
-    const int64_t join = (int64_t)a.pk.N * a.t.H * blocks_per_head;
+    const int64_t join = ssm_join_threads(a.pk.N, a.t.H, N * P) / 256;
     hipLaunchKernelGGL((kda_ssm_kernel<N, P, HPW, false, false>), grid, block, 0, stream, a);
     hipLaunchKernelGGL(kda_ssm_join_kernel, dim3((unsigned)join), dim3(256), 0, stream, a, blocks_per_head);
   }

@@ -142,6 +142,13 @@ struct TokenRanges {
   }
 };
 
+// whether the launches of a scan in pieces have few enough threads
+bool split_fits(const kda_ssm_problem* p, int64_t piece) {
+  const int64_t slots = kda::span_slots(p->packed, p->num_seqs, p->total_tokens, piece);
+  return kda::ssm_threads(slots, p->num_heads, p->head_dim) <= kda::kMaxThreads &&
+         kda::ssm_join_threads(p->num_seqs, p->num_heads, (int64_t)p->d_state * p->head_dim) <= kda::kMaxThreads;
+}
+
 kda_status check_ssm(const kda_ssm_problem* p) {
   if (!p) return KDA_ERR_INVALID_ARG;
   kda_status st = check_heads(p->num_heads, p->num_groups, p->head_dim, p->d_state, p->dt_softplus, p->state_dtype);
@@ -151,9 +158,9 @@ kda_status check_ssm(const kda_ssm_problem* p) {
   if (!flag(p->packed)) return KDA_ERR_INVALID_ARG;
   const int32_t piece = p->piece_tokens;
   if (piece < 0 || piece % 64 || !strides_ok(p)) return KDA_ERR_INVALID_ARG;
-  // workgroups: at most one per 64 tokens (plus one per sequence) and head
-  if ((p->total_tokens / 64 + p->num_seqs + 8) * p->num_heads > kInt32Max) return KDA_ERR_TOO_LARGE;
-  return KDA_OK;
+  const int64_t H = p->num_heads, unsplit = kda::span_slots(p->packed, p->num_seqs, p->total_tokens, kda::kUnsplit);
+  if (kda::ssm_threads(unsplit, H, p->head_dim) > kda::kMaxThreads) return KDA_ERR_TOO_LARGE;
+  return piece && !split_fits(p, piece) ? KDA_ERR_TOO_LARGE : KDA_OK;
 }
 
 // The piece length of a scan, 0: no split.  A workgroup runs its chunks of 32
@@ -218,7 +225,7 @@ int32_t ssm_pieces(const kda_ssm_problem* p) {
       if (len < mean) consider(len, spans, model.equal(spans, len / 32));
     }
   }
-  return piece;
+  return piece && split_fits(p, piece) ? piece : 0;
 }
 
 // workspace of a split: a state and a decay per piece and head
@@ -243,8 +250,7 @@ kda_status kda_conv_validate(const kda_conv_problem* p, const void* x, const voi
   const int64_t T = p->total_tokens, N = p->num_seqs, D = p->dim;
   if (!cu_seqlens && T % N) return KDA_ERR_INVALID_ARG;
   if (!weight || (T > 0 && (!x || !out))) return KDA_ERR_INVALID_ARG;
-  // one wave per 8 tokens at most and 512 channels
-  if ((T / 8 + N) * ((D + 511) / 512) > kInt32Max) return KDA_ERR_TOO_LARGE;
+  if (kda::conv_waves(cu_seqlens, N, T, D) * 64 > kda::kMaxThreads - 255) return KDA_ERR_TOO_LARGE;
   if (!all_aligned({x, weight, bias, cu_seqlens, initial_state, out, final_state})) return KDA_ERR_ALIGNMENT;
   const uint64_t state = (uint64_t)N * (p->width - 1) * D * 2;
   const Range rx = rows_of(x, T, p->x_stride, D), rw = range_of(weight, (uint64_t)D * p->width * 2);
@@ -289,7 +295,7 @@ kda_status kda_conv_decode_validate(const kda_conv_decode_problem* p, const void
   if (st != KDA_OK) return st;
   const int64_t N = p->num_seqs, rows = N * p->tokens_per_seq, D = p->dim;
   if (N > 0 && (!x || !weight || !state_pool || !state_indices || !out)) return KDA_ERR_INVALID_ARG;
-  if (N * ((D + 511) / 512) > kInt32Max) return KDA_ERR_TOO_LARGE;
+  if (N * kda::conv_blocks(D) * 64 > kda::kMaxThreads - 255) return KDA_ERR_TOO_LARGE;
   if (!all_aligned({x, weight, bias, state_pool, state_indices, out})) return KDA_ERR_ALIGNMENT;
   const Range rx = rows_of(x, rows, p->x_stride, D), rw = range_of(weight, (uint64_t)D * p->width * 2);
   const Range rb = range_of(bias, (uint64_t)D * 2), ridx = range_of(state_indices, (uint64_t)N * 4);
@@ -401,7 +407,8 @@ kda_status kda_ssm_decode_validate(const kda_ssm_decode_problem* p, const void* 
   if (st != KDA_OK) return st;
   if (!strides_ok(p)) return KDA_ERR_INVALID_ARG;
   const int64_t N = p->num_seqs, H = p->num_heads, rows = N * p->tokens_per_seq;
-  if (N * H > kInt32Max / 8) return KDA_ERR_TOO_LARGE;
+  if (kda::ssm_step_threads(N, H, p->head_dim, p->state_dtype == KDA_STATE_BF16) > kda::kMaxThreads)
+    return KDA_ERR_TOO_LARGE;
   if (N > 0 && (!x || !dt || !A || !B || !C || !state_pool || !state_indices || !out)) return KDA_ERR_INVALID_ARG;
   if (!all_aligned({x, dt, A, B, C, D, z, dt_bias, state_pool, state_indices, out})) return KDA_ERR_ALIGNMENT;
   const TokenRanges r(p, rows, x, dt, A, B, C, D, z, dt_bias, out);
@@ -447,7 +454,7 @@ kda_status kda_add_rmsnorm_validate(const kda_norm_problem* p, const void* x, co
   if (p->scale_group != 0 && !(e4m3 && p->scale_group == 128)) return KDA_ERR_UNSUPPORTED;
   const int64_t R = p->rows, D = p->dim;
   if (!stride_ok(p->x_stride, D)) return KDA_ERR_INVALID_ARG;
-  if (R > kInt32Max) return KDA_ERR_TOO_LARGE;
+  if (R > kInt32Max || R * kda::norm_lanes(R, p->dim) > kda::kMaxThreads - 255) return KDA_ERR_TOO_LARGE;
   if (R > 0 && (!x || !weight || !out)) return KDA_ERR_INVALID_ARG;
   if (R > 0 && e4m3 != (scales != nullptr)) return KDA_ERR_INVALID_ARG;
   if (residual_out && !residual) return KDA_ERR_INVALID_ARG;

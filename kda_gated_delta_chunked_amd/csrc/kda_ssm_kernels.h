@@ -65,6 +65,30 @@ inline int64_t span_slots(bool packed, int64_t N, int64_t T_total, int64_t len) 
   return N * (T ? (T + len - 1) / len : 1);
 }
 
+// Sizes of launches, for the launch and its check: a launch has fewer than 2^32
+// threads.
+constexpr int64_t kMaxThreads = 0xffffffffLL;
+inline int64_t conv_blocks(int64_t D) { return (D + 511) / 512; }  // waves per row
+// Spans of 16 tokens, of 8 where that leaves few waves: the W - 1 rows ahead
+// of each span are read twice, mostly from a cache, and short spans keep more
+// rows in flight.  us on one MI355X at spans of 8 / 16 / 32 / 64 tokens: B8
+// T8192 D4608 261 / 242 / 237 / 253 (at 16 from 216 to 242 on different cards:
+// 5.6 to 5.0 TB/s of its bytes), six ragged prompts D1792 16.0 / 16.9 / 20.1 /
+// 22.3, T2048 D4608 10.8 / 12.0 / 12.9 / 20.6, T300 D1536 4.6 / 6.5 / 10.2 / 17.8.
+inline int conv_shift(int64_t T_total, int64_t D) { return (T_total >> 4) * conv_blocks(D) < 6144 ? 3 : 4; }
+inline int64_t conv_waves(bool packed, int64_t N, int64_t T_total, int64_t D) {
+  return span_slots(packed, N, T_total, (int64_t)1 << conv_shift(T_total, D)) * conv_blocks(D);
+}
+inline int64_t ssm_threads(int64_t slots, int64_t H, int64_t P) { return (slots + 7) / 8 * 8 * H * P * 2; }
+inline int64_t ssm_join_threads(int64_t N, int64_t H, int64_t state) { return N * H * (state / 4); }
+constexpr int kSsmStepColumnsF32 = 32, kSsmStepColumnsBf16 = 64;  // of a workgroup of 256 threads
+inline int64_t ssm_step_threads(int64_t N, int64_t H, int64_t P, bool bf16) {
+  return (N * H + 7) / 8 * 8 * (P / (bf16 ? kSsmStepColumnsBf16 : kSsmStepColumnsF32)) * 256;
+}
+inline int norm_lanes(int64_t rows, int D) {
+  return D <= 128 ? 16 : D <= 256 ? 32 : D <= 512 || (D <= 2048 && rows >= 1024) ? 64 : 256;
+}
+
 __device__ __forceinline__ int64_t cu_at(const Packing& p, int i) {
   int64_t v;
   if (!p.cu) return (int64_t)i * p.T_fixed;

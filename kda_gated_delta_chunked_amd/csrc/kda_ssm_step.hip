@@ -42,7 +42,7 @@ __device__ __forceinline__ void store_state(void* base, int64_t e, const float* 
 
 template <int N, int P, bool BF>
 __global__ __launch_bounds__(256) void kda_ssm_step_kernel(SsmStepArgs a) {
-  constexpr int CPT = BF ? 8 : 4, WC = 8 * CPT, PARTS = P / WC, ROWS = N / 32, GROUP = 4;
+  constexpr int WC = BF ? kSsmStepColumnsBf16 : kSsmStepColumnsF32, CPT = WC / 8, PARTS = P / WC, ROWS = N / 32, GROUP = 4;
   static_assert(N + WC < 256, "one thread per staged value");
   __shared__ float sB[GROUP][N], sC[GROUP][N], sx[GROUP][WC], sz[GROUP][WC], sstep[GROUP];
   __shared__ float red[GROUP][4][WC];
@@ -149,8 +149,7 @@ __global__ __launch_bounds__(256) void kda_ssm_step_kernel(SsmStepArgs a) {
 
 template <int N, int P, bool BF>
 void launch(const SsmStepArgs& a, hipStream_t stream) {
-  constexpr int parts = P / (BF ? 64 : 32);
-  const int64_t blocks = ((int64_t)a.seqs * a.t.H + 7) / 8 * 8 * parts;
+  const int64_t blocks = ssm_step_threads(a.seqs, a.t.H, P, BF) / 256;
   hipLaunchKernelGGL((kda_ssm_step_kernel<N, P, BF>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
 }
 template <int N, int P>

@@ -214,3 +214,37 @@ def test_binding_refuses_before_the_library():
         K.add_rmsnorm(x, w[:, 0])
     with pytest.raises(ValueError, match="x must be"):
         K.ssm_prefill(x, None, None, None, None)
+
+
+@pytest.mark.parametrize("call", [
+    # a launch has fewer than 2^32 threads: 64 per 8 or 16 tokens and 512
+    # channels, 64 per request and 512 channels
+    lambda far: conv(T=(1 << 30) + (1 << 29), N=1, D=8, x=at(0), out=at(0) + far),
+    lambda far: conv(T=0, N=(1 << 26) + 1, D=8, x=0, out=0, cu=at(0), s0=0, fin=0),
+    lambda far: conv_step(n=1 << 26, T=1, D=8, pool=4, x=at(0), out=at(0) + far),
+    # two per sequence, head and column of an unsplit scan, or per piece of one
+    lambda far: ssm(N=1 << 25, T=1 << 25, H=1, G=1, P=64, S_=64, s0=0, fin=0, x=at(0), out=at(0) + far),
+    # one per four state elements of all sequences in a split's join
+    lambda far: ssm(ws_bytes=1 << 47, N=100000, T=10000000, H=11, G=1, P=128, S_=128, piece=64, s0=0, fin=0, x=at(0),
+                    out=at(0) + far, ws=at(0) + 2 * far),
+    # 256 per request, head and 32 or 64 columns
+    lambda far: ssm_step(n=1 << 22, T=1, H=1, G=1, P=128, x=at(0), out=at(0) + far),
+    # 16 to 256 per row
+    lambda far: norm(rows=1 << 28, D=8, x=at(0), out=at(0) + far, res=0, ro=0),
+    lambda far: norm(rows=1 << 24, D=2056, x=at(0), out=at(0) + far, res=0, ro=0),
+])
+def test_more_threads_than_a_launch_takes_are_refused(call):
+    assert call(1 << 50) == TOO_LARGE
+
+
+@pytest.mark.parametrize("call", [
+    # 2^26 - 7 waves of 64, in workgroups of four
+    lambda far: conv(T=(1 << 30) - 128, N=1, D=8, x=at(0), out=at(0) + far),
+    lambda far: ssm(N=1 << 24, T=1 << 24, H=1, G=1, P=64, S_=64, s0=0, fin=0, x=at(0), out=at(0) + far),
+    lambda far: norm(rows=(1 << 28) - 16, D=8, x=at(0), out=at(0) + far, res=0, ro=0),
+    # an automatic piece length whose join would be too large: unsplit
+    lambda far: ssm(ws_bytes=0, N=100000, T=100000000, H=11, G=1, P=128, S_=128, s0=0, fin=0, x=at(0),
+                    out=at(0) + far, ws=0),
+])
+def test_the_largest_launches_are_accepted(call):
+    assert call(1 << 50) == OK

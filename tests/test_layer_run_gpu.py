@@ -568,3 +568,16 @@ def test_a_bad_step_stays_in_its_head_and_a_bad_read_in_its_token(dims, piece):
     assert torch.isnan(out[bad].float()).all() and torch.isnan(fin[0, 0]).all()
     R.assert_scan_out(out[~bad], ref[~bad], mag[~bad])
     R.assert_state(fin[0, 1:], final[0, 1:], smag[0, 1:])
+
+
+@pytest.mark.parametrize("piece", [0, 64])
+def test_outputs_do_not_depend_on_the_final_state(piece):
+    lens, H, P, N = [1, 130, 0, 64, 40], 2, 64, 128
+    g = torch.Generator().manual_seed(94)
+    a, kw = scan_args(on_gpu(scan_case(g, sum(lens), H, 1, P, N, z=False, softplus=True, skip=False)))
+    kw |= dict(cu_seqlens=offsets(lens).cuda(), piece_tokens=piece)
+    out, fin = K().ssm_prefill(*a, **kw)
+    bare, none = K().ssm_prefill(*a, **kw, output_final_state=False)
+    assert none is None and torch.equal(out, bare)
+    half, fin16 = K().ssm_prefill(*a, **kw, state_dtype=BF)
+    assert torch.equal(out, half) and torch.equal(fin.to(BF), fin16)
