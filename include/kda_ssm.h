@@ -142,6 +142,10 @@ typedef struct {
   int64_t out_stride;
 } kda_ssm_problem;
 
+/* With piece_tokens 0, sequences of up to this many tokens in the mean are not
+ * split: no workspace. */
+#define KDA_SSM_SPLIT_TOKENS 128
+
 /* The piece length (0: no split) kda_ssm_prefill takes for this problem, given
  * the workspace of kda_ssm_prefill_workspace_size bytes (host only).  With
  * piece_tokens 0 a smaller workspace, or none, runs the scan unsplit; with

@@ -203,6 +203,7 @@ int32_t ssm_pieces(const kda_ssm_problem* p) {
   if (p->piece_tokens) return p->piece_tokens < p->total_tokens ? p->piece_tokens : 0;
   const SsmModel model(p);
   const double N = p->num_seqs, T = (double)p->total_tokens, mean = T / N;
+  if (T <= KDA_SSM_SPLIT_TOKENS * N) return 0;
   const bool ragged = p->packed && p->num_seqs > 1;
   double best = model.equal(N, (ragged ? std::min(T, 2 * mean) : mean) / 32);
   int32_t piece = 0;

@@ -15,6 +15,7 @@ from .ops import STATE_DTYPES, _check, _ptr, load_library
 _i32, _i64, _f32, _P = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
 
 ACTIVATIONS = {"none": 0, "silu": 1}
+SPLIT_TOKENS = 128  # KDA_SSM_SPLIT_TOKENS
 
 
 class ConvProblem(ctypes.Structure):
@@ -147,10 +148,9 @@ def _check_tensor(name: str, t, dtype, shape, dev, contiguous: bool = True):
 
 
 def _gpu(t):
-    dev = t.device
-    if dev.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("libkda runs on the GPU: tensors must be on a cuda (HIP) device")
-    return dev
+    return t.device
 
 
 def _like(x, dtype=None):
@@ -203,13 +203,14 @@ def _offsets(cu_seqlens, dev):
 def _batch(x, inner: int, cu_seqlens, what: str):
     """(leading dimensions, sequences, tokens) of a packed [T, ...] or fixed
     [B, T, ...] input with `inner` dimensions per token."""
-    if x.dim() == inner + 2:
+    shape = x.shape
+    if len(shape) == inner + 2:
         if cu_seqlens is not None:
             raise ValueError("cu_seqlens is for packed inputs")
-        return 2, x.shape[0], x.shape[0] * x.shape[1]
-    if x.dim() != inner + 1:
+        return 2, shape[0], shape[0] * shape[1]
+    if len(shape) != inner + 1:
         raise ValueError(f"x must be {what}")
-    return 1, 1 if cu_seqlens is None else cu_seqlens.numel() - 1, x.shape[0]
+    return 1, 1 if cu_seqlens is None else cu_seqlens.numel() - 1, shape[0]
 
 
 def conv_prefill(x, weight, bias=None, *, cu_seqlens=None, initial_state=None, final_state=None,
@@ -358,7 +359,8 @@ def ssm_prefill(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, dt_softplus: bo
                    _row_stride("B", B, lead), _row_stride("C", C, lead),
                    0 if z is None else _row_stride("z", z, lead), _row_stride("out", out, lead))
     if workspace is None:
-        need = ssm_workspace_size(p)
+        # (short sequences are never split unless asked for: not worth a call)
+        need = ssm_workspace_size(p) if piece_tokens or T > SPLIT_TOKENS * N else 0
         if need:
             workspace = x.new_empty((need,), dtype=torch.uint8)
             mine.append(workspace)

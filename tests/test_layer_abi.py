@@ -248,3 +248,15 @@ def test_more_threads_than_a_launch_takes_are_refused(call):
 ])
 def test_the_largest_launches_are_accepted(call):
     assert call(1 << 50) == OK
+
+
+def test_short_sequences_are_not_split_unasked():
+    # the binding relies on it: no workspace, and no call to ask for one
+    text = open(HEADER).read()
+    assert f"#define KDA_SSM_SPLIT_TOKENS {S.SPLIT_TOKENS}\n" in text
+    for N in (1, 2, 7, 64, 300):
+        for H, P, D in ((1, 64, 64), (4, 128, 128), (12, 128, 128), (64, 64, 128)):
+            for packed in (0, 1):
+                for T in (0, N, S.SPLIT_TOKENS * N):
+                    assert S.ssm_plan(ssm_problem(N=N, T=T, H=H, G=1, P=P, S_=D, packed=packed)) == 0
+    assert S.ssm_plan(ssm_problem(N=1, T=129, H=1, G=1, P=64, S_=64, piece=64)) == 64
