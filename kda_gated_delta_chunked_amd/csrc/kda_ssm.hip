@@ -200,24 +200,26 @@ template <int COLS, int THREADS>
 struct RowCopy {
   static constexpr int PER_ROW = COLS / 8, COUNT = L * PER_ROW / THREADS, STEP = THREADS / PER_ROW;
   static constexpr int KINDS = STEP % 16 ? 16 / STEP : 1;  // the swizzle repeats every 16 rows
-  int at[KINDS];
-  __device__ __forceinline__ RowCopy(int row_bytes) {
+  int in_row[KINDS];  // the lane's chunk in its row, bytes
+  __device__ __forceinline__ RowCopy() {
 #pragma unroll
     for (int v = 0; v < KINDS; ++v) {
       const int row = v * STEP + threadIdx.x / PER_ROW, chunk = threadIdx.x % PER_ROW;
-      at[v] = row * row_bytes + ((tile_at<COLS>(row, chunk) >> 4) & (PER_ROW - 1)) * 16;
+      in_row[v] = ((tile_at<COLS>(row, chunk) >> 4) & (PER_ROW - 1)) * 16;
     }
   }
+  // (one address per tile in a register is one too many: a product per copy)
   __device__ __forceinline__ void start(const Cursor& c, int rows, uint8_t* tile, int wave) const {
 #if defined(__HIP_DEVICE_COMPILE__)  // the host pass has no 16-byte form of the builtin
+    int row = threadIdx.x / PER_ROW;
+    forget(row);
     typedef __attribute__((address_space(3))) void* lds_ptr;
     const __amdgpu_buffer_rsrc_t w = c.window(rows);
 #pragma unroll
     for (int i = 0; i < COUNT; ++i) {
-      int from = at[i % KINDS];
-      forget(from);
+      const int from = __umul24(row, c.row_bytes) + in_row[i % KINDS];
       __builtin_amdgcn_raw_ptr_buffer_load_lds(w, (lds_ptr)(tile + (i * THREADS + wave * 64) * 16), 16,
-                                               from + i / KINDS * (KINDS * STEP) * c.row_bytes, 0, 0, 0);
+                                               from + i * STEP * c.row_bytes, 0, 0, 0);
     }
 #else
     (void)c, (void)rows, (void)tile, (void)wave;
@@ -388,8 +390,8 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
   Cursor cB(Bp, from, k.b_stride * 2, N * 2), cC(Cp, from, k.c_stride * 2, N * 2), cX(Xp, from, k.x_stride * 2, XC * 2);
   Cursor cO(Op, from, k.out_stride * 2, XC * 2), cZ(Zp, from, k.z_stride * 2, XC * 2);
   Cursor cT(k.dt + head0, from, (int64_t)k.H * 4, HPW * 4);
-  const RowCopy<N, THREADS> copyB(cB.row_bytes), copyC(cC.row_bytes);
-  const RowCopy<XC, THREADS> copyX(cX.row_bytes), copyZ(cZ.row_bytes);
+  const RowCopy<N, THREADS> copyB, copyC;
+  const RowCopy<XC, THREADS> copyX, copyZ;
   constexpr int NEXT_COPIES = RowCopy<N, THREADS>::COUNT + RowCopy<XC, THREADS>::COUNT;
   // Decays, by the last wave: lane = token, the upper half of the wave the
   // second head (HPW 2) or the second chunk of a block of two.
@@ -459,9 +461,7 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
   const int m_block = hh * 3 * M_BLOCK, m_row = m_block + m_at(l16, up), m_zeros = m_block + m_at(0, 1);
   const int m_diag = l16 < 8 && up ? m_zeros : m_row + (l32 < 16 ? 0 : 2 * M_BLOCK);
   int at_m0 = l32 < 16 ? m_diag : m_row + M_BLOCK, at_m1 = l32 < 16 ? m_zeros : m_diag;
-  const int at_lost = m_block + (l32 < 16 ? 0 : 2 * M_BLOCK) + lost_at(l16);
   int at_s = tile_at<XC>(lane >> 2, xcol + (lane & 3));
-  const int scol = (xcol + (lane & 3)) * 16;
 
   while (rem > 0) {
 #pragma unroll
@@ -485,6 +485,7 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
     // this chunk's gate, then the next chunk's rows; nobody reads the other
     // buffer any more
     if constexpr (GATE) copyZ.start(cZ, min(rem, L), tZ, wave);
+    asm volatile("" ::: "memory");  // in this order: the wait for the gate counts what came after it
     cB.advance(L);
     cX.advance(L);
     copyB.start(cB, min(rem - L, L), buf ? b0 : b1, wave);
@@ -517,7 +518,11 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
                      bf16_pair(mv[2], mv[3]));
           if (PARTS == 3 && blk16 != 1 && l16 >> 2 == q4) {
             const float v = l16 & 2 ? (l16 & 1 ? mv[3] : mv[2]) : (l16 & 1 ? mv[1] : mv[0]);
-            lds_write4(tM + (q * 3 + blk16) * M_BLOCK + lost_at(l16), v - bf16_f32(bf16_pair(v, 0.f) & 0xffff));
+            int at = l16;
+            forget(at);
+            at = lost_at(at);
+            forget(at);
+            lds_write4(tM + (q * 3 + blk16) * M_BLOCK + at, v - bf16_f32(bf16_pair(v, 0.f) & 0xffff));
           }
         }
       }
@@ -649,7 +654,14 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
       // x's place in the tile, for stores of whole 64-byte runs.
       // x_t's coefficient is the skip term and what M's diagonal lost when it was
       // rounded, which a short sequence has little else to even out.
-      const float own = PARTS == 3 ? Dh + *reinterpret_cast<const float*>(tM + at_lost) : Dh;
+      float own = Dh;
+      if constexpr (PARTS == 3) {
+        int t = l32;
+        forget(t);
+        int at_lost = m_block + (t < 16 ? 0 : 2 * M_BLOCK) + lost_at(t & 15);
+        forget(at_lost);
+        own += *reinterpret_cast<const float*>(tM + at_lost);
+      }
       uint8_t* yt = buf ? x1 : x0;
       constexpr int PRODUCTS = PARTS * NB;
 #pragma unroll
@@ -676,8 +688,10 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
           }
         __builtin_amdgcn_sched_barrier(0);
       }
-      int srow = lane >> 2;
+      int srow = lane;
       forget(srow);
+      const int scol = (xcol + (srow & 3)) * 16;
+      srow >>= 2;
       const __amdgpu_buffer_rsrc_t ow = cO.window(min(rem, L));
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
