@@ -35,16 +35,17 @@
 // all pieces side by side from them.
 //
 // What bounds it (MI355X, H12, 128 x 128): the instructions that a chunk issues.
-// A wave of the full pass issues 26 (34 where a final state is exact) products
+// A wave of the full pass issues 26 (34 in a sequence's last piece) products
 // of 32 x 32 x 16, four of 16 x 16 x 32 and about 290 vector instructions, 130
 // more with a gate, and one product hides about four vector instructions, from
-// whichever wave of its SIMD.  So a CU finishes a chunk of four waves every 1.7
-// us with one workgroup on it, 1.6 with two and 1.45 with three (2.2, 2.0 and 1.8
+// whichever wave of its SIMD.  So a CU finishes a chunk of four waves every 1.9
+// us with one workgroup on it, 1.6 with two and 1.5 with three (2.3, 2.1 and 1.9
 // with a gate): more waves gain little, and so did a third buffer, another order
 // of the waves' priorities, and chunks of 64 tokens (339 against 307 us for B8
-// T8192 at the time).  B8 T8192: 78 us for the first launch, 14 and 130 for the
-// others with pieces of 1024 tokens, at 3.2 to 3.8 TB/s; B1 T8192, gated, 21 +
-// 13 + 35.
+// T8192 at the time).  What did cost was a register reloaded from scratch behind
+// the copies, which waits for them: 32 ragged prompts 364 against 352 us.  The
+// three launches: B8 T8192 78 + 14 + 130 us with pieces of 1024 tokens (3.2 to
+// 4.2 TB/s); B1 T8192, gated, 20 + 13 + 34; the ragged prompts 108 + 27 + 217.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

@@ -176,7 +176,7 @@ kda_status check_ssm(const kda_ssm_problem* p) {
 // last pieces to run leave half of the device idle.  Measured with a gate,
 // unsplit / split where the rule splits: B1 T8192 H12 609 / 65, B1 T1024 H12
 // 83 / 34, B8 T1024 H12 84 / 68, B8 T8192 H12 679 / 288, 32 ragged prompts of 24
-// heads 470 / 360; and where it does not: B32 T512 H12 65 / 87.
+// heads 470 / 352; and where it does not: B32 T512 H12 65 / 87.
 struct SsmModel {
   double groups, alone, rate = 1.4, state;
   explicit SsmModel(const kda_ssm_problem* p) {
