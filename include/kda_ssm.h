@@ -103,7 +103,9 @@ kda_status kda_conv_decode(const kda_conv_decode_problem* p, const uint16_t* x, 
  *   S    <- exp(step A[h]) S + step B[t, g] x[t, h]^T
  *   y     = S^T C[t, g] + D[h] x[t, h]
  *   out   = y, or y z sigmoid(z) with a gate z
- * A <= 0 and step >= 0 are the caller's contract (a decay is at most 1).
+ * A <= 0 and step >= 0 are the caller's contract (a decay is at most 1).  With
+ * dt_softplus a logit of minus infinity, or of the lowest float, is a step of
+ * zero: the token leaves the state as it is.
  *
  *   x, z, out       bf16 [T_total, H, head_dim] with row strides (z may be NULL)
  *   B, C            bf16 [T_total, G, d_state] with row strides

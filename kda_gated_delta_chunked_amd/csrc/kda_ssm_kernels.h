@@ -219,8 +219,10 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
 // place.  log(1 + e) = 2 artanh(u) with u = e / (2 + e) <= 1/3, by its series
 // (the first term left out is below u 2^-27); the exponential's argument is
 // carried in two parts, so that e keeps its accuracy where it is all there is.
+// Below -200 e is zero: the bound keeps the two parts finite where v is an
+// infinity or near the largest float (a masked token's step, say).
 __device__ __forceinline__ float softplus(float v) {
-  const float a = -fabsf(v), hi = a * 1.44269502f;  // log2(e) = 1.44269502 + 1.92596e-8
+  const float a = fmaxf(-fabsf(v), -200.f), hi = a * 1.44269502f;  // log2(e) = 1.44269502 + 1.92596e-8
   const float lo = __builtin_fmaf(a, 1.44269502f, -hi) + a * 1.92596e-8f;
   const float e0 = __builtin_amdgcn_exp2f(hi), e = __builtin_fmaf(e0, lo * 0.693147182f, e0);
   const float u = e * __builtin_amdgcn_rcpf(2.f + e), q = u * u;
