@@ -5,6 +5,11 @@ decode) and the residual RMS norm with its 8-bit output.
 Argument marshalling only, as in ``ops``: tensors are checked for dtype, shape
 and device, their pointers and row strides and the current HIP stream go to
 the library, and there is no fallback.
+
+With ``stream=`` a call runs on that stream instead: the caller sees to it that
+its inputs are ready there and are kept until the stream is done with them, and
+that it is before the results are used on another stream.  Results and
+workspaces that the call allocates are the stream's own from the start.
 """
 from __future__ import annotations
 
@@ -153,17 +158,31 @@ def _gpu(t):
     return t.device
 
 
-def _like(x, dtype=None):
+def _like(x, stream, dtype=None):
     """A packed tensor of x's shape (about 1 us cheaper than one from a shape)."""
     import torch
 
-    return torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
+    if stream is None:
+        return torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
+
+
+def _new(x, stream, shape, dtype):
+    import torch
+
+    if stream is None:
+        return x.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return x.new_empty(shape, dtype=dtype)
 
 
 def _launch(name: str, dev, stream, problem, args, mine=()):
-    """Enqueue on `stream` (None: the current one).  Buffers the binding took
-    from torch's allocator (`mine`) belong to the current stream; on another
-    one the allocator is told, so that it does not hand them out early."""
+    """Enqueue on `stream` (None: the current one).  Buffers of the binding's own
+    come out of that stream's part of torch's allocator: from the current stream's
+    a block could be one that work queued there still uses.  Results (`mine`) are
+    read on the current stream next, and freed there: the allocator is told, so
+    that a later call on `stream` does not get them early."""
     import torch
 
     current = torch._C._cuda_getCurrentRawStream(dev.index)
@@ -174,8 +193,9 @@ def _launch(name: str, dev, stream, problem, args, mine=()):
         with torch.cuda.device(dev):
             status = call_raw(name, problem, *args, raw)
     if raw != current:
+        here = torch.cuda.current_stream(dev)
         for t in mine:
-            t.record_stream(stream)
+            t.record_stream(here)
     if status:
         _check(status, name)
 
@@ -242,10 +262,10 @@ def conv_prefill(x, weight, bias=None, *, cu_seqlens=None, initial_state=None, f
     cu64 = _offsets(cu_seqlens, dev)
     mine = []
     if out is None:
-        out = _like(x)
+        out = _like(x, stream)
         mine.append(out)
     if final_state is None and output_final_state:
-        final_state = x.new_empty(state)
+        final_state = _new(x, stream, state, bf)
         mine.append(final_state)
     p = ConvProblem(N, T, D, W, _activation(activation), cu64, _row_stride("x", x, lead),
                     _row_stride("out", out, lead))
@@ -279,7 +299,7 @@ def conv_decode(x, weight, bias, state_pool, state_indices, *, activation: str =
     _check_tensor("out", out, bf, shape, dev, False)
     mine = []
     if out is None:
-        out = _like(x)
+        out = _like(x, stream)
         mine.append(out)
     p = ConvDecodeProblem(N, T, D, W, _activation(activation), size,
                           _row_stride("x", x, 2), _row_stride("out", out, 2))
@@ -349,10 +369,10 @@ def ssm_prefill(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, dt_softplus: bo
     cu64 = _offsets(cu_seqlens, dev)
     mine = []
     if out is None:
-        out = _like(x)
+        out = _like(x, stream)
         mine.append(out)
     if final_state is None and output_final_state:
-        final_state = x.new_empty(shape, dtype=state_dtype)
+        final_state = _new(x, stream, shape, state_dtype)
         mine.append(final_state)
     p = SsmProblem(N, T, H, G, P, S, int(dt_softplus), kind, cu64, int(piece_tokens),
                    int(cu_seqlens is not None), _row_stride("x", x, lead),
@@ -362,8 +382,7 @@ def ssm_prefill(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, dt_softplus: bo
         # (short sequences are never split unless asked for: not worth a call)
         need = ssm_workspace_size(p) if piece_tokens or T > SPLIT_TOKENS * N else 0
         if need:
-            workspace = x.new_empty((need,), dtype=torch.uint8)
-            mine.append(workspace)
+            workspace = _new(x, stream, (need,), torch.uint8)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on {dev}")
     size = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -397,7 +416,7 @@ def ssm_decode(x, dt, A, B, C, state_pool, state_indices, *, D=None, z=None, dt_
     _check_tensor("state_indices", state_indices, torch.int32, (N,), dev)
     mine = []
     if out is None:
-        out = _like(x)
+        out = _like(x, stream)
         mine.append(out)
     p = SsmDecodeProblem(N, T, H, G, P, S, int(dt_softplus), kind, size,
                          _row_stride("x", x, 2), _row_stride("B", B, 2), _row_stride("C", C, 2),
@@ -439,13 +458,13 @@ def add_rmsnorm(x, weight, *, residual=None, eps: float = 1e-6, out_dtype=None, 
     if residual is None or residual_out is False:
         residual_out = None
     elif residual_out is None:
-        residual_out = _like(x)
+        residual_out = _like(x, stream)
         mine.append(residual_out)
     if out is None:
-        out = _like(x, out_dtype)
+        out = _like(x, stream, out_dtype)
         mine.append(out)
     if fp8 and scales is None:
-        scales = x.new_empty(groups, dtype=torch.float32)
+        scales = _new(x, stream, groups, torch.float32)
         mine.append(scales)
     _check_tensor("x", x, bf, shape, dev, False)
     _check_tensor("residual", residual, bf, shape, dev)

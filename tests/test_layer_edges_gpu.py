@@ -73,3 +73,86 @@ def test_masked_time_steps_of_single_tokens(dims, dtype):
     out = K().ssm_decode(*a, pd, torch.arange(reqs, dtype=torch.int32).cuda(), **kw)
     R.assert_scan_out(out.cpu().flatten(0, 1), ref, mag)
     R.assert_state(pd.cpu(), final, smag)
+
+
+# ---------------------------------------------------------------------------
+# calls on a given stream beside work that is still queued on the current one
+
+def stream_calls(seed):
+    """name -> call(stream, **inputs) -> outputs, with two sets of inputs."""
+    k = K()
+    g = torch.Generator().manual_seed(seed)
+    w, rw = rand(g, 520, 4).cuda(), rand(g, 520).cuda()
+    idx = torch.tensor([3, -1, 0], dtype=torch.int32).cuda()
+    scan = on_gpu(scan_case(g, 2048, 2, 1, 128, 128, z=False, softplus=False, skip=False))
+    step = on_gpu(scan_case(g, 6, 4, 1, 64, 128, z=True, softplus=True, skip=True))
+    step = {n: v.unflatten(0, (3, 2)) if n in ("x", "B", "C", "z", "dt") else v for n, v in step.items()}
+    s_a, s_kw = scan_args(scan)
+    t_a, t_kw = scan_args(step)
+    rows, states = rand(g, 5, 3, 520).cuda(), rand(g, 5, 4, 128, 64, dtype=torch.float32).cuda()
+    cu = offsets([2048]).cuda()
+    two = lambda *shape: [rand(g, *shape).cuda() for _ in range(2)]
+    return {
+        "conv": (two(2048, 520), lambda s, x: k.conv_prefill(x, w, stream=s)),
+        "conv_step": (two(3, 2, 520), lambda s, x: [k.conv_decode(x, w, None, rows, idx, stream=s)]),
+        "scan": (two(2048, 2, 128), lambda s, x: k.ssm_prefill(x, *s_a[1:], **s_kw, cu_seqlens=cu, stream=s)),
+        "scan_step": (two(3, 2, 4, 64), lambda s, x: [k.ssm_decode(x, *t_a[1:], states, idx, **t_kw, stream=s)]),
+        "norm": (two(2048, 520), lambda s, x: k.add_rmsnorm(x, rw, residual=x, out_dtype=torch.float8_e4m3fn,
+                                                            scale_group=128, stream=s)),
+    }, [rows, states]
+
+
+def slow(n=24):
+    a = torch.ones(8192, 8192, dtype=BF, device="cuda")
+    for _ in range(n):
+        a @ a
+
+
+def as_bytes(outs):
+    return [t.contiguous().view(torch.uint8) for t in outs]
+
+
+@pytest.mark.parametrize("name", ["conv", "conv_step", "scan", "scan_step", "norm"])
+def test_results_on_a_given_stream_are_not_memory_that_queued_work_still_writes(name):
+    calls, pools = stream_calls(111)
+    (x, _), call = calls[name]
+    start = [p.clone() for p in pools]
+    want = [t.clone() for t in as_bytes(call(None, x))]
+    workspace = 2048 // 64 * 2 * (128 * 128 + 1) * 4
+    side = torch.cuda.Stream()
+    slow(2)
+    for p, s in zip(pools, start):
+        p.copy_(s)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    slow()
+    for size in [t.numel() for t in want] + [workspace // n for n in (1, 2, 4, 8, 16)]:
+        # freed with the fill still queued
+        junk = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(3)]
+        for t in junk:
+            t.fill_(0xff)
+        del junk, t
+    got = call(side, x)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(as_bytes(got), want))
+
+
+@pytest.mark.parametrize("name", ["conv", "conv_step", "scan", "scan_step", "norm"])
+def test_results_of_a_given_stream_stay_while_the_current_one_reads_them(name):
+    calls, pools = stream_calls(112)
+    (x, other), call = calls[name]
+    start = [p.clone() for p in pools]
+    want = [t.clone() for t in as_bytes(call(None, x))]
+    for p, s in zip(pools, start):
+        p.copy_(s)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = as_bytes(call(side, x))
+    torch.cuda.current_stream().wait_stream(side)
+    slow()
+    kept = [t.clone() for t in got]
+    del got
+    more = [call(side, other) for _ in range(3)]
+    torch.cuda.synchronize()
+    del more
+    assert all(torch.equal(a, b) for a, b in zip(kept, want))
