@@ -5,9 +5,15 @@ and device, their device pointers and the current HIP stream are handed to
 ``kda_prefill``, and every step of the computation runs in the library's HIP
 kernels.  There is no fallback: if the library cannot be loaded, calls raise.
 PyTorch provides device memory and streams.
+
+With ``stream=`` a call runs on that stream instead of the current one: the
+caller sees to it that its inputs are ready there and are kept until the stream
+is done with them, and that it is before the results are used on another
+stream.  Buffers that the call allocates are the stream's own from the start.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -214,6 +220,28 @@ def _ptr(t) -> int:
     return 0 if t is None else int(t.data_ptr())
 
 
+def _allocating(stream):
+    """The context in which a call allocates its own buffers: out of the stream's
+    part of torch's caching allocator (None: the current stream's).  A block of
+    another stream's part could be one that work queued there still uses."""
+    import torch
+
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _results_of(stream, dev, *tensors):
+    """Results that a call on another stream than the current one allocated are
+    read on the current one next, and freed there: the allocator is told, so that
+    a later call on `stream` does not get their blocks early."""
+    import torch
+
+    here = torch.cuda.current_stream(dev)
+    if stream != here:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(here)
+
+
 def prefill(q, k, v, g, beta, *, cu_seqlens=None, initial_state=None, scale: Optional[float] = None,
             out=None, final_state=None, output_final_state: bool = True, ckpt_offsets=None,
             ckpt_state=None, gate_lower_bound: float = -5.0, variant: str = "auto",
@@ -315,38 +343,29 @@ def prefill(q, k, v, g, beta, *, cu_seqlens=None, initial_state=None, scale: Opt
                         seq_order=_ptr(seq_order), chain_parts=chain_parts)
     if seq_order is not None and tuple(seq_order.shape) != (N,):
         raise ValueError(f"seq_order must be [{N}]")
-    out_given, final_given = out, final_state
-    if out is None:
-        out = torch.empty_like(v)
-    elif out.shape != q.shape:
+    if out is not None and out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    if final_state is None and output_final_state:
-        final_state = torch.empty(state_shape, dtype=state_dtype, device=dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    own_ws = False
+    out_given, final_given = out, final_state
+    with _allocating(stream):
+        if out is None:
+            out = torch.empty_like(v)
+        if final_state is None and output_final_state:
+            final_state = torch.empty(state_shape, dtype=state_dtype, device=dev)
     with torch.cuda.device(dev):
         if workspace is None:
             # a workspace only for the two-launch schedule (AUTO: when the
             # library's table picks it on this device)
             need = workspace_size(prob)
             if need and variant != "fused" and (variant != "auto" or plan(prob)[0] == "decomp"):
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-                own_ws = True
+                with _allocating(stream):
+                    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         st = prefill_raw(prob, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_seqlens),
                          _ptr(initial_state), _ptr(out), _ptr(final_state), _ptr(ckpt_offsets),
                          _ptr(ckpt_state), _ptr(workspace), ws_bytes, int(stream.cuda_stream))
-        # Blocks allocated here belong to the current stream in torch's caching
-        # allocator.  When the call runs on another stream, tell the allocator
-        # that stream uses them, so that a block (above all the workspace,
-        # dropped on return) is not handed to a new allocation on the current
-        # stream while the kernels still read or write it.
-        if stream != torch.cuda.current_stream(dev):
-            for t, mine in ((workspace, own_ws), (out, out_given is None),
-                            (final_state, final_given is None)):
-                if mine and t is not None:
-                    t.record_stream(stream)
+    _results_of(stream, dev, out if out_given is None else None, final_state if final_given is None else None)
     _check(st, "kda_prefill")
     return out, final_state
 
@@ -433,11 +452,12 @@ def _decode_setup(q, k, v, g, beta, state_pool, state_indices, scale, gate_lower
                                state_dtype="bf16" if state_pool.dtype == torch.bfloat16 else "fp32")
 
 
-def _decode_out(q, v, out):
+def _decode_out(q, v, out, stream):
     import torch
 
     if out is None:
-        return torch.empty_like(v)
+        with _allocating(stream):
+            return torch.empty_like(v)
     if out.shape != q.shape or out.dtype != torch.bfloat16:
         raise ValueError("out must be bf16 with q's shape")
     return out
@@ -457,13 +477,15 @@ def decode(q, k, v, g, beta, state_pool, state_indices, *, scale: Optional[float
 
     prob = _decode_setup(q, k, v, g, beta, state_pool, state_indices, scale, gate_lower_bound,
                          qk_l2norm, beta_logit)
-    out = _decode_out(q, v, out)
+    given = out
+    out = _decode_out(q, v, out, stream)
     dev = q.device
     if stream is None:
         stream = torch.cuda.current_stream(dev)
     with torch.cuda.device(dev):
         st = decode_raw(prob, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state_pool),
                         _ptr(state_indices), _ptr(out), int(stream.cuda_stream))
+    _results_of(stream, dev, out if given is None else None)
     _check(st, "kda_decode")
     return out
 
@@ -481,12 +503,14 @@ def decode_verify(q, k, v, g, beta, state_pool, state_indices, *, scale: Optiona
 
     prob = _decode_setup(q, k, v, g, beta, state_pool, state_indices, scale, gate_lower_bound,
                          qk_l2norm, beta_logit)
-    out = _decode_out(q, v, out)
+    given, trace_given = out, state_trace is not None
+    out = _decode_out(q, v, out, stream)
     N, T, H, D = q.shape
     dev = q.device
     sdt = state_pool.dtype
     if state_trace is None:
-        state_trace = torch.empty((N, T, H, D, D), dtype=sdt, device=dev)
+        with _allocating(stream):
+            state_trace = torch.empty((N, T, H, D, D), dtype=sdt, device=dev)
     elif state_trace is False:
         state_trace = None
     elif (tuple(state_trace.shape) != (N, T, H, D, D) or state_trace.dtype != sdt
@@ -498,6 +522,7 @@ def decode_verify(q, k, v, g, beta, state_pool, state_indices, *, scale: Optiona
         st = decode_verify_raw(prob, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
                                _ptr(state_pool), _ptr(state_indices), _ptr(out),
                                0 if state_trace is None else _ptr(state_trace), int(stream.cuda_stream))
+    _results_of(stream, dev, out if given is None else None, None if trace_given else state_trace)
     _check(st, "kda_decode_verify")
     return out, state_trace
 
