@@ -181,16 +181,19 @@ struct Split {
 
 // A buffer's rows from one chunk's first on, bounded by the hardware: rows past
 // the end read as zeros and are not written.  Row strides are below 2^23
-// elements, so a chunk's offsets stay below 2^31 bytes.
+// elements, so a chunk's offsets stay below 2^31 bytes.  (window<MOST>: of the
+// rows that are left, MOST at most.)
 struct Cursor {
   uint64_t base;
   int row_bytes, width;  // of a row: its distance to the next, and what of it is ours
   __device__ __forceinline__ Cursor(const void* p, int64_t tok, int64_t row_bytes_, int width_)
       : base(reinterpret_cast<uint64_t>(p) + tok * row_bytes_), row_bytes((int)row_bytes_), width(width_) {}
   __device__ __forceinline__ void advance(int rows) { base += (int64_t)rows * row_bytes; }
-  __device__ __forceinline__ __amdgpu_buffer_rsrc_t window(int rows) const {
-    const int bytes = (rows - 1) * row_bytes + width;
-    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), 0, rows > 0 ? bytes : 0, 0x00020000);
+  template <int MOST>
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t window(int left) const {
+    static_assert(MOST <= 64, "offsets below 2^31");
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), 0,
+                                             window_bytes(left, MOST, row_bytes, width), 0x00020000);
   }
 };
 
@@ -210,12 +213,12 @@ struct RowCopy {
     }
   }
   // (one address per tile in a register is one too many: a product per copy)
-  __device__ __forceinline__ void start(const Cursor& c, int rows, uint8_t* tile, int wave) const {
+  __device__ __forceinline__ void start(const Cursor& c, int left, uint8_t* tile, int wave) const {
 #if defined(__HIP_DEVICE_COMPILE__)  // the host pass has no 16-byte form of the builtin
     int row = threadIdx.x / PER_ROW;
     forget(row);
     typedef __attribute__((address_space(3))) void* lds_ptr;
-    const __amdgpu_buffer_rsrc_t w = c.window(rows);
+    const __amdgpu_buffer_rsrc_t w = c.window<L>(left);
 #pragma unroll
     for (int i = 0; i < COUNT; ++i) {
       const int from = __umul24(row, c.row_bytes) + in_row[i % KINDS];
@@ -223,7 +226,7 @@ struct RowCopy {
                                                from + i * STEP * c.row_bytes, 0, 0, 0);
     }
 #else
-    (void)c, (void)rows, (void)tile, (void)wave;
+    (void)c, (void)left, (void)tile, (void)wave;
 #endif
   }
 };
@@ -404,11 +407,11 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
   float scale_left = 0.f;    // the accumulators' scale behind the last chunk
   int gbuf = 0;
   float rdt;
-  auto fetch_steps = [&](int rows) {
+  auto fetch_steps = [&](int left) {
     int tok = gate_tok;
     forget(tok);
     rdt = __uint_as_float(
-        __builtin_amdgcn_raw_buffer_load_b32(cT.window(rows), tok * cT.row_bytes + (HPW == 2 ? up * 4 : 0), 0, 0));
+        __builtin_amdgcn_raw_buffer_load_b32(cT.window<BLOCK>(left), tok * cT.row_bytes + (HPW == 2 ? up * 4 : 0), 0, 0));
   };
   auto make_gates = [&](int rows, Gates& gt) {
     const float step = gate_tok < rows ? ssm_step_of(rdt, gate_bias, k.softplus) : 0.f;
@@ -441,9 +444,9 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
     lf[0] = HPW == 1 ? lf[1] : lane_of(fold0 ? 0.0 : next0, 0);
   };
   fetch_steps(rem);
-  copyB.start(cB, min(rem, L), b0, wave);
-  if constexpr (FULL) copyC.start(cC, min(rem, L), tC, wave);
-  copyX.start(cX, min(rem, L), x0, wave);
+  copyB.start(cB, rem, b0, wave);
+  if constexpr (FULL) copyC.start(cC, rem, tC, wave);
+  copyX.start(cX, rem, x0, wave);
   if (gate_wave) make_gates(rem, gates[0]);
   cT.advance(BLOCK);
   fetch_steps(rem - BLOCK);
@@ -485,12 +488,12 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
     }
     // this chunk's gate, then the next chunk's rows; nobody reads the other
     // buffer any more
-    if constexpr (GATE) copyZ.start(cZ, min(rem, L), tZ, wave);
+    if constexpr (GATE) copyZ.start(cZ, rem, tZ, wave);
     asm volatile("" ::: "memory");  // in this order: the wait for the gate counts what came after it
     cB.advance(L);
     cX.advance(L);
-    copyB.start(cB, min(rem - L, L), buf ? b0 : b1, wave);
-    copyX.start(cX, min(rem - L, L), buf ? x0 : x1, wave);
+    copyB.start(cB, rem - L, buf ? b0 : b1, wave);
+    copyX.start(cX, rem - L, buf ? x0 : x1, wave);
 
     f32x16 Y = {};
     if constexpr (FULL) {
@@ -623,7 +626,7 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
       lds_only_barrier();
       // C has been read
       cC.advance(L);
-      copyC.start(cC, min(rem - L, L), tC, wave);
+      copyC.start(cC, rem - L, tC, wave);
       // y^T += x^T M^T.  A product with the zeros of M above the diagonal would
       // carry a later token's infinity or NaN to an earlier one: those elements
       // of x are left out of it and added to the tokens behind them alone.
@@ -693,7 +696,7 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
       forget(srow);
       const int scol = (xcol + (srow & 3)) * 16;
       srow >>= 2;
-      const __amdgpu_buffer_rsrc_t ow = cO.window(min(rem, L));
+      const __amdgpu_buffer_rsrc_t ow = cO.window<L>(rem);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));

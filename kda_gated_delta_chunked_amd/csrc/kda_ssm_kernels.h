@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "kda_kernels.h"
+#include "kda_spans.h"
 
 namespace kda {
 

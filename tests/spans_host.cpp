@@ -1,0 +1,6 @@
+// Host build of the span arithmetic (kda_spans.h) for tests/test_layer_spans.py.
+#include "kda_spans.h"
+
+extern "C" int kda_test_window_bytes(int left, int most, int row_bytes, int width) {
+  return kda::window_bytes(left, most, row_bytes, width);
+}
