@@ -9,6 +9,9 @@
 
 namespace kda {
 
+// Tokens from `from` to `to` of a batch, which has fewer than 2^31.
+__host__ __device__ inline int rows_left(int64_t from, int64_t to) { return (int)(to - from); }
+
 // Bytes of a window on the rows of a chunk, from the first one's first byte to
 // the last one's last: `most` rows, or the `left` ones of the sequence.  At most
 // 64 rows less than 2^24 bytes apart: below 2^30 + 2^24, whatever is left.

@@ -389,8 +389,7 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
   const float Dh = k.D ? k.D[head] : 0.f;
   const bool gate_wave = wave == WAVES - 1;
 
-  // rows left in the piece (a long one counts down from 2^30)
-  int rem = to - from < (1 << 30) ? (int)(to - from) : 1 << 30;
+  int rem = rows_left(from, to);  // in the piece
   Cursor cB(Bp, from, k.b_stride * 2, N * 2), cC(Cp, from, k.c_stride * 2, N * 2), cX(Xp, from, k.x_stride * 2, XC * 2);
   Cursor cO(Op, from, k.out_stride * 2, XC * 2), cZ(Zp, from, k.z_stride * 2, XC * 2);
   Cursor cT(k.dt + head0, from, (int64_t)k.H * 4, HPW * 4);

@@ -4,3 +4,5 @@
 extern "C" int kda_test_window_bytes(int left, int most, int row_bytes, int width) {
   return kda::window_bytes(left, most, row_bytes, width);
 }
+
+extern "C" int kda_test_rows_left(int64_t from, int64_t to) { return kda::rows_left(from, to); }

@@ -37,3 +37,14 @@ def test_every_window_has_a_bound():
     text = open(os.path.join(CSRC, "kda_ssm.hip")).read()
     assert len(re.findall(r"make_buffer_rsrc", text)) == 1 and "window_bytes(left, MOST, row_bytes, width)" in text
     assert set(re.findall(r"\.window<(\w+)>\(", text)) == {"L", "BLOCK"} and ".window(" not in text
+
+
+def test_no_row_of_a_long_sequence_is_left_out(lib):
+    lib.kda_test_rows_left.argtypes = [ctypes.c_int64, ctypes.c_int64]
+    for start in (0, 1, 1 << 30):
+        for rows in (0, 1, (1 << 30) - 1, 1 << 30, (1 << 30) + 1, (1 << 31) - 1 - start):
+            if rows <= (1 << 31) - 1 - start:
+                assert lib.kda_test_rows_left(start, start + rows) == rows
+    # the scan counts with it, from all rows down
+    text = open(os.path.join(CSRC, "kda_ssm.hip")).read()
+    assert re.findall(r"int rem = (.*?);", text) == ["rows_left(from, to)"]
