@@ -15,7 +15,8 @@
  * call writes overlap no other buffer except where an exact alias is named.
  * A buffer with a row stride counts as its whole span, first element to last.
  * KDA_ERR_TOO_LARGE: 2^31 tokens or rows or more, or so much work that a launch
- * would have 2^32 threads (2^32 / 16 rows of the norm, say).
+ * would have 2^32 threads (2^32 / 16 rows of the norm, say), or packed rows of
+ * a scan of 2^23 elements or more (H head_dim; G d_state for prompts).
  *
  * Sequences.  A batch is N sequences of T_total tokens in all: fixed
  * (cu_seqlens NULL, T_total / N tokens each) or packed, with cu_seqlens int32

@@ -21,10 +21,13 @@ using kda::range_of;
 
 bool flag(int32_t v) { return v == 0 || v == 1; }
 
+// Rows are less than this many elements apart, so that a kernel may address 64
+// of them with 32 bits, and form their offsets from 24.
+constexpr int64_t kRowElements = 1 << 23;
+
 // a row stride: 0 stands for the packed row; else a multiple of 8 that holds it
-// (below 2^23, so that a kernel may address 64 rows with 32 bits)
 bool stride_ok(int64_t stride, int64_t row) {
-  return stride == 0 || (stride >= row && stride % 8 == 0 && stride < (1 << 23));
+  return stride == 0 || (stride >= row && stride % 8 == 0 && stride < kRowElements);
 }
 int64_t stride_of(int64_t stride, int64_t row) { return stride ? stride : row; }
 
@@ -85,7 +88,7 @@ kda_status check_heads(int32_t H, int32_t G, int32_t P, int32_t N, int32_t softp
   if ((P != 64 && P != 128) || (N != 64 && N != 128)) return KDA_ERR_UNSUPPORTED;
   if (H < 1 || G < 1 || H % G || !flag(softplus)) return KDA_ERR_INVALID_ARG;
   if (state_dtype != KDA_STATE_F32 && state_dtype != KDA_STATE_BF16) return KDA_ERR_UNSUPPORTED;
-  return (int64_t)H * P >= (1 << 23) ? KDA_ERR_TOO_LARGE : KDA_OK;
+  return (int64_t)H * P >= kRowElements ? KDA_ERR_TOO_LARGE : KDA_OK;
 }
 
 template <class Problem>
@@ -158,6 +161,8 @@ kda_status check_ssm(const kda_ssm_problem* p) {
   if (!flag(p->packed)) return KDA_ERR_INVALID_ARG;
   const int32_t piece = p->piece_tokens;
   if (piece < 0 || piece % 64 || !strides_ok(p)) return KDA_ERR_INVALID_ARG;
+  // (the heads' rows: check_heads)
+  if ((int64_t)p->num_groups * p->d_state >= kRowElements) return KDA_ERR_TOO_LARGE;
   const int64_t H = p->num_heads, unsplit = kda::span_slots(p->packed, p->num_seqs, p->total_tokens, kda::kUnsplit);
   if (kda::ssm_threads(unsplit, H, p->head_dim) > kda::kMaxThreads) return KDA_ERR_TOO_LARGE;
   return piece && !split_fits(p, piece) ? KDA_ERR_TOO_LARGE : KDA_OK;
