@@ -412,14 +412,16 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
     rdt = __uint_as_float(
         __builtin_amdgcn_raw_buffer_load_b32(cT.window<BLOCK>(left), tok * cT.row_bytes + (HPW == 2 ? up * 4 : 0), 0, 0));
   };
-  auto make_gates = [&](int rows, Gates& gt) {
-    const float step = gate_tok < rows ? ssm_step_of(rdt, gate_bias, k.softplus) : 0.f;
+  auto make_gates = [&](int left, Gates& gt) {
+    const float step = gate_tok < left ? ssm_step_of(rdt, gate_bias, k.softplus) : 0.f;
     float A = gate_A;
     settle(A);
     // A token that keeps less than 2^-256 keeps nothing in fp32: without the bound
     // its logarithm would take the bits of the small ones behind it from the sums.
+    // Behind the last token nothing decays, also where A is infinite (and 0 A a NaN).
     double log = (double)step * (double)A * kLog2e;
     log = log < -256.0 ? -256.0 : log;
+    log = gate_tok < left ? log : 0.0;
     const double cum = prefix_sums(log);
     const double sum0 = lane_of(cum, 31), sum1 = lane_of(cum, 63);
     if (!FULL) {

@@ -156,3 +156,23 @@ def test_results_of_a_given_stream_stay_while_the_current_one_reads_them(name):
     torch.cuda.synchronize()
     del more
     assert all(torch.equal(a, b) for a, b in zip(kept, want))
+
+
+# ---------------------------------------------------------------------------
+# a head that keeps nothing
+
+@pytest.mark.parametrize("dims", DIMS, ids=str)
+@pytest.mark.parametrize("piece", [0, 64])
+def test_a_head_with_an_infinite_rate_keeps_its_last_token_alone(dims, piece):
+    P, N = dims
+    lens, H = [37, 1, 70, 0, 64, 130], 2
+    g = torch.Generator().manual_seed(121)
+    c = scan_case(g, sum(lens), H, 1, P, N, z=False, softplus=True, skip=True)
+    c["A"][1] = -INF
+    s0 = rand(g, len(lens), H, N, P, dtype=torch.float32)
+    ref, final, mag, smag = scan_ref(c, s0, lens)
+    assert torch.isfinite(ref).all() and torch.isfinite(final).all()
+    a, kw = scan_args(on_gpu(c))
+    out, fin = K().ssm_prefill(*a, **kw, cu_seqlens=offsets(lens).cuda(), initial_state=s0.cuda(), piece_tokens=piece)
+    R.assert_scan_out(out.cpu(), ref, mag)
+    R.assert_state(fin.cpu(), final, smag)
