@@ -296,16 +296,17 @@ __device__ __forceinline__ bf16x8 finite_only(const bf16x8& f) {
 // two heads.  c_t is taken from the chunk's first token, in fp32: its error,
 // 2^-24 of the sum, is 2^-12 at most (32 logarithms of -256) and matters least
 // where the decays, and so the sums, are large.
-// The state is held scaled: it is the accumulators times 2^lf, lf <= 0 going
-// down with the chunks' decays, until 2^lf would fall below 2^kLeast: then the
-// accumulators take the factor in and lf is zero again.  Most chunks then need
-// no pass over the accumulators.
+// The state is held scaled: it is the accumulators times 2^lf, lf going down from
+// kScale with the chunks' decays, until it would fall below zero: then the
+// accumulators take the factor in and lf is kScale again.  Most chunks then need
+// no pass over the accumulators.  They are never larger than the state, so they
+// overflow where it does; elements of it below 2^-106 keep 2^-129.
 struct __attribute__((aligned(16))) Gates {
   float cum[64];     // lf + log2(e) c_t
   float step[64];    // s_t
   float to_end[64];  // w_t over the accumulators' scale behind the chunk
 };
-constexpr float kLeast = -20.f;
+constexpr float kScale = 20.f;
 
 // M's lower triangle as 16 x 16 blocks of rows t and columns j, (0, 0), (1, 0),
 // (1, 1); a row's two 16-byte chunks change places from row 8 on (no bank
@@ -390,6 +391,12 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
   const bool gate_wave = wave == WAVES - 1;
 
   int rem = rows_left(from, to);  // in the piece
+  if (rem > 0 && (s0 || a.initial)) {  // (a state that nothing comes into stays exactly as it is)
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) S[nb][r] *= 1.f / (1 << (int)kScale);
+  }
   Cursor cB(Bp, from, k.b_stride * 2, N * 2), cC(Cp, from, k.c_stride * 2, N * 2), cX(Xp, from, k.x_stride * 2, XC * 2);
   Cursor cO(Op, from, k.out_stride * 2, XC * 2), cZ(Zp, from, k.z_stride * 2, XC * 2);
   Cursor cT(k.dt + head0, from, (int64_t)k.H * 4, HPW * 4);
@@ -402,7 +409,7 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
   const int gate_head = head0 + (HPW == 2 ? up : 0), gate_tok = HPW == 2 ? l32 : lane;
   const float gate_A = k.A[gate_head], gate_bias = k.dt_bias ? k.dt_bias[gate_head] : 0.f;
   double log_decay[2] = {};  // of the whole piece, per half of the wave
-  double lf[2] = {};         // its head's or heads' scale
+  double lf[2] = {kScale, kScale};  // its head's or heads' scale
   float scale_left = 0.f;    // the accumulators' scale behind the last chunk
   int gbuf = 0;
   float rdt;
@@ -432,17 +439,17 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
     // one head's chunks one after the other
     double lf1 = lf[1];
     const double next0 = lf[0] + sum0;
-    const bool fold0 = (float)next0 < kLeast;
-    if (HPW == 1) lf1 = fold0 ? 0.0 : next0;
+    const bool fold0 = (float)next0 < 0.f;
+    if (HPW == 1) lf1 = fold0 ? kScale : next0;
     const double next1 = lf1 + sum1;
-    const bool fold1 = (float)next1 < kLeast;
+    const bool fold1 = (float)next1 < 0.f;
     gt.cum[lane] = (float)(cum + (up ? lf1 : lf[0]));
     gt.step[lane] = step;
-    const double off = up ? (fold1 ? sum1 : -lf1) : (fold0 ? sum0 : -lf[0]);
+    const double off = up ? (fold1 ? sum1 - kScale : -lf1) : (fold0 ? sum0 - kScale : -lf[0]);
     gt.to_end[lane] = exp2_of(off - cum) * step;
     // (uniform values, kept in scalar registers)
-    lf[1] = lane_of(fold1 ? 0.0 : next1, 0);
-    lf[0] = HPW == 1 ? lf[1] : lane_of(fold0 ? 0.0 : next0, 0);
+    lf[1] = lane_of(fold1 ? kScale : next1, 0);
+    lf[0] = HPW == 1 ? lf[1] : lane_of(fold0 ? kScale : next0, 0);
   };
   fetch_steps(rem);
   copyB.start(cB, rem, b0, wave);
@@ -583,13 +590,13 @@ __device__ __forceinline__ void run_piece(const SsmArgs& a, const Span& sp, int6
       for (int i = 0; i < 4; ++i) xs[0].template pair<PARTS>(i, xf[0], w[0][2 * i], w[0][2 * i + 1]);
     }
     scale_left = next;
-    if (next < kLeast) {
-      const float f = __builtin_amdgcn_exp2f(next);
+    if (next < 0.f) {
+      const float f = __builtin_amdgcn_exp2f(next - kScale);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int r = 0; r < 16; ++r) S[nb][r] *= f;
-      scale_left = 0.f;
+      scale_left = kScale;
     }
     // neighbouring products go to different accumulators
     forget(at_b);

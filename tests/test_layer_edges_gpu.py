@@ -176,3 +176,26 @@ def test_a_head_with_an_infinite_rate_keeps_its_last_token_alone(dims, piece):
     out, fin = K().ssm_prefill(*a, **kw, cu_seqlens=offsets(lens).cuda(), initial_state=s0.cuda(), piece_tokens=piece)
     R.assert_scan_out(out.cpu(), ref, mag)
     R.assert_state(fin.cpu(), final, smag)
+
+
+# ---------------------------------------------------------------------------
+# the scan is linear in x and the initial state: their scale leaves the relative
+# errors as they are, up to near the largest float
+
+@pytest.mark.parametrize("dims", DIMS, ids=str)
+@pytest.mark.parametrize("piece", [0, 64])
+@pytest.mark.parametrize("power", [112, -80])
+def test_states_far_from_one(dims, piece, power):
+    P, N = dims
+    lens, H = [150, 33, 0, 90], 2
+    g = torch.Generator().manual_seed(131)
+    c = scan_case(g, sum(lens), H, 1, P, N, z=True, softplus=True, skip=True)
+    s0 = rand(g, len(lens), H, N, P, dtype=torch.float32)
+    ref, final, mag, smag = scan_ref(c, s0, lens)
+    far = 2.0 ** power
+    c["x"] = c["x"] * far
+    a, kw = scan_args(on_gpu(c))
+    out, fin = K().ssm_prefill(*a, **kw, cu_seqlens=offsets(lens).cuda(), initial_state=(s0 * far).cuda(),
+                               piece_tokens=piece)
+    R.assert_scan_out(out.cpu().to(R.F64) / far, ref, mag)
+    R.assert_state(fin.cpu().to(R.F64) / far, final, smag)
