@@ -220,6 +220,11 @@ def _ptr(t) -> int:
     return 0 if t is None else int(t.data_ptr())
 
 
+def _check_stream(stream, dev):
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, expected {dev}")
+
+
 def _allocating(stream):
     """The context in which a call allocates its own buffers: out of the stream's
     part of torch's caching allocator (None: the current stream's).  A block of
@@ -289,6 +294,7 @@ def prefill(q, k, v, g, beta, *, cu_seqlens=None, initial_state=None, scale: Opt
     dev = q.device
     if dev.type != "cuda":
         raise ValueError("libkda runs on the GPU: tensors must be on a cuda (HIP) device")
+    _check_stream(stream, dev)
     for name, t, dt in (("q", q, torch.bfloat16), ("k", k, torch.bfloat16), ("v", v, torch.bfloat16),
                         ("g", g, torch.float32), ("beta", beta, torch.float32)):
         if t.dtype != dt:
@@ -415,7 +421,7 @@ def decode_validate_raw(problem: DecodeProblem, q, k, v, g, beta, state_pool, st
 
 
 def _decode_setup(q, k, v, g, beta, state_pool, state_indices, scale, gate_lower_bound, qk_l2norm,
-                  beta_logit):
+                  beta_logit, stream):
     """Shape, dtype and device checks shared by decode and decode_verify;
     returns the problem struct."""
     import torch
@@ -426,6 +432,7 @@ def _decode_setup(q, k, v, g, beta, state_pool, state_indices, scale, gate_lower
     dev = q.device
     if dev.type != "cuda":
         raise ValueError("libkda runs on the GPU: tensors must be on a cuda (HIP) device")
+    _check_stream(stream, dev)
     if state_pool.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"state_pool must be float32 or bfloat16, got {state_pool.dtype}")
     for name, t, dt in (("q", q, torch.bfloat16), ("k", k, torch.bfloat16), ("v", v, torch.bfloat16),
@@ -476,7 +483,7 @@ def decode(q, k, v, g, beta, state_pool, state_indices, *, scale: Optional[float
     import torch
 
     prob = _decode_setup(q, k, v, g, beta, state_pool, state_indices, scale, gate_lower_bound,
-                         qk_l2norm, beta_logit)
+                         qk_l2norm, beta_logit, stream)
     given = out
     out = _decode_out(q, v, out, stream)
     dev = q.device
@@ -502,7 +509,7 @@ def decode_verify(q, k, v, g, beta, state_pool, state_indices, *, scale: Optiona
     import torch
 
     prob = _decode_setup(q, k, v, g, beta, state_pool, state_indices, scale, gate_lower_bound,
-                         qk_l2norm, beta_logit)
+                         qk_l2norm, beta_logit, stream)
     given, trace_given = out, state_trace is not None
     out = _decode_out(q, v, out, stream)
     N, T, H, D = q.shape
@@ -536,7 +543,7 @@ def decode_advance(q, k, v, g, beta, state_pool, state_indices, accepted, *,
     import torch
 
     prob = _decode_setup(q, k, v, g, beta, state_pool, state_indices, scale, gate_lower_bound,
-                         qk_l2norm, beta_logit)
+                         qk_l2norm, beta_logit, stream)
     N = q.shape[0]
     dev = q.device
     if accepted.dtype != torch.int32 or tuple(accepted.shape) != (N,) or accepted.device != dev \
@@ -572,6 +579,7 @@ def decode_commit(state_pool, state_indices, state_trace, accepted, *, stream=No
             raise ValueError(f"{name} must be contiguous on {dev}")
     if dev.type != "cuda":
         raise ValueError("libkda runs on the GPU: tensors must be on a cuda (HIP) device")
+    _check_stream(stream, dev)
     if state_pool.dim() != 4 or tuple(state_pool.shape[1:]) != (H, D, D):
         raise ValueError(f"state_pool must be [P, {H}, {D}, {D}]")
     if tuple(state_indices.shape) != (N,) or tuple(accepted.shape) != (N,):

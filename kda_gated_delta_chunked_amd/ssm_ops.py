@@ -15,7 +15,7 @@ from __future__ import annotations
 
 import ctypes
 
-from .ops import STATE_DTYPES, _check, _ptr, load_library
+from .ops import STATE_DTYPES, _check, _check_stream, _ptr, load_library
 
 _i32, _i64, _f32, _P = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
 
@@ -152,10 +152,13 @@ def _check_tensor(name: str, t, dtype, shape, dev, contiguous: bool = True):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _gpu(t):
+def _gpu(t, stream):
     if not t.is_cuda:
         raise ValueError("libkda runs on the GPU: tensors must be on a cuda (HIP) device")
-    return t.device
+    dev = t.device
+    if stream is not None:
+        _check_stream(stream, dev)
+    return dev
 
 
 def _like(x, stream, dtype=None):
@@ -247,7 +250,7 @@ def conv_prefill(x, weight, bias=None, *, cu_seqlens=None, initial_state=None, f
     in place; out must not be x."""
     import torch
 
-    dev = _gpu(x)
+    dev = _gpu(x, stream)
     bf = torch.bfloat16
     lead, N, T = _batch(x, 1, cu_seqlens, "[T, D] or [B, T, D]")
     shape = x.shape
@@ -284,7 +287,7 @@ def conv_decode(x, weight, bias, state_pool, state_indices, *, activation: str =
     overwrites x)."""
     import torch
 
-    dev = _gpu(x)
+    dev = _gpu(x, stream)
     bf = torch.bfloat16
     if x.dim() != 3 or state_pool.dim() != 3:
         raise ValueError("x must be [N, T, D] and state_pool [P, W - 1, D]")
@@ -308,11 +311,11 @@ def conv_decode(x, weight, bias, state_pool, state_indices, *, activation: str =
     return out
 
 
-def _ssm_tokens(x, dt, A, B, C, D, z, dt_bias, out, lead):
+def _ssm_tokens(x, dt, A, B, C, D, z, dt_bias, out, lead, stream):
     """Checks what the scan's two forms share; returns (H, G, P, N)."""
     import torch
 
-    dev = _gpu(x)
+    dev = _gpu(x, stream)
     bf, f32 = torch.bfloat16, torch.float32
     shape = x.shape
     tok, (H, P) = shape[:lead], shape[lead:]
@@ -357,7 +360,7 @@ def ssm_prefill(x, dt, A, B, C, *, D=None, z=None, dt_bias=None, dt_softplus: bo
     import torch
 
     lead, N, T = _batch(x, 2, cu_seqlens, "[T, H, P] or [B, T, H, P]")
-    H, G, P, S = _ssm_tokens(x, dt, A, B, C, D, z, dt_bias, out, lead)
+    H, G, P, S = _ssm_tokens(x, dt, A, B, C, D, z, dt_bias, out, lead, stream)
     dev = x.device
     if state_dtype is None:
         given = initial_state if initial_state is not None else final_state
@@ -405,7 +408,7 @@ def ssm_decode(x, dt, A, B, C, state_pool, state_indices, *, D=None, z=None, dt_
 
     if x.dim() != 4:
         raise ValueError("x must be [N, T, H, P]")
-    H, G, P, S = _ssm_tokens(x, dt, A, B, C, D, z, dt_bias, out, 2)
+    H, G, P, S = _ssm_tokens(x, dt, A, B, C, D, z, dt_bias, out, 2, stream)
     dev = x.device
     N, T = x.shape[:2]
     kind = _state_dtype(state_pool.dtype)
@@ -440,7 +443,7 @@ def add_rmsnorm(x, weight, *, residual=None, eps: float = 1e-6, out_dtype=None, 
     None); scales are [..., 1] or [..., ceil(D / 128)]."""
     import torch
 
-    dev = _gpu(x)
+    dev = _gpu(x, stream)
     bf = torch.bfloat16
     shape = x.shape
     D = shape[-1]
