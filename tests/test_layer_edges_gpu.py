@@ -199,3 +199,42 @@ def test_states_far_from_one(dims, piece, power):
                                piece_tokens=piece)
     R.assert_scan_out(out.cpu().to(R.F64) / far, ref, mag)
     R.assert_state(fin.cpu().to(R.F64) / far, final, smag)
+
+
+# ---------------------------------------------------------------------------
+# offsets that break the contract (their arithmetic is swept on the CPU by
+# test_layer_spans.py)
+
+def guarded(*shape, dtype=BF):
+    """A tensor inside a larger one of sentinels, and a check that they are whole."""
+    n, pad = torch.Size(shape).numel(), 1 << 14
+    wide = torch.full((n + 2 * pad,), 7.0, dtype=dtype, device="cuda")
+
+    def whole():
+        return bool((wide[:pad] == 7.0).all()) and bool((wide[pad + n:] == 7.0).all())
+
+    return wide[pad:pad + n].view(shape), whole
+
+
+@pytest.mark.parametrize("bad", [[-5, 40, 20, 1000], [10, 5, 90, 91], [0, 1 << 30, 3, 90], [90, 90, 90, 90],
+                                 [0, 90, 0, 90], [200, -200, 150, -1], [-(1 << 31), (1 << 31) - 1, 0, 64]], ids=str)
+@pytest.mark.parametrize("cu", [torch.int32, torch.int64])
+def test_bad_offsets_write_inside_the_buffers(bad, cu):
+    k = K()
+    H, G, P, N, T, D = 2, 1, 64, 64, 200, 64
+    g = torch.Generator().manual_seed(141)
+    c = scan_case(g, T, H, G, P, N, z=True, softplus=True, skip=True)
+    a, kw = scan_args(on_gpu(c))
+    off = torch.tensor(bad, dtype=cu).cuda()
+    s0 = rand(g, 3, H, N, P, dtype=torch.float32).cuda()
+    for piece in (0, 64, 128):
+        out, out_whole = guarded(T, H, P)
+        fin, fin_whole = guarded(3, H, N, P, dtype=torch.float32)
+        ws, ws_whole = guarded(((T // 64 + 3) * H * (N * P + 1) + 3) // 4 * 4, dtype=torch.float32)
+        k.ssm_prefill(*a, **kw, cu_seqlens=off, piece_tokens=piece, initial_state=s0, out=out, final_state=fin, workspace=ws)
+        assert out_whole() and fin_whole() and ws_whole()
+    x, w, r0 = rand(g, T, D).cuda(), rand(g, D, 4).cuda(), rand(g, 3, 3, D).cuda()
+    out, out_whole = guarded(T, D)
+    fin, fin_whole = guarded(3, 3, D)
+    k.conv_prefill(x, w, cu_seqlens=off, initial_state=r0, out=out, final_state=fin)
+    assert out_whole() and fin_whole()

@@ -6,6 +6,7 @@ import re
 import shutil
 import subprocess
 
+import numpy as np
 import pytest
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -48,3 +49,74 @@ def test_no_row_of_a_long_sequence_is_left_out(lib):
     # the scan counts with it, from all rows down
     text = open(os.path.join(CSRC, "kda_ssm.hip")).read()
     assert re.findall(r"int rem = (.*?);", text) == ["rows_left(from, to)"]
+
+
+def spans(lib, cu, T, length, N=None):
+    """[slots, 4] of (sequence, span, begin, end); cu None: N equal sequences."""
+    packed = cu is not None
+    N = len(cu) - 1 if packed else N
+    cu = np.ascontiguousarray(cu if packed else [0], np.int64)
+    out = np.full((T // length + N * (1 if packed else T // N // length + 2) + 1, 4), -7, np.int64)
+    lib.kda_test_spans.restype = ctypes.c_int64
+    n = lib.kda_test_spans(ctypes.c_void_p(cu.ctypes.data), int(packed), N, ctypes.c_int64(T), ctypes.c_uint32(length),
+                           ctypes.c_void_p(out.ctypes.data), ctypes.c_int64(len(out)))
+    assert n >= 0
+    joins = np.zeros((N, 2), np.int64)
+    for seq in range(N):
+        lib.kda_test_join_slots(ctypes.c_void_p(cu.ctypes.data), int(packed), N, ctypes.c_int64(T),
+                                ctypes.c_uint32(length), seq, ctypes.c_void_p(joins[seq:].ctypes.data))
+    return out[:n], joins
+
+
+def check_inside(got, joins, N, T, length):
+    """What a workgroup of each slot touches: tokens of its span, the initial and
+    final state of its sequence, its slot and (where pieces follow) the next."""
+    for slot, (seq, k, begin, end) in enumerate(got.tolist()):
+        assert 0 <= seq < N
+        if k < 0:
+            continue
+        first = begin + k * length
+        assert 0 <= begin <= end <= T and (first < end or (k == 0 and begin == end))
+        if end - first > length:
+            assert slot + 1 < len(got)
+    for first, pieces in joins.tolist():
+        assert 0 <= first and first + max(pieces, 1) <= len(got)
+
+
+LENGTHS = [8, 16, 64, 192, 1 << 31]
+
+
+@pytest.mark.parametrize("length", LENGTHS)
+def test_every_token_has_one_span(lib, length):
+    rng = np.random.default_rng(1)
+    for case in range(150):
+        N = int(rng.integers(1, 200)) if case % 3 else int(rng.integers(1, 4))
+        lens = rng.integers(0, rng.choice([2, 9, 70, 500]), N)
+        if case % 3 == 0:
+            lens[:] = lens[0]
+        cu = np.concatenate([[0], np.cumsum(lens)])
+        T = int(cu[-1]) + int(rng.integers(0, 40))
+        equal = case % 3 == 0 and T == cu[-1]
+        for got, joins in [spans(lib, cu, T, length)] + ([spans(lib, None, T, length, N)] if equal else []):
+            check_inside(got, joins, N, T, length)
+            want = [(n, k, int(cu[n]), int(cu[n + 1])) for n in range(N) for k in range(max(1, -(-int(lens[n]) // length)))]
+            assert [tuple(r) for r in got.tolist() if r[1] >= 0] == want
+            for n in range(N):  # a sequence's pieces follow one another where the join looks for them
+                at = [i for i, r in enumerate(got.tolist()) if r[1] >= 0 and r[0] == n]
+                assert at == list(range(joins[n, 0], joins[n, 0] + len(at)))
+
+
+@pytest.mark.parametrize("length", LENGTHS)
+def test_bad_offsets_stay_inside(lib, length):
+    rng = np.random.default_rng(2)
+    for case in range(300):
+        N, T = int(rng.integers(1, 300 if case % 4 == 0 else 12)), int(rng.integers(0, 600))
+        kind = case % 3
+        if kind == 0:    # any order
+            cu = rng.integers(0, T + 1, N + 1)
+        elif kind == 1:  # outside the batch
+            cu = rng.integers(-2 * T - 3, 3 * T + 3, N + 1)
+        else:            # far outside
+            cu = rng.choice([-(1 << 40), -1, 0, T, T + 1, 1 << 31, 1 << 33], N + 1)
+        got, joins = spans(lib, cu, T, length)
+        check_inside(got, joins, N, T, length)
