@@ -238,3 +238,106 @@ def test_bad_offsets_write_inside_the_buffers(bad, cu):
     fin, fin_whole = guarded(3, 3, D)
     k.conv_prefill(x, w, cu_seqlens=off, initial_state=r0, out=out, final_state=fin)
     assert out_whole() and fin_whole()
+
+
+# ---------------------------------------------------------------------------
+# accuracy in the mean, and calls that the other files do not make
+
+@pytest.mark.parametrize("dims", DIMS, ids=str)
+@pytest.mark.parametrize("piece", [0, 64, 256])
+def test_outputs_are_two_roundings_off_in_the_mean(dims, piece):
+    # an output's own rounding and one of each term (of a score or of the state):
+    # independent, each uniform over half a step to either side, 2^-8 of the value
+    # at most, so 2^-8 / sqrt(3) each in the mean square
+    P, N = dims
+    lens, H = [700, 64, 1, 300, 900], 2
+    g = torch.Generator().manual_seed(151)
+    c = scan_case(g, sum(lens), H, 1, P, N, z=True, softplus=True, skip=True)
+    s0 = rand(g, len(lens), H, N, P, dtype=torch.float32)
+    ref, *_ = scan_ref(c, s0, lens)
+    a, kw = scan_args(on_gpu(c))
+    out, _ = K().ssm_prefill(*a, **kw, cu_seqlens=offsets(lens).cuda(), initial_state=s0.cuda(), piece_tokens=piece)
+    rel = ((out.cpu().to(R.F64) - ref).norm() / ref.norm()).item()
+    assert rel <= 2.0 ** 0.5 * R.BF16 / 3.0 ** 0.5, rel
+
+
+@pytest.mark.parametrize("dims", DIMS, ids=str)
+@pytest.mark.parametrize("piece", [0, 64, 192])
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_states_updated_in_place_with_rows_behind_the_last_sequence(dims, piece, dtype):
+    P, N = dims
+    lens, H, tail = [300, 0, 65, 64, 1], 4, 9
+    g = torch.Generator().manual_seed(152)
+    c = scan_case(g, sum(lens), H, 2, P, N, z=True, softplus=True, skip=False)
+    s0 = rand(g, len(lens), H, N, P, dtype=dtype)
+    ref, final, mag, smag = scan_ref(c, s0, lens)
+    for k in ("x", "B", "C", "z", "dt"):
+        c[k] = torch.cat([c[k], torch.full((tail, *c[k].shape[1:]), float("nan"), dtype=c[k].dtype)])
+    a, kw = scan_args(on_gpu(c, True))
+    state = s0.cuda()
+    out = torch.full((sum(lens) + tail, H, P), 7.0, dtype=BF, device="cuda")
+    _, fin = K().ssm_prefill(*a, **kw, cu_seqlens=offsets(lens).cuda(), initial_state=state, final_state=state, out=out,
+                             piece_tokens=piece)
+    assert fin is state and (out[sum(lens):] == 7.0).all()
+    R.assert_scan_out(out[:sum(lens)].cpu(), ref, mag)
+    R.assert_state(fin.cpu(), final, smag)
+    assert torch.equal(fin[1].cpu(), s0[1])
+
+
+@pytest.mark.parametrize("T", [1, 4, 7])
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_ssm_decode_may_overwrite_its_input(T, dtype):
+    k = K()
+    H, P, N, reqs = 4, 128, 64, 3
+    g = torch.Generator().manual_seed(153)
+    c = on_gpu(scan_case(g, reqs * T, H, 2, P, N, z=True, softplus=True, skip=True))
+    c = {n: v.unflatten(0, (reqs, T)) if n in ("x", "B", "C", "z", "dt") else v for n, v in c.items()}
+    a, kw = scan_args(c)
+    pool = rand(g, reqs, H, N, P, dtype=dtype)
+    idx = torch.tensor([2, -1, 0], dtype=torch.int32).cuda()
+    p1, p2 = pool.cuda(), pool.cuda()
+    want = k.ssm_decode(*a, p1, idx, **kw)
+    x = a[0].clone()
+    got = k.ssm_decode(x, *a[1:], p2, idx, **kw, out=x)
+    assert got is x and torch.equal(got, want) and torch.equal(p1, p2)
+    wide = torch.zeros(reqs, T, H * P + 16, dtype=BF, device="cuda")
+    x = wide[..., 8:8 + H * P].unflatten(-1, (H, P))  # rows of a wider buffer
+    x.copy_(a[0])
+    k.ssm_decode(x, *a[1:], pool.cuda(), idx, **kw, out=x)
+    assert torch.equal(x, want) and not wide[..., :8].any() and not wide[..., -8:].any()
+
+
+def test_empty_fixed_batches_and_single_rows():
+    k = K()
+    s0 = torch.randn(2, 2, 64, 64, device="cuda")
+    e = lambda *s, dtype=BF: torch.zeros(s, dtype=dtype, device="cuda")
+    out, fin = k.ssm_prefill(e(2, 0, 2, 64), e(2, 0, 2, dtype=torch.float32), e(2, dtype=torch.float32),
+                             e(2, 0, 1, 64), e(2, 0, 1, 64), initial_state=s0)
+    assert out.shape == (2, 0, 2, 64) and torch.equal(fin, s0)
+    r0 = torch.randn(2, 3, 16, device="cuda").to(BF)
+    out, fin = k.conv_prefill(e(2, 0, 16), e(16, 4), initial_state=r0)
+    assert out.shape == (2, 0, 16) and torch.equal(fin, r0)
+    g = torch.Generator().manual_seed(154)
+    x, w = rand(g, 264), rand(g, 264)
+    y, _, s = k.add_rmsnorm(x.cuda(), w.cuda(), out_dtype=torch.float8_e4m3fn, scale_group=128)
+    assert y.shape == (264,) and s.shape == (3,)
+    R.assert_norm(y.cpu()[None], s.cpu()[None], R.norm(x[None], None, w, 1e-6)[0], 128)
+
+
+def test_q_k_and_v_from_columns_of_one_projection():
+    # three convolutions of a row's columns give the packed tensors that the
+    # recurrence takes, bit for bit those of one convolution over the whole row
+    k = K()
+    H, D, T = 2, 128, 150
+    g = torch.Generator().manual_seed(155)
+    u, w = rand(g, T, 3 * H * D + 8).cuda(), rand(g, 3 * H * D, 4, scale=0.4).cuda()
+    whole, _ = k.conv_prefill(u[:, :3 * H * D], w)
+    parts = []
+    for i in range(3):
+        cols = slice(i * H * D, (i + 1) * H * D)
+        y, _ = k.conv_prefill(u[:, cols], w[cols])
+        assert y.is_contiguous() and torch.equal(y, whole[:, cols])
+        parts.append(y.unflatten(-1, (H, D)))
+    decay, beta = torch.full((T, H, D), -0.1, device="cuda"), torch.full((T, H), 0.5, device="cuda")
+    out, _ = k.prefill(*parts, decay, beta, qk_l2norm=True)
+    assert out.shape == (T, H, D) and torch.isfinite(out).all()
