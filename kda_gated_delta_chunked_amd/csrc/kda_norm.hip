@@ -2,7 +2,10 @@
 // output, for gfx950 (MI355X).
 //
 //   s = x + residual,  y = s / sqrt(mean(s^2) + eps) w,  residual_out = bf16(s)
-//   out = bf16(y), or e4m3(y / scale) with scale = max(max |y| / 448, 2^-126)
+//   out = bf16(y), or e4m3(y (1 / scale)) with scale = max(max |y| / 448, 2^-126)
+// (a division per element would add to the vector units' 69 % of the time; the
+// product is within two roundings of fp32 of y / scale, so it may round to the
+// other code only where y / scale is that near the middle between two)
 //
 // LANES lanes per row, each with C pieces of eight columns that stay in
 // registers as fp32 between the sum of squares and the output, so the row is

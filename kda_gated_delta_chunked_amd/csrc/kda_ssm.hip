@@ -34,18 +34,23 @@
 // a second joins these into the states ahead of each piece, and a third runs
 // all pieces side by side from them.
 //
-// What bounds it (MI355X, H12, 128 x 128): the instructions that a chunk issues.
-// A wave of the full pass issues 26 (34 in a sequence's last piece) products
-// of 32 x 32 x 16, four of 16 x 16 x 32 and about 290 vector instructions, 130
-// more with a gate, and one product hides about four vector instructions, from
-// whichever wave of its SIMD.  So a CU finishes a chunk of four waves every 1.9
-// us with one workgroup on it, 1.6 with two and 1.5 with three (2.3, 2.1 and 1.9
-// with a gate): more waves gain little, and so did a third buffer, another order
-// of the waves' priorities, and chunks of 64 tokens (339 against 307 us for B8
-// T8192 at the time).  What did cost was a register reloaded from scratch behind
-// the copies, which waits for them: 32 ragged prompts 364 against 352 us.  The
-// three launches: B8 T8192 78 + 14 + 130 us with pieces of 1024 tokens (3.2 to
-// 4.2 TB/s); B1 T8192, gated, 20 + 13 + 34; the ragged prompts 108 + 27 + 217.
+// What bounds it (MI355X, H12, 128 x 128).  A wave of the full pass issues 26 (34
+// in a sequence's last piece) products of 32 x 32 x 16, four of 16 x 16 x 32 and
+// about 310 vector instructions a chunk, 140 more with a gate.  A CU finishes a
+// chunk of four waves every 1.9 us with one workgroup on it, 1.6 with two and
+// 1.5 with three (2.3, 2.1 and 1.9 with a gate).  With three, the vector units
+// are active 55 % of the time (the products' issue included), the matrix units
+// 35 %; of a wave's own time 32 % goes to executing, 36 % to waiting for its turn
+// to issue and 33 % to waiting for data and at the chunk's two barriers, so
+// neither unit bounds it alone.  B1 T8192, one or two workgroups on a CU: 38 %,
+// 16 %; 41, 22 and 38.  A third buffer, another order of the waves' priorities,
+// and chunks of 64 tokens (339 against 307 us for B8 T8192 at the time) gained
+// little or lost.  The 128-row variants with outputs spill scalar registers and
+// a few vector ones; a vector register reloaded from scratch behind the copies
+// waits for them (32 ragged prompts 364 against 352 us with such a reload every
+// chunk; heads of 64 keep one every two chunks, behind the stores).
+// The three launches: B8 T8192 78 + 14 + 130 us with pieces of 1024 tokens (3.2
+// to 4.2 TB/s); B1 T8192, gated, 20 + 13 + 34; the ragged prompts 111 + 27 + 222.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -294,7 +299,7 @@ __device__ __forceinline__ bf16x8 finite_only(const bf16x8& f) {
 
 // The decays of 64 (token, head) pairs: two chunks of one head, or a chunk of
 // two heads.  c_t is taken from the chunk's first token, in fp32: its error,
-// 2^-24 of the sum, is 2^-12 at most (32 logarithms of -256) and matters least
+// 2^-24 of the sum, is 2^-11 at most (32 logarithms of -256) and matters least
 // where the decays, and so the sums, are large.
 // The state is held scaled: it is the accumulators times 2^lf, lf going down from
 // kScale with the chunks' decays, until it would fall below zero: then the
@@ -325,8 +330,9 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 
 // One piece (or a whole sequence) and HPW heads of a group.  FULL: with
 // outputs; else the state that a piece's own tokens add.  PARTS: of x w.  The
-// chunk loop's memory accesses are the same on every path, so that waiting for
-// the next chunk's rows never waits for this one's stores.  Two buffers for B
+// chunk loop's memory accesses are the same on every path, so that the wait for
+// the next chunk's rows is a count that leaves this one's stores out (registers
+// that the compiler reloads from scratch wait for more).  Two buffers for B
 // and x, objects of their own: the copies in flight to one are then known not to
 // touch what is read from the other.  C is last read ahead of the chunk's second
 // barrier and copied behind it, to one buffer, so that three workgroups fit a CU.

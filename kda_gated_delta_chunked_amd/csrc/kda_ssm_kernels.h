@@ -42,8 +42,9 @@ __device__ __forceinline__ float silu(float v) { return v * __builtin_amdgcn_rcp
 constexpr int64_t kMaxThreads = 0xffffffffLL;
 inline int64_t conv_blocks(int64_t D) { return (D + 511) / 512; }  // waves per row
 // Spans of 16 tokens, of 8 where that leaves few waves: the W - 1 rows ahead
-// of each span are read twice, mostly from a cache, and short spans keep more
-// rows in flight.  us on one MI355X at spans of 8 / 16 / 32 / 64 tokens: B8
+// of each span are read twice, the second time from behind L2 too (neighbouring
+// spans go to different XCDs: 718 MB fetched for the 604 of B8 T8192 D4608), and
+// short spans keep more rows in flight.  us on one MI355X at spans of 8 / 16 / 32 / 64 tokens: B8
 // T8192 D4608 261 / 242 / 237 / 253 (at 16 from 216 to 242 on different cards:
 // 5.6 to 5.0 TB/s of its bytes), six ragged prompts D1792 16.0 / 16.9 / 20.1 /
 // 22.3, T2048 D4608 10.8 / 12.0 / 12.9 / 20.6, T300 D1536 4.6 / 6.5 / 10.2 / 17.8.

@@ -247,7 +247,8 @@ def conv_prefill(x, weight, bias=None, *, cu_seqlens=None, initial_state=None, f
     zeros).  activation: "silu" or "none".  Returns (out, final_state);
     final_state is the last W - 1 rows of each sequence, its state included,
     and None with output_final_state=False.  final_state=initial_state updates
-    in place; out must not be x."""
+    in place; out must not be x.  (For ``prefill``, whose q, k and v are packed: a
+    call for each one's columns of a projection's row gives packed results.)"""
     import torch
 
     dev = _gpu(x, stream)
