@@ -125,7 +125,8 @@ kda_status kda_conv_decode(const kda_conv_decode_problem* p, const uint16_t* x, 
  * Range.  step x has to be finite in fp32.  An infinity or a NaN in x stays in
  * its column of its head: that column's state, and its outputs from the token on,
  * are infinite or NaN (which of them is not specified), everything else is as
- * if it were not there.
+ * if it were not there.  A prompt's states may come near the largest float;
+ * elements below 2^-106 are kept to 2^-129.
  *
  * States are fp32, or bf16 (state_dtype): widened on load, carried in fp32,
  * rounded to nearest even once on store.  x, B and C may be columns of one
