@@ -341,3 +341,28 @@ def test_q_k_and_v_from_columns_of_one_projection():
     decay, beta = torch.full((T, H, D), -0.1, device="cuda"), torch.full((T, H), 0.5, device="cuda")
     out, _ = k.prefill(*parts, decay, beta, qk_l2norm=True)
     assert out.shape == (T, H, D) and torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("name", ["conv", "scan", "norm"])
+def test_a_given_stream_inside_a_capture(name):
+    # forked from the captured stream and joined to it again; results and
+    # workspaces come out of the graph's pool
+    calls, _ = stream_calls(113)
+    (x, other), call = calls[name]
+    want = {i: [t.clone() for t in as_bytes(call(None, v))] for i, v in enumerate((x, other))}
+    graph, side, into = torch.cuda.CUDAGraph(), torch.cuda.Stream(), x.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = call(side, into)
+        torch.cuda.current_stream().wait_stream(side)
+    for i in (1, 0, 1, 0):
+        into.copy_((x, other)[i])
+        for t in got:
+            t.view(torch.uint8).fill_(0x55)
+        junk = [torch.full((1 << 20,), float("nan"), device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        del junk
+        assert all(torch.equal(a, b) for a, b in zip(as_bytes(got), want[i]))
