@@ -8,9 +8,13 @@ keeping the state of the accepted prefix.  Around a recurrent-state layer
 (include/kda_ssm.h): ``conv_prefill`` and ``conv_decode``, the short causal
 convolution; ``ssm_prefill`` and ``ssm_decode``, the selective state space
 scan; ``add_rmsnorm``, the residual RMS norm with an optional 8-bit output.
+The submodule ``attn`` (include/kda_attn.h) has the softmax attention of the
+layers between recurrent ones: ``attn.prefill`` over prompts, ``attn.decode``
+over a paged cache, ``attn.store`` and ``attn.assign_pages``, which fill it.
 ``synth`` draws the
 seeded synthetic workloads used by the tests and the benchmark.
 """
+from . import attn
 from .ops import (DecodeProblem, KDAError, Problem, decode, decode_advance, decode_advance_raw,
                   decode_commit, decode_commit_raw, decode_raw, decode_validate_raw, decode_verify,
                   decode_verify_raw,
@@ -28,4 +32,4 @@ __all__ = ["DecodeProblem", "KDAError", "Problem", "decode", "decode_advance", "
            "validate_raw", "workspace_size",
            "ConvDecodeProblem", "ConvProblem", "NormProblem", "SsmDecodeProblem", "SsmProblem",
            "add_rmsnorm", "conv_decode", "conv_prefill", "ssm_decode", "ssm_plan", "ssm_prefill",
-           "ssm_workspace_size"]
+           "ssm_workspace_size", "attn"]

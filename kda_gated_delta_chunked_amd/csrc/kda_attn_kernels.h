@@ -1,0 +1,94 @@
+// kda_attn_kernels.h -- launch interface between the C ABI layer of
+// include/kda_attn.h and its HIP kernels, and what the kernels share (internal;
+// not installed).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kda_ssm_kernels.h"
+
+namespace kda {
+
+constexpr int kAttnRows = 128;  // query rows of a workgroup of the prefill
+
+struct AttnArgs {
+  Packing pk;
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  uint16_t* out;
+  float* lse;             // [T_total, H] or NULL
+  int H, KV, D;
+  float scale;
+  int64_t slots;          // span_slots of kAttnRows tokens
+  int64_t q_stride, k_stride, v_stride, out_stride;
+};
+hipError_t launch_attn(const AttnArgs& a, hipStream_t stream);
+
+struct PagedCache {
+  void* k;
+  void* v;
+  const float* k_scale;   // [KV]; NULL: bf16 elements, else e4m3 codes
+  const float* v_scale;
+  int KV, D;
+  int page_shift;
+  int64_t pages;
+  int64_t k_page, k_token, v_page, v_token;  // strides, elements
+};
+
+struct AttnDecodeArgs {
+  PagedCache c;
+  const uint16_t* q;
+  const int32_t* table;
+  const int32_t* rows;    // or NULL
+  const int32_t* lens;
+  const uint64_t* tree;   // or NULL
+  uint16_t* out;
+  float* lse;             // [N * T, H] or NULL
+  int N, T, H;
+  int64_t table_rows;
+  int table_width;
+  int64_t tree_stride;    // 0 or T
+  float scale;
+  int64_t q_stride, out_stride;
+  int parts;              // a context's parts at most
+  float* part_out;        // [N, KV, parts, T H / KV, D], sums not divided yet; NULL with one part
+  float* part_ml;         // the same with two for D: maximum, sum
+};
+hipError_t launch_attn_decode(const AttnDecodeArgs& a, hipStream_t stream);
+
+struct KvStoreArgs {
+  PagedCache c;
+  const uint16_t* k;
+  const uint16_t* v;
+  const int64_t* slots;
+  int64_t T, k_stride, v_stride;
+};
+hipError_t launch_kv_store(const KvStoreArgs& a, hipStream_t stream);
+
+struct KvAssignArgs {
+  Packing pk;
+  const int32_t* lens;
+  const int32_t* rows;    // or NULL
+  int32_t* table;
+  const int32_t* free_pages;
+  const int32_t* free_head;
+  int64_t* slots;
+  int32_t* lens_out;
+  int32_t* head_out;
+  int page_shift, table_width;
+  int64_t table_rows, num_free;
+};
+hipError_t launch_kv_assign(const KvAssignArgs& a, hipStream_t stream);
+
+// Sizes of launches, for the launch and its check.
+inline int64_t attn_blocks(int64_t slots, int64_t H) { return slots * H; }
+inline int64_t attn_decode_row_blocks(int64_t T, int64_t G) { return (T * G + 31) / 32; }
+inline int64_t attn_decode_blocks(int64_t N, int64_t KV, int64_t T, int64_t G, int64_t parts) {
+  return N * KV * attn_decode_row_blocks(T, G) * parts;
+}
+inline int64_t kv_store_threads(int64_t T, int64_t KV, int64_t D) { return (T * KV * (D / 8) + 255) / 256 * 256; }
+constexpr int kAssignTokens = 1024;  // new tokens of a workgroup
+inline int64_t kv_assign_blocks(int64_t T) { return T ? (T + kAssignTokens - 1) / kAssignTokens : 1; }
+
+}  // namespace kda

@@ -180,7 +180,7 @@ def _new(x, stream, shape, dtype):
         return x.new_empty(shape, dtype=dtype)
 
 
-def _launch(name: str, dev, stream, problem, args, mine=()):
+def _launch(name: str, dev, stream, problem, args, mine=(), call=call_raw):
     """Enqueue on `stream` (None: the current one).  Buffers of the binding's own
     come out of that stream's part of torch's allocator: from the current stream's
     a block could be one that work queued there still uses.  Results (`mine`) are
@@ -191,10 +191,10 @@ def _launch(name: str, dev, stream, problem, args, mine=()):
     current = torch._C._cuda_getCurrentRawStream(dev.index)
     raw = current if stream is None else stream.cuda_stream
     if torch._C._cuda_getDevice() == dev.index:
-        status = call_raw(name, problem, *args, raw)
+        status = call(name, problem, *args, raw)
     else:
         with torch.cuda.device(dev):
-            status = call_raw(name, problem, *args, raw)
+            status = call(name, problem, *args, raw)
     if raw != current:
         here = torch.cuda.current_stream(dev)
         for t in mine:
