@@ -123,10 +123,10 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
   const int row = min(32 * block + (lane & 31), rows - 1);
   const int t = row / G;
   const int64_t q_row = (int64_t)n * a.T + t;
-  AttnRows<D> r;
+  AttnRows<D, 1> r;
   r.start();
   if (begin < end) {
-    r.load(a.q + q_row * a.q_stride + (kv * G + row % G) * D);
+    r.load(0, a.q + q_row * a.q_stride + (kv * G + row % G) * D);
     const uint64_t sees = a.tree ? a.tree[n * a.tree_stride + t] : ~0ull >> (63 - t);
     const Pages pages{a.table + (int64_t)req.row * a.table_width, a.c.page_shift, a.c.pages,
                       (int64_t)a.table_width << a.c.page_shift};
@@ -138,37 +138,59 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
     uint8_t *ktile = tiles[wave][0], *vtile = tiles[wave][1];
     Flight<D, E4M3> kf, vf;
     int page0 = -1, page1 = -1;  // of the tile in flight
-    auto fetch = [&](int pos) {
+    // finds the pages of a tile; bits tell which of its positions have one
+    auto set_pages = [&](int pos) {
       page0 = __builtin_amdgcn_readfirstlane(pos < end ? pages.page(pos) : -1);
       page1 = __builtin_amdgcn_readfirstlane(pos + 16 < end ? pages.page(pos + 16) : -1);
+      return (page0 >= 0 ? 0xffffu : 0u) | (page1 >= 0 ? 0xffff0000u : 0u);
+    };
+    auto fetch = [&](int pos) {
+      const uint32_t there = set_pages(pos);
       kf.load(kbase, a.c.k_page * size, a.c.k_token * size, pos, in_page, end - pos, page0, page1);
       vf.load(vbase, a.c.v_page * size, a.c.v_token * size, pos, in_page, end - pos, page0, page1);
+      return there;
     };
-    fetch(begin + wave * KEYS);
+    auto plain = [&](uint32_t there, int pos) { return pos + KEYS <= req.before && pos + KEYS <= end && there == ~0u; };
+    auto sees_key = [&](uint32_t there, int pos, int key) {
+      const int x = pos + key, own = x - req.before;
+      return (there >> key & 1) && x < end && (own < 0 || (own < a.T && (sees >> own & 1)));
+    };
+    bool not_finite = false;  // left out of a tile with masked rows
+    uint32_t next = fetch(begin + wave * KEYS);
     for (int pos = begin + wave * KEYS; pos < end; pos += STEP) {
-      const uint32_t there = (page0 >= 0 ? 0xffffu : 0u) | (page1 >= 0 ? 0xffff0000u : 0u);
+      const uint32_t there = next;
       wave_order();
       kf.store(ktile);
       vf.store(vtile);
       wave_order();
-      fetch(pos + STEP);
-      f32x16 s = r.scores(at, ktile, 0);
-      if (pos + KEYS <= req.before && pos + KEYS <= end && there == ~0u) {
-        r.weigh(s, c);
-        r.add(at, vtile, 0, s);
+      next = fetch(pos + STEP);
+      f32x16 s[1];
+      bf16x8 p[1][2];
+      r.scores(at, ktile, s);
+      if (plain(there, pos)) {
+        r.weigh(s, c, p);
+        r.add(at, vtile, p);
       } else {
-        uint32_t seen = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int key = key_of(i, h), x = pos + key, own = x - req.before;
-          const bool ok = (there >> key & 1) && x < end && (own < 0 || (own < a.T && (sees >> own & 1)));
-          seen |= (uint32_t)ok << i;
-          if (!ok) s[i] = kNone;
-        }
-        r.weigh(s, c);
-        r.add_masked(at, vtile, 0, s, seen);
+        for (int i = 0; i < 16; ++i)
+          if (!sees_key(there, pos, key_of(i, h))) s[0][i] = kNone;
+        r.weigh(s, c, p);
+        not_finite = r.add_masked(at, vtile, p) || not_finite;
       }
     }
+    if (__builtin_expect(not_finite, 0))
+      for (int pos = begin + wave * KEYS; pos < end; pos += STEP) {
+        const uint32_t there = set_pages(pos);
+        if (plain(there, pos)) continue;
+        for (int key = 0; key < KEYS; ++key) {
+          if (pos + key >= end || !(there >> key & 1)) continue;
+          const uint8_t* v = vbase + (key < 16 ? page0 : page1) * a.c.v_page * size + ((pos + key) & in_page) * a.c.v_token * size;
+          r.add_not_finite(0, sees_key(there, pos, key), [&](int d) {
+            if constexpr (E4M3) return __builtin_amdgcn_cvt_f32_fp8((int)v[d], 0);
+            else return bf16_f32(reinterpret_cast<const uint16_t*>(v)[d]);
+          });
+        }
+      }
   }
 
   // the waves' shares, joined through their tiles: O as [D][32 rows]
@@ -177,10 +199,10 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
 #pragma unroll
   for (int b = 0; b < D / 32; ++b)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) mine[(32 * b + key_of(i, h)) * 32 + (lane & 31)] = r.o[b][i];
-  const float total = r.total();
+    for (int i = 0; i < 16; ++i) mine[(32 * b + key_of(i, h)) * 32 + (lane & 31)] = r.o[0][b][i];
+  const float total = r.total(0);
   if (h == 0) {
-    stats[wave][0][lane] = r.m;
+    stats[wave][0][lane] = r.m[0];
     stats[wave][1][lane] = total;
   }
   tiles_barrier();

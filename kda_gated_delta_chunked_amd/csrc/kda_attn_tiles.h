@@ -40,8 +40,16 @@ __device__ __forceinline__ int attn_tile_at(int row, int chunk) {
 // The key of register i in half h of the wave.
 __device__ __forceinline__ int key_of(int i, int h) { return 8 * (i >> 2) + 4 * h + (i & 3); }
 
-// Places of a lane's operands in a tile: a row of keys (chunk h), and for the
-// transposed reads of values a row 4 h + m / 4 of four, in a group of 16 lanes m.
+// Keeps the compiler from holding everything derived from a value in registers
+// across a loop.
+__device__ __forceinline__ int forget(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// A lane's operands in a tile of a buffer of tiles (their distances multiples of
+// 256 bytes): rows of keys (chunk h), and for the transposed reads of values a
+// row 4 h + m / 4 of four, in a group of 16 lanes m.
 template <int D>
 struct TilePlaces {
   int row, col;
@@ -50,15 +58,18 @@ struct TilePlaces {
     row = attn_tile_at<D>(lane & 31, h);
     col = attn_tile_at<D>(4 * h + (m >> 2), 2 * g + ((m & 3) >> 1)) + (m & 1) * 8;
   }
-  // keys 32 block .. + 31, columns 16 step + 8 h .. + 7
-  __device__ __forceinline__ bf16x8 keys(const uint8_t* tile, int block, int step) const {
-    return *reinterpret_cast<const bf16x8*>(tile + block * 64 * D + (row ^ (step * 32)));
+  // the tile at `keys` and `values` bytes
+  __device__ __forceinline__ TilePlaces(const TilePlaces& at, int keys, int values)
+      : row(forget(at.row + keys)), col(forget(at.col + values)) {}
+  // columns 16 step + 8 h .. + 7 of the lane's key
+  __device__ __forceinline__ bf16x8 keys(const uint8_t* tiles, int step) const {
+    return *reinterpret_cast<const bf16x8*>(tiles + (row ^ (step * 32)));
   }
   // column 32 block + lane % 32, keys 16 step + 4 h + (0..3) and 8 more
-  __device__ __forceinline__ bf16x8 values(const uint8_t* tile, int block, int step) const {
+  __device__ __forceinline__ bf16x8 values(const uint8_t* tiles, int block, int step) const {
     typedef __attribute__((address_space(3))) s16x4* lds_ptr;
     const int at = col ^ (block * 64);
-    const uint8_t* t = tile + step * 32 * D;
+    const uint8_t* t = tiles + step * 32 * D;
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(t + at));
     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(t + 16 * D + (at ^ 32)));
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -77,13 +88,6 @@ __device__ __forceinline__ void tiles_barrier() {
 // what the other half of the wave holds for the same query row
 __device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32, 64); }
 
-// Registers 8 step .. + 7 of the weights as an operand.
-__device__ __forceinline__ bf16x8 weights_frag(const f32x16& p, int step) {
-  const int i = 8 * step;
-  return __builtin_bit_cast(bf16x8, make_uint4(bf16_pair(p[i], p[i + 1]), bf16_pair(p[i + 2], p[i + 3]),
-                                               bf16_pair(p[i + 4], p[i + 5]), bf16_pair(p[i + 6], p[i + 7])));
-}
-
 // Whether a fragment holds an infinity or a NaN (per lane).
 __device__ __forceinline__ bool not_finite(const bf16x8& f) {
   const uint4 u = __builtin_bit_cast(uint4, f);
@@ -94,145 +98,179 @@ __device__ __forceinline__ bool not_finite(const bf16x8& f) {
     bad = bad || (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
   return bad;
 }
-
-// Values that a row must not see are multiplied by weights of zero, which an
-// infinity or a NaN outlives.  Where a tile with masked rows holds any, its
-// finite values are added as usual, and a second product counts for every output which
-// kinds of others its row sees: a +inf counts 1, a -inf 2^8, a NaN 2^16 (at most 64
-// keys a tile: the counts stay apart, and exact in fp32).
-struct NotFinite {
-  bf16x8 finite, kinds;
-  __device__ __forceinline__ explicit NotFinite(const bf16x8& f) {
-    const uint4 u = __builtin_bit_cast(uint4, f);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    uint32_t fin[4], kin[4];
+// The fragment with zeros in the place of infinities and NaNs.
+__device__ __forceinline__ bf16x8 finite_only(const bf16x8& f) {
+  const uint4 u = __builtin_bit_cast(uint4, f);
+  uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      fin[i] = kin[i] = 0;
-#pragma unroll
-      for (int s = 0; s < 32; s += 16) {
-        const uint32_t e = (w[i] >> s) & 0xffffu;
-        const bool bad = (e & 0x7f80u) == 0x7f80u;
-        const uint32_t kind = (e & 0x7fu) ? 0x4780u : (e & 0x8000u) ? 0x4380u : 0x3f80u;  // 2^16, 2^8, 1
-        fin[i] |= (bad ? 0u : e) << s;
-        kin[i] |= (bad ? kind : 0u) << s;
-      }
-    }
-    finite = __builtin_bit_cast(bf16x8, make_uint4(fin[0], fin[1], fin[2], fin[3]));
-    kinds = __builtin_bit_cast(bf16x8, make_uint4(kin[0], kin[1], kin[2], kin[3]));
+  for (int i = 0; i < 4; ++i) {
+    if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
+    if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu;
   }
-  // what the counts add to an output
-  static __device__ __forceinline__ float added(float counts) {
-    const int n = (int)counts;
-    const float inf = __builtin_huge_valf();
-    float v = 0.f;
-    if (n & 0xff) v += inf;
-    if (n & 0xff00) v -= inf;
-    if (n >> 16) v = __builtin_nanf("");
-    return v;
-  }
-};
+  return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
+}
 
-// The softmax's state of a wave's rows, and their outputs so far.  m is the
-// maximum of the scores (of q . k, not scaled), l the sum of exp(c (s - m) ln 2) over this half's
-// keys, c = scale log2(e) > 0.
-template <int D>
+// The softmax's state of a wave's RB x 32 rows, and their outputs so far.  With c =
+// scale log2(e) > 0, weights are 2^(c (s - m)) for scores s = q . k; l is the sum of this half's,
+// o that of the weighted values.
+//
+// m follows the maximum of a row's scores at a distance: weights are taken
+// with the m that is there, and their sum over a block of keys tells whether one has
+// grown too far (or m is still that of no key).  Only then the scores' maximum is
+// looked for, and what has been summed is brought to it: a weight is at most kFar, which costs
+// no accuracy (sums are floating point), and most blocks need no maximum.
+template <int D, int RB>
 struct AttnRows {
-  bf16x8 q[D / 16];
-  f32x16 o[D / 32];
-  float m, l;
+  static constexpr float kFar = 4096.f;
+  bf16x8 q[RB][D / 16];
+  f32x16 o[RB][D / 32];
+  float m[RB], l[RB];
 
   __device__ __forceinline__ void start() {
-    m = kNone;
-    l = 0.f;
 #pragma unroll
-    for (int b = 0; b < D / 32; ++b)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[b][i] = 0.f;
-  }
-  // the lane's row of queries
-  __device__ __forceinline__ void load(const uint16_t* row) {
-    const int h = (threadIdx.x >> 5) & 1;
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s)
-      q[s] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(row + s * 16 + h * 8));
-  }
-  __device__ __forceinline__ f32x16 scores(const TilePlaces<D>& at, const uint8_t* tile, int block) const {
-    f32x16 s;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] = 0.f;
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) s = mfma32(at.keys(tile, block, k), q[k], s);
-    return s;
-  }
-  // Scores of 32 keys become weights; the state takes them in.
-  __device__ __forceinline__ void weigh(f32x16& s, float c) {
-    float top = s[0];
-#pragma unroll
-    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
-    top = fmaxf(top, other_half(top));
-    if (__any(top > m)) {
-      const float now = fmaxf(top, m), keep = now == kNone ? 1.f : __builtin_amdgcn_exp2f((m - now) * c);
-      m = now;
-      l *= keep;
+    for (int r = 0; r < RB; ++r) {
+      m[r] = kNone;
+      l[r] = 0.f;
 #pragma unroll
       for (int b = 0; b < D / 32; ++b)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[b][i] *= keep;
+        for (int i = 0; i < 16; ++i) o[r][b][i] = 0.f;
     }
-    const float mc = m == kNone ? 0.f : m * c;
+  }
+  // the lane's row of queries of block r
+  __device__ __forceinline__ void load(int r, const uint16_t* row) {
+    const int h = (threadIdx.x >> 5) & 1;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s)
+      q[r][s] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(row + s * 16 + h * 8));
+  }
+  // scores of a tile's 32 keys
+  __device__ __forceinline__ void scores(const TilePlaces<D>& at, const uint8_t* tile, f32x16 (&s)[RB]) const {
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[r][i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      const bf16x8 f = at.keys(tile, k);
+#pragma unroll
+      for (int r = 0; r < RB; ++r) s[r] = mfma32(f, q[r][k], s[r]);
+    }
+  }
+  // The scores of keys behind a row's own become none; rows from `top` on, keys from `key` on.
+  __device__ __forceinline__ void mask(f32x16 (&s)[RB], int key, int top) const {
+    const int lane = forget(threadIdx.x & 63);
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (key + key_of(i, lane >> 5) > top + 32 * r + (lane & 31)) s[r][i] = kNone;
+  }
+  // weights of scores from a maximum, as operands, and their sum
+  static __device__ __forceinline__ float weights(const f32x16& s, float c, float mc, bf16x8 (&p)[2]) {
+    float e[16], sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      s[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -mc));
-      l += s[i];
+      e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -mc));
+      sum[i & 1] += e[i];
     }
-  }
-  // o += V^T P^T for the tile's 32 keys from 32 block on
-  __device__ __forceinline__ void add(const TilePlaces<D>& at, const uint8_t* tile, int block, const f32x16& p) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const bf16x8 w = weights_frag(p, k);
+      const float* f = e + 8 * k;
+      p[k] = __builtin_bit_cast(bf16x8, make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]),
+                                                   bf16_pair(f[6], f[7])));
+    }
+    return sum[0] + sum[1];
+  }
+  // Weights of the scores of 32 keys and their sums; whether a sum went too far.
+  __device__ __forceinline__ bool try_weights(const f32x16 (&s)[RB], float c, bf16x8 (&p)[RB][2], float (&sum)[RB]) const {
+    bool far = false;
 #pragma unroll
-      for (int b = 0; b < D / 32; ++b) o[b] = mfma32(at.values(tile, b, 2 * block + k), w, o[b]);
+    for (int r = 0; r < RB; ++r) {
+      sum[r] = weights(s[r], c, m[r] * c, p[r]);
+      far = far || !(sum[r] <= kFar);
+    }
+    return __any(far);
+  }
+  // The same from the scores' maximum, to which the state is brought.
+  __device__ __forceinline__ void weights_from_maximum(const f32x16 (&s)[RB], float c, bf16x8 (&p)[RB][2], float (&sum)[RB]) {
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      float top = s[r][0];
+#pragma unroll
+      for (int i = 1; i < 16; ++i) top = fmaxf(top, s[r][i]);
+      top = fmaxf(top, other_half(top));
+      const float now = fmaxf(top, m[r]), keep = now == kNone ? 1.f : __builtin_amdgcn_exp2f((m[r] - now) * c);
+      m[r] = now;
+      l[r] *= keep;
+#pragma unroll
+      for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[r][b][i] *= keep;
+      sum[r] = weights(s[r], c, now == kNone ? 0.f : now * c, p[r]);
     }
   }
-  // The same where rows see different keys: bit i of `seen` tells whether the
-  // lane's row sees the key of register i.
-  __device__ __forceinline__ void add_masked(const TilePlaces<D>& at, const uint8_t* tile, int block, const f32x16& p,
-                                             uint32_t seen) {
+  __device__ __forceinline__ void take(const float (&sum)[RB]) {
+#pragma unroll
+    for (int r = 0; r < RB; ++r) l[r] += sum[r];
+  }
+  // Scores of 32 keys become weights; the state takes them in.
+  __device__ __forceinline__ void weigh(const f32x16 (&s)[RB], float c, bf16x8 (&p)[RB][2]) {
+    float sum[RB];
+    if (__builtin_expect(try_weights(s, c, p, sum), 0)) weights_from_maximum(s, c, p, sum);
+    take(sum);
+  }
+  // o += V^T P^T for a tile's 32 keys
+  __device__ __forceinline__ void add(const TilePlaces<D>& at, const uint8_t* tile, const bf16x8 (&p)[RB][2]) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int b = 0; b < D / 32; ++b) {
+        const bf16x8 v = at.values(tile, b, k);
+#pragma unroll
+        for (int r = 0; r < RB; ++r) o[r][b] = mfma32(v, p[r][k], o[r][b]);
+      }
+  }
+  // The same where rows see different keys.  A weight of zero does not keep an
+  // infinity or a NaN from a row, so where the tile holds any they are left out here:
+  // the answer is true then, and add_not_finite has to bring them to the rows that see them.
+  __device__ __forceinline__ bool add_masked(const TilePlaces<D>& at, const uint8_t* tiles, const bf16x8 (&p)[RB][2]) {
     bool bad = false;
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int b = 0; b < D / 32; ++b) bad = bad || not_finite(at.values(tile, b, 2 * block + k));
-    if (!__any(bad)) {
-      add(at, tile, block, p);
-      return;
+      for (int b = 0; b < D / 32; ++b) bad = bad || not_finite(at.values(tiles, b, k));
+    bad = __any(bad);
+    if (__builtin_expect(!bad, 1)) {
+      add(at, tiles, p);
+      return false;
     }
 #pragma unroll
-    for (int b = 0; b < D / 32; ++b) {
-      f32x16 n;
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) n[i] = 0.f;
+      for (int b = 0; b < D / 32; ++b) {
+        const bf16x8 v = finite_only(at.values(tiles, b, k));
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const NotFinite v(at.values(tile, b, 2 * block + k));
-        uint32_t one[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t two = seen >> (8 * k + 2 * i);
-          one[i] = (two & 1 ? 0x3f80u : 0u) | (two & 2 ? 0x3f800000u : 0u);
-        }
-        o[b] = mfma32(v.finite, weights_frag(p, k), o[b]);
-        n = mfma32(v.kinds, __builtin_bit_cast(bf16x8, make_uint4(one[0], one[1], one[2], one[3])), n);
+        for (int r = 0; r < RB; ++r) o[r][b] = mfma32(v, p[r][k], o[r][b]);
+        __builtin_amdgcn_sched_barrier(0);
       }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[b][i] += NotFinite::added(n[i]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+    return true;
   }
-  // the row's whole sum
-  __device__ __forceinline__ float total() const { return l + other_half(l); }
+  // The infinities and NaNs of one key's values, column(d) of it, to row block r if
+  // the lane's row sees the key.
+  template <class Column>
+  __device__ __forceinline__ void add_not_finite(int r, bool sees, Column column) {
+    const int h = (threadIdx.x >> 5) & 1;
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float v = column(32 * b + key_of(i, h));
+        o[r][b][i] += sees && !(fabsf(v) < __builtin_huge_valf()) ? v : 0.f;
+      }
+  }
+  // a row's whole sum
+  __device__ __forceinline__ float total(int r) const { return l[r] + other_half(l[r]); }
 };
 
 // log sum exp(scale s) from a maximum of s, c = scale log2(e), and the sum

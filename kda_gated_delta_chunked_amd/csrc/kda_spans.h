@@ -20,6 +20,12 @@ __host__ __device__ inline int window_bytes(int left, int most, int row_bytes, i
   return rows > 0 ? (rows - 1) * row_bytes + width : 0;
 }
 
+// The same for the rows first .. first + most - 1 of a sequence of `length` rows,
+// where the first may be ahead of the sequence or behind it: no byte then.
+__host__ __device__ inline int window_bytes_at(int first, int length, int most, int row_bytes, int width) {
+  return first < 0 ? 0 : window_bytes(rows_left(first, length), most, row_bytes, width);
+}
+
 // Token spans.  A batch is covered by spans of `len` tokens that start at each
 // sequence's first token.  Where all sequences are equally long, their spans
 // follow one another (an empty sequence has one).  Of a packed batch, sequence
