@@ -164,7 +164,7 @@ kda_status check_decode(const kda_attn_decode_problem* p) {
   const int64_t row = (int64_t)p->num_heads * p->cache.head_dim;
   if (!stride_ok(p->q_stride, row) || !stride_ok(p->out_stride, row)) return KDA_ERR_INVALID_ARG;
   const int64_t N = p->num_seqs, KV = p->cache.num_kv_heads, T = p->tokens_per_seq;
-  if (N * T > kInt32Max || N * T * p->num_heads * 64 > kda::kMaxThreads - 255 ||
+  if (N * T > kInt32Max || N * T * p->num_heads * 256 > kda::kMaxThreads ||
       kda::attn_decode_blocks(N, KV, T, p->num_heads / KV, 1) * 256 > kda::kMaxThreads)
     return KDA_ERR_TOO_LARGE;
   return KDA_OK;
@@ -176,8 +176,8 @@ int decode_parts(const kda_attn_decode_problem* p) {
   const int64_t KV = p->cache.num_kv_heads;
   const int64_t blocks = kda::attn_decode_blocks(p->num_seqs, KV, p->tokens_per_seq, p->num_heads / KV, 1);
   if (blocks == 0) return 1;
-  const int64_t most = ((int64_t)p->table_width * p->cache.page_size + 255) / 256;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({most, 1024 / blocks, 256}));
+  const int64_t most = ((int64_t)p->table_width * p->cache.page_size + 511) / 512;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({most, 4096 / blocks, kda::kAttnParts}));
 }
 
 // workspace of a split: sums and outputs of each part's rows

@@ -13,6 +13,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "kda_attn_kernels.h"
 #include "kda_attn_tiles.h"
@@ -37,51 +38,92 @@ __device__ __forceinline__ uint2 widen4(uint32_t codes) {
   return make_uint2(bf16_pair(lo[0], lo[1]), bf16_pair(hi[0], hi[1]));
 }
 
-// The pages of a request's row in the table.
-struct Pages {
-  const int32_t* row;
-  int shift;
-  int64_t pages, end;  // positions that the table's width holds
-  // the page of a position, or -1
-  __device__ __forceinline__ int page(int pos) const {
-    if (pos >= end) return -1;
-    const int p = row[pos >> shift];
-    return p >= 0 && p < pages ? p : -1;
+// Half a tile, 16 positions, lies in one page.  Lane i holds the pages of the
+// halves of the wave's tile i of 64 in a row: found together, with no load to wait for
+// ahead of a tile's own.  -1: no page of the cache.
+struct TilePages {
+  int page0, page1;
+  // tile 0's first position, positions between tiles; positions are below `end`
+  __device__ __forceinline__ void find(const AttnDecodeArgs& a, const int32_t* row, int first, int step, int end) {
+    const int pos = first + (int)(threadIdx.x & 63) * step;
+    auto page = [&](int x) {
+      const int p = x < end ? row[x >> a.c.page_shift] : -1;
+      return p < a.c.pages ? p : -1;
+    };
+    page0 = page(pos);
+    page1 = page(pos + 16);
   }
 };
 
-// A tile's rows of one head, keys or values, in flight in registers.
+// Tiles of KEYS rows of one head, keys and values, from pages to the wave's own
+// part of LDS, asynchronously, 1 KiB a copy in LDS order.  Half a tile lies in one page, so
+// whatever a tile holds, its addresses are inside a page of the cache (page 0 for none): rows
+// that are no position are copied like others and masked.  bf16 rows take the swizzle of
+// their tile; codes lie as they come and become a tile of bf16 later.
 template <int D, bool E4M3>
-struct Flight {
-  static constexpr int ROW_BYTES = E4M3 ? D : 2 * D, PER_ROW = ROW_BYTES / 16, ROWS = 64 / PER_ROW, COUNT = KEYS / ROWS;
-  uint4 v[COUNT];
-  // row's page is that of the first or of the second 16 of the tile; -1: zeros
-  __device__ __forceinline__ void load(const uint8_t* base, int64_t page_bytes, int64_t token_bytes, int pos0, int in_page,
-                                       int left, int page0, int page1) {
-    const int lane = threadIdx.x & 63, sub = lane / PER_ROW, at = lane % PER_ROW * 16;
-#pragma unroll
-    for (int i = 0; i < COUNT; ++i) {
-      const int r = i * ROWS + sub, page = r < 16 ? page0 : page1;
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (r < left && page >= 0)
-        v[i] = *reinterpret_cast<const uint4*>(base + page * page_bytes + ((pos0 + r) & in_page) * token_bytes + at);
-    }
+struct PageCopies {
+  static constexpr int SIZE = E4M3 ? 1 : 2, PER_ROW = D * SIZE / 16, ROWS = 64 / PER_ROW, PARTS = KEYS / ROWS;
+  static constexpr int COUNT = 2 * PARTS, BYTES = 2 * KEYS * D * SIZE;  // of a tile's keys and values
+  static_assert(ROWS <= 16, "halves lie in one page each");
+  const uint8_t *kbase, *vbase;
+  int64_t kpage, vpage;
+  int ktoken, vtoken, in_page;
+  int kfrom, vfrom, sub;
+  __device__ __forceinline__ PageCopies(const PagedCache& c, int kv)
+      : kbase(static_cast<const uint8_t*>(c.k) + (int64_t)kv * D * SIZE), vbase(static_cast<const uint8_t*>(c.v) + (int64_t)kv * D * SIZE),
+        kpage(c.k_page * SIZE), vpage(c.v_page * SIZE), ktoken((int)c.k_token * SIZE), vtoken((int)c.v_token * SIZE),
+        in_page((1 << c.page_shift) - 1) {
+    const int lane = threadIdx.x & 63;
+    sub = lane / PER_ROW;
+    kfrom = sub * ktoken;
+    vfrom = sub * vtoken;
   }
-  __device__ __forceinline__ void store(uint8_t* tile) const {
-    const int lane = threadIdx.x & 63, sub = lane / PER_ROW, at = lane % PER_ROW;
+  __device__ __forceinline__ void start(int pos, int page0, int page1, uint8_t* to) const {
+#if defined(__HIP_DEVICE_COMPILE__)
+    typedef __attribute__((address_space(3))) const uint8_t* lds_ptr;
+    const uint32_t lds = (uint32_t)(uintptr_t)(lds_ptr)to;
+    const int lane = forget(threadIdx.x & 63);
 #pragma unroll
-    for (int i = 0; i < COUNT; ++i) {
-      const int r = i * ROWS + sub;
-      if constexpr (E4M3) {
-        const uint2 a = widen4(v[i].x), b = widen4(v[i].y), c = widen4(v[i].z), d = widen4(v[i].w);
-        *reinterpret_cast<uint4*>(tile + attn_tile_at<D>(r, 2 * at)) = make_uint4(a.x, a.y, b.x, b.y);
-        *reinterpret_cast<uint4*>(tile + attn_tile_at<D>(r, 2 * at + 1)) = make_uint4(c.x, c.y, d.x, d.y);
-      } else {
-        *reinterpret_cast<uint4*>(tile + attn_tile_at<D>(r, at)) = v[i];
-      }
+    for (int u = 0; u < COUNT; ++u) {
+      const int i = u % PARTS, half = i / (PARTS / 2), page = max(half ? page1 : page0, 0);
+      const int token = u < PARTS ? ktoken : vtoken;
+      // rows are less than 2^24 bytes apart: 32 bits hold 16 of them
+      const uint64_t rows = reinterpret_cast<uint64_t>(u < PARTS ? kbase : vbase) + page * (u < PARTS ? kpage : vpage) +
+                            (int64_t)(((pos + 16 * half) & in_page) + i % (PARTS / 2) * ROWS) * token;
+      const int in_row = E4M3 ? lane % PER_ROW * 16 : attn_tile_at<D>(i * ROWS + lane / PER_ROW, lane % PER_ROW) & (2 * D - 1);
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                   :
+                   : "s"(lds + u * 1024), "v"((u < PARTS ? kfrom : vfrom) + in_row), "s"(rows)
+                   : "memory");
     }
+#else
+    (void)pos, (void)page0, (void)page1, (void)to;
+#endif
   }
 };
+
+// A tile's codes to bf16, in the tile's order.
+template <int D>
+__device__ __forceinline__ void widen_tile(const uint8_t* codes, uint8_t* tile) {
+  constexpr int PER_ROW = D / 16, ROWS = 64 / PER_ROW, PARTS = 2 * KEYS / ROWS;
+  const int lane = forget(threadIdx.x & 63), sub = lane / PER_ROW, at = lane % PER_ROW;
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i) {
+    const uint4 v = *reinterpret_cast<const uint4*>(codes + i * 1024 + lane * 16);
+    const uint2 a = widen4(v.x), b = widen4(v.y), c = widen4(v.z), d = widen4(v.w);
+    const int r = i * ROWS + sub;  // (rows of values follow those of keys, and KEYS is a multiple of 16)
+    *reinterpret_cast<uint4*>(tile + attn_tile_at<D>(r, 2 * at)) = make_uint4(a.x, a.y, b.x, b.y);
+    *reinterpret_cast<uint4*>(tile + attn_tile_at<D>(r, 2 * at + 1)) = make_uint4(c.x, c.y, d.x, d.y);
+  }
+}
+
+// Waits until at most `left` of the wave's memory accesses are under way.
+template <int LEFT>
+__device__ __forceinline__ void memory_left() {
+  static_assert(LEFT < 64, "six bits");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (LEFT & 15) | (LEFT >> 4) << 14);
+  asm volatile("" ::: "memory");
+}
 
 // Keys of a part of a context of `length` positions: `parts` parts at most, whole
 // turns of a workgroup each.
@@ -105,7 +147,12 @@ struct Request {
 
 template <int D, bool E4M3>
 __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeArgs a) {
-  __shared__ __attribute__((aligned(1024))) uint8_t tiles[WAVES][2][KEYS * D * 2];
+  using Copies = PageCopies<D, E4M3>;
+  constexpr int TILE = 2 * KEYS * D * 2;  // keys and values as bf16
+  // of a wave: two tiles as they come, and for codes one of bf16; at the end its outputs
+  constexpr int WAVE_BYTES = 2 * Copies::BYTES + (E4M3 ? TILE : 0);
+  static_assert(WAVE_BYTES >= 32 * D * 4, "32 rows of outputs");
+  __shared__ __attribute__((aligned(1024))) uint8_t tiles[WAVES][WAVE_BYTES];
   __shared__ float stats[WAVES][2][32];
   const int KV = a.c.KV, G = a.H / KV, rows = a.T * G, row_blocks = (rows + 31) / 32;
   uint32_t at_block = blockIdx.x;
@@ -127,65 +174,114 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
   r.start();
   if (begin < end) {
     r.load(0, a.q + q_row * a.q_stride + (kv * G + row % G) * D);
-    const uint64_t sees = a.tree ? a.tree[n * a.tree_stride + t] : ~0ull >> (63 - t);
-    const Pages pages{a.table + (int64_t)req.row * a.table_width, a.c.page_shift, a.c.pages,
-                      (int64_t)a.table_width << a.c.page_shift};
-    const int size = E4M3 ? 1 : 2, in_page = (1 << a.c.page_shift) - 1;
-    const uint8_t* kbase = static_cast<const uint8_t*>(a.c.k) + (int64_t)kv * D * size;
-    const uint8_t* vbase = static_cast<const uint8_t*>(a.c.v) + (int64_t)kv * D * size;
+    // the request's own tokens that the row sees
+    const uint64_t sees = (a.tree ? a.tree[n * a.tree_stride + t] : ~0ull >> (63 - t)) & (~0ull >> (64 - a.T));
+    const int32_t* table = a.table + (int64_t)req.row * a.table_width;
     const float c = a.scale * kLog2e * (E4M3 ? a.c.k_scale[kv] : 1.f);
-    const TilePlaces<D> at;
-    uint8_t *ktile = tiles[wave][0], *vtile = tiles[wave][1];
-    Flight<D, E4M3> kf, vf;
-    int page0 = -1, page1 = -1;  // of the tile in flight
-    // finds the pages of a tile; bits tell which of its positions have one
-    auto set_pages = [&](int pos) {
-      page0 = __builtin_amdgcn_readfirstlane(pos < end ? pages.page(pos) : -1);
-      page1 = __builtin_amdgcn_readfirstlane(pos + 16 < end ? pages.page(pos + 16) : -1);
-      return (page0 >= 0 ? 0xffffu : 0u) | (page1 >= 0 ? 0xffff0000u : 0u);
+    const TilePlaces<D> places;
+    const Copies copies(a.c, kv);
+    uint8_t* const ring = tiles[wave];
+    uint8_t* const wide = ring + (E4M3 ? 2 * Copies::BYTES : 0);
+    const int first = begin + wave * KEYS, count = (end - first + STEP - 1) / STEP;  // the wave's tiles
+
+    TilePages pages;
+    struct Two { int a, b; };  // the pages of a tile's halves
+    auto pages_of = [&](int tile) {
+      if ((tile & 63) == 0) pages.find(a, table, first + tile * STEP, STEP, end);
+      return Two{__builtin_amdgcn_readlane(pages.page0, tile & 63), __builtin_amdgcn_readlane(pages.page1, tile & 63)};
     };
-    auto fetch = [&](int pos) {
-      const uint32_t there = set_pages(pos);
-      kf.load(kbase, a.c.k_page * size, a.c.k_token * size, pos, in_page, end - pos, page0, page1);
-      vf.load(vbase, a.c.v_page * size, a.c.v_token * size, pos, in_page, end - pos, page0, page1);
-      return there;
+    Two now{-1, -1}, next{-1, -1}, after{-1, -1};
+    auto fetch = [&](int tile) {
+      after = pages_of(tile);
+      copies.start(first + tile * STEP, after.a, after.b, ring + (tile & 1) * Copies::BYTES);
     };
-    auto plain = [&](uint32_t there, int pos) { return pos + KEYS <= req.before && pos + KEYS <= end && there == ~0u; };
-    auto sees_key = [&](uint32_t there, int pos, int key) {
-      const int x = pos + key, own = x - req.before;
-      return (there >> key & 1) && x < end && (own < 0 || (own < a.T && (sees >> own & 1)));
+    if (count > 0) {
+      fetch(0);
+      now = after;
+    }
+    if (count > 1) {
+      fetch(1);
+      next = after;
+    }
+    // the keys of the tile at `pos` that the lane's row sees, a bit each
+    auto seen_of = [&](int pos) {
+      const int own = pos - req.before, left = end - pos;
+      uint64_t seen = ~0ull;
+      if (own >= 64) seen = 0;
+      else if (own >= 0) seen = sees >> own;
+      else if (own > -KEYS) seen = sees << -own | ((1ull << -own) - 1);
+      uint32_t there = (now.a < 0 ? 0u : 0xffffu) | (now.b < 0 ? 0u : 0xffff0000u);
+      if (left < KEYS) there &= (1u << left) - 1;
+      return (uint32_t)seen & there;
     };
     bool not_finite = false;  // left out of a tile with masked rows
-    uint32_t next = fetch(begin + wave * KEYS);
-    for (int pos = begin + wave * KEYS; pos < end; pos += STEP) {
-      const uint32_t there = next;
-      wave_order();
-      kf.store(ktile);
-      vf.store(vtile);
-      wave_order();
-      next = fetch(pos + STEP);
-      f32x16 s[1];
-      bf16x8 p[1][2];
-      r.scores(at, ktile, s);
-      if (plain(there, pos)) {
-        r.weigh(s, c, p);
-        r.add(at, vtile, p);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (!sees_key(there, pos, key_of(i, h))) s[0][i] = kNone;
-        r.weigh(s, c, p);
-        not_finite = r.add_masked(at, vtile, p) || not_finite;
+    f32x16 s[1];
+    bf16x8 p[1][2];
+    float sum[1];
+    int tile = 0;
+    // the tile's bytes, once they are there
+    auto land = [&]() {
+      if (tile + 1 < count) memory_left<Copies::COUNT>();
+      else memory_left<0>();
+      int at = (tile & 1) * Copies::BYTES;
+      if constexpr (E4M3) {
+        widen_tile<D>(ring + at, wide);
+        wave_order();
+        at = 0;
       }
+      return TilePlaces<D>(places, at, at + TILE / 2);
+    };
+    // the tile is done with: its place takes the one after the next
+    auto leave = [&]() {
+      if constexpr (!E4M3) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (tile + 2 < count) fetch(tile + 2);
+    };
+    auto step = [&]() {
+      now = next;
+      next = after;
+      ++tile;
+    };
+    while (tile < count) {
+      bool far = false;
+      while (first + tile * STEP + KEYS <= min(req.before, end) && now.a >= 0 && now.b >= 0) {
+        // a tile that all rows see
+        const TilePlaces<D> at = land();
+        if (E4M3) leave();
+        r.scores(at, wide, s);
+        far = r.try_weights(s, c, p, sum);
+        if (__builtin_expect(far, 0)) break;
+        r.take(sum);
+        r.add(at, wide, p);
+        if (!E4M3) leave();
+        step();
+      }
+      if (tile >= count) break;
+      if (!far) {
+        const TilePlaces<D> at = land();
+        if (E4M3) leave();
+        r.scores(at, wide, s);
+        const uint32_t seen = seen_of(first + tile * STEP) >> (4 * h);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[0][i] = seen & 1u << key_of(i, 0) ? s[0][i] : kNone;
+        far = r.try_weights(s, c, p, sum);
+      }
+      const int at0 = E4M3 ? 0 : (tile & 1) * Copies::BYTES;
+      const TilePlaces<D> at(places, at0, at0 + TILE / 2);
+      if (far) r.weights_from_maximum(s, c, p, sum);
+      r.take(sum);
+      not_finite = r.add_masked(at, wide, p) || not_finite;
+      if (!E4M3) leave();
+      step();
     }
     if (__builtin_expect(not_finite, 0))
-      for (int pos = begin + wave * KEYS; pos < end; pos += STEP) {
-        const uint32_t there = set_pages(pos);
-        if (plain(there, pos)) continue;
+      for (int tile = 0; tile < count; ++tile) {
+        const Two of = pages_of(tile);
+        const int pos = first + tile * STEP;
         for (int key = 0; key < KEYS; ++key) {
-          if (pos + key >= end || !(there >> key & 1)) continue;
-          const uint8_t* v = vbase + (key < 16 ? page0 : page1) * a.c.v_page * size + ((pos + key) & in_page) * a.c.v_token * size;
-          r.add_not_finite(0, sees_key(there, pos, key), [&](int d) {
+          const int page = key < 16 ? of.a : of.b, own = pos + key - req.before;
+          if (pos + key >= end || page < 0) continue;
+          const uint8_t* v = copies.vbase + page * copies.vpage + (int64_t)((pos + key) & copies.in_page) * copies.vtoken;
+          r.add_not_finite(0, own < 0 || (sees >> (own & 63) & 1), [&](int d) {
             if constexpr (E4M3) return __builtin_amdgcn_cvt_f32_fp8((int)v[d], 0);
             else return bf16_f32(reinterpret_cast<const uint16_t*>(v)[d]);
           });
@@ -246,38 +342,69 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
   if (a.lse && cols == 0) a.lse[out_row * a.H + head] = lse_of(m, c, sum);
 }
 
-// The parts of a context: a wave per row, its lanes D / 64 columns each.
+// The parts of a context, a workgroup per row: the parts' weights first, a thread
+// each, then their sums, D / 4 threads a part, several parts side by side.
 template <int D>
 __global__ __launch_bounds__(THREADS) void kda_attn_join_kernel(AttnDecodeArgs a) {
+  constexpr int LANES = D / 4, SIDE = THREADS / LANES;
+  __shared__ float weight[kAttnParts], red[2][WAVES];
+  __shared__ float4 sums[SIDE][LANES];
   const int KV = a.c.KV, G = a.H / KV, rows = a.T * G;
-  const int64_t at = (int64_t)blockIdx.x * (THREADS / 64) + (threadIdx.x >> 6);  // (request, kv head, row)
-  if (at >= (int64_t)a.N * KV * rows) return;
-  const int row = (int)(at % rows), kv = (int)(at / rows % KV), n = (int)(at / rows / KV);
-  const int lane = threadIdx.x & 63;
+  const int row = (int)(blockIdx.x % (unsigned)rows), at = (int)(blockIdx.x / (unsigned)rows);  // at: (request, kv head)
+  const int kv = at % KV, n = at / KV;
   const Request req(a, n);
   const int per_part = part_keys(req.length, a.parts);
   const int parts = per_part ? (req.length + per_part - 1) / per_part : 0;
-  const int64_t slot = ((int64_t)n * KV + kv) * a.parts * rows + row;
+  const int64_t slot = (int64_t)at * a.parts * rows + row;
   const float c = a.scale * kLog2e * (a.c.k_scale ? a.c.k_scale[kv] : 1.f);
-  float m = kNone, sum = 0.f, o[D / 64] = {};
-  for (int p = 0; p < parts; ++p) {
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (slot + (int64_t)p * rows) * 2);
-    const float now = fmaxf(m, ml.x);
-    const float keep = m == kNone ? 0.f : __builtin_amdgcn_exp2f((m - now) * c);
-    const float more = ml.x == kNone ? 0.f : __builtin_amdgcn_exp2f((ml.x - now) * c);
-    sum = (sum != sum ? sum : keep * sum) + (ml.y != ml.y ? ml.y : more * ml.y);
-    const float* from = a.part_out + (slot + (int64_t)p * rows) * D + lane * (D / 64);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  float2 ml = make_float2(kNone, 0.f);
+  if ((int)threadIdx.x < parts) ml = *reinterpret_cast<const float2*>(a.part_ml + (slot + (int64_t)threadIdx.x * rows) * 2);
+  float m = ml.x;
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) o[i] = (keep == 0.f ? 0.f : keep * o[i]) + (more == 0.f ? 0.f : more * from[i]);
-    m = now;
+  for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+  if (lane == 0) red[0][wave] = m;
+  lds_barrier();
+  m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+  const float w = ml.x == kNone ? 0.f : __builtin_amdgcn_exp2f((ml.x - m) * c);
+  if (threadIdx.x < kAttnParts) weight[threadIdx.x] = w;
+  // (a part whose scores are all NaN has no maximum, and a sum that is NaN)
+  float sum = ml.y != ml.y ? ml.y : w * ml.y;
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
+  if (lane == 0) red[1][wave] = sum;
+  lds_barrier();
+  sum = red[1][0] + red[1][1] + red[1][2] + red[1][3];
+
+  const int side = threadIdx.x / LANES, col = threadIdx.x % LANES;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int p = side; p < parts; p += SIDE) {
+    const float4 v = *reinterpret_cast<const float4*>(a.part_out + (slot + (int64_t)p * rows) * D + col * 4);
+    const float wp = weight[p];
+    if (wp == 0.f) continue;  // (what it has may be infinite)
+    o.x += wp * v.x;
+    o.y += wp * v.y;
+    o.z += wp * v.z;
+    o.w += wp * v.w;
+  }
+  sums[side][col] = o;
+  lds_barrier();
+  if (side) return;
+#pragma unroll
+  for (int i = 1; i < SIDE; ++i) {
+    const float4 v = sums[i][col];
+    o.x += v.x;
+    o.y += v.y;
+    o.z += v.z;
+    o.w += v.w;
   }
   const float inv = sum == 0.f ? 0.f : (a.c.v_scale ? a.c.v_scale[kv] : 1.f) / sum;
   const int64_t out_row = (int64_t)n * a.T + row / G;
   const int head = kv * G + row % G;
-  uint16_t* to = a.out + out_row * a.out_stride + head * D + lane * (D / 64);
-  if constexpr (D == 128) *reinterpret_cast<uint32_t*>(to) = bf16_pair(o[0] * inv, o[1] * inv);
-  else *to = (uint16_t)bf16_pair(o[0] * inv, 0.f);
-  if (a.lse && lane == 0) a.lse[out_row * a.H + head] = lse_of(m, c, sum);
+  *reinterpret_cast<uint2*>(a.out + out_row * a.out_stride + head * D + col * 4) =
+      make_uint2(bf16_pair(o.x * inv, o.y * inv), bf16_pair(o.z * inv, o.w * inv));
+  if (a.lse && col == 0) a.lse[out_row * a.H + head] = lse_of(m, c, sum);
 }
 
 template <int D>
@@ -287,8 +414,7 @@ void launch(const AttnDecodeArgs& a, hipStream_t stream) {
   if (a.c.k_scale) hipLaunchKernelGGL((kda_attn_decode_kernel<D, true>), grid, dim3(THREADS), 0, stream, a);
   else hipLaunchKernelGGL((kda_attn_decode_kernel<D, false>), grid, dim3(THREADS), 0, stream, a);
   if (a.part_out) {
-    const int64_t join = ((int64_t)a.N * a.T * a.H + THREADS / 64 - 1) / (THREADS / 64);
-    hipLaunchKernelGGL(kda_attn_join_kernel<D>, dim3((unsigned)join), dim3(THREADS), 0, stream, a);
+    hipLaunchKernelGGL(kda_attn_join_kernel<D>, dim3((unsigned)((int64_t)a.N * a.T * a.H)), dim3(THREADS), 0, stream, a);
   }
 }
 

@@ -87,6 +87,7 @@ inline int64_t attn_decode_row_blocks(int64_t T, int64_t G) { return (T * G + 31
 inline int64_t attn_decode_blocks(int64_t N, int64_t KV, int64_t T, int64_t G, int64_t parts) {
   return N * KV * attn_decode_row_blocks(T, G) * parts;
 }
+constexpr int kAttnParts = 256;  // of a context at most
 inline int64_t kv_store_threads(int64_t T, int64_t KV, int64_t D) { return (T * KV * (D / 8) + 255) / 256 * 256; }
 constexpr int kAssignTokens = 1024;  // new tokens of a workgroup
 inline int64_t kv_assign_blocks(int64_t T) { return T ? (T + kAssignTokens - 1) / kAssignTokens : 1; }

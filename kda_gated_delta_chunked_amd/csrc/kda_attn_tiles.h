@@ -164,7 +164,7 @@ struct AttnRows {
     for (int r = 0; r < RB; ++r)
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        if (key + key_of(i, lane >> 5) > top + 32 * r + (lane & 31)) s[r][i] = kNone;
+        s[r][i] = key + key_of(i, lane >> 5) > top + 32 * r + (lane & 31) ? kNone : s[r][i];
   }
   // weights of scores from a maximum, as operands, and their sum
   static __device__ __forceinline__ float weights(const f32x16& s, float c, float mc, bf16x8 (&p)[2]) {
