@@ -15,69 +15,70 @@
 namespace kda {
 namespace {
 
-constexpr int KEYS = 32;  // of a step
-constexpr int AHEAD = 2;  // steps that copies run ahead of their use
+constexpr int WAVES = kAttnRows / 32;
+constexpr int KEYS = 32;  // of a block
+constexpr int AHEAD = 2;  // turns that copies run ahead of their use
 
-// Waits until at most `left` of the wave's memory accesses are under way.
-template <int LEFT>
-__device__ __forceinline__ void memory_left() {
-  static_assert(LEFT < 64, "six bits");
-  __builtin_amdgcn_s_waitcnt(0x0F70 | (LEFT & 15) | (LEFT >> 4) << 14);
-}
-
-// KEYS rows of one head's keys and of its values from memory to LDS,
-// asynchronously, each wave 1 KiB at a time in LDS order: the swizzle is in the
-// addresses that its lanes read.
-template <int D, int WAVES>
-struct Copies {
+// The keys and values of one head of a sequence, for a wave of rows from `top` on.
+template <int D>
+struct PromptSource {
+  using Places = TilePlaces<D, false>;
+  static constexpr int RING = AHEAD + 1, TILE = Places::BYTES;
   static constexpr int PER_ROW = D / 8, ROWS = 64 / PER_ROW, PARTS = KEYS / ROWS;  // a copy's rows, a tile's copies
   static constexpr int COUNT = 2 * PARTS / WAVES;                                  // of a wave, keys and values
-  static_assert(COUNT >= 1, "a copy for each wave at least");
+  static_assert(COUNT >= 1 && PARTS <= WAVES, "whole tiles by all waves");
+  uint8_t *ktiles, *vtiles;
+  Places places;
+  int open;
   uint64_t kbase, vbase;
-  int kbytes, vbytes, kfrom, vfrom;
-  __device__ __forceinline__ Copies(const AttnArgs& a, int64_t token, int kv, int wave)
-      : kbase(reinterpret_cast<uint64_t>(a.k + token * a.k_stride + kv * D)),
-        vbase(reinterpret_cast<uint64_t>(a.v + token * a.v_stride + kv * D)),
-        kbytes((int)a.k_stride * 2), vbytes((int)a.v_stride * 2) {
-    const int lane = threadIdx.x & 63, row = wave % PARTS * ROWS + lane / PER_ROW;
-    const int in_row = attn_tile_at<D>(row, lane % PER_ROW) & (D * 2 - 1);
-    kfrom = row * kbytes + in_row;
-    vfrom = row * vbytes + in_row;
+  int kbytes, vbytes, kfrom, vfrom, length, wave, row;
+  int kslot = 0, put_slot = 0;  // ring places that are read and filled next
+
+  __device__ __forceinline__ PromptSource(const AttnArgs& a, int64_t token, int length_, int kv, int wave_, int top,
+                                          uint8_t* kt, uint8_t* vt)
+      : ktiles(kt), vtiles(vt), open(top / KEYS), kbase(reinterpret_cast<uint64_t>(a.k + token * a.k_stride + kv * D)),
+        vbase(reinterpret_cast<uint64_t>(a.v + token * a.v_stride + kv * D)), kbytes((int)a.k_stride * 2),
+        vbytes((int)a.v_stride * 2), length(length_), wave(wave_) {
+    const int lane = threadIdx.x & 63, r = wave % PARTS * ROWS + lane / PER_ROW;
+    const int in_row = attn_tile_at<D, false>(r, lane % PER_ROW) & (D * 2 - 1);
+    kfrom = r * kbytes + in_row;
+    vfrom = r * vbytes + in_row;
+    row = top + (lane & 31);
+    put(0, -2);  // (no row is ahead of the sequence: zeros)
+    put(1, -1);
   }
-  // keys from row k0 of the sequence on, values from row v0 on; `length` rows are
-  // there.  (Written out: for the builtin the compiler would wait ahead of every
-  // transposed read of LDS until no copy is under way.  memory_left waits for
-  // them; M0, which nothing else here uses, is the place in LDS and takes effect one
-  // wait state later.)
-  __device__ __forceinline__ void start(int k0, int v0, int length, const uint8_t* ktile, const uint8_t* vtile, int wave) const {
-#if defined(__HIP_DEVICE_COMPILE__)
-    typedef __attribute__((address_space(3))) const uint8_t* lds_ptr;
-    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  static __device__ __forceinline__ void next(int& slot) { slot = slot == (RING - 1) * TILE ? 0 : slot + TILE; }
+  __device__ __forceinline__ void put(int kblock, int vblock) {
 #pragma unroll
     for (int i = 0; i < COUNT; ++i) {
       const int u = i * WAVES + wave;  // the copies of the keys' tile, then of the values'
       const bool key = u < PARTS;
-      const int bytes = key ? kbytes : vbytes, first = key ? k0 : v0;
+      const int bytes = key ? kbytes : vbytes, first = (key ? kblock : vblock) * KEYS;
       const uint64_t base = (key ? kbase : vbase) + (int64_t)first * bytes;
-      const int size = window_bytes_at(first, length, KEYS, bytes, D * 2);
-      const u32x4 window = {(uint32_t)base, (uint32_t)(base >> 32) & 0xffffu, (uint32_t)size, 0x00020000u};
-      const uint32_t to = (uint32_t)(uintptr_t)(lds_ptr)(key ? ktile : vtile) + (u % PARTS) * 1024;
-      const int from = (key ? kfrom : vfrom) + (u % PARTS - wave % PARTS) * ROWS * bytes;
-      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                   :
-                   : "s"(to), "v"(from), "s"(window)
-                   : "memory");
+      const u32x4 window = {(uint32_t)base, (uint32_t)(base >> 32) & 0xffffu,
+                            (uint32_t)window_bytes_at(first, length, KEYS, bytes, D * 2), 0x00020000u};
+      copy_to_lds(lds_place((key ? ktiles : vtiles) + put_slot) + (u % PARTS) * 1024, window, key ? kfrom : vfrom);
     }
-#else
-    (void)k0, (void)v0, (void)length, (void)ktile, (void)vtile, (void)wave;
-#endif
+    next(put_slot);
+  }
+  __device__ __forceinline__ Places turn(int j) {
+    memory_left<(AHEAD - 1) * COUNT>();
+    tiles_barrier();
+    put(j + 1 + AHEAD, j - 1 + AHEAD);
+    const Places at(places, kslot, kslot);
+    next(kslot);
+    return at;
+  }
+  __device__ __forceinline__ uint32_t seen(int j) const {
+    const int n = row - j * KEYS;  // the last key that the row sees
+    return n < 0 ? 0u : n >= 31 ? ~0u : (2u << n) - 1;
   }
 };
 
-template <int D, int RB, int WAVES>
-__global__ __launch_bounds__(WAVES * 64, WAVES / 4) void kda_attn_kernel(AttnArgs a) {
-  constexpr int TILE = KEYS * D * 2, RING = AHEAD + 1;
-  __shared__ __attribute__((aligned(1024))) uint8_t ktiles[RING * TILE], vtiles[RING * TILE];
+template <int D>
+__global__ __launch_bounds__(WAVES * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void kda_attn_kernel(AttnArgs a) {
+  using Source = PromptSource<D>;
+  __shared__ __attribute__((aligned(1024))) uint8_t ktiles[Source::RING * Source::TILE], vtiles[Source::RING * Source::TILE];
   // The heads of a slot side by side, a group's on one XCD where there are at least
   // as many groups as XCDs; a sequence's last, longest rows first.
   const int in = (int)(blockIdx.x % (unsigned)a.H), kv = in % a.KV, head = kv * (a.H / a.KV) + in / a.KV;
@@ -88,123 +89,41 @@ __global__ __launch_bounds__(WAVES * 64, WAVES / 4) void kda_attn_kernel(AttnArg
   if (span.k < 0 || length == 0) return;
   const int first = span.k * kAttnRows;
 
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, h = lane >> 5;
-  const int top = first + wave * 32 * RB;  // the wave's first row
-  AttnRows<D, RB> r;
-#pragma unroll
-  for (int b = 0; b < RB; ++b) {
-    const int row = min(top + 32 * b + (lane & 31), length - 1);
-    r.load(b, a.q + (span.begin + row) * a.q_stride + head * D);
-  }
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int top = first + wave * 32, row = top + (lane & 31);  // the wave's first row, the lane's
+  AttnRows<D> r;
+  r.load(a.q + (span.begin + min(row, length - 1)) * a.q_stride + head * D);
   r.start();
-  const TilePlaces<D> places;
-  const Copies<D, WAVES> copies(a, span.begin, kv, wave);
   const float c = a.scale * kLog2e;
-  const int blocks = (min(first + kAttnRows, length) + KEYS - 1) / KEYS;          // that any row sees
-  const int mine = top < length ? min(blocks, top / KEYS + RB) : 0, open = min(mine, top / KEYS);  // of the wave, and without a mask
-
-  // Step j: scores of block j + 1, weights of block j, the product of block j - 1's
-  // weights with its values, which do not depend on each other.  The copies of
-  // keys are one step ahead of the weights, those of values one behind.
-  int kslot = 0, vslot = 0, kput = 0, vput = 0;  // ring places that are read next, and filled next
-  auto next = [](int& slot) { slot = slot == (RING - 1) * TILE ? 0 : slot + TILE; };
-  auto put = [&](int kblock, int vblock) {
-    copies.start(kblock * KEYS, vblock * KEYS, length, ktiles + kput, vtiles + vput, wave);
-    next(kput);
-    next(vput);
-  };
-  f32x16 s[RB];
-  bf16x8 p[RB][2];
-#pragma unroll
-  for (int b = 0; b < RB; ++b) p[b][0] = p[b][1] = bf16x8{};
-  bool not_finite = false;  // left out of a masked block
-  put(0, -2);
-  put(1, -1);
-  int j = -1;
-  auto turn = [&]() {
-    memory_left<(AHEAD - 1) * Copies<D, WAVES>::COUNT>();
-    tiles_barrier();
-    put(j + 1 + AHEAD, j - 1 + AHEAD);
-    const TilePlaces<D> at(places, kslot, vslot);
-    next(kslot);
-    next(vslot);
-    return at;
-  };
-  while (j <= blocks) {
-    if (j > 0 && j < open) {
-      f32x16 n[RB];
-      float sum[RB];
-      bool far;
-      do {
-        const TilePlaces<D> at = turn();
-        r.scores(at, ktiles, n);
-        r.add(at, vtiles, p);
-        far = r.try_weights(s, c, p, sum);
-        if (__builtin_expect(far, 0)) break;
-        r.take(sum);
-#pragma unroll
-        for (int b = 0; b < RB; ++b) s[b] = n[b];
-      } while (++j < open);
-      if (!far) continue;
-      r.weights_from_maximum(s, c, p, sum);
-      r.take(sum);
-#pragma unroll
-      for (int b = 0; b < RB; ++b) s[b] = n[b];
-    } else {
-      const TilePlaces<D> at = turn();
-      if (j > 0 && j <= mine) {
-        if (j - 1 < open) r.add(at, vtiles, p);
-        else not_finite = r.add_masked(at, vtiles, p) || not_finite;
-      }
-      if (j >= 0 && j < mine) {
-        if (j >= open) r.mask(s, j * KEYS, top);
-        r.weigh(s, c, p);
-      }
-      if (j + 1 < mine) r.scores(at, ktiles, s);
-    }
-    ++j;
-  }
-  memory_left<0>();  // no copy outlives the workgroup
-
-  if (__builtin_expect(not_finite, 0))
-    for (int key = open * KEYS; key < min(mine * KEYS, length); ++key) {
+  const int blocks = (min(first + kAttnRows, length) + KEYS - 1) / KEYS;  // that any row sees
+  const int mine = top < length ? min(blocks, top / KEYS + 1) : 0;        // any row of the wave
+  Source source(a, span.begin, length, kv, wave, top, ktiles, vtiles);
+  source.open = min(source.open, mine);
+  r.settle();
+  if (__builtin_expect(attend(r, source, c, blocks, mine), 0))
+    for (int key = source.open * KEYS; key < min(mine * KEYS, length); ++key) {
       const uint16_t* v = a.v + (span.begin + key) * a.v_stride + kv * D;
-#pragma unroll
-      for (int b = 0; b < RB; ++b)
-        r.add_not_finite(b, key <= top + 32 * b + (lane & 31), [&](int d) { return bf16_f32(v[d]); });
+      r.add_not_finite(key <= row, [&](int d) { return bf16_f32(v[d]); });
     }
-
-#pragma unroll
-  for (int b = 0; b < RB; ++b) {
-    const int row = top + 32 * b + (lane & 31);
-    const float total = r.total(b), inv = 1.f / total;
-    if (row >= length) continue;
-    const int64_t token = span.begin + row;
-    uint16_t* out = a.out + token * a.out_stride + head * D + 4 * h;
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; i += 4)
-        *reinterpret_cast<uint2*>(out + 32 * d + 2 * i) =
-            make_uint2(bf16_pair(r.o[b][d][i] * inv, r.o[b][d][i + 1] * inv),
-                       bf16_pair(r.o[b][d][i + 2] * inv, r.o[b][d][i + 3] * inv));
-    if (a.lse && h == 0) a.lse[token * a.H + head] = lse_of(r.m[b], c, total);
-  }
+  const float total = r.total();
+  if (row >= length) return;
+  const int64_t token = span.begin + row;
+  r.store(a.out + token * a.out_stride + head * D, 1.f / total);
+  if (a.lse && lane < 32) a.lse[token * a.H + head] = lse_of(r.m, c, total);
 }
 
-template <int D, int RB, int WAVES>
+template <int D>
 void launch(const AttnArgs& a, hipStream_t stream) {
-  static_assert(RB * WAVES * 32 == kAttnRows, "rows of a workgroup");
   const dim3 grid((unsigned)attn_blocks(a.slots, a.H));
-  hipLaunchKernelGGL((kda_attn_kernel<D, RB, WAVES>), grid, dim3(WAVES * 64), 0, stream, a);
+  hipLaunchKernelGGL(kda_attn_kernel<D>, grid, dim3(WAVES * 64), 0, stream, a);
 }
 
 }  // namespace
 
 hipError_t launch_attn(const AttnArgs& a, hipStream_t stream) {
   if (a.pk.T_total == 0) return hipSuccess;
-  if (a.D == 128) launch<128, 1, 8 / 1>(a, stream);
-  else launch<64, 1, 8 / 1>(a, stream);
+  if (a.D == 128) launch<128>(a, stream);
+  else launch<64>(a, stream);
   return hipGetLastError();
 }
 

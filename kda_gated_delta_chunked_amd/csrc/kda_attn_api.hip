@@ -176,8 +176,8 @@ int decode_parts(const kda_attn_decode_problem* p) {
   const int64_t KV = p->cache.num_kv_heads;
   const int64_t blocks = kda::attn_decode_blocks(p->num_seqs, KV, p->tokens_per_seq, p->num_heads / KV, 1);
   if (blocks == 0) return 1;
-  const int64_t most = ((int64_t)p->table_width * p->cache.page_size + 511) / 512;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({most, 4096 / blocks, kda::kAttnParts}));
+  const int64_t most = ((int64_t)p->table_width * p->cache.page_size + 1023) / 1024;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({most, 256 / blocks, kda::kAttnParts}));
 }
 
 // workspace of a split: sums and outputs of each part's rows

@@ -31,13 +31,6 @@ __device__ __forceinline__ void wave_order() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// four e4m3 codes to four bf16 (exact)
-__device__ __forceinline__ uint2 widen4(uint32_t codes) {
-  typedef float f32x2 __attribute__((ext_vector_type(2)));
-  const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, true);
-  return make_uint2(bf16_pair(lo[0], lo[1]), bf16_pair(hi[0], hi[1]));
-}
-
 // Half a tile, 16 positions, lies in one page.  Lane i holds the pages of the
 // halves of the wave's tile i of 64 in a row: found together, with no load to wait for
 // ahead of a tile's own.  -1: no page of the cache.
@@ -55,75 +48,46 @@ struct TilePages {
   }
 };
 
-// Tiles of KEYS rows of one head, keys and values, from pages to the wave's own
-// part of LDS, asynchronously, 1 KiB a copy in LDS order.  Half a tile lies in one page, so
+// Tiles of KEYS rows of one head, keys and values, from pages to LDS,
+// asynchronously, 1 KiB a copy in LDS order, the swizzle in the addresses.  Half a tile lies in one page, so
 // whatever a tile holds, its addresses are inside a page of the cache (page 0 for none): rows
-// that are no position are copied like others and masked.  bf16 rows take the swizzle of
-// their tile; codes lie as they come and become a tile of bf16 later.
+// that are no position are copied like others, and masked.
 template <int D, bool E4M3>
 struct PageCopies {
   static constexpr int SIZE = E4M3 ? 1 : 2, PER_ROW = D * SIZE / 16, ROWS = 64 / PER_ROW, PARTS = KEYS / ROWS;
-  static constexpr int COUNT = 2 * PARTS, BYTES = 2 * KEYS * D * SIZE;  // of a tile's keys and values
-  static_assert(ROWS <= 16, "halves lie in one page each");
+  static constexpr int COUNT = 2 * PARTS, TILE = KEYS * D * SIZE;  // of a tile's keys and values; bytes of either
+  static_assert(ROWS <= 16 && PARTS >= 2, "halves lie in one page each");
   const uint8_t *kbase, *vbase;
   int64_t kpage, vpage;
   int ktoken, vtoken, in_page;
-  int kfrom, vfrom, sub;
   __device__ __forceinline__ PageCopies(const PagedCache& c, int kv)
       : kbase(static_cast<const uint8_t*>(c.k) + (int64_t)kv * D * SIZE), vbase(static_cast<const uint8_t*>(c.v) + (int64_t)kv * D * SIZE),
         kpage(c.k_page * SIZE), vpage(c.v_page * SIZE), ktoken((int)c.k_token * SIZE), vtoken((int)c.v_token * SIZE),
-        in_page((1 << c.page_shift) - 1) {
-    const int lane = threadIdx.x & 63;
-    sub = lane / PER_ROW;
-    kfrom = sub * ktoken;
-    vfrom = sub * vtoken;
+        in_page((1 << c.page_shift) - 1) {}
+  // copy `part` of the tile from position pos on, whose halves are in these pages
+  __device__ __forceinline__ void start(bool keys, int part, int pos, int page0, int page1, uint32_t lds) const {
+    const int lane = forget(threadIdx.x & 63), row = part * ROWS, half = part / (PARTS / 2);
+    const int page = max(half ? page1 : page0, 0), token = keys ? ktoken : vtoken;
+    // rows are less than 2^24 bytes apart: 32 bits hold 16 of them
+    const uint64_t rows = reinterpret_cast<uint64_t>(keys ? kbase : vbase) + page * (keys ? kpage : vpage) +
+                          (int64_t)(((pos + 16 * half) & in_page) + row % 16) * token;
+    const int in_row = attn_tile_at<D, E4M3>(row + lane / PER_ROW, lane % PER_ROW) & (D * SIZE - 1);
+    copy_to_lds(lds + part * 1024, rows, (uint32_t)(lane / PER_ROW * token + in_row));
   }
+  // keys, and behind them values
   __device__ __forceinline__ void start(int pos, int page0, int page1, uint8_t* to) const {
-#if defined(__HIP_DEVICE_COMPILE__)
-    typedef __attribute__((address_space(3))) const uint8_t* lds_ptr;
-    const uint32_t lds = (uint32_t)(uintptr_t)(lds_ptr)to;
-    const int lane = forget(threadIdx.x & 63);
+    const uint32_t lds = lds_place(to);
 #pragma unroll
-    for (int u = 0; u < COUNT; ++u) {
-      const int i = u % PARTS, half = i / (PARTS / 2), page = max(half ? page1 : page0, 0);
-      const int token = u < PARTS ? ktoken : vtoken;
-      // rows are less than 2^24 bytes apart: 32 bits hold 16 of them
-      const uint64_t rows = reinterpret_cast<uint64_t>(u < PARTS ? kbase : vbase) + page * (u < PARTS ? kpage : vpage) +
-                            (int64_t)(((pos + 16 * half) & in_page) + i % (PARTS / 2) * ROWS) * token;
-      const int in_row = E4M3 ? lane % PER_ROW * 16 : attn_tile_at<D>(i * ROWS + lane / PER_ROW, lane % PER_ROW) & (2 * D - 1);
-      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                   :
-                   : "s"(lds + u * 1024), "v"((u < PARTS ? kfrom : vfrom) + in_row), "s"(rows)
-                   : "memory");
-    }
-#else
-    (void)pos, (void)page0, (void)page1, (void)to;
-#endif
+    for (int u = 0; u < PARTS; ++u) start(true, u, pos, page0, page1, lds);
+#pragma unroll
+    for (int u = 0; u < PARTS; ++u) start(false, u, pos, page0, page1, lds + TILE);
+  }
+  __device__ __forceinline__ float value(int pos, int page, int d) const {
+    const uint8_t* v = vbase + page * vpage + (int64_t)(pos & in_page) * vtoken;
+    if constexpr (E4M3) return __builtin_amdgcn_cvt_f32_fp8((int)v[d], 0);
+    else return bf16_f32(reinterpret_cast<const uint16_t*>(v)[d]);
   }
 };
-
-// A tile's codes to bf16, in the tile's order.
-template <int D>
-__device__ __forceinline__ void widen_tile(const uint8_t* codes, uint8_t* tile) {
-  constexpr int PER_ROW = D / 16, ROWS = 64 / PER_ROW, PARTS = 2 * KEYS / ROWS;
-  const int lane = forget(threadIdx.x & 63), sub = lane / PER_ROW, at = lane % PER_ROW;
-#pragma unroll
-  for (int i = 0; i < PARTS; ++i) {
-    const uint4 v = *reinterpret_cast<const uint4*>(codes + i * 1024 + lane * 16);
-    const uint2 a = widen4(v.x), b = widen4(v.y), c = widen4(v.z), d = widen4(v.w);
-    const int r = i * ROWS + sub;  // (rows of values follow those of keys, and KEYS is a multiple of 16)
-    *reinterpret_cast<uint4*>(tile + attn_tile_at<D>(r, 2 * at)) = make_uint4(a.x, a.y, b.x, b.y);
-    *reinterpret_cast<uint4*>(tile + attn_tile_at<D>(r, 2 * at + 1)) = make_uint4(c.x, c.y, d.x, d.y);
-  }
-}
-
-// Waits until at most `left` of the wave's memory accesses are under way.
-template <int LEFT>
-__device__ __forceinline__ void memory_left() {
-  static_assert(LEFT < 64, "six bits");
-  __builtin_amdgcn_s_waitcnt(0x0F70 | (LEFT & 15) | (LEFT >> 4) << 14);
-  asm volatile("" ::: "memory");
-}
 
 // Keys of a part of a context of `length` positions: `parts` parts at most, whole
 // turns of a workgroup each.
@@ -148,9 +112,8 @@ struct Request {
 template <int D, bool E4M3>
 __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeArgs a) {
   using Copies = PageCopies<D, E4M3>;
-  constexpr int TILE = 2 * KEYS * D * 2;  // keys and values as bf16
-  // of a wave: two tiles as they come, and for codes one of bf16; at the end its outputs
-  constexpr int WAVE_BYTES = 2 * Copies::BYTES + (E4M3 ? TILE : 0);
+  constexpr int TILE = Copies::TILE;
+  constexpr int WAVE_BYTES = 4 * TILE;  // two tiles of keys and of values; at the end the wave's outputs
   static_assert(WAVE_BYTES >= 32 * D * 4, "32 rows of outputs");
   __shared__ __attribute__((aligned(1024))) uint8_t tiles[WAVES][WAVE_BYTES];
   __shared__ float stats[WAVES][2][32];
@@ -170,18 +133,17 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
   const int row = min(32 * block + (lane & 31), rows - 1);
   const int t = row / G;
   const int64_t q_row = (int64_t)n * a.T + t;
-  AttnRows<D, 1> r;
+  AttnRows<D> r;
   r.start();
   if (begin < end) {
-    r.load(0, a.q + q_row * a.q_stride + (kv * G + row % G) * D);
+    r.load(a.q + q_row * a.q_stride + (kv * G + row % G) * D);
     // the request's own tokens that the row sees
     const uint64_t sees = (a.tree ? a.tree[n * a.tree_stride + t] : ~0ull >> (63 - t)) & (~0ull >> (64 - a.T));
     const int32_t* table = a.table + (int64_t)req.row * a.table_width;
     const float c = a.scale * kLog2e * (E4M3 ? a.c.k_scale[kv] : 1.f);
-    const TilePlaces<D> places;
+    const TilePlaces<D, E4M3> places;
     const Copies copies(a.c, kv);
     uint8_t* const ring = tiles[wave];
-    uint8_t* const wide = ring + (E4M3 ? 2 * Copies::BYTES : 0);
     const int first = begin + wave * KEYS, count = (end - first + STEP - 1) / STEP;  // the wave's tiles
 
     TilePages pages;
@@ -193,9 +155,11 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
     Two now{-1, -1}, next{-1, -1}, after{-1, -1};
     auto fetch = [&](int tile) {
       after = pages_of(tile);
-      copies.start(first + tile * STEP, after.a, after.b, ring + (tile & 1) * Copies::BYTES);
+      copies.start(first + tile * STEP, after.a, after.b, ring + (tile & 1) * 2 * TILE);
     };
     if (count > 0) {
+      pages_of(0);
+      r.settle();
       fetch(0);
       now = after;
     }
@@ -215,25 +179,22 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
       return (uint32_t)seen & there;
     };
     bool not_finite = false;  // left out of a tile with masked rows
-    f32x16 s[1];
-    bf16x8 p[1][2];
-    float sum[1];
+    f32x16 s;
+    bf16x8 p[2];
+    float sum;
     int tile = 0;
-    // the tile's bytes, once they are there
+    auto place = [&]() {
+      const int at = (tile & 1) * 2 * TILE;
+      return TilePlaces<D, E4M3>(places, at, at + TILE);
+    };
+    // the tile is there
     auto land = [&]() {
       if (tile + 1 < count) memory_left<Copies::COUNT>();
       else memory_left<0>();
-      int at = (tile & 1) * Copies::BYTES;
-      if constexpr (E4M3) {
-        widen_tile<D>(ring + at, wide);
-        wave_order();
-        at = 0;
-      }
-      return TilePlaces<D>(places, at, at + TILE / 2);
     };
     // the tile is done with: its place takes the one after the next
     auto leave = [&]() {
-      if constexpr (!E4M3) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       if (tile + 2 < count) fetch(tile + 2);
     };
     auto step = [&]() {
@@ -245,32 +206,28 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
       bool far = false;
       while (first + tile * STEP + KEYS <= min(req.before, end) && now.a >= 0 && now.b >= 0) {
         // a tile that all rows see
-        const TilePlaces<D> at = land();
-        if (E4M3) leave();
-        r.scores(at, wide, s);
+        land();
+        const auto at = place();
+        s = r.scores(at, ring);
         far = r.try_weights(s, c, p, sum);
         if (__builtin_expect(far, 0)) break;
-        r.take(sum);
-        r.add(at, wide, p);
-        if (!E4M3) leave();
+        r.l += sum;
+        r.add(at, ring, p);
+        leave();
         step();
       }
       if (tile >= count) break;
+      const auto at = place();
       if (!far) {
-        const TilePlaces<D> at = land();
-        if (E4M3) leave();
-        r.scores(at, wide, s);
-        const uint32_t seen = seen_of(first + tile * STEP) >> (4 * h);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[0][i] = seen & 1u << key_of(i, 0) ? s[0][i] : kNone;
+        land();
+        s = r.scores(at, ring);
+        mask_scores(s, seen_of(first + tile * STEP));
         far = r.try_weights(s, c, p, sum);
       }
-      const int at0 = E4M3 ? 0 : (tile & 1) * Copies::BYTES;
-      const TilePlaces<D> at(places, at0, at0 + TILE / 2);
       if (far) r.weights_from_maximum(s, c, p, sum);
-      r.take(sum);
-      not_finite = r.add_masked(at, wide, p) || not_finite;
-      if (!E4M3) leave();
+      r.l += sum;
+      not_finite = r.add_masked(at, ring, p) || not_finite;
+      leave();
       step();
     }
     if (__builtin_expect(not_finite, 0))
@@ -280,11 +237,7 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
         for (int key = 0; key < KEYS; ++key) {
           const int page = key < 16 ? of.a : of.b, own = pos + key - req.before;
           if (pos + key >= end || page < 0) continue;
-          const uint8_t* v = copies.vbase + page * copies.vpage + (int64_t)((pos + key) & copies.in_page) * copies.vtoken;
-          r.add_not_finite(0, own < 0 || (sees >> (own & 63) & 1), [&](int d) {
-            if constexpr (E4M3) return __builtin_amdgcn_cvt_f32_fp8((int)v[d], 0);
-            else return bf16_f32(reinterpret_cast<const uint16_t*>(v)[d]);
-          });
+          r.add_not_finite(own < 0 || (sees >> (own & 63) & 1), [&](int d) { return copies.value(pos + key, page, d); });
         }
       }
   }
@@ -295,10 +248,10 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
 #pragma unroll
   for (int b = 0; b < D / 32; ++b)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) mine[(32 * b + key_of(i, h)) * 32 + (lane & 31)] = r.o[0][b][i];
-  const float total = r.total(0);
+    for (int i = 0; i < 16; ++i) mine[(32 * b + key_of(i, h)) * 32 + (lane & 31)] = r.o[b][i];
+  const float total = r.total();
   if (h == 0) {
-    stats[wave][0][lane] = r.m[0];
+    stats[wave][0][lane] = r.m;
     stats[wave][1][lane] = total;
   }
   tiles_barrier();

@@ -12,12 +12,15 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "kda_ssm_kernels.h"
 
 namespace kda {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
@@ -27,12 +30,14 @@ __device__ __forceinline__ f32x16 mfma32(const bf16x8& a, const bf16x8& b, const
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// Place of a 16-byte chunk of a tile's row, rows of D bf16: chunks are swizzled
-// within a row so that 32 rows' chunk c (a read with lane = row) and the chunks of
-// four rows in a row (a transposed read) are spread over the banks.  The swizzle
+// Place of a 16-byte chunk of a tile's row, rows of D bf16 or of D codes: chunks are
+// swizzled within a row so that 32 rows' chunk c (a read with lane = row) and the chunks of
+// the rows of a transposed read are spread over the banks.  The swizzle
 // repeats every 16 rows and is an exclusive or.
-template <int D>
+template <int D, bool E4M3>
 __device__ __forceinline__ int attn_tile_at(int row, int chunk) {
+  if constexpr (E4M3 && D == 128) return row * 128 + ((chunk ^ ((row >> 1) & 7)) << 4);
+  if constexpr (E4M3) return row * 64 + ((chunk ^ ((row >> 2) & 3)) << 4);
   if constexpr (D == 128) return row * 256 + ((chunk ^ (((row & 3) << 2) | ((row >> 2) & 3))) << 4);
   return row * 128 + ((chunk ^ ((((row >> 1) & 1) << 2) | ((row >> 2) & 3))) << 4);
 }
@@ -47,34 +52,104 @@ __device__ __forceinline__ int forget(int v) {
   return v;
 }
 
-// A lane's operands in a tile of a buffer of tiles (their distances multiples of
-// 256 bytes): rows of keys (chunk h), and for the transposed reads of values a
-// row 4 h + m / 4 of four, in a group of 16 lanes m.
-template <int D>
+// eight e4m3 codes to bf16 (exact)
+__device__ __forceinline__ bf16x8 widen8(const uint2& u) {
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  const b2 r[4] = {__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(u.x, 1.f, false),
+                   __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(u.x, 1.f, true),
+                   __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(u.y, 1.f, false),
+                   __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(u.y, 1.f, true)};
+  return bf16x8{r[0][0], r[0][1], r[1][0], r[1][1], r[2][0], r[2][1], r[3][0], r[3][1]};
+}
+
+// A lane's operands in tiles of 32 keys and of their values, of bf16 or of codes (at
+// multiples of 256 bytes): rows of keys, and transposed reads of values.  In a
+// group of 16 lanes, lane m of a transposed read of bf16 points to four columns of
+// row m / 4 of four, of codes to eight columns of row m / 2 of eight; lane i receives
+// column i of the 16.
+template <int D, bool E4M3>
 struct TilePlaces {
+  static constexpr int BYTES = 32 * D * (E4M3 ? 1 : 2);  // of a tile
   int row, col;
   __device__ __forceinline__ TilePlaces() {
     const int lane = threadIdx.x & 63, h = lane >> 5, m = lane & 15, g = (lane >> 4) & 1;
-    row = attn_tile_at<D>(lane & 31, h);
-    col = attn_tile_at<D>(4 * h + (m >> 2), 2 * g + ((m & 3) >> 1)) + (m & 1) * 8;
+    if constexpr (E4M3) {
+      row = attn_tile_at<D, true>(lane & 31, 0) + h * 8;
+      col = attn_tile_at<D, true>(4 * h + ((m >> 1) & 3) + (m & 8), g) + (m & 1) * 8;
+    } else {
+      row = attn_tile_at<D, false>(lane & 31, h);
+      col = attn_tile_at<D, false>(4 * h + (m >> 2), 2 * g + ((m & 3) >> 1)) + (m & 1) * 8;
+    }
   }
-  // the tile at `keys` and `values` bytes
+  // the tiles at `keys` and `values` bytes
   __device__ __forceinline__ TilePlaces(const TilePlaces& at, int keys, int values)
       : row(forget(at.row + keys)), col(forget(at.col + values)) {}
+  // an operand as it is read, and as it is used
+  using Raw = std::conditional_t<E4M3, uint2, bf16x8>;
+  static __device__ __forceinline__ bf16x8 use(const Raw& r) {
+    if constexpr (E4M3) return widen8(r);
+    else return r;
+  }
   // columns 16 step + 8 h .. + 7 of the lane's key
-  __device__ __forceinline__ bf16x8 keys(const uint8_t* tiles, int step) const {
-    return *reinterpret_cast<const bf16x8*>(tiles + (row ^ (step * 32)));
+  __device__ __forceinline__ Raw read_keys(const uint8_t* tiles, int step) const {
+    return *reinterpret_cast<const Raw*>(tiles + (row ^ (step * (E4M3 ? 16 : 32))));
   }
   // column 32 block + lane % 32, keys 16 step + 4 h + (0..3) and 8 more
+  __device__ __forceinline__ Raw read_values(const uint8_t* tiles, int block, int step) const {
+    if constexpr (E4M3) {
+      typedef __attribute__((address_space(3))) i32x2* lds_ptr;
+      return __builtin_bit_cast(
+          uint2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_ptr)(tiles + step * 16 * D + (col ^ (block * 32)))));
+    } else {
+      typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+      const int at = col ^ (block * 64);
+      const uint8_t* t = tiles + step * 32 * D;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(t + at));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(t + 16 * D + (at ^ 32)));
+      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  }
+  __device__ __forceinline__ bf16x8 keys(const uint8_t* tiles, int step) const { return use(read_keys(tiles, step)); }
   __device__ __forceinline__ bf16x8 values(const uint8_t* tiles, int block, int step) const {
-    typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-    const int at = col ^ (block * 64);
-    const uint8_t* t = tiles + step * 32 * D;
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(t + at));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(t + 16 * D + (at ^ 32)));
-    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    return use(read_values(tiles, block, step));
   }
 };
+
+// Waits until at most `left` of the wave's memory accesses are under way.
+template <int LEFT>
+__device__ __forceinline__ void memory_left() {
+  static_assert(LEFT < 64, "six bits");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (LEFT & 15) | (LEFT >> 4) << 14);
+  asm volatile("" ::: "memory");
+}
+
+// A copy of 1 KiB from memory to LDS, 16 bytes a lane in order, asynchronous: `from` + the
+// lane's offset, or a window's bytes (those behind its end are zeros).  Written out: for the
+// builtins the compiler would wait ahead of every transposed read of LDS until no copy is
+// under way.  memory_left waits for them; M0, which nothing else in these kernels uses, is
+// the place in LDS and takes effect one wait state later.
+__device__ __forceinline__ uint32_t lds_place(const uint8_t* p) {
+  typedef __attribute__((address_space(3))) const uint8_t* lds_ptr;
+  return (uint32_t)(uintptr_t)(lds_ptr)p;
+}
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+#if defined(__HIP_DEVICE_COMPILE__)
+__device__ __forceinline__ void copy_to_lds(uint32_t lds, uint64_t from, uint32_t offset) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(lds), "v"(offset), "s"(from)
+               : "memory");
+}
+__device__ __forceinline__ void copy_to_lds(uint32_t lds, const u32x4& window, uint32_t offset) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(lds), "v"(offset), "s"(window)
+               : "memory");
+}
+#else
+__device__ inline void copy_to_lds(uint32_t, uint64_t, uint32_t) {}
+__device__ inline void copy_to_lds(uint32_t, const u32x4&, uint32_t) {}
+#endif
 
 // A barrier for tiles that copies fill: it waits for the wave's reads and writes of
 // LDS, not (as one on all of LDS does) for its copies under way to other tiles.
@@ -110,7 +185,7 @@ __device__ __forceinline__ bf16x8 finite_only(const bf16x8& f) {
   return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
 }
 
-// The softmax's state of a wave's RB x 32 rows, and their outputs so far.  With c =
+// The softmax's state of a wave's 32 rows, and their outputs so far.  With c =
 // scale log2(e) > 0, weights are 2^(c (s - m)) for scores s = q . k; l is the sum of this half's,
 // o that of the weighted values.
 //
@@ -119,52 +194,51 @@ __device__ __forceinline__ bf16x8 finite_only(const bf16x8& f) {
 // grown too far (or m is still that of no key).  Only then the scores' maximum is
 // looked for, and what has been summed is brought to it: a weight is at most kFar, which costs
 // no accuracy (sums are floating point), and most blocks need no maximum.
-template <int D, int RB>
+template <int D>
 struct AttnRows {
   static constexpr float kFar = 4096.f;
-  bf16x8 q[RB][D / 16];
-  f32x16 o[RB][D / 32];
-  float m[RB], l[RB];
+  bf16x8 q[D / 16];
+  f32x16 o[D / 32];
+  float m, l;
 
   __device__ __forceinline__ void start() {
+    m = kNone;
+    l = 0.f;
 #pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      m[r] = kNone;
-      l[r] = 0.f;
+    for (int b = 0; b < D / 32; ++b)
 #pragma unroll
-      for (int b = 0; b < D / 32; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[r][b][i] = 0.f;
-    }
+      for (int i = 0; i < 16; ++i) o[b][i] = 0.f;
   }
-  // the lane's row of queries of block r
-  __device__ __forceinline__ void load(int r, const uint16_t* row) {
+  // the lane's row of queries
+  __device__ __forceinline__ void load(const uint16_t* row) {
     const int h = (threadIdx.x >> 5) & 1;
 #pragma unroll
     for (int s = 0; s < D / 16; ++s)
-      q[r][s] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(row + s * 16 + h * 8));
+      q[s] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(row + s * 16 + h * 8));
+  }
+  // They are there from here on: a wait for them later would be one for copies too.
+  __device__ __forceinline__ void settle() {
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) asm volatile("" : "+v"(q[s]));
   }
   // scores of a tile's 32 keys
-  __device__ __forceinline__ void scores(const TilePlaces<D>& at, const uint8_t* tile, f32x16 (&s)[RB]) const {
+  template <class Places>
+  __device__ __forceinline__ f32x16 scores(const Places& at, const uint8_t* tiles) const {
+    f32x16 s;
 #pragma unroll
-    for (int r = 0; r < RB; ++r)
+    for (int i = 0; i < 16; ++i) s[i] = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[r][i] = 0.f;
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      const bf16x8 f = at.keys(tile, k);
-#pragma unroll
-      for (int r = 0; r < RB; ++r) s[r] = mfma32(f, q[r][k], s[r]);
-    }
+    for (int k = 0; k < D / 16; ++k) s = mfma32(at.keys(tiles, k), q[k], s);
+    return s;
   }
-  // The scores of keys behind a row's own become none; rows from `top` on, keys from `key` on.
-  __device__ __forceinline__ void mask(f32x16 (&s)[RB], int key, int top) const {
-    const int lane = forget(threadIdx.x & 63);
+  // weights as operands
+  static __device__ __forceinline__ void operands(const float (&e)[16], bf16x8 (&p)[2]) {
 #pragma unroll
-    for (int r = 0; r < RB; ++r)
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        s[r][i] = key + key_of(i, lane >> 5) > top + 32 * r + (lane & 31) ? kNone : s[r][i];
+    for (int k = 0; k < 2; ++k) {
+      const float* f = e + 8 * k;
+      p[k] = __builtin_bit_cast(bf16x8, make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]),
+                                                   bf16_pair(f[6], f[7])));
+    }
   }
   // weights of scores from a maximum, as operands, and their sum
   static __device__ __forceinline__ float weights(const f32x16& s, float c, float mc, bf16x8 (&p)[2]) {
@@ -174,67 +248,84 @@ struct AttnRows {
       e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -mc));
       sum[i & 1] += e[i];
     }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float* f = e + 8 * k;
-      p[k] = __builtin_bit_cast(bf16x8, make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]),
-                                                   bf16_pair(f[6], f[7])));
-    }
+    operands(e, p);
     return sum[0] + sum[1];
   }
-  // Weights of the scores of 32 keys and their sums; whether a sum went too far.
-  __device__ __forceinline__ bool try_weights(const f32x16 (&s)[RB], float c, bf16x8 (&p)[RB][2], float (&sum)[RB]) const {
-    bool far = false;
+  // scores(n), add(p) and try_weights(s) of three blocks in one, in an order in which
+  // each covers the others: behind every product of matrices come the read of an operand
+  // DEPTH products ahead and the weights that execute in the product's shadow.  (The
+  // compiler, left to itself, puts all products ahead of all weights.)
+  template <class Places>
+  __device__ __forceinline__ bool turn(const Places& at, const uint8_t* ktiles, const uint8_t* vtiles, const f32x16& s,
+                                       float c, f32x16& n, bf16x8 (&p)[2], float& sum) {
+    constexpr int HALF = D / 16, COUNT = 2 * HALF, DEPTH = 3, EACH = 16 / COUNT;  // products of scores, all; weights each
+    typename Places::Raw f[COUNT];
+    auto read = [&](int i) {
+      f[i] = i < HALF ? at.read_keys(ktiles, i) : at.read_values(vtiles, (i - HALF) % (D / 32), (i - HALF) / (D / 32));
+    };
 #pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      sum[r] = weights(s[r], c, m[r] * c, p[r]);
-      far = far || !(sum[r] <= kFar);
+    for (int i = 0; i < DEPTH; ++i) read(i);
+    __builtin_amdgcn_sched_barrier(0);
+    const float mc = m * c;
+    float e[16], part[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) n[i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+      if (i + DEPTH < COUNT) read(i + DEPTH);
+      if (i < HALF) n = mfma32(Places::use(f[i]), q[i], n);
+      else o[(i - HALF) % (D / 32)] = mfma32(Places::use(f[i]), p[(i - HALF) / (D / 32)], o[(i - HALF) % (D / 32)]);
+#pragma unroll
+      for (int w = EACH * i; w < EACH * (i + 1); ++w) {
+        e[w] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[w], c, -mc));
+        part[w & 1] += e[w];
+        asm volatile("" : "+v"(e[w]), "+v"(part[w & 1]));  // here, not later
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    return __any(far);
+    operands(e, p);
+    sum = part[0] + part[1];
+    return __any(!(sum <= kFar));
+  }
+  // Weights of the scores of 32 keys and their sum; whether one went too far.
+  __device__ __forceinline__ bool try_weights(const f32x16& s, float c, bf16x8 (&p)[2], float& sum) const {
+    sum = weights(s, c, m * c, p);
+    return __any(!(sum <= kFar));
   }
   // The same from the scores' maximum, to which the state is brought.
-  __device__ __forceinline__ void weights_from_maximum(const f32x16 (&s)[RB], float c, bf16x8 (&p)[RB][2], float (&sum)[RB]) {
+  __device__ __forceinline__ void weights_from_maximum(const f32x16& s, float c, bf16x8 (&p)[2], float& sum) {
+    float top = s[0];
 #pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      float top = s[r][0];
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+    top = fmaxf(top, other_half(top));
+    const float now = fmaxf(top, m), keep = now == kNone ? 1.f : __builtin_amdgcn_exp2f((m - now) * c);
+    m = now;
+    l *= keep;
 #pragma unroll
-      for (int i = 1; i < 16; ++i) top = fmaxf(top, s[r][i]);
-      top = fmaxf(top, other_half(top));
-      const float now = fmaxf(top, m[r]), keep = now == kNone ? 1.f : __builtin_amdgcn_exp2f((m[r] - now) * c);
-      m[r] = now;
-      l[r] *= keep;
+    for (int b = 0; b < D / 32; ++b)
 #pragma unroll
-      for (int b = 0; b < D / 32; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[r][b][i] *= keep;
-      sum[r] = weights(s[r], c, now == kNone ? 0.f : now * c, p[r]);
-    }
-  }
-  __device__ __forceinline__ void take(const float (&sum)[RB]) {
-#pragma unroll
-    for (int r = 0; r < RB; ++r) l[r] += sum[r];
+      for (int i = 0; i < 16; ++i) o[b][i] *= keep;
+    sum = weights(s, c, now == kNone ? 0.f : now * c, p);
   }
   // Scores of 32 keys become weights; the state takes them in.
-  __device__ __forceinline__ void weigh(const f32x16 (&s)[RB], float c, bf16x8 (&p)[RB][2]) {
-    float sum[RB];
+  __device__ __forceinline__ void weigh(const f32x16& s, float c, bf16x8 (&p)[2]) {
+    float sum;
     if (__builtin_expect(try_weights(s, c, p, sum), 0)) weights_from_maximum(s, c, p, sum);
-    take(sum);
+    l += sum;
   }
   // o += V^T P^T for a tile's 32 keys
-  __device__ __forceinline__ void add(const TilePlaces<D>& at, const uint8_t* tile, const bf16x8 (&p)[RB][2]) {
+  template <class Places>
+  __device__ __forceinline__ void add(const Places& at, const uint8_t* tiles, const bf16x8 (&p)[2]) {
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int b = 0; b < D / 32; ++b) {
-        const bf16x8 v = at.values(tile, b, k);
-#pragma unroll
-        for (int r = 0; r < RB; ++r) o[r][b] = mfma32(v, p[r][k], o[r][b]);
-      }
+      for (int b = 0; b < D / 32; ++b) o[b] = mfma32(at.values(tiles, b, k), p[k], o[b]);
   }
   // The same where rows see different keys.  A weight of zero does not keep an
   // infinity or a NaN from a row, so where the tile holds any they are left out here:
   // the answer is true then, and add_not_finite has to bring them to the rows that see them.
-  __device__ __forceinline__ bool add_masked(const TilePlaces<D>& at, const uint8_t* tiles, const bf16x8 (&p)[RB][2]) {
+  template <class Places>
+  __device__ __forceinline__ bool add_masked(const Places& at, const uint8_t* tiles, const bf16x8 (&p)[2]) {
     bool bad = false;
 #pragma unroll
     for (int k = 0; k < 2; ++k)
@@ -249,29 +340,94 @@ struct AttnRows {
     for (int k = 0; k < 2; ++k)
 #pragma unroll
       for (int b = 0; b < D / 32; ++b) {
-        const bf16x8 v = finite_only(at.values(tiles, b, k));
-#pragma unroll
-        for (int r = 0; r < RB; ++r) o[r][b] = mfma32(v, p[r][k], o[r][b]);
+        o[b] = mfma32(finite_only(at.values(tiles, b, k)), p[k], o[b]);
         __builtin_amdgcn_sched_barrier(0);
       }
     return true;
   }
-  // The infinities and NaNs of one key's values, column(d) of it, to row block r if
-  // the lane's row sees the key.
+  // The infinities and NaNs of one key's values, column(d) of it, if the lane's row
+  // sees the key.
   template <class Column>
-  __device__ __forceinline__ void add_not_finite(int r, bool sees, Column column) {
+  __device__ __forceinline__ void add_not_finite(bool sees, Column column) {
     const int h = (threadIdx.x >> 5) & 1;
 #pragma unroll
     for (int b = 0; b < D / 32; ++b)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float v = column(32 * b + key_of(i, h));
-        o[r][b][i] += sees && !(fabsf(v) < __builtin_huge_valf()) ? v : 0.f;
+        o[b][i] += sees && !(fabsf(v) < __builtin_huge_valf()) ? v : 0.f;
       }
   }
-  // a row's whole sum
-  __device__ __forceinline__ float total(int r) const { return l[r] + other_half(l[r]); }
+  // the row's whole sum
+  __device__ __forceinline__ float total() const { return l + other_half(l); }
+  // the lane's part of a row of outputs, times f
+  __device__ __forceinline__ void store(uint16_t* row, float f) const {
+    uint16_t* out = row + 4 * ((threadIdx.x >> 5) & 1);
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<uint2*>(out + 32 * b + 2 * i) =
+            make_uint2(bf16_pair(o[b][i] * f, o[b][i + 1] * f), bf16_pair(o[b][i + 2] * f, o[b][i + 3] * f));
+  }
 };
+
+// The scores of keys whose bit in `seen` is not set become none (bit of key_of(i, h)).
+__device__ __forceinline__ void mask_scores(f32x16& s, uint32_t seen) {
+  const uint32_t mine = seen >> (4 * ((threadIdx.x >> 5) & 1));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s[i] = mine & 1u << key_of(i, 0) ? s[i] : kNone;
+}
+
+// A wave's rows over the blocks of 32 keys that the waves of a workgroup copy
+// together, in turns: turn j takes the scores of block j + 1, the weights of block j
+// and the product of block j - 1's weights with its values, which do not
+// depend on each other.  The source, in turn(j), waits for block j + 1's keys and block
+// j - 1's values, lets all waves pass, starts further copies and gives the
+// tiles' places; seen(j) has the bits of the keys of block j that the lane's row sees.
+// `blocks`: of the workgroup; `mine`: of them, those that any of the wave's rows sees;
+// source.open: below it all rows see all keys (turn(j) may lower it to above j).
+// Whether infinities or NaNs were left out of masked blocks.
+template <int D, class Source>
+__device__ __forceinline__ bool attend(AttnRows<D>& r, Source& source, float c, int blocks, int mine) {
+  const uint8_t *kt = source.ktiles, *vt = source.vtiles;
+  bool left_out = false;
+  f32x16 s;
+  bf16x8 p[2] = {};
+  int j = -1;
+  while (j <= blocks) {
+    if (j > 0 && j < source.open) {
+      f32x16 n;
+      float sum;
+      bool far;
+      do {
+        const auto at = source.turn(j);
+        far = r.turn(at, kt, vt, s, c, n, p, sum);
+        if (__builtin_expect(far, 0)) break;
+        r.l += sum;
+        s = n;
+      } while (++j < source.open);
+      if (!far) continue;
+      r.weights_from_maximum(s, c, p, sum);
+      r.l += sum;
+      s = n;
+    } else {
+      const auto at = source.turn(j);
+      if (j > 0 && j <= mine) {
+        if (j - 1 < source.open) r.add(at, vt, p);
+        else left_out = r.add_masked(at, vt, p) || left_out;
+      }
+      if (j >= 0 && j < mine) {
+        if (j >= source.open) mask_scores(s, source.seen(j));
+        r.weigh(s, c, p);
+      }
+      if (j + 1 < mine) s = r.scores(at, kt);
+    }
+    ++j;
+  }
+  memory_left<0>();  // no copy outlives the workgroup
+  return left_out;
+}
 
 // log sum exp(scale s) from a maximum of s, c = scale log2(e), and the sum
 __device__ __forceinline__ float lse_of(float m, float c, float total) {
