@@ -17,22 +17,22 @@ namespace {
 
 constexpr int WAVES = kAttnRows / 32;
 constexpr int KEYS = 32;  // of a block
-constexpr int AHEAD = 2;  // turns that copies run ahead of their use
+constexpr int RING = 4;   // tiles of keys, and of values, in LDS
 
 // The keys and values of one head of a sequence, for a wave of rows from `top` on.
 template <int D>
 struct PromptSource {
   using Places = TilePlaces<D, false>;
-  static constexpr int RING = AHEAD + 1, TILE = Places::BYTES;
+  static constexpr int TILE = Places::BYTES;
   static constexpr int PER_ROW = D / 8, ROWS = 64 / PER_ROW, PARTS = KEYS / ROWS;  // a copy's rows, a tile's copies
   static constexpr int COUNT = 2 * PARTS / WAVES;                                  // of a wave, keys and values
-  static_assert(COUNT >= 1 && PARTS <= WAVES, "whole tiles by all waves");
+  static_assert(COUNT >= 1 && (PARTS <= WAVES || WAVES * ROWS == 16), "a lane's rows have one swizzle");
   uint8_t *ktiles, *vtiles;
   Places places;
   int open;
   uint64_t kbase, vbase;
   int kbytes, vbytes, kfrom, vfrom, length, wave, row;
-  int kslot = 0, put_slot = 0;  // ring places that are read and filled next
+  int copied = 0, slot = 0;  // blocks of keys so far (values are two behind), and the next one's place
 
   __device__ __forceinline__ PromptSource(const AttnArgs& a, int64_t token, int length_, int kv, int wave_, int top,
                                           uint8_t* kt, uint8_t* vt)
@@ -44,30 +44,37 @@ struct PromptSource {
     kfrom = r * kbytes + in_row;
     vfrom = r * vbytes + in_row;
     row = top + (lane & 31);
-    put(0, -2);  // (no row is ahead of the sequence: zeros)
-    put(1, -1);
+    for (int i = 0; i < RING - 1; ++i) put();
   }
-  static __device__ __forceinline__ void next(int& slot) { slot = slot == (RING - 1) * TILE ? 0 : slot + TILE; }
-  __device__ __forceinline__ void put(int kblock, int vblock) {
+  // One of the COUNT copies of the next block of keys, and of the one of values two behind it
+  // (of block 0 while there is none).  A window's rows behind the sequence's end read as zeros.
+  __device__ __forceinline__ void put(int i) {
+    const int u = i * WAVES + wave;  // the copies of the keys' tile, then of the values'
+    const bool key = COUNT == 1 ? u < PARTS : i < COUNT / 2;
+    const int bytes = key ? kbytes : vbytes, first = (key ? copied : max(copied - 2, 0)) * KEYS;
+    const uint64_t base = key ? kbase : vbase;
+    const u32x4 window = {(uint32_t)base, (uint32_t)(base >> 32), (uint32_t)rows_bytes(first, length, KEYS, bytes), 0x00020000u};
+    const int more = PARTS > WAVES ? i % (PARTS / WAVES) * 16 * bytes : 0;
+    copy_to_lds(lds_place(key ? ktiles : vtiles) + (uint32_t)(slot + (u % PARTS) * 1024), window, (key ? kfrom : vfrom) + more);
+    if (i < COUNT - 1) return;
+    kbase += KEYS * (int64_t)kbytes;
+    if (copied >= 2) vbase += KEYS * (int64_t)vbytes;
+    ++copied;
+    slot = (slot + TILE) & (RING * TILE - 1);
+  }
+  __device__ __forceinline__ void put() {
 #pragma unroll
-    for (int i = 0; i < COUNT; ++i) {
-      const int u = i * WAVES + wave;  // the copies of the keys' tile, then of the values'
-      const bool key = u < PARTS;
-      const int bytes = key ? kbytes : vbytes, first = (key ? kblock : vblock) * KEYS;
-      const uint64_t base = (key ? kbase : vbase) + (int64_t)first * bytes;
-      const u32x4 window = {(uint32_t)base, (uint32_t)(base >> 32) & 0xffffu,
-                            (uint32_t)window_bytes_at(first, length, KEYS, bytes, D * 2), 0x00020000u};
-      copy_to_lds(lds_place((key ? ktiles : vtiles) + put_slot) + (u % PARTS) * 1024, window, key ? kfrom : vfrom);
-    }
-    next(put_slot);
+    for (int i = 0; i < COUNT; ++i) put(i);
   }
-  __device__ __forceinline__ Places turn(int j) {
-    memory_left<(AHEAD - 1) * COUNT>();
-    tiles_barrier();
-    put(j + 1 + AHEAD, j - 1 + AHEAD);
-    const Places at(places, kslot, kslot);
-    next(kslot);
-    return at;
+  // Of the block of keys b, and of values b - 2: the b-th ones copied.
+  __device__ __forceinline__ Places place(int b) const {
+    const int at = (b & (RING - 1)) * TILE;
+    return Places(places, at, at);
+  }
+  template <int READS>
+  __device__ __forceinline__ void turn() {
+    memory_left<COUNT>();
+    tiles_barrier<READS>();
   }
   __device__ __forceinline__ uint32_t seen(int j) const {
     const int n = row - j * KEYS;  // the last key that the row sees
@@ -76,9 +83,9 @@ struct PromptSource {
 };
 
 template <int D>
-__global__ __launch_bounds__(WAVES * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void kda_attn_kernel(AttnArgs a) {
+__global__ __launch_bounds__(WAVES * 64, 2) void kda_attn_kernel(AttnArgs a) {
   using Source = PromptSource<D>;
-  __shared__ __attribute__((aligned(1024))) uint8_t ktiles[Source::RING * Source::TILE], vtiles[Source::RING * Source::TILE];
+  __shared__ __attribute__((aligned(1024))) uint8_t ktiles[RING * Source::TILE], vtiles[RING * Source::TILE];
   // The heads of a slot side by side, a group's on one XCD where there are at least
   // as many groups as XCDs; a sequence's last, longest rows first.
   const int in = (int)(blockIdx.x % (unsigned)a.H), kv = in % a.KV, head = kv * (a.H / a.KV) + in / a.KV;

@@ -254,7 +254,7 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
     stats[wave][0][lane] = r.m;
     stats[wave][1][lane] = total;
   }
-  tiles_barrier();
+  tiles_barrier<0>();
   const int mine_row = threadIdx.x & 31, row_at = 32 * block + mine_row, cols = (threadIdx.x >> 5) * (D / 8);
   if (row_at >= rows) return;
   const float c = a.scale * kLog2e * (E4M3 && begin < end ? a.c.k_scale[kv] : 1.f);

@@ -9,7 +9,7 @@
 
 namespace kda {
 
-constexpr int kAttnRows = 256;  // query rows of a workgroup of the prefill
+constexpr int kAttnRows = 128;  // query rows of a workgroup of the prefill
 
 struct AttnArgs {
   Packing pk;

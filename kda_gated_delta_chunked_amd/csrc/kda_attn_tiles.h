@@ -70,6 +70,7 @@ __device__ __forceinline__ bf16x8 widen8(const uint2& u) {
 template <int D, bool E4M3>
 struct TilePlaces {
   static constexpr int BYTES = 32 * D * (E4M3 ? 1 : 2);  // of a tile
+  static constexpr int READS = E4M3 ? 2 : 3;             // of LDS for an operand of keys and one of values
   int row, col;
   __device__ __forceinline__ TilePlaces() {
     const int lane = threadIdx.x & 63, h = lane >> 5, m = lane & 15, g = (lane >> 4) & 1;
@@ -152,10 +153,13 @@ __device__ inline void copy_to_lds(uint32_t, const u32x4&, uint32_t) {}
 #endif
 
 // A barrier for tiles that copies fill: it waits for the wave's reads and writes of
-// LDS, not (as one on all of LDS does) for its copies under way to other tiles.
+// LDS but the last READS, not (as one on all of LDS does) for its copies under way to
+// other tiles.
+template <int READS>
 __device__ __forceinline__ void tiles_barrier() {
+  static_assert(READS < 16, "four bits");
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_s_waitcnt(0xC07F | READS << 8);  // lgkmcnt
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
@@ -231,15 +235,6 @@ struct AttnRows {
     for (int k = 0; k < D / 16; ++k) s = mfma32(at.keys(tiles, k), q[k], s);
     return s;
   }
-  // weights as operands
-  static __device__ __forceinline__ void operands(const float (&e)[16], bf16x8 (&p)[2]) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float* f = e + 8 * k;
-      p[k] = __builtin_bit_cast(bf16x8, make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]),
-                                                   bf16_pair(f[6], f[7])));
-    }
-  }
   // weights of scores from a maximum, as operands, and their sum
   static __device__ __forceinline__ float weights(const f32x16& s, float c, float mc, bf16x8 (&p)[2]) {
     float e[16], sum[2] = {0.f, 0.f};
@@ -248,44 +243,76 @@ struct AttnRows {
       e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -mc));
       sum[i & 1] += e[i];
     }
-    operands(e, p);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float* f = e + 8 * k;
+      p[k] = __builtin_bit_cast(bf16x8, make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]),
+                                                   bf16_pair(f[6], f[7])));
+    }
     return sum[0] + sum[1];
   }
-  // scores(n), add(p) and try_weights(s) of three blocks in one, in an order in which
-  // each covers the others: behind every product of matrices come the read of an operand
-  // DEPTH products ahead and the weights that execute in the product's shadow.  (The
-  // compiler, left to itself, puts all products ahead of all weights.)
+  // Products of a turn, one of scores and one of outputs alternately, and the
+  // operands that are read ahead.
+  static constexpr int COUNT = D / 8, DEPTH = 2;
+  static_assert(COUNT % DEPTH == 0, "operands of the next turn in the same places");
   template <class Places>
-  __device__ __forceinline__ bool turn(const Places& at, const uint8_t* ktiles, const uint8_t* vtiles, const f32x16& s,
-                                       float c, f32x16& n, bf16x8 (&p)[2], float& sum) {
-    constexpr int HALF = D / 16, COUNT = 2 * HALF, DEPTH = 3, EACH = 16 / COUNT;  // products of scores, all; weights each
-    typename Places::Raw f[COUNT];
-    auto read = [&](int i) {
-      f[i] = i < HALF ? at.read_keys(ktiles, i) : at.read_values(vtiles, (i - HALF) % (D / 32), (i - HALF) / (D / 32));
-    };
-#pragma unroll
-    for (int i = 0; i < DEPTH; ++i) read(i);
-    __builtin_amdgcn_sched_barrier(0);
+  static __device__ __forceinline__ typename Places::Raw operand(const Places& at, const uint8_t* ktiles,
+                                                                 const uint8_t* vtiles, int i) {
+    if (i % 2) return at.read_values(vtiles, i / 2 % (D / 32), i / 2 / (D / 32));
+    return at.read_keys(ktiles, i / 2);
+  }
+  // scores(n), add(p) and try_weights(s, next_p) of three blocks in one, in an order in which
+  // each covers the others: behind every product of matrices come the read of the operand
+  // DEPTH products ahead (f holds them; the last ones are those of the turn at `next`) and
+  // weights that execute in its shadow.  The weights are done three quarters through, so that
+  // nothing waits for them at the end.  (The compiler, left to itself, puts all products
+  // ahead of all weights.)
+  template <class Source, class Places = typename Source::Places>
+  __device__ __forceinline__ bool turn(Source& source, int j, typename Places::Raw (&f)[DEPTH], const f32x16& s, float c,
+                                       f32x16& n, const bf16x8 (&p)[2], bf16x8 (&next_p)[2], float& sum) {
+    const uint8_t *ktiles = source.ktiles, *vtiles = source.vtiles;
+    const Places at = source.place(j + 1), next = source.place(j + 2);
+    constexpr int EVERY = (COUNT - 2) / Source::COUNT;  // products between copies
+    static_assert(EVERY >= 1, "a copy behind a product");
+    constexpr int BUSY = COUNT * 3 / 4;
     const float mc = m * c;
-    float e[16], part[2] = {0.f, 0.f};
+    float e = 0.f, part[2] = {0.f, 0.f};
+    uint32_t pair[8];
+    bool far = false;
 #pragma unroll
     for (int i = 0; i < 16; ++i) n[i] = 0.f;
 #pragma unroll
     for (int i = 0; i < COUNT; ++i) {
-      if (i + DEPTH < COUNT) read(i + DEPTH);
-      if (i < HALF) n = mfma32(Places::use(f[i]), q[i], n);
-      else o[(i - HALF) % (D / 32)] = mfma32(Places::use(f[i]), p[(i - HALF) / (D / 32)], o[(i - HALF) % (D / 32)]);
+      const bf16x8 v = Places::use(f[i % DEPTH]);
+      if (i % 2) o[i / 2 % (D / 32)] = mfma32(v, p[i / 2 / (D / 32)], o[i / 2 % (D / 32)]);
+      else n = mfma32(v, q[i / 2], n);
+      const int ahead = i + DEPTH;
+      f[i % DEPTH] = ahead < COUNT ? operand(at, ktiles, vtiles, ahead) : operand(next, ktiles, vtiles, ahead - COUNT);
+      if (i < BUSY) {
 #pragma unroll
-      for (int w = EACH * i; w < EACH * (i + 1); ++w) {
-        e[w] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[w], c, -mc));
-        part[w & 1] += e[w];
-        asm volatile("" : "+v"(e[w]), "+v"(part[w & 1]));  // here, not later
+        for (int w = 16 * i / BUSY; w < 16 * (i + 1) / BUSY; ++w) {
+          const float now = __builtin_amdgcn_exp2f(__builtin_fmaf(s[w], c, -mc));
+          part[w & 1] += now;
+          if (w & 1) {
+            pair[w / 2] = bf16_pair(e, now);
+            asm volatile("" : "+v"(pair[w / 2]), "+v"(part[1]));  // here, not later
+          } else {
+            e = now;
+            asm volatile("" : "+v"(e), "+v"(part[0]));
+          }
+        }
+      }
+      if (i % EVERY == 1 % EVERY && i / EVERY < Source::COUNT) source.put(i / EVERY);
+      if (i == BUSY) {
+        sum = part[0] + part[1];
+        far = __any(!(sum <= kFar));
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    operands(e, p);
-    sum = part[0] + part[1];
-    return __any(!(sum <= kFar));
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      next_p[k] = __builtin_bit_cast(bf16x8, make_uint4(pair[4 * k], pair[4 * k + 1], pair[4 * k + 2], pair[4 * k + 3]));
+    return far;
   }
   // Weights of the scores of 32 keys and their sum; whether one went too far.
   __device__ __forceinline__ bool try_weights(const f32x16& s, float c, bf16x8 (&p)[2], float& sum) const {
@@ -382,48 +409,68 @@ __device__ __forceinline__ void mask_scores(f32x16& s, uint32_t seen) {
 // A wave's rows over the blocks of 32 keys that the waves of a workgroup copy
 // together, in turns: turn j takes the scores of block j + 1, the weights of block j
 // and the product of block j - 1's weights with its values, which do not
-// depend on each other.  The source, in turn(j), waits for block j + 1's keys and block
-// j - 1's values, lets all waves pass, starts further copies and gives the
-// tiles' places; seen(j) has the bits of the keys of block j that the lane's row sees.
+// depend on each other.  The source, in turn<READS>(), waits for the keys up to block j + 2
+// and the values up to block j and lets all waves pass (READS of a wave's reads of these
+// tiles may be under way); then its COUNT further copies are started, put(i); place(j + 1) is where block j + 1's
+// keys and block j - 1's values are; seen(j) has the bits of the keys of block j that the lane's row sees.
 // `blocks`: of the workgroup; `mine`: of them, those that any of the wave's rows sees;
-// source.open: below it all rows see all keys (turn(j) may lower it to above j).
+// source.open: below it all rows see all keys (a put may lower it to the block of keys it copies).
 // Whether infinities or NaNs were left out of masked blocks.
 template <int D, class Source>
 __device__ __forceinline__ bool attend(AttnRows<D>& r, Source& source, float c, int blocks, int mine) {
+  using Rows = AttnRows<D>;
+  using Places = typename Source::Places;
   const uint8_t *kt = source.ktiles, *vt = source.vtiles;
   bool left_out = false;
-  f32x16 s;
-  bf16x8 p[2] = {};
-  int j = -1;
-  while (j <= blocks) {
-    if (j > 0 && j < source.open) {
-      f32x16 n;
-      float sum;
-      bool far;
-      do {
-        const auto at = source.turn(j);
-        far = r.turn(at, kt, vt, s, c, n, p, sum);
-        if (__builtin_expect(far, 0)) break;
-        r.l += sum;
-        s = n;
-      } while (++j < source.open);
-      if (!far) continue;
-      r.weights_from_maximum(s, c, p, sum);
+  float sum;
+  bf16x8 p[2];
+  auto turn = [&](int j) {
+    source.template turn<0>();
+    source.put();
+    return source.place(j + 1);
+  };
+  f32x16 s = r.scores(turn(-1), kt);
+  f32x16 n = r.scores(turn(0), kt);
+  if (source.open < 1) mask_scores(s, source.seen(0));
+  r.weights_from_maximum(s, c, p, sum);
+  r.l += sum;
+  s = n;
+  int j = 1;
+  if (j < source.open) {
+    typename Places::Raw f[Rows::DEPTH];
+    bf16x8 next_p[2];
+    source.template turn<0>();
+    const Places at = source.place(j + 1);
+#pragma unroll
+    for (int i = 0; i < Rows::DEPTH; ++i) f[i] = Rows::operand(at, kt, vt, i);
+    // two turns, so that no scores and weights move from register to register
+    for (;;) {
+      if (__builtin_expect(r.turn(source, j, f, s, c, n, p, next_p, sum), 0)) r.weights_from_maximum(s, c, next_p, sum);
       r.l += sum;
-      s = n;
-    } else {
-      const auto at = source.turn(j);
-      if (j > 0 && j <= mine) {
-        if (j - 1 < source.open) r.add(at, vt, p);
-        else left_out = r.add_masked(at, vt, p) || left_out;
+      if (++j >= source.open) {
+        s = n;
+        p[0] = next_p[0];
+        p[1] = next_p[1];
+        break;
       }
-      if (j >= 0 && j < mine) {
-        if (j >= source.open) mask_scores(s, source.seen(j));
-        r.weigh(s, c, p);
-      }
-      if (j + 1 < mine) s = r.scores(at, kt);
+      source.template turn<Rows::DEPTH / 2 * Places::READS>();
+      if (__builtin_expect(r.turn(source, j, f, n, c, s, next_p, p, sum), 0)) r.weights_from_maximum(n, c, p, sum);
+      r.l += sum;
+      if (++j >= source.open) break;
+      source.template turn<Rows::DEPTH / 2 * Places::READS>();
     }
-    ++j;
+  }
+  for (; j <= blocks; ++j) {
+    const Places at = turn(j);
+    if (j <= mine) {
+      if (j - 1 < source.open) r.add(at, vt, p);
+      else left_out = r.add_masked(at, vt, p) || left_out;
+    }
+    if (j < mine) {
+      if (j >= source.open) mask_scores(s, source.seen(j));
+      r.weigh(s, c, p);
+    }
+    if (j + 1 < mine) s = r.scores(at, kt);
   }
   memory_left<0>();  // no copy outlives the workgroup
   return left_out;

@@ -20,10 +20,11 @@ __host__ __device__ inline int window_bytes(int left, int most, int row_bytes, i
   return rows > 0 ? (rows - 1) * row_bytes + width : 0;
 }
 
-// The same for the rows first .. first + most - 1 of a sequence of `length` rows,
-// where the first may be ahead of the sequence or behind it: no byte then.
-__host__ __device__ inline int window_bytes_at(int first, int length, int most, int row_bytes, int width) {
-  return first < 0 ? 0 : window_bytes(rows_left(first, length), most, row_bytes, width);
+// Bytes of a window on the rows first .. first + most - 1, `row_bytes` apart, that a sequence
+// of `length` rows has: it holds these rows' columns and none of the rows behind them.
+__host__ __device__ inline int rows_bytes(int first, int length, int most, int row_bytes) {
+  const int left = rows_left(first, length);
+  return left >= most ? most * row_bytes : (left > 0 ? left : 0) * row_bytes;
 }
 
 // Token spans.  A batch is covered by spans of `len` tokens that start at each
