@@ -24,7 +24,11 @@ __host__ __device__ inline int window_bytes(int left, int most, int row_bytes, i
 // of `length` rows has: it holds these rows' columns and none of the rows behind them.
 __host__ __device__ inline int rows_bytes(int first, int length, int most, int row_bytes) {
   const int left = rows_left(first, length);
-  return left >= most ? most * row_bytes : (left > 0 ? left : 0) * row_bytes;
+  int there = left > 0 ? left : 0;
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm("" : "+s"(there));  // two scalar instructions: together they would become a vector one
+#endif
+  return (there < most ? there : most) * row_bytes;
 }
 
 // Token spans.  A batch is covered by spans of `len` tokens that start at each

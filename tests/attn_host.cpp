@@ -2,6 +2,6 @@
 // for tests/test_attn_bounds.py.
 #include "kda_spans.h"
 
-extern "C" int kda_test_window_bytes_at(int first, int length, int most, int row_bytes, int width) {
-  return kda::window_bytes_at(first, length, most, row_bytes, width);
+extern "C" int kda_test_rows_bytes(int first, int length, int most, int row_bytes) {
+  return kda::rows_bytes(first, length, most, row_bytes);
 }

@@ -25,16 +25,20 @@ def lib(tmp_path_factory):
 
 @pytest.mark.parametrize("row_bytes,width", [(128, 128), (3328, 256), ((1 << 24) - 16, 256)])
 def test_a_window_holds_rows_of_the_sequence_alone(lib, row_bytes, width):
-    for most in (32, 64):
-        for length in (1, 31, 32, 33, 300, (1 << 31) - 1):
-            for first in (-64, -32, -1, 0, 1, 32, length - 1, length, min(length + 96, (1 << 31) - 1)):
-                rows = 0 if first < 0 else max(0, min(most, length - first))
-                want = (rows - 1) * row_bytes + width if rows else 0
-                assert lib.kda_test_window_bytes_at(first, length, most, row_bytes, width) == want < 1 << 31
+    most = 32
+    for length in (1, 31, 32, 33, 300, (1 << 31) - 1):
+        for first in (0, 1, 32, length - 1, length, min(length + 96, (1 << 31) - 1)):
+            rows = max(0, min(most, length - first))
+            assert lib.kda_test_rows_bytes(first, length, most, row_bytes) == rows * row_bytes < 1 << 31
+            # which holds these rows' columns, and nothing of others
+            assert all(r * row_bytes + width <= rows * row_bytes for r in range(rows))
+            assert all(r * row_bytes >= rows * row_bytes for r in range(rows, most))
 
 
 def test_every_copy_goes_through_a_window():
     text = open(os.path.join(CSRC, "kda_attn.hip")).read()
-    assert len(re.findall(r" lds\"", text)) == 1 and len(re.findall(r"window_bytes_at\(first, length, KEYS, bytes, D \* 2\)", text)) == 1
-    # and is waited for before the workgroup ends
-    assert "memory_left<0>();" in text
+    # one kind of copy, of a window whose rows are counted, from the sequence's first row on
+    assert len(re.findall(r"copy_to_lds\(", text)) == 1 and "rows_bytes(first, length, KEYS, bytes)" in text
+    assert "(key ? copied : max(copied - 2, 0)) * KEYS" in text
+    # and all are waited for before the workgroup ends
+    assert "memory_left<0>();  // no copy outlives the workgroup" in open(os.path.join(CSRC, "kda_attn_tiles.h")).read()
