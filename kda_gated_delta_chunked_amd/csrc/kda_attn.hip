@@ -15,12 +15,13 @@
 namespace kda {
 namespace {
 
-constexpr int WAVES = kAttnRows / 32;
-constexpr int KEYS = 32;  // of a block
-constexpr int RING = 4;   // tiles of keys, and of values, in LDS
+constexpr int WAVES = kAttnRows / 32;  // that share rows' keys
+constexpr int KEYS = 32;               // of a block
+constexpr int RING = 4;                // tiles of keys, and of values, in LDS
 
-// The keys and values of one head of a sequence, for a wave of rows from `top` on.
-template <int D>
+// The keys and values of one head of a sequence, every SPLIT-th block of them from
+// block `side` on, for a wave of rows from `top` on.
+template <int D, int SPLIT>
 struct PromptSource {
   using Places = TilePlaces<D, false>;
   static constexpr int TILE = Places::BYTES;
@@ -31,14 +32,15 @@ struct PromptSource {
   Places places;
   int open;
   uint64_t kbase, vbase;
-  int kbytes, vbytes, kfrom, vfrom, length, wave, row;
+  int kbytes, vbytes, kfrom, vfrom, length, wave, side, row;
   int copied = 0, slot = 0;  // blocks of keys so far (values are two behind), and the next one's place
 
-  __device__ __forceinline__ PromptSource(const AttnArgs& a, int64_t token, int length_, int kv, int wave_, int top,
-                                          uint8_t* kt, uint8_t* vt)
-      : ktiles(kt), vtiles(vt), open(top / KEYS), kbase(reinterpret_cast<uint64_t>(a.k + token * a.k_stride + kv * D)),
-        vbase(reinterpret_cast<uint64_t>(a.v + token * a.v_stride + kv * D)), kbytes((int)a.k_stride * 2),
-        vbytes((int)a.v_stride * 2), length(length_), wave(wave_) {
+  __device__ __forceinline__ PromptSource(const AttnArgs& a, int64_t token, int length_, int kv, int wave_, int side_, int top,
+                                          uint8_t* tiles)
+      : ktiles(tiles), vtiles(tiles + RING * TILE), open(count(top / KEYS, side_)),
+        kbase(reinterpret_cast<uint64_t>(a.k + (token + side_ * KEYS) * a.k_stride + kv * D)),
+        vbase(reinterpret_cast<uint64_t>(a.v + (token + side_ * KEYS) * a.v_stride + kv * D)), kbytes((int)a.k_stride * 2),
+        vbytes((int)a.v_stride * 2), length(length_ - side_ * KEYS), wave(wave_), side(side_) {
     const int lane = threadIdx.x & 63, r = wave % PARTS * ROWS + lane / PER_ROW;
     const int in_row = attn_tile_at<D, false>(r, lane % PER_ROW) & (D * 2 - 1);
     kfrom = r * kbytes + in_row;
@@ -46,19 +48,21 @@ struct PromptSource {
     row = top + (lane & 31);
     for (int i = 0; i < RING - 1; ++i) put();
   }
+  // how many of the first n blocks are this side's
+  static __device__ __forceinline__ int count(int n, int side) { return (n - side + SPLIT - 1) / SPLIT; }
   // One of the COUNT copies of the next block of keys, and of the one of values two behind it
   // (of block 0 while there is none).  A window's rows behind the sequence's end read as zeros.
   __device__ __forceinline__ void put(int i) {
     const int u = i * WAVES + wave;  // the copies of the keys' tile, then of the values'
     const bool key = COUNT == 1 ? u < PARTS : i < COUNT / 2;
-    const int bytes = key ? kbytes : vbytes, first = (key ? copied : max(copied - 2, 0)) * KEYS;
+    const int bytes = key ? kbytes : vbytes, first = (key ? copied : max(copied - 2, 0)) * (KEYS * SPLIT);
     const uint64_t base = key ? kbase : vbase;
     const u32x4 window = {(uint32_t)base, (uint32_t)(base >> 32), (uint32_t)rows_bytes(first, length, KEYS, bytes), 0x00020000u};
     const int more = PARTS > WAVES ? i % (PARTS / WAVES) * 16 * bytes : 0;
     copy_to_lds(lds_place(key ? ktiles : vtiles) + (uint32_t)(slot + (u % PARTS) * 1024), window, (key ? kfrom : vfrom) + more);
     if (i < COUNT - 1) return;
-    kbase += KEYS * (int64_t)kbytes;
-    if (copied >= 2) vbase += KEYS * (int64_t)vbytes;
+    kbase += KEYS * SPLIT * (int64_t)kbytes;
+    if (copied >= 2) vbase += KEYS * SPLIT * (int64_t)vbytes;
     ++copied;
     slot = (slot + TILE) & (RING * TILE - 1);
   }
@@ -77,41 +81,84 @@ struct PromptSource {
     tiles_barrier<READS>();
   }
   __device__ __forceinline__ uint32_t seen(int j) const {
-    const int n = row - j * KEYS;  // the last key that the row sees
+    const int n = row - (SPLIT * j + side) * KEYS;  // the last key that the row sees
     return n < 0 ? 0u : n >= 31 ? ~0u : (2u << n) - 1;
   }
 };
 
-template <int D>
-__global__ __launch_bounds__(WAVES * 64, 2) void kda_attn_kernel(AttnArgs a) {
-  using Source = PromptSource<D>;
-  __shared__ __attribute__((aligned(1024))) uint8_t ktiles[RING * Source::TILE], vtiles[RING * Source::TILE];
+// The span of a slot, as span_of; of a packed batch of fewer than 64 sequences with one load
+// of all offsets.
+__device__ __forceinline__ Span rows_of_slot(const Packing& p, int64_t slot) {
+  if (!p.cu || p.N >= 64) return span_of(p, kAttnRows, slot);
+  const int lane = threadIdx.x & 63;
+  const uint32_t at = (uint32_t)cu_at(p, min(lane, p.N));
+  const uint64_t ahead = __ballot(lane == 0 || (lane < p.N && (int64_t)(at / kAttnRows) + lane <= slot));
+  const int seq = ~ahead ? __ffsll((long long)~ahead) - 2 : 63;
+  Span s;
+  s.seq = seq;
+  s.begin = (uint32_t)__builtin_amdgcn_readlane((int)at, seq);
+  s.end = (uint32_t)__builtin_amdgcn_readlane((int)at, seq + 1);
+  if (s.end < s.begin) s.end = s.begin;
+  const int64_t k = slot - first_slot(p, kAttnRows, seq, s.begin);
+  s.k = k < 0 || (k > 0 && k * kAttnRows >= s.end - s.begin) ? -1 : (int)k;
+  return s;
+}
+
+template <int D, int SPLIT>
+__global__ __launch_bounds__(SPLIT * WAVES * 64, 2) void kda_attn_kernel(AttnArgs a) {
+  using Source = PromptSource<D, SPLIT>;
+  __shared__ __attribute__((aligned(1024))) uint8_t tiles[SPLIT][2 * RING * Source::TILE];
   // The heads of a slot side by side, a group's on one XCD where there are at least
   // as many groups as XCDs; a sequence's last, longest rows first.
   const int in = (int)(blockIdx.x % (unsigned)a.H), kv = in % a.KV, head = kv * (a.H / a.KV) + in / a.KV;
   int64_t slot = a.slots - 1 - blockIdx.x / (unsigned)a.H;
   if (!a.pk.cu) slot = (slot % a.pk.N) * fixed_slots(a.pk, kAttnRows) + slot / a.pk.N;
-  const Span span = span_of(a.pk, kAttnRows, slot);
+  const Span span = rows_of_slot(a.pk, slot);
   const int length = rows_left(span.begin, span.end);
   if (span.k < 0 || length == 0) return;
   const int first = span.k * kAttnRows;
 
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int top = first + wave * 32, row = top + (lane & 31);  // the wave's first row, the lane's
+  const int of_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = of_all % WAVES, side = of_all / WAVES;
+  const int lane = threadIdx.x & 63, top = first + wave * 32, row = top + (lane & 31);  // the wave's first row, the lane's
   AttnRows<D> r;
   r.load(a.q + (span.begin + min(row, length - 1)) * a.q_stride + head * D);
   r.start();
   const float c = a.scale * kLog2e;
   const int blocks = (min(first + kAttnRows, length) + KEYS - 1) / KEYS;  // that any row sees
   const int mine = top < length ? min(blocks, top / KEYS + 1) : 0;        // any row of the wave
-  Source source(a, span.begin, length, kv, wave, top, ktiles, vtiles);
-  source.open = min(source.open, mine);
+  Source source(a, span.begin, length, kv, wave, side, top, tiles[side]);
   r.settle();
-  if (__builtin_expect(attend(r, source, c, blocks, mine), 0))
-    for (int key = source.open * KEYS; key < min(mine * KEYS, length); ++key) {
+  if (__builtin_expect(attend(r, source, c, Source::count(blocks, 0), Source::count(mine, side)), 0))
+    for (int key = 0; key < min(mine * KEYS, length); ++key) {
+      if (key / KEYS % SPLIT != side) continue;
       const uint16_t* v = a.v + (span.begin + key) * a.v_stride + kv * D;
       r.add_not_finite(key <= row, [&](int d) { return bf16_f32(v[d]); });
     }
+  if constexpr (SPLIT == 2) {
+    // the sides, joined lane by lane
+    constexpr int REGS = D / 2 + 2;
+    float* mine_of = reinterpret_cast<float*>(tiles) + wave * REGS * 64 + lane;
+    static_assert(WAVES * REGS * 64 * 4 <= (int)sizeof(tiles), "a side's outputs");
+    tiles_barrier<0>();
+    if (side) {
+#pragma unroll
+      for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) mine_of[(16 * b + i) * 64] = r.o[b][i];
+      mine_of[(D / 2) * 64] = r.m;
+      mine_of[(D / 2 + 1) * 64] = r.l;
+    }
+    tiles_barrier<0>();
+    if (side) return;
+    const float m = mine_of[(D / 2) * 64], top_m = fmaxf(m, r.m);
+    const float here = __builtin_amdgcn_exp2f((r.m - top_m) * c), there = m == kNone ? 0.f : __builtin_amdgcn_exp2f((m - top_m) * c);
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) r.o[b][i] = here * r.o[b][i] + there * mine_of[(16 * b + i) * 64];
+    r.l = here * r.l + there * mine_of[(D / 2 + 1) * 64];
+    r.m = top_m;
+  }
   const float total = r.total();
   if (row >= length) return;
   const int64_t token = span.begin + row;
@@ -121,8 +168,9 @@ __global__ __launch_bounds__(WAVES * 64, 2) void kda_attn_kernel(AttnArgs a) {
 
 template <int D>
 void launch(const AttnArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)attn_blocks(a.slots, a.H));
-  hipLaunchKernelGGL(kda_attn_kernel<D>, grid, dim3(WAVES * 64), 0, stream, a);
+  const int64_t blocks = attn_blocks(a.slots, a.H);
+  if (blocks <= 512) hipLaunchKernelGGL((kda_attn_kernel<D, 2>), dim3((unsigned)blocks), dim3(2 * WAVES * 64), 0, stream, a);
+  else hipLaunchKernelGGL((kda_attn_kernel<D, 1>), dim3((unsigned)blocks), dim3(WAVES * 64), 0, stream, a);
 }
 
 }  // namespace

@@ -167,16 +167,19 @@ __device__ __forceinline__ void tiles_barrier() {
 // what the other half of the wave holds for the same query row
 __device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32, 64); }
 
-// Whether a fragment holds an infinity or a NaN (per lane).
-__device__ __forceinline__ bool not_finite(const bf16x8& f) {
-  const uint4 u = __builtin_bit_cast(uint4, f);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  bool bad = false;
+// The largest exponents of two columns of halves (bf16 without their signs), over fragments:
+// whether any of them was an infinity or a NaN.
+struct Exponents {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 top = {0, 0};
+  __device__ __forceinline__ void take(const bf16x8& f) {
+    const uint4 u = __builtin_bit_cast(uint4, f);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    bad = bad || (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u;
-  return bad;
-}
+    for (int i = 0; i < 4; ++i) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu));
+  }
+  __device__ __forceinline__ bool not_finite() const { return top[0] >= 0x7f80 || top[1] >= 0x7f80; }
+};
 // The fragment with zeros in the place of infinities and NaNs.
 __device__ __forceinline__ bf16x8 finite_only(const bf16x8& f) {
   const uint4 u = __builtin_bit_cast(uint4, f);
@@ -319,7 +322,8 @@ struct AttnRows {
     sum = weights(s, c, m * c, p);
     return __any(!(sum <= kFar));
   }
-  // The same from the scores' maximum, to which the state is brought.
+  // The same from the scores' maximum, to which the state is brought (FIRST: there is none yet).
+  template <bool FIRST = false>
   __device__ __forceinline__ void weights_from_maximum(const f32x16& s, float c, bf16x8 (&p)[2], float& sum) {
     float top = s[0];
 #pragma unroll
@@ -327,11 +331,13 @@ struct AttnRows {
     top = fmaxf(top, other_half(top));
     const float now = fmaxf(top, m), keep = now == kNone ? 1.f : __builtin_amdgcn_exp2f((m - now) * c);
     m = now;
-    l *= keep;
+    if (!FIRST) {
+      l *= keep;
 #pragma unroll
-    for (int b = 0; b < D / 32; ++b)
+      for (int b = 0; b < D / 32; ++b)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[b][i] *= keep;
+        for (int i = 0; i < 16; ++i) o[b][i] *= keep;
+    }
     sum = weights(s, c, now == kNone ? 0.f : now * c, p);
   }
   // Scores of 32 keys become weights; the state takes them in.
@@ -353,14 +359,15 @@ struct AttnRows {
   // the answer is true then, and add_not_finite has to bring them to the rows that see them.
   template <class Places>
   __device__ __forceinline__ bool add_masked(const Places& at, const uint8_t* tiles, const bf16x8 (&p)[2]) {
-    bool bad = false;
+    Exponents most;
+    typename Places::Raw v[2 * (D / 32)];
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int i = 0; i < 2 * (D / 32); ++i) v[i] = at.read_values(tiles, i % (D / 32), i / (D / 32));
 #pragma unroll
-      for (int b = 0; b < D / 32; ++b) bad = bad || not_finite(at.values(tiles, b, k));
-    bad = __any(bad);
-    if (__builtin_expect(!bad, 1)) {
-      add(at, tiles, p);
+    for (int i = 0; i < 2 * (D / 32); ++i) most.take(Places::use(v[i]));
+    if (__builtin_expect(!__any(most.not_finite()), 1)) {
+#pragma unroll
+      for (int i = 0; i < 2 * (D / 32); ++i) o[i % (D / 32)] = mfma32(Places::use(v[i]), p[i / (D / 32)], o[i % (D / 32)]);
       return false;
     }
 #pragma unroll
@@ -424,44 +431,53 @@ __device__ __forceinline__ bool attend(AttnRows<D>& r, Source& source, float c, 
   bool left_out = false;
   float sum;
   bf16x8 p[2];
-  auto turn = [&](int j) {
-    source.template turn<0>();
-    source.put();
-    return source.place(j + 1);
-  };
-  f32x16 s = r.scores(turn(-1), kt);
-  f32x16 n = r.scores(turn(0), kt);
+  // blocks 0 and 1: their keys are there with the first turn
+  source.template turn<0>();
+  source.put();
+  f32x16 s = r.scores(source.place(0), kt), n = r.scores(source.place(1), kt);
   if (source.open < 1) mask_scores(s, source.seen(0));
-  r.weights_from_maximum(s, c, p, sum);
+  r.template weights_from_maximum<true>(s, c, p, sum);
   r.l += sum;
   s = n;
+  source.template turn<0>();
+  source.put();
   int j = 1;
-  if (j < source.open) {
-    typename Places::Raw f[Rows::DEPTH];
-    bf16x8 next_p[2];
-    source.template turn<0>();
+  typename Places::Raw f[Rows::DEPTH];
+  auto read_ahead = [&]() {
     const Places at = source.place(j + 1);
 #pragma unroll
     for (int i = 0; i < Rows::DEPTH; ++i) f[i] = Rows::operand(at, kt, vt, i);
-    // two turns, so that no scores and weights move from register to register
+  };
+  bf16x8 next_p[2];
+  if (j < source.open) {
+    source.template turn<0>();
+    read_ahead();
     for (;;) {
       if (__builtin_expect(r.turn(source, j, f, s, c, n, p, next_p, sum), 0)) r.weights_from_maximum(s, c, next_p, sum);
       r.l += sum;
-      if (++j >= source.open) {
-        s = n;
-        p[0] = next_p[0];
-        p[1] = next_p[1];
-        break;
-      }
-      source.template turn<Rows::DEPTH / 2 * Places::READS>();
-      if (__builtin_expect(r.turn(source, j, f, n, c, s, next_p, p, sum), 0)) r.weights_from_maximum(n, c, p, sum);
-      r.l += sum;
+      s = n;
+      p[0] = next_p[0];
+      p[1] = next_p[1];
       if (++j >= source.open) break;
       source.template turn<Rows::DEPTH / 2 * Places::READS>();
     }
   }
+  if (j == source.open && j < mine) {
+    // the first block with masked scores, behind one without
+    source.template turn<0>();
+    read_ahead();
+    mask_scores(s, source.seen(j));
+    if (__builtin_expect(r.turn(source, j, f, s, c, n, p, next_p, sum), 0)) r.weights_from_maximum(s, c, next_p, sum);
+    r.l += sum;
+    s = n;
+    p[0] = next_p[0];
+    p[1] = next_p[1];
+    ++j;
+  }
   for (; j <= blocks; ++j) {
-    const Places at = turn(j);
+    source.template turn<0>();
+    source.put();
+    const Places at = source.place(j + 1);
     if (j <= mine) {
       if (j - 1 < source.open) r.add(at, vt, p);
       else left_out = r.add_masked(at, vt, p) || left_out;
