@@ -75,7 +75,7 @@ kda_status kda_attn_prefill(const kda_attn_problem* p, const uint16_t* q, const 
 
 /* ---------------------------------------------------------------------------
  * The cache.  Keys and values lie in pages of page_size tokens, in two buffers
- * [num_pages, page_size, num_kv_heads, head_dim] (they may be halves of one): elements are
+ * [num_pages, page_size, num_kv_heads, head_dim] of the same strides (they may be halves of one): elements are
  * bf16, or e4m3 codes that stand for code * scale with an fp32 scale > 0 per
  * head.  A token's slot is page * page_size + its place in the page.  A block
  * table int32 [table_rows, table_width] names each request's pages in order: position
@@ -89,12 +89,10 @@ typedef struct {
   int32_t dtype;             /* kda_cache_dtype */
   int32_t page_size;         /* a power of two in 16..1024 */
   int64_t num_pages;         /* 1 .. 2^31 - 1 */
-  int64_t k_page_stride;     /* elements between pages: a multiple of 16, at least the page and
+  int64_t page_stride;       /* elements between pages: a multiple of 16, at least the page and
                                 at most 2^40; 0 = page_size token strides */
-  int64_t k_token_stride;    /* elements between a page's tokens: a multiple of 16, at least
+  int64_t token_stride;      /* elements between a page's tokens: a multiple of 16, at least
                                 num_kv_heads * head_dim and below 2^23; 0 = packed */
-  int64_t v_page_stride;
-  int64_t v_token_stride;
 } kda_kv_cache;
 
 /* Attention of T tokens of each of N requests over the cache, which holds their

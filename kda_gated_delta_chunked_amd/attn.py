@@ -37,8 +37,7 @@ class KvCache(ctypes.Structure):
     """Mirror of ``kda_kv_cache``."""
 
     _fields_ = [("num_kv_heads", _i32), ("head_dim", _i32), ("dtype", _i32), ("page_size", _i32),
-                ("num_pages", _i64), ("k_page_stride", _i64), ("k_token_stride", _i64), ("v_page_stride", _i64),
-                ("v_token_stride", _i64)]
+                ("num_pages", _i64), ("page_stride", _i64), ("token_stride", _i64)]
 
 
 class DecodeProblem(ctypes.Structure):
@@ -184,9 +183,10 @@ def _cache(k_cache, v_cache, k_scale, v_scale, dev) -> KvCache:
         if e4m3 != (s is not None):
             raise ValueError(f"{name} is for a float8_e4m3fn cache" if s is not None else f"an 8-bit cache needs {name}")
         _check_tensor(name, s, torch.float32, (KV,), dev)
-    kp, kt = _strides("k_cache", k_cache)
-    vp, vt = _strides("v_cache", v_cache)
-    return KvCache(KV, D, int(e4m3), size, P, kp, kt, vp, vt)
+    strides = _strides("k_cache", k_cache)
+    if strides != _strides("v_cache", v_cache):
+        raise ValueError("k_cache and v_cache must have the same strides")
+    return KvCache(KV, D, int(e4m3), size, P, *strides)
 
 
 def _table(table, rows, N, dev):

@@ -71,12 +71,10 @@ kda_status check_heads(int32_t H, int32_t KV, int32_t D, float scale) {
 // ---------------------------------------------------------------------------
 // cache
 
-int64_t token_stride(int64_t stride, const kda_kv_cache& c) {
-  return stride_of(stride, (int64_t)c.num_kv_heads * c.head_dim);
-}
-int64_t page_stride(int64_t stride, int64_t token, const kda_kv_cache& c) {
-  return stride ? stride : token * c.page_size;
-}
+int64_t row_elements(const kda_kv_cache& c) { return (int64_t)c.num_kv_heads * c.head_dim; }
+int64_t token_stride(const kda_kv_cache& c) { return stride_of(c.token_stride, row_elements(c)); }
+int64_t page_stride(const kda_kv_cache& c) { return stride_of(c.page_stride, token_stride(c) * c.page_size); }
+int64_t page_elements(const kda_kv_cache& c) { return token_stride(c) * (c.page_size - 1) + row_elements(c); }
 
 bool page_size_ok(int32_t s) { return s >= 16 && s <= 1024 && (s & (s - 1)) == 0; }
 int page_shift(int32_t s) { return __builtin_ctz((unsigned)s); }
@@ -86,39 +84,28 @@ kda_status check_cache(const kda_kv_cache& c) {
   if (c.dtype != KDA_CACHE_BF16 && c.dtype != KDA_CACHE_E4M3) return KDA_ERR_UNSUPPORTED;
   if (!page_size_ok(c.page_size)) return KDA_ERR_UNSUPPORTED;
   if (c.num_kv_heads < 1 || c.num_pages < 1) return KDA_ERR_INVALID_ARG;
-  const int64_t row = (int64_t)c.num_kv_heads * c.head_dim;
+  const int64_t row = row_elements(c), token = c.token_stride, page = c.page_stride;
   if (c.num_pages > kInt32Max || row >= kRowElements) return KDA_ERR_TOO_LARGE;
-  for (int64_t s : {c.k_token_stride, c.v_token_stride})
-    if (s && (s < row || s % 16 || s >= kRowElements)) return KDA_ERR_INVALID_ARG;
-  for (auto [s, t] : {std::pair{c.k_page_stride, c.k_token_stride}, std::pair{c.v_page_stride, c.v_token_stride}}) {
-    const int64_t page = token_stride(t, c) * (c.page_size - 1) + row;
-    if (s && (s < page || s % 16)) return KDA_ERR_INVALID_ARG;
-    if (s > (int64_t)1 << 40) return KDA_ERR_TOO_LARGE;
-  }
-  return KDA_OK;
+  if (token && (token < row || token % 16 || token >= kRowElements)) return KDA_ERR_INVALID_ARG;
+  if (page && (page < page_elements(c) || page % 16)) return KDA_ERR_INVALID_ARG;
+  return page > (int64_t)1 << 40 ? KDA_ERR_TOO_LARGE : KDA_OK;
 }
 
+uint64_t element_bytes(const kda_kv_cache& c) { return c.dtype == KDA_CACHE_BF16 ? 2 : 1; }
 // (strides are at most 2^40 elements, pages below 2^31: at the worst 2^72 bytes)
-Range cache_range(const void* p, int64_t page, int64_t token, const kda_kv_cache& c) {
-  const int64_t t = token_stride(token, c), s = page_stride(page, t, c);
-  const int64_t row = (int64_t)c.num_kv_heads * c.head_dim, in_page = t * (c.page_size - 1) + row;
+Range cache_range(const void* p, const kda_kv_cache& c) {
   const unsigned __int128 n =
-      ((unsigned __int128)(c.num_pages - 1) * s + in_page) * (c.dtype == KDA_CACHE_BF16 ? 2 : 1);
+      ((unsigned __int128)(c.num_pages - 1) * page_stride(c) + page_elements(c)) * element_bytes(c);
   const uint64_t most = ~(uint64_t)0 - reinterpret_cast<uintptr_t>(p);
   return range_of(p, n > most ? most : (uint64_t)n);
 }
-// Whether keys' and values' buffers may be read and written side by side: apart, or
-// each other's gaps (halves of one buffer: pages or tokens of both in turn).
+// Whether keys' and values' buffers may be written side by side: apart, or in each
+// other's gaps (halves of one buffer: pages or tokens of both in turn).
 bool caches_apart(const void* k, const void* v, const kda_kv_cache& c) {
-  const Range rk = cache_range(k, c.k_page_stride, c.k_token_stride, c);
-  const Range rv = cache_range(v, c.v_page_stride, c.v_token_stride, c);
+  const Range rk = cache_range(k, c), rv = cache_range(v, c);
   if (!overlaps(rk, rv)) return true;
-  const int64_t kt = token_stride(c.k_token_stride, c), vt = token_stride(c.v_token_stride, c);
-  const int64_t kp = page_stride(c.k_page_stride, kt, c), vp = page_stride(c.v_page_stride, vt, c);
-  if (kt != vt || kp != vp) return false;
-  const uint64_t size = c.dtype == KDA_CACHE_BF16 ? 2 : 1;
-  const uint64_t row = (uint64_t)c.num_kv_heads * c.head_dim * size, page = (uint64_t)kp * size, token = (uint64_t)kt * size;
-  const uint64_t in_page = token * (c.page_size - 1) + row;
+  const uint64_t size = element_bytes(c), row = row_elements(c) * size, page = page_stride(c) * size;
+  const uint64_t token = token_stride(c) * size, in_page = page_elements(c) * size;
   const uint64_t gap = rk.lo < rv.lo ? rv.lo - rk.lo : rk.lo - rv.lo;
   const uint64_t at = gap % page;  // of a page of one in a page of the other
   if (at >= in_page && page - at >= in_page) return true;
@@ -136,10 +123,8 @@ kda::PagedCache cache_of(const kda_kv_cache& c, void* k, void* v, const float* k
   p.D = c.head_dim;
   p.page_shift = page_shift(c.page_size);
   p.pages = c.num_pages;
-  p.k_token = token_stride(c.k_token_stride, c);
-  p.v_token = token_stride(c.v_token_stride, c);
-  p.k_page = page_stride(c.k_page_stride, p.k_token, c);
-  p.v_page = page_stride(c.v_page_stride, p.v_token, c);
+  p.token_stride = token_stride(c);
+  p.page_stride = page_stride(c);
   return p;
 }
 
@@ -173,11 +158,12 @@ kda_status check_decode(const kda_attn_decode_problem* p) {
 // The parts that a context is cut into at most, so that few requests fill the
 // device.
 int decode_parts(const kda_attn_decode_problem* p) {
-  const int64_t KV = p->cache.num_kv_heads;
-  const int64_t blocks = kda::attn_decode_blocks(p->num_seqs, KV, p->tokens_per_seq, p->num_heads / KV, 1);
+  const int64_t KV = p->cache.num_kv_heads, G = p->num_heads / KV;
+  const int64_t blocks = kda::attn_decode_blocks(p->num_seqs, KV, p->tokens_per_seq, G, 1);
   if (blocks == 0) return 1;
-  const int64_t most = ((int64_t)p->table_width * p->cache.page_size + 1023) / 1024;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({most, 256 / blocks, kda::kAttnParts}));
+  const bool many = p->tokens_per_seq * G > kda::kAttnFewRows;
+  const int64_t positions = (int64_t)p->table_width * p->cache.page_size, least = many ? 512 : 1024, fill = many ? 2048 : 256;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({(positions + least - 1) / least, fill / blocks, kda::kAttnParts}));
 }
 
 // workspace of a split: sums and outputs of each part's rows
@@ -264,8 +250,8 @@ kda_status kda_attn_decode_validate(const kda_attn_decode_problem* p, const void
   if (!all_aligned({q, k_cache, v_cache, table, rows, lens, tree, k_scale, v_scale, out, lse, workspace}))
     return KDA_ERR_ALIGNMENT;
   const Range rq = rows_of(q, N * T, p->q_stride, row), ro = rows_of(out, N * T, p->out_stride, row);
-  const Range rk = cache_range(k_cache, c.k_page_stride, c.k_token_stride, c);
-  const Range rv = cache_range(v_cache, c.v_page_stride, c.v_token_stride, c);
+  const Range rk = cache_range(k_cache, c);
+  const Range rv = cache_range(v_cache, c);
   const Range rt = range_of(table, (uint64_t)p->table_rows * p->table_width * 4);
   const Range rr = range_of(rows, (uint64_t)N * 4), rn = range_of(lens, (uint64_t)N * 4);
   const Range rtree = range_of(tree, (uint64_t)(p->tree_per_seq ? N * T : T) * 8);
@@ -329,8 +315,7 @@ kda_status kda_kv_store_validate(const kda_kv_store_problem* p, const void* k, c
   const Range rk = rows_of(k, T, p->k_stride, row), rv = rows_of(v, T, p->v_stride, row);
   const Range rs = range_of(slots, (uint64_t)T * 8);
   const Range rks = range_of(k_scale, (uint64_t)KV * 4), rvs = range_of(v_scale, (uint64_t)KV * 4);
-  for (const Range& r : {cache_range(k_cache, c.k_page_stride, c.k_token_stride, c),
-                         cache_range(v_cache, c.v_page_stride, c.v_token_stride, c)})
+  for (const Range& r : {cache_range(k_cache, c), cache_range(v_cache, c)})
     if (any_overlap(r, {rk, rv, rs, rks, rvs})) return KDA_ERR_OVERLAP;
   return k_cache && v_cache && !caches_apart(k_cache, v_cache, c) ? KDA_ERR_OVERLAP : KDA_OK;
 }

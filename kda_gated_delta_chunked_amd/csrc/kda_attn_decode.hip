@@ -31,63 +31,101 @@ __device__ __forceinline__ void wave_order() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// Half a tile, 16 positions, lies in one page.  Lane i holds the pages of the
-// halves of the wave's tile i of 64 in a row: found together, with no load to wait for
-// ahead of a tile's own.  -1: no page of the cache.
-struct TilePages {
-  int page0, page1;
-  // tile 0's first position, positions between tiles; positions are below `end`
-  __device__ __forceinline__ void find(const AttnDecodeArgs& a, const int32_t* row, int first, int step, int end) {
+// The page of a position below `end`, or less than zero.
+__device__ __forceinline__ int page_of(const AttnDecodeArgs& a, const int32_t* row, int pos, int end) {
+  const int p = pos < end ? row[pos >> a.c.page_shift] : -1;
+  return p < a.c.pages ? p : -1;
+}
+// Elements from a cache's start to those of a position in `page`.
+__device__ __forceinline__ int64_t in_cache(const PagedCache& c, int page, int pos) {
+  return page * c.page_stride + (pos & ((1 << c.page_shift) - 1)) * c.token_stride;
+}
+
+// The request's own tokens that token t sees, a bit each.
+__device__ __forceinline__ uint64_t own_seen(const AttnDecodeArgs& a, int n, int t) {
+  return (a.tree ? a.tree[n * a.tree_stride + t] : ~0ull >> (63 - t)) & (~0ull >> (64 - a.T));
+}
+
+// The keys of the 32 positions from pos on that a row sees, a bit each: those below `end`
+// in halves that have pages, and of the request's own tokens (from `before` on) those it sees.
+__device__ __forceinline__ uint32_t seen_keys(int pos, int end, int before, uint64_t sees, bool half0, bool half1) {
+  const int own = pos - before, left = end - pos;
+  uint64_t seen = ~0ull;
+  if (own >= 64) seen = 0;
+  else if (own >= 0) seen = sees >> own;
+  else if (own > -KEYS) seen = sees << -own | ((1ull << -own) - 1);
+  uint32_t there = (half0 ? 0xffffu : 0u) | (half1 ? 0xffff0000u : 0u);
+  if (left < KEYS) there &= left > 0 ? (1u << left) - 1 : 0u;
+  return (uint32_t)seen & there;
+}
+
+// Half a tile, 16 positions, lies in one page.  Lane i holds where the halves of tile i of
+// 64 in a row start, bytes from the cache's start, found together so that no load is waited
+// for ahead of a tile's own.  Whatever a tile holds, its addresses are inside a page of the
+// cache (page 0's for none): rows that are no position are copied like others, and masked.
+template <int SIZE>  // of an element
+struct TileStarts {
+  int lo[2], hi[2];
+  uint64_t there[2];  // which halves have pages, a bit per tile
+  // tile 0's first position, positions between tiles; positions are from `begin` on and below `end`
+  __device__ __forceinline__ void find(const AttnDecodeArgs& a, const int32_t* row, int first, int step, int begin, int end) {
     const int pos = first + (int)(threadIdx.x & 63) * step;
-    auto page = [&](int x) {
-      const int p = x < end ? row[x >> a.c.page_shift] : -1;
-      return p < a.c.pages ? p : -1;
-    };
-    page0 = page(pos);
-    page1 = page(pos + 16);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int page = pos < begin ? -1 : page_of(a, row, pos + 16 * h, end);
+      const int64_t at = in_cache(a.c, max(page, 0), pos + 16 * h) * SIZE;
+      lo[h] = (int)at;
+      hi[h] = (int)(at >> 32);
+      there[h] = __ballot(page >= 0);
+    }
   }
+  __device__ __forceinline__ int64_t start(int tile, int h) const {
+    const uint32_t low = __builtin_amdgcn_readlane(lo[h], tile);
+    return (int64_t)__builtin_amdgcn_readlane(hi[h], tile) << 32 | low;
+  }
+  __device__ __forceinline__ bool has(int tile, int h) const { return there[h] >> tile & 1; }
 };
 
-// Tiles of KEYS rows of one head, keys and values, from pages to LDS,
-// asynchronously, 1 KiB a copy in LDS order, the swizzle in the addresses.  Half a tile lies in one page, so
-// whatever a tile holds, its addresses are inside a page of the cache (page 0 for none): rows
-// that are no position are copied like others, and masked.
+// Tiles of KEYS rows of one head, keys or values, from the cache to LDS, asynchronously, 1 KiB
+// a copy in LDS order, the swizzle in the addresses.
 template <int D, bool E4M3>
 struct PageCopies {
   static constexpr int SIZE = E4M3 ? 1 : 2, PER_ROW = D * SIZE / 16, ROWS = 64 / PER_ROW, PARTS = KEYS / ROWS;
   static constexpr int COUNT = 2 * PARTS, TILE = KEYS * D * SIZE;  // of a tile's keys and values; bytes of either
   static_assert(ROWS <= 16 && PARTS >= 2, "halves lie in one page each");
-  const uint8_t *kbase, *vbase;
-  int64_t kpage, vpage;
-  int ktoken, vtoken, in_page;
+  uint64_t kbase, vbase;
+  int token;  // bytes
   __device__ __forceinline__ PageCopies(const PagedCache& c, int kv)
-      : kbase(static_cast<const uint8_t*>(c.k) + (int64_t)kv * D * SIZE), vbase(static_cast<const uint8_t*>(c.v) + (int64_t)kv * D * SIZE),
-        kpage(c.k_page * SIZE), vpage(c.v_page * SIZE), ktoken((int)c.k_token * SIZE), vtoken((int)c.v_token * SIZE),
-        in_page((1 << c.page_shift) - 1) {}
-  // copy `part` of the tile from position pos on, whose halves are in these pages
-  __device__ __forceinline__ void start(bool keys, int part, int pos, int page0, int page1, uint32_t lds) const {
-    const int lane = forget(threadIdx.x & 63), row = part * ROWS, half = part / (PARTS / 2);
-    const int page = max(half ? page1 : page0, 0), token = keys ? ktoken : vtoken;
-    // rows are less than 2^24 bytes apart: 32 bits hold 16 of them
-    const uint64_t rows = reinterpret_cast<uint64_t>(keys ? kbase : vbase) + page * (keys ? kpage : vpage) +
-                          (int64_t)(((pos + 16 * half) & in_page) + row % 16) * token;
-    const int in_row = attn_tile_at<D, E4M3>(row + lane / PER_ROW, lane % PER_ROW) & (D * SIZE - 1);
-    copy_to_lds(lds + part * 1024, rows, (uint32_t)(lane / PER_ROW * token + in_row));
+      : kbase(reinterpret_cast<uint64_t>(c.k) + (int64_t)kv * D * SIZE),
+        vbase(reinterpret_cast<uint64_t>(c.v) + (int64_t)kv * D * SIZE), token((int)c.token_stride * SIZE) {}
+  // the lane's bytes of a copy's first row (rows are less than 2^24 bytes apart: 32 bits hold 16)
+  __device__ __forceinline__ int lane_from(int part) const {
+    const int lane = forget(threadIdx.x & 63), row = part * ROWS + lane / PER_ROW;
+    return lane / PER_ROW * token + (attn_tile_at<D, E4M3>(row, lane % PER_ROW) & (D * SIZE - 1));
   }
-  // keys, and behind them values
-  __device__ __forceinline__ void start(int pos, int page0, int page1, uint8_t* to) const {
+  static __device__ __forceinline__ int half(int part) { return part / (PARTS / 2); }
+  // copy `part` of a tile of keys or values whose half starts at `start`
+  __device__ __forceinline__ void copy(bool keys, int part, int64_t start, int from, uint32_t lds) const {
+    copy_to_lds(lds + part * 1024, (keys ? kbase : vbase) + start + part % (PARTS / 2) * ROWS * token, (uint32_t)from);
+  }
+  // a tile's keys, and behind them its values
+  __device__ __forceinline__ void tile(const TileStarts<SIZE>& starts, int tile, uint8_t* to) const {
     const uint32_t lds = lds_place(to);
+    const int64_t start[2] = {starts.start(tile, 0), starts.start(tile, 1)};
 #pragma unroll
-    for (int u = 0; u < PARTS; ++u) start(true, u, pos, page0, page1, lds);
+    for (int u = 0; u < PARTS; ++u) copy(true, u, start[half(u)], lane_from(u), lds);
 #pragma unroll
-    for (int u = 0; u < PARTS; ++u) start(false, u, pos, page0, page1, lds + TILE);
-  }
-  __device__ __forceinline__ float value(int pos, int page, int d) const {
-    const uint8_t* v = vbase + page * vpage + (int64_t)(pos & in_page) * vtoken;
-    if constexpr (E4M3) return __builtin_amdgcn_cvt_f32_fp8((int)v[d], 0);
-    else return bf16_f32(reinterpret_cast<const uint16_t*>(v)[d]);
+    for (int u = 0; u < PARTS; ++u) copy(false, u, start[half(u)], lane_from(u), lds + TILE);
   }
 };
+
+// A value of a position in `page`.
+template <bool E4M3>
+__device__ __forceinline__ float value_at(const PagedCache& c, int kv, int page, int pos, int d) {
+  const int64_t at = in_cache(c, page, pos) + (int64_t)kv * c.D + d;
+  if constexpr (E4M3) return __builtin_amdgcn_cvt_f32_fp8((int)static_cast<const uint8_t*>(c.v)[at], 0);
+  else return bf16_f32(static_cast<const uint16_t*>(c.v)[at]);
+}
 
 // Keys of a part of a context of `length` positions: `parts` parts at most, whole
 // turns of a workgroup each.
@@ -117,12 +155,10 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
   static_assert(WAVE_BYTES >= 32 * D * 4, "32 rows of outputs");
   __shared__ __attribute__((aligned(1024))) uint8_t tiles[WAVES][WAVE_BYTES];
   __shared__ float stats[WAVES][2][32];
-  const int KV = a.c.KV, G = a.H / KV, rows = a.T * G, row_blocks = (rows + 31) / 32;
+  const int KV = a.c.KV, G = a.H / KV, rows = a.T * G;
   uint32_t at_block = blockIdx.x;
   const int kv = (int)(at_block % (uint32_t)KV);
   at_block /= (uint32_t)KV;
-  const int block = (int)(at_block % (uint32_t)row_blocks);
-  at_block /= (uint32_t)row_blocks;
   const int part = (int)(at_block % (uint32_t)a.parts), n = (int)(at_block / (uint32_t)a.parts);
   const Request req(a, n);
   const int per_part = part_keys(req.length, a.parts);
@@ -130,15 +166,14 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
   if (a.part_out && begin >= end) return;
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, h = lane >> 5;
-  const int row = min(32 * block + (lane & 31), rows - 1);
+  const int row = min(lane & 31, rows - 1);
   const int t = row / G;
   const int64_t q_row = (int64_t)n * a.T + t;
   AttnRows<D> r;
   r.start();
   if (begin < end) {
     r.load(a.q + q_row * a.q_stride + (kv * G + row % G) * D);
-    // the request's own tokens that the row sees
-    const uint64_t sees = (a.tree ? a.tree[n * a.tree_stride + t] : ~0ull >> (63 - t)) & (~0ull >> (64 - a.T));
+    const uint64_t sees = own_seen(a, n, t);
     const int32_t* table = a.table + (int64_t)req.row * a.table_width;
     const float c = a.scale * kLog2e * (E4M3 ? a.c.k_scale[kv] : 1.f);
     const TilePlaces<D, E4M3> places;
@@ -146,19 +181,17 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
     uint8_t* const ring = tiles[wave];
     const int first = begin + wave * KEYS, count = (end - first + STEP - 1) / STEP;  // the wave's tiles
 
-    TilePages pages;
-    struct Two { int a, b; };  // the pages of a tile's halves
-    auto pages_of = [&](int tile) {
-      if ((tile & 63) == 0) pages.find(a, table, first + tile * STEP, STEP, end);
-      return Two{__builtin_amdgcn_readlane(pages.page0, tile & 63), __builtin_amdgcn_readlane(pages.page1, tile & 63)};
-    };
-    Two now{-1, -1}, next{-1, -1}, after{-1, -1};
+    TileStarts<Copies::SIZE> starts;
+    struct Halves { bool a, b; };  // of a tile that have pages
+    Halves now{}, next{}, after{};
+    auto find = [&](int tile) { starts.find(a, table, first + tile * STEP, STEP, begin, end); };
     auto fetch = [&](int tile) {
-      after = pages_of(tile);
-      copies.start(first + tile * STEP, after.a, after.b, ring + (tile & 1) * 2 * TILE);
+      if (tile && (tile & 63) == 0) find(tile);
+      after = {starts.has(tile & 63, 0), starts.has(tile & 63, 1)};
+      copies.tile(starts, tile & 63, ring + (tile & 1) * 2 * TILE);
     };
     if (count > 0) {
-      pages_of(0);
+      find(0);
       r.settle();
       fetch(0);
       now = after;
@@ -167,17 +200,6 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
       fetch(1);
       next = after;
     }
-    // the keys of the tile at `pos` that the lane's row sees, a bit each
-    auto seen_of = [&](int pos) {
-      const int own = pos - req.before, left = end - pos;
-      uint64_t seen = ~0ull;
-      if (own >= 64) seen = 0;
-      else if (own >= 0) seen = sees >> own;
-      else if (own > -KEYS) seen = sees << -own | ((1ull << -own) - 1);
-      uint32_t there = (now.a < 0 ? 0u : 0xffffu) | (now.b < 0 ? 0u : 0xffff0000u);
-      if (left < KEYS) there &= (1u << left) - 1;
-      return (uint32_t)seen & there;
-    };
     bool not_finite = false;  // left out of a tile with masked rows
     f32x16 s;
     bf16x8 p[2];
@@ -204,7 +226,7 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
     };
     while (tile < count) {
       bool far = false;
-      while (first + tile * STEP + KEYS <= min(req.before, end) && now.a >= 0 && now.b >= 0) {
+      while (first + tile * STEP + KEYS <= min(req.before, end) && now.a && now.b) {
         // a tile that all rows see
         land();
         const auto at = place();
@@ -221,7 +243,7 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
       if (!far) {
         land();
         s = r.scores(at, ring);
-        mask_scores(s, seen_of(first + tile * STEP));
+        mask_scores(s, seen_keys(first + tile * STEP, end, req.before, sees, now.a, now.b));
         far = r.try_weights(s, c, p, sum);
       }
       if (far) r.weights_from_maximum(s, c, p, sum);
@@ -231,15 +253,12 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
       step();
     }
     if (__builtin_expect(not_finite, 0))
-      for (int tile = 0; tile < count; ++tile) {
-        const Two of = pages_of(tile);
-        const int pos = first + tile * STEP;
-        for (int key = 0; key < KEYS; ++key) {
-          const int page = key < 16 ? of.a : of.b, own = pos + key - req.before;
-          if (pos + key >= end || page < 0) continue;
-          r.add_not_finite(own < 0 || (sees >> (own & 63) & 1), [&](int d) { return copies.value(pos + key, page, d); });
+      for (int tile = 0; tile < count; ++tile)
+        for (int pos = first + tile * STEP; pos < min(end, first + tile * STEP + KEYS); ++pos) {
+          const int page = page_of(a, table, pos, end), own = pos - req.before;
+          if (page < 0) continue;
+          r.add_not_finite(own < 0 || (sees >> (own & 63) & 1), [&](int d) { return value_at<E4M3>(a.c, kv, page, pos, d); });
         }
-      }
   }
 
   // the waves' shares, joined through their tiles: O as [D][32 rows]
@@ -255,7 +274,7 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
     stats[wave][1][lane] = total;
   }
   tiles_barrier<0>();
-  const int mine_row = threadIdx.x & 31, row_at = 32 * block + mine_row, cols = (threadIdx.x >> 5) * (D / 8);
+  const int mine_row = threadIdx.x & 31, row_at = mine_row, cols = (threadIdx.x >> 5) * (D / 8);
   if (row_at >= rows) return;
   const float c = a.scale * kLog2e * (E4M3 && begin < end ? a.c.k_scale[kv] : 1.f);
   float m = kNone;
@@ -293,6 +312,133 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
 #pragma unroll
   for (int i = 0; i < D / 8; i += 8) *reinterpret_cast<uint4*>(to + i) = f32_bf16x8(o + i);
   if (a.lse && cols == 0) a.lse[out_row * a.H + head] = lse_of(m, c, sum);
+}
+
+// The blocks of 32 positions of a part, for a wave of rows of a request.
+template <int D, bool E4M3>
+struct PagedSource {
+  using Places = TilePlaces<D, E4M3>;
+  using Copies = PageCopies<D, E4M3>;
+  static constexpr int RING = 4, TILE = Places::BYTES, COUNT = Copies::COUNT / WAVES;
+  static_assert(COUNT >= 1 && Copies::PARTS % 2 == 0, "a copy for each wave at least");
+  static constexpr int HALVES = Copies::PARTS > WAVES ? 2 : 1;  // of a tile that a wave copies
+  static constexpr int GROUP = 62;  // blocks that starts are found for together, with two ahead of them
+  uint8_t *ktiles, *vtiles;
+  Places places;
+  int open;
+  Copies copies;
+  const AttnDecodeArgs& a;
+  const int32_t* table;
+  int begin, end, before, wave, from;
+  uint64_t sees;  // the request's own tokens that the lane's row sees
+  TileStarts<Copies::SIZE> starts;
+  int copied = 0, slot = 0;  // blocks of keys so far (values are two behind), and the next one's place
+  int at = 0;                // the block of values that is copied next, in its group
+  uint64_t there = 0;        // which halves have pages, two bits a block of keys, the last one lowest
+
+  __device__ __forceinline__ PagedSource(const AttnDecodeArgs& a_, int kv, const int32_t* table_, int begin_, int end_,
+                                         int before_, uint64_t sees_, int wave_, uint8_t* tiles)
+      : ktiles(tiles), vtiles(tiles + RING * TILE), open(max(min(before_, end_) - begin_, 0) / KEYS), copies(a_.c, kv), a(a_),
+        table(table_), begin(begin_), end(end_), before(before_), wave(wave_), from(copies.lane_from(wave_ % Copies::PARTS)),
+        sees(sees_) {
+    find();
+  }
+  __device__ __forceinline__ void find() {
+    starts.find(a, table, begin + (copied - 2) * KEYS, KEYS, begin, end);
+    if (HALVES == 1 && Copies::half(wave % Copies::PARTS)) {
+      starts.lo[0] = starts.lo[1];
+      starts.hi[0] = starts.hi[1];
+    }
+    at = 0;
+  }
+  // One of the COUNT copies of the next block of keys, and of the one of values two behind it
+  // (of page 0 while there is none).
+  __device__ __forceinline__ void put(int i) {
+    if (i == 0) {
+      const bool h0 = starts.has(at + 2, 0), h1 = starts.has(at + 2, 1);
+      there = there << 2 | (h0 ? 1u : 0u) | (h1 ? 2u : 0u);
+      open = h0 && h1 ? open : min(open, copied);
+    }
+    const int u = i * WAVES + wave, part = u % Copies::PARTS;  // the copies of the keys' tile, then of the values'
+    const bool key = COUNT == 1 ? u < Copies::PARTS : i < COUNT / 2;
+    // (a wave's copies of a tile are 16 rows apart: their lanes' bytes are the same)
+    static_assert(HALVES == 1 || WAVES * Copies::ROWS == 16, "a lane's rows have one swizzle");
+    copies.copy(key, part, starts.start(key ? at + 2 : at, i % HALVES), from,
+                lds_place(key ? ktiles : vtiles) + (uint32_t)slot);
+    if (i < COUNT - 1) return;
+    ++copied;
+    ++at;
+    slot = (slot + TILE) & (RING * TILE - 1);
+  }
+  __device__ __forceinline__ void put() {
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) put(i);
+  }
+  __device__ __forceinline__ Places place(int b) const {
+    const int at = (b & (RING - 1)) * TILE;
+    return Places(places, at, at);
+  }
+  template <int READS>
+  __device__ __forceinline__ void turn() {
+    memory_left<COUNT>();
+    tiles_barrier<READS>();
+    if (at == GROUP) find();
+  }
+  __device__ __forceinline__ uint32_t seen(int j) const {
+    const uint32_t halves = (uint32_t)(there >> (2 * (copied - 1 - j)));
+    return seen_keys(begin + j * KEYS, end, before, sees, halves & 1, halves & 2);
+  }
+};
+
+template <int D, bool E4M3>
+__global__ __launch_bounds__(THREADS, 2) void kda_attn_drafts_kernel(AttnDecodeArgs a) {
+  using Source = PagedSource<D, E4M3>;
+  __shared__ __attribute__((aligned(1024))) uint8_t tiles[2 * Source::RING * Source::TILE];
+  const int KV = a.c.KV, G = a.H / KV, rows = a.T * G, row_blocks = (rows + kAttnManyRows - 1) / kAttnManyRows;
+  uint32_t at_block = blockIdx.x;
+  const int kv = (int)(at_block % (uint32_t)KV);
+  at_block /= (uint32_t)KV;
+  const int block = (int)(at_block % (uint32_t)row_blocks);
+  at_block /= (uint32_t)row_blocks;
+  const int part = (int)(at_block % (uint32_t)a.parts), n = (int)(at_block / (uint32_t)a.parts);
+  const Request req(a, n);
+  const int per_part = part_keys(req.length, a.parts);
+  const int begin = part * per_part, end = min(req.length, begin + per_part);
+  if (a.part_out && begin >= end) return;
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int top = block * kAttnManyRows + wave * 32, row = top + (lane & 31), read = min(row, rows - 1);
+  const int t = read / G;
+  const int64_t q_row = (int64_t)n * a.T + t;
+  float c = 0.f;
+  AttnRows<D> r;
+  r.start();
+  if (begin < end) {
+    r.load(a.q + q_row * a.q_stride + (kv * G + read % G) * D);
+    const uint64_t sees = own_seen(a, n, t);
+    c = a.scale * kLog2e * (E4M3 ? a.c.k_scale[kv] : 1.f);
+    const int blocks = (end - begin + KEYS - 1) / KEYS;
+    Source source(a, kv, a.table + (int64_t)req.row * a.table_width, begin, end, req.before, sees, wave, tiles);
+    r.settle();
+    for (int i = 0; i < Source::RING - 1; ++i) source.put();
+    if (__builtin_expect(attend(r, source, c, blocks, top < rows ? blocks : 0), 0))
+      for (int pos = begin; pos < end; ++pos) {
+        const int page = page_of(a, source.table, pos, end), own = pos - req.before;
+        if (page < 0) continue;
+        r.add_not_finite(own < 0 || (sees >> (own & 63) & 1), [&](int d) { return value_at<E4M3>(a.c, kv, page, pos, d); });
+      }
+  }
+  const float total = r.total();
+  if (row >= rows) return;
+  if (a.part_out) {
+    const int64_t slot = (((int64_t)n * KV + kv) * a.parts + part) * rows + row;
+    r.store_sums(a.part_out + slot * D);
+    if (lane < 32) *reinterpret_cast<float2*>(a.part_ml + slot * 2) = make_float2(r.m, total);
+    return;
+  }
+  const int head = kv * G + row % G;
+  r.store(a.out + q_row * a.out_stride + head * D, total == 0.f ? 0.f : (E4M3 ? a.c.v_scale[kv] : 1.f) / total);
+  if (a.lse && lane < 32) a.lse[q_row * a.H + head] = lse_of(r.m, c, total);
 }
 
 // The parts of a context, a workgroup per row: the parts' weights first, a thread
@@ -364,8 +510,9 @@ template <int D>
 void launch(const AttnDecodeArgs& a, hipStream_t stream) {
   const int64_t G = a.H / a.c.KV;
   const dim3 grid((unsigned)attn_decode_blocks(a.N, a.c.KV, a.T, G, a.parts));
-  if (a.c.k_scale) hipLaunchKernelGGL((kda_attn_decode_kernel<D, true>), grid, dim3(THREADS), 0, stream, a);
-  else hipLaunchKernelGGL((kda_attn_decode_kernel<D, false>), grid, dim3(THREADS), 0, stream, a);
+  auto kernel = a.T * G <= kAttnFewRows ? (a.c.k_scale ? kda_attn_decode_kernel<D, true> : kda_attn_decode_kernel<D, false>)
+                                        : (a.c.k_scale ? kda_attn_drafts_kernel<D, true> : kda_attn_drafts_kernel<D, false>);
+  hipLaunchKernelGGL(kernel, grid, dim3(THREADS), 0, stream, a);
   if (a.part_out) {
     hipLaunchKernelGGL(kda_attn_join_kernel<D>, dim3((unsigned)((int64_t)a.N * a.T * a.H)), dim3(THREADS), 0, stream, a);
   }

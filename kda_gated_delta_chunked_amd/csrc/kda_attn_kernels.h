@@ -33,7 +33,7 @@ struct PagedCache {
   int KV, D;
   int page_shift;
   int64_t pages;
-  int64_t k_page, k_token, v_page, v_token;  // strides, elements
+  int64_t page_stride, token_stride;  // elements
 };
 
 struct AttnDecodeArgs {
@@ -83,7 +83,12 @@ hipError_t launch_kv_assign(const KvAssignArgs& a, hipStream_t stream);
 
 // Sizes of launches, for the launch and its check.
 inline int64_t attn_blocks(int64_t slots, int64_t H) { return slots * H; }
-inline int64_t attn_decode_row_blocks(int64_t T, int64_t G) { return (T * G + 31) / 32; }
+// Rows of a request that read the same keys, and those of a workgroup: up to 32 rows
+// its waves share the keys out, beyond they share the rows.
+constexpr int kAttnFewRows = 32, kAttnManyRows = 128;
+inline int64_t attn_decode_row_blocks(int64_t T, int64_t G) {
+  return T * G <= kAttnFewRows ? 1 : (T * G + kAttnManyRows - 1) / kAttnManyRows;
+}
 inline int64_t attn_decode_blocks(int64_t N, int64_t KV, int64_t T, int64_t G, int64_t parts) {
   return N * KV * attn_decode_row_blocks(T, G) * parts;
 }

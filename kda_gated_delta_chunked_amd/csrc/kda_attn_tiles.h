@@ -394,6 +394,15 @@ struct AttnRows {
   }
   // the row's whole sum
   __device__ __forceinline__ float total() const { return l + other_half(l); }
+  // the lane's part of a row of sums
+  __device__ __forceinline__ void store_sums(float* row) const {
+    float* to = row + 4 * ((threadIdx.x >> 5) & 1);
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<float4*>(to + 32 * b + 2 * i) = make_float4(o[b][i], o[b][i + 1], o[b][i + 2], o[b][i + 3]);
+  }
   // the lane's part of a row of outputs, times f
   __device__ __forceinline__ void store(uint16_t* row, float f) const {
     uint16_t* out = row + 4 * ((threadIdx.x >> 5) & 1);

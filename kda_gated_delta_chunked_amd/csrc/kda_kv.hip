@@ -43,14 +43,14 @@ __global__ __launch_bounds__(THREADS) void kda_kv_store_kernel(KvStoreArgs a) {
   const int64_t page = slot >> a.c.page_shift, in = slot & ((1 << a.c.page_shift) - 1);
   const uint4 k = *reinterpret_cast<const uint4*>(a.k + t * a.k_stride + col);
   const uint4 v = *reinterpret_cast<const uint4*>(a.v + t * a.v_stride + col);
-  const int64_t kt = page * a.c.k_page + in * a.c.k_token + col, vt = page * a.c.v_page + in * a.c.v_token + col;
+  const int64_t to = page * a.c.page_stride + in * a.c.token_stride + col;
   if constexpr (E4M3) {
     const int head = col / a.c.D;
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.c.k) + kt) = codes_of(k, a.c.k_scale[head]);
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.c.v) + vt) = codes_of(v, a.c.v_scale[head]);
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.c.k) + to) = codes_of(k, a.c.k_scale[head]);
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.c.v) + to) = codes_of(v, a.c.v_scale[head]);
   } else {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.c.k) + kt) = k;
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.c.v) + vt) = v;
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.c.k) + to) = k;
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.c.v) + to) = v;
   }
 }
 

@@ -78,8 +78,8 @@ def test_prompt_checks(want, kw):
     assert prompt(**kw) == want
 
 
-def cache(KV=2, D=64, dt=0, size=16, pages=10, kp=0, kt=0, vp=0, vt=0):
-    return A.KvCache(KV, D, dt, size, pages, kp, kt, vp, vt)
+def cache(KV=2, D=64, dt=0, size=16, pages=10, page=0, token=0):
+    return A.KvCache(KV, D, dt, size, pages, page, token)
 
 
 STEP = ["q", "kc", "vc", "table", "rows", "lens", "tree", "ks", "vs", "out", "lse", "ws"]
@@ -106,9 +106,9 @@ E4M3 = dict(ks=at(7), vs=at(8))
     (INVALID, dict(out=0)), (INVALID, E4M3), (INVALID, dict(c=cache(dt=1))), (INVALID, dict(c=cache(dt=1), ks=at(7))),
     (UNSUPPORTED, dict(c=cache(dt=2))), (UNSUPPORTED, dict(c=cache(D=96))), (UNSUPPORTED, dict(c=cache(size=8))),
     (UNSUPPORTED, dict(c=cache(size=48))), (UNSUPPORTED, dict(c=cache(size=2048))), (INVALID, dict(c=cache(KV=0))),
-    (INVALID, dict(c=cache(pages=0))), (TOO_LARGE, dict(c=cache(pages=1 << 31))), (INVALID, dict(c=cache(kt=120))),
-    (INVALID, dict(c=cache(vt=136))), (INVALID, dict(c=cache(kp=2032))), (INVALID, dict(c=cache(vp=-2048))),
-    (TOO_LARGE, dict(c=cache(kp=1 << 41))),
+    (INVALID, dict(c=cache(pages=0))), (TOO_LARGE, dict(c=cache(pages=1 << 31))), (INVALID, dict(c=cache(token=120))),
+    (INVALID, dict(c=cache(token=136))), (INVALID, dict(c=cache(page=2032))), (INVALID, dict(c=cache(page=-2048))),
+    (TOO_LARGE, dict(c=cache(page=1 << 41))),
     (ALIGN, dict(lens=at(5) + 4)), (ALIGN, dict(kc=at(1) + 8)), (OVERLAP, dict(out=at(0) + 16)),
     (OVERLAP, dict(out=at(0), qs=512)), (OVERLAP, dict(out=at(1))), (OVERLAP, dict(out=at(3))),
     (OVERLAP, dict(lse=at(0))), (OVERLAP, dict(lse=at(6))), (OVERLAP, dict(ws=at(9))), (OVERLAP, dict(ws=at(2))),
@@ -165,7 +165,7 @@ def test_caches_may_be_halves_of_one_buffer():
         return A.call_raw("kda_kv_store_validate", A.StoreProblem(4, 0, 0, cache(KV, D, 0, size, pages, **c)),
                           at(0), at(1), at(2), 0, 0, at(5), at(5) + gap * 2)
 
-    both = lambda p, t: dict(kp=p, kt=t, vp=p, vt=t)
+    both = lambda p, t: dict(page=p, token=t)
     assert call(page, **both(2 * page, 0)) == OK                  # [pages, 2, size, KV, D]
     assert call(row, **both(2 * page, 2 * row)) == OK             # [pages, size, 2, KV, D]
     assert call(page * pages) == OK                               # [2, pages, size, KV, D]
@@ -173,7 +173,6 @@ def test_caches_may_be_halves_of_one_buffer():
     assert call(page + 8, **both(2 * page, 0)) == OVERLAP
     assert call(row - 8, **both(2 * page, 2 * row)) == OVERLAP
     assert call(row + 8, **both(2 * page, 2 * row)) == OVERLAP
-    assert call(page, kp=2 * page, vp=4 * page) == OVERLAP
     assert call(page) == OVERLAP
 
 

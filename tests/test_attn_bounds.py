@@ -39,6 +39,6 @@ def test_every_copy_goes_through_a_window():
     text = open(os.path.join(CSRC, "kda_attn.hip")).read()
     # one kind of copy, of a window whose rows are counted, from the sequence's first row on
     assert len(re.findall(r"copy_to_lds\(", text)) == 1 and "rows_bytes(first, length, KEYS, bytes)" in text
-    assert "(key ? copied : max(copied - 2, 0)) * KEYS" in text
+    assert "(key ? copied : max(copied - 2, 0)) * (KEYS * SPLIT)" in text
     # and all are waited for before the workgroup ends
     assert "memory_left<0>();  // no copy outlives the workgroup" in open(os.path.join(CSRC, "kda_attn_tiles.h")).read()
