@@ -150,25 +150,25 @@ kda_status check_decode(const kda_attn_decode_problem* p) {
   if (!stride_ok(p->q_stride, row) || !stride_ok(p->out_stride, row)) return KDA_ERR_INVALID_ARG;
   const int64_t N = p->num_seqs, KV = p->cache.num_kv_heads, T = p->tokens_per_seq;
   if (N * T > kInt32Max || N * T * p->num_heads * 256 > kda::kMaxThreads ||
-      kda::attn_decode_blocks(N, KV, T, p->num_heads / KV, 1) * 256 > kda::kMaxThreads)
+      kda::attn_decode_blocks(N, KV, T, p->num_heads / KV) * 256 > kda::kMaxThreads)
     return KDA_ERR_TOO_LARGE;
   return KDA_OK;
 }
 
-// The parts that a context is cut into at most, so that few requests fill the
-// device.
+// The stretches that the contexts are cut into where they are few, so that all
+// workgroups of the device have the same work; 0: a workgroup takes a whole context.
 int decode_parts(const kda_attn_decode_problem* p) {
-  const int64_t KV = p->cache.num_kv_heads, G = p->num_heads / KV;
-  const int64_t blocks = kda::attn_decode_blocks(p->num_seqs, KV, p->tokens_per_seq, G, 1);
-  if (blocks == 0) return 1;
-  const bool many = p->tokens_per_seq * G > kda::kAttnFewRows;
-  const int64_t positions = (int64_t)p->table_width * p->cache.page_size, least = many ? 512 : 1024, fill = many ? 2048 : 256;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({(positions + least - 1) / least, fill / blocks, kda::kAttnParts}));
+  const int64_t KV = p->cache.num_kv_heads, G = p->num_heads / KV, T = p->tokens_per_seq;
+  const int64_t per_item = kda::attn_decode_blocks(1, KV, T, G), blocks = p->num_seqs * per_item;
+  static const int64_t limit = getenv("KLIM") ? atoi(getenv("KLIM")) : 2048, fw = getenv("KFEW") ? atoi(getenv("KFEW")) : 256, mn = getenv("KMANY") ? atoi(getenv("KMANY")) : 512;
+  if (blocks >= limit || (int64_t)p->table_width * p->cache.page_size <= (getenv("KCAP") ? atoi(getenv("KCAP")) : 1024)) return 0;
+  const int64_t parts = (T * G > kda::kAttnFewRows ? mn : fw) / per_item;
+  return parts > 1 ? (int)std::min<int64_t>(parts, kda::kAttnParts) : 0;
 }
 
-// workspace of a split: sums and outputs of each part's rows
+// workspace of a split: sums and outputs of the rows of each piece of a context
 int64_t part_rows(const kda_attn_decode_problem* p, int parts) {
-  return parts > 1 ? (int64_t)p->num_seqs * p->tokens_per_seq * p->num_heads * parts : 0;
+  return parts ? ((int64_t)p->num_seqs + parts) * p->tokens_per_seq * p->num_heads : 0;
 }
 size_t decode_bytes(const kda_attn_decode_problem* p) {
   return (size_t)part_rows(p, decode_parts(p)) * (p->cache.head_dim + 2) * 4;
@@ -295,6 +295,7 @@ kda_status kda_attn_decode(const kda_attn_decode_problem* p, const uint16_t* q, 
   const int64_t in_parts = part_rows(p, a.parts);
   a.part_out = in_parts ? static_cast<float*>(workspace) : nullptr;
   a.part_ml = in_parts ? a.part_out + in_parts * p->cache.head_dim : nullptr;
+  a.join_rows = 1;
   return done(kda::launch_attn_decode(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -108,14 +108,12 @@ struct PageCopies {
   __device__ __forceinline__ void copy(bool keys, int part, int64_t start, int from, uint32_t lds) const {
     copy_to_lds(lds + part * 1024, (keys ? kbase : vbase) + start + part % (PARTS / 2) * ROWS * token, (uint32_t)from);
   }
-  // a tile's keys, and behind them its values
-  __device__ __forceinline__ void tile(const TileStarts<SIZE>& starts, int tile, uint8_t* to) const {
+  // a tile of keys or of values
+  __device__ __forceinline__ void tile(bool keys, const TileStarts<SIZE>& starts, int tile, uint8_t* to) const {
     const uint32_t lds = lds_place(to);
     const int64_t start[2] = {starts.start(tile, 0), starts.start(tile, 1)};
 #pragma unroll
-    for (int u = 0; u < PARTS; ++u) copy(true, u, start[half(u)], lane_from(u), lds);
-#pragma unroll
-    for (int u = 0; u < PARTS; ++u) copy(false, u, start[half(u)], lane_from(u), lds + TILE);
+    for (int u = 0; u < PARTS; ++u) copy(keys, u, start[half(u)], lane_from(u), lds);
   }
 };
 
@@ -125,13 +123,6 @@ __device__ __forceinline__ float value_at(const PagedCache& c, int kv, int page,
   const int64_t at = in_cache(c, page, pos) + (int64_t)kv * c.D + d;
   if constexpr (E4M3) return __builtin_amdgcn_cvt_f32_fp8((int)static_cast<const uint8_t*>(c.v)[at], 0);
   else return bf16_f32(static_cast<const uint16_t*>(c.v)[at]);
-}
-
-// Keys of a part of a context of `length` positions: `parts` parts at most, whole
-// turns of a workgroup each.
-__host__ __device__ __forceinline__ int part_keys(int length, int parts) {
-  const int turns = (int)(((uint32_t)length + STEP - 1) / STEP);
-  return (turns + parts - 1) / parts * STEP;
 }
 
 // The positions of a request's context with its own tokens, 0 for an empty slot.
@@ -145,35 +136,103 @@ struct Request {
     before = before_;
     length = row < 0 ? 0 : (int)(all < most ? all : most);
   }
+  __device__ __forceinline__ int units() const { return length > STEP ? (length + STEP - 1) / STEP : 1; }
+};
+
+// The workgroup's sums of a and b; every thread gets them.  At `upto`, where asked, the thread's own place in those of a.
+__device__ __forceinline__ void sums_of(int64_t& a, int64_t& b, int64_t (*red)[2], int64_t* upto = nullptr) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  int64_t sum = a;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int64_t v = __shfl_up(sum, o, 64), w = __shfl_xor(b, o, 64);
+    if (lane >= o) sum += v;
+    b += w;
+  }
+  if (lane == 63) red[wave][0] = sum, red[wave][1] = b;
+  lds_barrier();
+  if (upto) {
+    *upto = sum - a;
+    for (int w = 0; w < wave; ++w) *upto += red[w][0];
+  }
+  a = red[0][0] + red[1][0] + red[2][0] + red[3][0];
+  b = red[0][1] + red[1][1] + red[2][1] + red[3][1];
+}
+
+// Where there are few contexts, they are laid one behind another in units of STEP positions
+// (one at least), and cut into a.parts stretches of the same length, whatever request they fall
+// to.  A workgroup takes a stretch: the last units of a request, whole ones, the first of another.
+struct Stretch {
+  int n, unit, left;  // the request, the unit in it and the units of the stretch from there on
+  struct Share { int64_t upto, sum, length; };  // units ahead of the thread's requests, of them, of a stretch
+  static __device__ __forceinline__ int64_t length_of(int64_t all, int parts) { return (all + parts - 1) / parts; }
+  // stretch w of the workgroup; red: LDS
+  __device__ __forceinline__ Stretch(const AttnDecodeArgs& a, int w, int64_t (*red)[2]) {
+    const int each = (a.N + THREADS - 1) / THREADS, from = (int)threadIdx.x * each, to = min(from + each, a.N);
+    int64_t mine = 0, upto = 0;
+    for (int i = from; i < to; ++i) mine += Request(a, i).units();
+    int64_t all = mine, none = 0;
+    sums_of(all, none, red, &upto);
+    const int64_t length = length_of(all, a.parts), start = w * length;
+    int* const found = reinterpret_cast<int*>(red + WAVES);
+    if (start >= upto && start < upto + mine) {
+      int i = from;
+      int64_t behind = start - upto;
+      for (int units; behind >= (units = Request(a, i).units()); ++i) behind -= units;
+      found[0] = i;
+      found[1] = (int)behind;
+    }
+    lds_barrier();
+    n = __builtin_amdgcn_readfirstlane(found[0]);
+    unit = __builtin_amdgcn_readfirstlane(found[1]);
+    left = __builtin_amdgcn_readfirstlane((int)min(length, all - start));  // (less than one: no stretch, nothing found)
+    lds_barrier();
+  }
+  // a request on its own
+  __device__ __forceinline__ Stretch(int n_) : n(n_), unit(0), left(1) {}
+};
+
+// A workgroup's place in the launch.  Row blocks of the same keys follow each other on the same
+// of the eight dies, whose cache they share.
+struct Place {
+  int kv, block, item;  // item: request or stretch
+  __device__ __forceinline__ Place(int KV, int row_blocks, int items) {
+    const uint32_t all = (uint32_t)items * KV, group = blockIdx.x / (8u * row_blocks) * 8u, in = blockIdx.x % (8u * row_blocks);
+    const uint32_t size = min(8u, all - group), unit = group + in % size;
+    block = (int)(in / size);
+    kv = (int)(unit % (uint32_t)KV);
+    item = (int)(unit / (uint32_t)KV);
+  }
 };
 
 template <int D, bool E4M3>
 __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeArgs a) {
   using Copies = PageCopies<D, E4M3>;
   constexpr int TILE = Copies::TILE;
-  constexpr int WAVE_BYTES = 4 * TILE;  // two tiles of keys and of values; at the end the wave's outputs
-  static_assert(WAVE_BYTES >= 32 * D * 4, "32 rows of outputs");
+  constexpr int OUTPUTS = 32 * D * 4, WAVE_BYTES = 2 * TILE > OUTPUTS ? 2 * TILE : OUTPUTS;  // a tile of keys and one of values; at the end the wave's outputs
   __shared__ __attribute__((aligned(1024))) uint8_t tiles[WAVES][WAVE_BYTES];
   __shared__ float stats[WAVES][2][32];
   const int KV = a.c.KV, G = a.H / KV, rows = a.T * G;
-  uint32_t at_block = blockIdx.x;
-  const int kv = (int)(at_block % (uint32_t)KV);
-  at_block /= (uint32_t)KV;
-  const int part = (int)(at_block % (uint32_t)a.parts), n = (int)(at_block / (uint32_t)a.parts);
-  const Request req(a, n);
-  const int per_part = part_keys(req.length, a.parts);
-  const int begin = part * per_part, end = min(req.length, begin + per_part);
-  if (a.part_out && begin >= end) return;
-
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, h = lane >> 5;
+  const Place at_place(KV, 1, a.part_out ? a.parts : a.N);
+  const int kv = at_place.kv, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, h = lane >> 5;
   const int row = min(lane & 31, rows - 1);
   const int t = row / G;
+  Stretch piece(at_place.item);
+  if (a.part_out) piece = Stretch(a, at_place.item, reinterpret_cast<int64_t(*)[2]>(tiles));
+  for (; piece.left > 0; ++piece.n, piece.unit = 0) {
+  const int n = piece.n;
+  const Request req(a, n);
+  const int units = req.units(), take = a.part_out ? min(units - piece.unit, piece.left) : units;
+  const bool whole = take == units;
+  const int begin = piece.unit * STEP, end = min(req.length, begin + take * STEP);
+  piece.left -= take;
   const int64_t q_row = (int64_t)n * a.T + t;
   AttnRows<D> r;
   r.start();
   if (begin < end) {
     r.load(a.q + q_row * a.q_stride + (kv * G + row % G) * D);
-    const uint64_t sees = own_seen(a, n, t);
+    uint64_t sees = own_seen(a, n, t);
+    asm volatile("" : "+v"(sees));  // there ahead of the copies
     const int32_t* table = a.table + (int64_t)req.row * a.table_width;
     const float c = a.scale * kLog2e * (E4M3 ? a.c.k_scale[kv] : 1.f);
     const TilePlaces<D, E4M3> places;
@@ -181,76 +240,43 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
     uint8_t* const ring = tiles[wave];
     const int first = begin + wave * KEYS, count = (end - first + STEP - 1) / STEP;  // the wave's tiles
 
+    // Keys' and values' places are filled again as soon as the wave has read them: keys while
+    // their weights and products are worked out, values under the next tile's scores.
     TileStarts<Copies::SIZE> starts;
-    struct Halves { bool a, b; };  // of a tile that have pages
-    Halves now{}, next{}, after{};
-    auto find = [&](int tile) { starts.find(a, table, first + tile * STEP, STEP, begin, end); };
-    auto fetch = [&](int tile) {
-      if (tile && (tile & 63) == 0) find(tile);
-      after = {starts.has(tile & 63, 0), starts.has(tile & 63, 1)};
-      copies.tile(starts, tile & 63, ring + (tile & 1) * 2 * TILE);
+    bool half0 = false, half1 = false;  // whether the halves of the last tile of keys have pages
+    auto fetch_keys = [&](int tile) {
+      if ((tile & 63) == 0) starts.find(a, table, first + tile * STEP, STEP, begin, end);
+      half0 = starts.has(tile & 63, 0);
+      half1 = starts.has(tile & 63, 1);
+      copies.tile(true, starts, tile & 63, ring);
     };
-    if (count > 0) {
-      find(0);
-      r.settle();
-      fetch(0);
-      now = after;
-    }
-    if (count > 1) {
-      fetch(1);
-      next = after;
-    }
+    auto fetch_values = [&](int tile) { copies.tile(false, starts, tile & 63, ring + TILE); };
+    auto reads_done = [&]() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
     bool not_finite = false;  // left out of a tile with masked rows
-    f32x16 s;
-    bf16x8 p[2];
-    float sum;
-    int tile = 0;
-    auto place = [&]() {
-      const int at = (tile & 1) * 2 * TILE;
-      return TilePlaces<D, E4M3>(places, at, at + TILE);
-    };
-    // the tile is there
-    auto land = [&]() {
-      if (tile + 1 < count) memory_left<Copies::COUNT>();
-      else memory_left<0>();
-    };
-    // the tile is done with: its place takes the one after the next
-    auto leave = [&]() {
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      if (tile + 2 < count) fetch(tile + 2);
-    };
-    auto step = [&]() {
-      now = next;
-      next = after;
-      ++tile;
-    };
-    while (tile < count) {
-      bool far = false;
-      while (first + tile * STEP + KEYS <= min(req.before, end) && now.a && now.b) {
-        // a tile that all rows see
-        land();
-        const auto at = place();
-        s = r.scores(at, ring);
-        far = r.try_weights(s, c, p, sum);
-        if (__builtin_expect(far, 0)) break;
-        r.l += sum;
-        r.add(at, ring, p);
-        leave();
-        step();
-      }
-      if (tile >= count) break;
-      const auto at = place();
-      if (!far) {
-        land();
-        s = r.scores(at, ring);
-        mask_scores(s, seen_keys(first + tile * STEP, end, req.before, sees, now.a, now.b));
-        far = r.try_weights(s, c, p, sum);
-      }
-      if (far) r.weights_from_maximum(s, c, p, sum);
+    if (count > 0) {
+      fetch_keys(0);
+      fetch_values(0);
+      r.settle();
+    }
+    const TilePlaces<D, E4M3> at(places, 0, TILE);
+    for (int tile = 0; tile < count; ++tile) {
+      memory_left<Copies::PARTS>();
+      f32x16 s = r.scores(at, ring);
+      reads_done();
+      const bool all = first + tile * STEP + KEYS <= min(req.before, end) && half0 && half1;
+      if (!all) mask_scores(s, seen_keys(first + tile * STEP, end, req.before, sees, half0, half1));
+      const bool more = tile + 1 < count;
+      if (more) fetch_keys(tile + 1);
+      bf16x8 p[2];
+      float sum;
+      if (__builtin_expect(r.try_weights(s, c, p, sum), 0)) r.weights_from_maximum(s, c, p, sum);
       r.l += sum;
-      not_finite = r.add_masked(at, ring, p) || not_finite;
-      leave();
-      step();
+      if (more) memory_left<Copies::PARTS>();
+      else memory_left<0>();
+      if (all) r.add(at, ring, p);
+      else not_finite = r.add_masked(at, ring, p) || not_finite;
+      reads_done();
+      if (more) fetch_values(tile + 1);
     }
     if (__builtin_expect(not_finite, 0))
       for (int tile = 0; tile < count; ++tile)
@@ -275,7 +301,7 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
   }
   tiles_barrier<0>();
   const int mine_row = threadIdx.x & 31, row_at = mine_row, cols = (threadIdx.x >> 5) * (D / 8);
-  if (row_at >= rows) return;
+  if (row_at < rows) {
   const float c = a.scale * kLog2e * (E4M3 && begin < end ? a.c.k_scale[kv] : 1.f);
   float m = kNone;
 #pragma unroll
@@ -297,14 +323,13 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
   }
   const int64_t out_row = (int64_t)n * a.T + row_at / G;
   const int head = kv * G + row_at % G;
-  if (a.part_out) {
-    const int64_t slot = (((int64_t)n * KV + kv) * a.parts + part) * rows + row_at;
+  if (!whole) {
+    const int64_t slot = ((int64_t)(at_place.item + n) * KV + kv) * rows + row_at;
     float* to = a.part_out + slot * D + cols;
 #pragma unroll
     for (int i = 0; i < D / 8; i += 4) *reinterpret_cast<float4*>(to + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
     if (cols == 0) *reinterpret_cast<float2*>(a.part_ml + slot * 2) = make_float2(m, sum);
-    return;
-  }
+  } else {
   const float inv = sum == 0.f ? 0.f : (E4M3 ? a.c.v_scale[kv] : 1.f) / sum;
   uint16_t* to = a.out + out_row * a.out_stride + head * D + cols;
 #pragma unroll
@@ -312,6 +337,10 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
 #pragma unroll
   for (int i = 0; i < D / 8; i += 8) *reinterpret_cast<uint4*>(to + i) = f32_bf16x8(o + i);
   if (a.lse && cols == 0) a.lse[out_row * a.H + head] = lse_of(m, c, sum);
+  }
+  }
+  if (piece.left > 0) tiles_barrier<0>();  // the tiles are copied to again
+  }
 }
 
 // The blocks of 32 positions of a part, for a wave of rows of a request.
@@ -395,27 +424,27 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_drafts_kernel(AttnDecodeA
   using Source = PagedSource<D, E4M3>;
   __shared__ __attribute__((aligned(1024))) uint8_t tiles[2 * Source::RING * Source::TILE];
   const int KV = a.c.KV, G = a.H / KV, rows = a.T * G, row_blocks = (rows + kAttnManyRows - 1) / kAttnManyRows;
-  uint32_t at_block = blockIdx.x;
-  const int kv = (int)(at_block % (uint32_t)KV);
-  at_block /= (uint32_t)KV;
-  const int block = (int)(at_block % (uint32_t)row_blocks);
-  at_block /= (uint32_t)row_blocks;
-  const int part = (int)(at_block % (uint32_t)a.parts), n = (int)(at_block / (uint32_t)a.parts);
-  const Request req(a, n);
-  const int per_part = part_keys(req.length, a.parts);
-  const int begin = part * per_part, end = min(req.length, begin + per_part);
-  if (a.part_out && begin >= end) return;
-
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int top = block * kAttnManyRows + wave * 32, row = top + (lane & 31), read = min(row, rows - 1);
+  const Place at_place(KV, row_blocks, a.part_out ? a.parts : a.N);
+  const int kv = at_place.kv, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int top = at_place.block * kAttnManyRows + wave * 32, row = top + (lane & 31), read = min(row, rows - 1);
   const int t = read / G;
+  Stretch piece(at_place.item);
+  if (a.part_out) piece = Stretch(a, at_place.item, reinterpret_cast<int64_t(*)[2]>(tiles));
+  for (; piece.left > 0; ++piece.n, piece.unit = 0) {
+  const int n = piece.n;
+  const Request req(a, n);
+  const int units = req.units(), take = a.part_out ? min(units - piece.unit, piece.left) : units;
+  const bool whole = take == units;
+  const int begin = piece.unit * STEP, end = min(req.length, begin + take * STEP);
+  piece.left -= take;
   const int64_t q_row = (int64_t)n * a.T + t;
   float c = 0.f;
   AttnRows<D> r;
   r.start();
   if (begin < end) {
     r.load(a.q + q_row * a.q_stride + (kv * G + read % G) * D);
-    const uint64_t sees = own_seen(a, n, t);
+    uint64_t sees = own_seen(a, n, t);
+    asm volatile("" : "+v"(sees));  // there ahead of the copies
     c = a.scale * kLog2e * (E4M3 ? a.c.k_scale[kv] : 1.f);
     const int blocks = (end - begin + KEYS - 1) / KEYS;
     Source source(a, kv, a.table + (int64_t)req.row * a.table_width, begin, end, req.before, sees, wave, tiles);
@@ -429,93 +458,132 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_drafts_kernel(AttnDecodeA
       }
   }
   const float total = r.total();
-  if (row >= rows) return;
-  if (a.part_out) {
-    const int64_t slot = (((int64_t)n * KV + kv) * a.parts + part) * rows + row;
+  if (row < rows && !whole) {
+    const int64_t slot = ((int64_t)(at_place.item + n) * KV + kv) * rows + row;
     r.store_sums(a.part_out + slot * D);
     if (lane < 32) *reinterpret_cast<float2*>(a.part_ml + slot * 2) = make_float2(r.m, total);
-    return;
+  } else if (row < rows) {
+    const int head = kv * G + row % G;
+    r.store(a.out + q_row * a.out_stride + head * D, total == 0.f ? 0.f : (E4M3 ? a.c.v_scale[kv] : 1.f) / total);
+    if (a.lse && lane < 32) a.lse[q_row * a.H + head] = lse_of(r.m, c, total);
   }
-  const int head = kv * G + row % G;
-  r.store(a.out + q_row * a.out_stride + head * D, total == 0.f ? 0.f : (E4M3 ? a.c.v_scale[kv] : 1.f) / total);
-  if (a.lse && lane < 32) a.lse[q_row * a.H + head] = lse_of(r.m, c, total);
+  if (piece.left > 0) tiles_barrier<0>();  // the tiles are copied to again
+  }
 }
 
-// The parts of a context, a workgroup per row: the parts' weights first, a thread
-// each, then their sums, D / 4 threads a part, several parts side by side.
+// Pieces of a row's sums, joined: what they have is brought to the largest maximum.
+struct Joined {
+  float m = kNone, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  static __device__ __forceinline__ float weight(float m, float top, float c) {
+    return m == kNone ? 0.f : __builtin_amdgcn_exp2f((m - top) * c);
+  }
+  // (a piece whose scores are all NaN has no maximum, and a sum that is NaN)
+  static __device__ __forceinline__ float times(float w, float l) { return l != l ? l : w * l; }
+  __device__ __forceinline__ void bring_to(float top, float c) {
+    const float w = weight(m, top, c);
+    l = times(w, l);
+    o = w != 0.f ? make_float4(w * o.x, w * o.y, w * o.z, w * o.w) : make_float4(0.f, 0.f, 0.f, 0.f);
+    m = top;
+  }
+  // a piece whose maximum is not above m
+  __device__ __forceinline__ void add(const float2& ml, const float4& v, float c) {
+    const float w = weight(ml.x, m, c);
+    l += times(w, ml.y);
+    if (w == 0.f) return;  // (what it has may be infinite)
+    o.x += w * v.x;
+    o.y += w * v.y;
+    o.z += w * v.z;
+    o.w += w * v.w;
+  }
+};
+
+// The pieces of a context that stretches' ends have cut.  D / 4 threads go over a row's pieces,
+// eight at a time; as many of them share a row as gives each some eight pieces.  A workgroup
+// takes one row where rows are few, and else as many as it has room for at once.
 template <int D>
 __global__ __launch_bounds__(THREADS) void kda_attn_join_kernel(AttnDecodeArgs a) {
-  constexpr int LANES = D / 4, SIDE = THREADS / LANES;
-  __shared__ float weight[kAttnParts], red[2][WAVES];
-  __shared__ float4 sums[SIDE][LANES];
-  const int KV = a.c.KV, G = a.H / KV, rows = a.T * G;
-  const int row = (int)(blockIdx.x % (unsigned)rows), at = (int)(blockIdx.x / (unsigned)rows);  // at: (request, kv head)
+  constexpr int LANES = D / 4, SIDES = THREADS / LANES, AHEAD = 8;
+  __shared__ int64_t units_red[WAVES][2];
+  __shared__ float4 sums[SIDES][LANES];
+  __shared__ float2 stats[SIDES];
+  const int KV = a.c.KV, G = a.H / KV, rows = a.T * G, row_blocks = (rows + a.join_rows - 1) / a.join_rows;
+  const int block = (int)(blockIdx.x % (unsigned)row_blocks), at = (int)(blockIdx.x / (unsigned)row_blocks);
   const int kv = at % KV, n = at / KV;
-  const Request req(a, n);
-  const int per_part = part_keys(req.length, a.parts);
-  const int parts = per_part ? (req.length + per_part - 1) / per_part : 0;
-  const int64_t slot = (int64_t)at * a.parts * rows + row;
+  int64_t ahead = 0, all = 0;
+  for (int i = threadIdx.x; i < a.N; i += THREADS) {
+    const int units = Request(a, i).units();
+    all += units;
+    ahead += i < n ? units : 0;
+  }
+  sums_of(ahead, all, units_red);
+  const int64_t length = Stretch::length_of(all, a.parts);
+  const int first = (int)(ahead / length), parts = (int)((ahead + Request(a, n).units() - 1) / length) - first + 1;
+  if (parts == 1) return;  // it was written
+  const int64_t step = (int64_t)KV * rows;
   const float c = a.scale * kLog2e * (a.c.k_scale ? a.c.k_scale[kv] : 1.f);
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  float2 ml = make_float2(kNone, 0.f);
-  if ((int)threadIdx.x < parts) ml = *reinterpret_cast<const float2*>(a.part_ml + (slot + (int64_t)threadIdx.x * rows) * 2);
-  float m = ml.x;
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-  if (lane == 0) red[0][wave] = m;
-  lds_barrier();
-  m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-  const float w = ml.x == kNone ? 0.f : __builtin_amdgcn_exp2f((ml.x - m) * c);
-  if (threadIdx.x < kAttnParts) weight[threadIdx.x] = w;
-  // (a part whose scores are all NaN has no maximum, and a sum that is NaN)
-  float sum = ml.y != ml.y ? ml.y : w * ml.y;
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
-  if (lane == 0) red[1][wave] = sum;
-  lds_barrier();
-  sum = red[1][0] + red[1][1] + red[1][2] + red[1][3];
-
   const int side = threadIdx.x / LANES, col = threadIdx.x % LANES;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int p = side; p < parts; p += SIDE) {
-    const float4 v = *reinterpret_cast<const float4*>(a.part_out + (slot + (int64_t)p * rows) * D + col * 4);
-    const float wp = weight[p];
-    if (wp == 0.f) continue;  // (what it has may be infinite)
-    o.x += wp * v.x;
-    o.y += wp * v.y;
-    o.z += wp * v.z;
-    o.w += wp * v.w;
-  }
-  sums[side][col] = o;
-  lds_barrier();
-  if (side) return;
+  int share = a.join_rows == 1 ? SIDES : 1;  // sides of a row
+  while (share < SIDES && parts > share * AHEAD) share *= 2;
+  const int last = min(rows, (block + 1) * a.join_rows);
+  for (int base = block * a.join_rows; base < last; base += SIDES / share) {
+    const int row = min(base + side / share, last - 1);
+    const int64_t slot = ((int64_t)(first + n) * KV + kv) * rows + row;
+    Joined r;
+    for (int p = side % share; p < parts; p += share * AHEAD) {
+      float2 ml[AHEAD];
+      float4 v[AHEAD];
+      float top = r.m;
 #pragma unroll
-  for (int i = 1; i < SIDE; ++i) {
-    const float4 v = sums[i][col];
-    o.x += v.x;
-    o.y += v.y;
-    o.z += v.z;
-    o.w += v.w;
+      for (int i = 0; i < AHEAD; ++i) {
+        const int64_t from = slot + min(p + i * share, parts - 1) * step;
+        ml[i] = *reinterpret_cast<const float2*>(a.part_ml + from * 2);
+        v[i] = *reinterpret_cast<const float4*>(a.part_out + from * D + col * 4);
+      }
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        if (p + i * share >= parts) ml[i] = make_float2(kNone, 0.f);
+        top = fmaxf(top, ml[i].x);
+      }
+      r.bring_to(top, c);
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) r.add(ml[i], v[i], c);
+    }
+    if (share > 1) {
+      lds_barrier();
+      sums[side][col] = r.o;
+      if (col == 0) stats[side] = make_float2(r.m, r.l);
+      lds_barrier();
+    }
+    if (side % share || base + side / share >= last) continue;
+    if (share > 1) {
+      float top = r.m;
+      for (int i = 1; i < share; ++i) top = fmaxf(top, stats[side + i].x);
+      r.bring_to(top, c);
+      for (int i = 1; i < share; ++i) r.add(stats[side + i], sums[side + i][col], c);
+    }
+    const float inv = r.l == 0.f ? 0.f : (a.c.v_scale ? a.c.v_scale[kv] : 1.f) / r.l;
+    const int64_t out_row = (int64_t)n * a.T + row / G;
+    const int head = kv * G + row % G;
+    *reinterpret_cast<uint2*>(a.out + out_row * a.out_stride + head * D + col * 4) =
+        make_uint2(bf16_pair(r.o.x * inv, r.o.y * inv), bf16_pair(r.o.z * inv, r.o.w * inv));
+    if (a.lse && col == 0) a.lse[out_row * a.H + head] = lse_of(r.m, c, r.l);
   }
-  const float inv = sum == 0.f ? 0.f : (a.c.v_scale ? a.c.v_scale[kv] : 1.f) / sum;
-  const int64_t out_row = (int64_t)n * a.T + row / G;
-  const int head = kv * G + row % G;
-  *reinterpret_cast<uint2*>(a.out + out_row * a.out_stride + head * D + col * 4) =
-      make_uint2(bf16_pair(o.x * inv, o.y * inv), bf16_pair(o.z * inv, o.w * inv));
-  if (a.lse && col == 0) a.lse[out_row * a.H + head] = lse_of(m, c, sum);
 }
 
 template <int D>
 void launch(const AttnDecodeArgs& a, hipStream_t stream) {
   const int64_t G = a.H / a.c.KV;
-  const dim3 grid((unsigned)attn_decode_blocks(a.N, a.c.KV, a.T, G, a.parts));
+  const dim3 grid((unsigned)attn_decode_blocks(a.part_out ? a.parts : a.N, a.c.KV, a.T, G));
   auto kernel = a.T * G <= kAttnFewRows ? (a.c.k_scale ? kda_attn_decode_kernel<D, true> : kda_attn_decode_kernel<D, false>)
                                         : (a.c.k_scale ? kda_attn_drafts_kernel<D, true> : kda_attn_drafts_kernel<D, false>);
   hipLaunchKernelGGL(kernel, grid, dim3(THREADS), 0, stream, a);
-  if (a.part_out) {
-    hipLaunchKernelGGL(kda_attn_join_kernel<D>, dim3((unsigned)((int64_t)a.N * a.T * a.H)), dim3(THREADS), 0, stream, a);
-  }
+  if (!a.part_out) return;
+  AttnDecodeArgs join = a;
+  static int jl = getenv("KJOIN") ? atoi(getenv("KJOIN")) : 4096;
+  join.join_rows = (int64_t)a.N * a.T * a.H <= jl ? 1 : THREADS / (D / 4);
+  const int64_t row_blocks = (a.T * G + join.join_rows - 1) / join.join_rows;
+  hipLaunchKernelGGL(kda_attn_join_kernel<D>, dim3((unsigned)(a.N * a.c.KV * row_blocks)), dim3(THREADS), 0, stream, join);
 }
 
 }  // namespace

@@ -51,9 +51,10 @@ struct AttnDecodeArgs {
   int64_t tree_stride;    // 0 or T
   float scale;
   int64_t q_stride, out_stride;
-  int parts;              // a context's parts at most
-  float* part_out;        // [N, KV, parts, T H / KV, D], sums not divided yet; NULL with one part
+  int parts;              // stretches that the contexts are cut into together
+  float* part_out;        // [parts + N, KV, T H / KV, D], sums not divided yet; NULL: a workgroup takes a whole context
   float* part_ml;         // the same with two for D: maximum, sum
+  int join_rows;          // of a workgroup that joins pieces
 };
 hipError_t launch_attn_decode(const AttnDecodeArgs& a, hipStream_t stream);
 
@@ -89,10 +90,10 @@ constexpr int kAttnFewRows = 32, kAttnManyRows = 128;
 inline int64_t attn_decode_row_blocks(int64_t T, int64_t G) {
   return T * G <= kAttnFewRows ? 1 : (T * G + kAttnManyRows - 1) / kAttnManyRows;
 }
-inline int64_t attn_decode_blocks(int64_t N, int64_t KV, int64_t T, int64_t G, int64_t parts) {
-  return N * KV * attn_decode_row_blocks(T, G) * parts;
+inline int64_t attn_decode_blocks(int64_t items, int64_t KV, int64_t T, int64_t G) {
+  return items * KV * attn_decode_row_blocks(T, G);
 }
-constexpr int kAttnParts = 256;  // of a context at most
+constexpr int kAttnParts = 512;  // stretches at most
 inline int64_t kv_store_threads(int64_t T, int64_t KV, int64_t D) { return (T * KV * (D / 8) + 255) / 256 * 256; }
 constexpr int kAssignTokens = 1024;  // new tokens of a workgroup
 inline int64_t kv_assign_blocks(int64_t T) { return T ? (T + kAssignTokens - 1) / kAssignTokens : 1; }
