@@ -160,15 +160,16 @@ kda_status check_decode(const kda_attn_decode_problem* p) {
 int decode_parts(const kda_attn_decode_problem* p) {
   const int64_t KV = p->cache.num_kv_heads, G = p->num_heads / KV, T = p->tokens_per_seq;
   const int64_t per_item = kda::attn_decode_blocks(1, KV, T, G), blocks = p->num_seqs * per_item;
-  static const int64_t limit = getenv("KLIM") ? atoi(getenv("KLIM")) : 2048, fw = getenv("KFEW") ? atoi(getenv("KFEW")) : 256, mn = getenv("KMANY") ? atoi(getenv("KMANY")) : 512;
-  if (blocks >= limit || (int64_t)p->table_width * p->cache.page_size <= (getenv("KCAP") ? atoi(getenv("KCAP")) : 1024)) return 0;
-  const int64_t parts = (T * G > kda::kAttnFewRows ? mn : fw) / per_item;
-  return parts > 1 ? (int)std::min<int64_t>(parts, kda::kAttnParts) : 0;
+  static const int64_t limit = getenv("KLIM") ? atoi(getenv("KLIM")) : 2048, fw = getenv("KFEW") ? atoi(getenv("KFEW")) : 512;
+  const bool many = T * G > kda::kAttnFewRows;
+  if ((many && blocks >= limit) || (int64_t)p->table_width * p->cache.page_size <= 1024) return 0;
+  const int64_t parts = (many ? 512 : blocks <= 256 ? 256 : fw) / per_item;
+  return parts > 1 ? (int)parts : 0;
 }
 
-// workspace of a split: sums and outputs of the rows of each piece of a context
+// workspace of a split: sums and outputs of the rows of cut contexts, two a stretch
 int64_t part_rows(const kda_attn_decode_problem* p, int parts) {
-  return parts ? ((int64_t)p->num_seqs + parts) * p->tokens_per_seq * p->num_heads : 0;
+  return (int64_t)2 * parts * p->tokens_per_seq * p->num_heads;
 }
 size_t decode_bytes(const kda_attn_decode_problem* p) {
   return (size_t)part_rows(p, decode_parts(p)) * (p->cache.head_dim + 2) * 4;

@@ -139,57 +139,54 @@ struct Request {
   __device__ __forceinline__ int units() const { return length > STEP ? (length + STEP - 1) / STEP : 1; }
 };
 
-// The workgroup's sums of a and b; every thread gets them.  At `upto`, where asked, the thread's own place in those of a.
-__device__ __forceinline__ void sums_of(int64_t& a, int64_t& b, int64_t (*red)[2], int64_t* upto = nullptr) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  int64_t sum = a;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int64_t v = __shfl_up(sum, o, 64), w = __shfl_xor(b, o, 64);
-    if (lane >= o) sum += v;
-    b += w;
-  }
-  if (lane == 63) red[wave][0] = sum, red[wave][1] = b;
-  lds_barrier();
-  if (upto) {
-    *upto = sum - a;
-    for (int w = 0; w < wave; ++w) *upto += red[w][0];
-  }
-  a = red[0][0] + red[1][0] + red[2][0] + red[3][0];
-  b = red[0][1] + red[1][1] + red[2][1] + red[3][1];
-}
-
-// Where there are few contexts, they are laid one behind another in units of STEP positions
-// (one at least), and cut into a.parts stretches of the same length, whatever request they fall
-// to.  A workgroup takes a stretch: the last units of a request, whole ones, the first of another.
+// Contexts lie one behind another in units of STEP positions (one at least), and are cut into
+// a.parts stretches of the same length, whatever request they fall to: a workgroup has a
+// stretch, the last units of a request, whole ones, the first of another.
 struct Stretch {
-  int n, unit, left;  // the request, the unit in it and the units of the stretch from there on
-  struct Share { int64_t upto, sum, length; };  // units ahead of the thread's requests, of them, of a stretch
-  static __device__ __forceinline__ int64_t length_of(int64_t all, int parts) { return (all + parts - 1) / parts; }
-  // stretch w of the workgroup; red: LDS
-  __device__ __forceinline__ Stretch(const AttnDecodeArgs& a, int w, int64_t (*red)[2]) {
+  struct Lds {
+    int64_t sums[WAVES];
+    int found[2];
+  };
+  int n, unit, left;  // the request, the unit in it, and the units of the stretch from there on
+  int length;         // of a stretch
+  // stretch w, of the workgroup
+  __device__ __forceinline__ Stretch(const AttnDecodeArgs& a, int w, Lds& lds) {
     const int each = (a.N + THREADS - 1) / THREADS, from = (int)threadIdx.x * each, to = min(from + each, a.N);
-    int64_t mine = 0, upto = 0;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    int64_t mine = 0;
     for (int i = from; i < to; ++i) mine += Request(a, i).units();
-    int64_t all = mine, none = 0;
-    sums_of(all, none, red, &upto);
-    const int64_t length = length_of(all, a.parts), start = w * length;
-    int* const found = reinterpret_cast<int*>(red + WAVES);
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int64_t v = __shfl_up(upto, o, 64);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 63) lds.sums[wave] = upto;
+    lds_barrier();
+    int64_t all = 0;
+    upto -= mine;
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) {
+      if (i < wave) upto += lds.sums[i];
+      all += lds.sums[i];
+    }
+    const int64_t each_of = (all + a.parts - 1) / a.parts, start = w * each_of;
     if (start >= upto && start < upto + mine) {
       int i = from;
       int64_t behind = start - upto;
       for (int units; behind >= (units = Request(a, i).units()); ++i) behind -= units;
-      found[0] = i;
-      found[1] = (int)behind;
+      lds.found[0] = i;
+      lds.found[1] = (int)behind;
     }
     lds_barrier();
-    n = __builtin_amdgcn_readfirstlane(found[0]);
-    unit = __builtin_amdgcn_readfirstlane(found[1]);
-    left = __builtin_amdgcn_readfirstlane((int)min(length, all - start));  // (less than one: no stretch, nothing found)
+    n = __builtin_amdgcn_readfirstlane(lds.found[0]);
+    unit = __builtin_amdgcn_readfirstlane(lds.found[1]);
+    length = __builtin_amdgcn_readfirstlane((int)min(each_of, (int64_t)0x7fffffff));
+    left = __builtin_amdgcn_readfirstlane((int)min(each_of, all - start));  // (less than one: no stretch, nothing found)
     lds_barrier();
   }
   // a request on its own
-  __device__ __forceinline__ Stretch(int n_) : n(n_), unit(0), left(1) {}
+  __device__ __forceinline__ Stretch(int n_) : n(n_), unit(0), left(1), length(1) {}
 };
 
 // A workgroup's place in the launch.  Row blocks of the same keys follow each other on the same
@@ -206,7 +203,7 @@ struct Place {
 };
 
 template <int D, bool E4M3>
-__global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeArgs a) {
+__global__ __launch_bounds__(THREADS, D == 64 ? 3 : 2) void kda_attn_decode_kernel(AttnDecodeArgs a) {
   using Copies = PageCopies<D, E4M3>;
   constexpr int TILE = Copies::TILE;
   constexpr int OUTPUTS = 32 * D * 4, WAVE_BYTES = 2 * TILE > OUTPUTS ? 2 * TILE : OUTPUTS;  // a tile of keys and one of values; at the end the wave's outputs
@@ -218,8 +215,8 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
   const int row = min(lane & 31, rows - 1);
   const int t = row / G;
   Stretch piece(at_place.item);
-  if (a.part_out) piece = Stretch(a, at_place.item, reinterpret_cast<int64_t(*)[2]>(tiles));
-  for (; piece.left > 0; ++piece.n, piece.unit = 0) {
+  if (a.part_out) piece = Stretch(a, at_place.item, *reinterpret_cast<Stretch::Lds*>(tiles));
+  for (int cut = 2 * at_place.item; piece.left > 0; ++piece.n, piece.unit = 0, cut |= 1) {
   const int n = piece.n;
   const Request req(a, n);
   const int units = req.units(), take = a.part_out ? min(units - piece.unit, piece.left) : units;
@@ -324,7 +321,7 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
   const int64_t out_row = (int64_t)n * a.T + row_at / G;
   const int head = kv * G + row_at % G;
   if (!whole) {
-    const int64_t slot = ((int64_t)(at_place.item + n) * KV + kv) * rows + row_at;
+    const int64_t slot = ((int64_t)cut * KV + kv) * rows + row_at;
     float* to = a.part_out + slot * D + cols;
 #pragma unroll
     for (int i = 0; i < D / 8; i += 4) *reinterpret_cast<float4*>(to + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
@@ -429,8 +426,8 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_drafts_kernel(AttnDecodeA
   const int top = at_place.block * kAttnManyRows + wave * 32, row = top + (lane & 31), read = min(row, rows - 1);
   const int t = read / G;
   Stretch piece(at_place.item);
-  if (a.part_out) piece = Stretch(a, at_place.item, reinterpret_cast<int64_t(*)[2]>(tiles));
-  for (; piece.left > 0; ++piece.n, piece.unit = 0) {
+  if (a.part_out) piece = Stretch(a, at_place.item, *reinterpret_cast<Stretch::Lds*>(tiles));
+  for (int cut = 2 * at_place.item; piece.left > 0; ++piece.n, piece.unit = 0, cut |= 1) {
   const int n = piece.n;
   const Request req(a, n);
   const int units = req.units(), take = a.part_out ? min(units - piece.unit, piece.left) : units;
@@ -459,7 +456,7 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_drafts_kernel(AttnDecodeA
   }
   const float total = r.total();
   if (row < rows && !whole) {
-    const int64_t slot = ((int64_t)(at_place.item + n) * KV + kv) * rows + row;
+    const int64_t slot = ((int64_t)cut * KV + kv) * rows + row;
     r.store_sums(a.part_out + slot * D);
     if (lane < 32) *reinterpret_cast<float2*>(a.part_ml + slot * 2) = make_float2(r.m, total);
   } else if (row < rows) {
@@ -498,29 +495,24 @@ struct Joined {
   }
 };
 
-// The pieces of a context that stretches' ends have cut.  D / 4 threads go over a row's pieces,
-// eight at a time; as many of them share a row as gives each some eight pieces.  A workgroup
-// takes one row where rows are few, and else as many as it has room for at once.
+// The pieces of a context that stretches' ends have cut; the first of these ends has the
+// workgroups that join them.  D / 4 threads go over a row's pieces, eight at a time; as many of
+// them share a row as gives each some eight pieces.  A workgroup takes one row where
+// rows are few, and else as many as it has room for at once.
 template <int D>
 __global__ __launch_bounds__(THREADS) void kda_attn_join_kernel(AttnDecodeArgs a) {
   constexpr int LANES = D / 4, SIDES = THREADS / LANES, AHEAD = 8;
-  __shared__ int64_t units_red[WAVES][2];
+  __shared__ Stretch::Lds lds;
   __shared__ float4 sums[SIDES][LANES];
   __shared__ float2 stats[SIDES];
   const int KV = a.c.KV, G = a.H / KV, rows = a.T * G, row_blocks = (rows + a.join_rows - 1) / a.join_rows;
   const int block = (int)(blockIdx.x % (unsigned)row_blocks), at = (int)(blockIdx.x / (unsigned)row_blocks);
-  const int kv = at % KV, n = at / KV;
-  int64_t ahead = 0, all = 0;
-  for (int i = threadIdx.x; i < a.N; i += THREADS) {
-    const int units = Request(a, i).units();
-    all += units;
-    ahead += i < n ? units : 0;
-  }
-  sums_of(ahead, all, units_red);
-  const int64_t length = Stretch::length_of(all, a.parts);
-  const int first = (int)(ahead / length), parts = (int)((ahead + Request(a, n).units() - 1) / length) - first + 1;
-  if (parts == 1) return;  // it was written
-  const int64_t step = (int64_t)KV * rows;
+  const int kv = at % KV, second = at / KV + 1;
+  const Stretch cut(a, second, lds);
+  if (cut.left <= 0 || cut.unit == 0 || cut.unit > cut.length) return;
+  const int n = cut.n, parts = 1 + (Request(a, n).units() - cut.unit + cut.length - 1) / cut.length;
+  const int64_t step = (int64_t)KV * rows;  // of slots; a stretch has two
+  const int64_t first = 2 * (second - 1), head_slot = cut.unit < cut.length ? first + 1 : first;
   const float c = a.scale * kLog2e * (a.c.k_scale ? a.c.k_scale[kv] : 1.f);
   const int side = threadIdx.x / LANES, col = threadIdx.x % LANES;
   int share = a.join_rows == 1 ? SIDES : 1;  // sides of a row
@@ -528,7 +520,7 @@ __global__ __launch_bounds__(THREADS) void kda_attn_join_kernel(AttnDecodeArgs a
   const int last = min(rows, (block + 1) * a.join_rows);
   for (int base = block * a.join_rows; base < last; base += SIDES / share) {
     const int row = min(base + side / share, last - 1);
-    const int64_t slot = ((int64_t)(first + n) * KV + kv) * rows + row;
+    const int64_t lane_slot = (int64_t)kv * rows + row;
     Joined r;
     for (int p = side % share; p < parts; p += share * AHEAD) {
       float2 ml[AHEAD];
@@ -536,7 +528,8 @@ __global__ __launch_bounds__(THREADS) void kda_attn_join_kernel(AttnDecodeArgs a
       float top = r.m;
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) {
-        const int64_t from = slot + min(p + i * share, parts - 1) * step;
+        const int piece = min(p + i * share, parts - 1);
+        const int64_t from = lane_slot + (piece ? first + 2 * piece : head_slot) * step;
         ml[i] = *reinterpret_cast<const float2*>(a.part_ml + from * 2);
         v[i] = *reinterpret_cast<const float4*>(a.part_out + from * D + col * 4);
       }
@@ -580,10 +573,9 @@ void launch(const AttnDecodeArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL(kernel, grid, dim3(THREADS), 0, stream, a);
   if (!a.part_out) return;
   AttnDecodeArgs join = a;
-  static int jl = getenv("KJOIN") ? atoi(getenv("KJOIN")) : 4096;
-  join.join_rows = (int64_t)a.N * a.T * a.H <= jl ? 1 : THREADS / (D / 4);
+  join.join_rows = (int64_t)a.parts * a.T * a.H <= 4096 ? 1 : THREADS / (D / 4);
   const int64_t row_blocks = (a.T * G + join.join_rows - 1) / join.join_rows;
-  hipLaunchKernelGGL(kda_attn_join_kernel<D>, dim3((unsigned)(a.N * a.c.KV * row_blocks)), dim3(THREADS), 0, stream, join);
+  hipLaunchKernelGGL(kda_attn_join_kernel<D>, dim3((unsigned)((a.parts - 1) * a.c.KV * row_blocks)), dim3(THREADS), 0, stream, join);
 }
 
 }  // namespace

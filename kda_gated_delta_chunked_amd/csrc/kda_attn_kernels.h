@@ -52,7 +52,7 @@ struct AttnDecodeArgs {
   float scale;
   int64_t q_stride, out_stride;
   int parts;              // stretches that the contexts are cut into together
-  float* part_out;        // [parts + N, KV, T H / KV, D], sums not divided yet; NULL: a workgroup takes a whole context
+  float* part_out;        // [2 parts, KV, T H / KV, D], sums not divided yet; NULL: a workgroup takes a whole context
   float* part_ml;         // the same with two for D: maximum, sum
   int join_rows;          // of a workgroup that joins pieces
 };
@@ -93,7 +93,6 @@ inline int64_t attn_decode_row_blocks(int64_t T, int64_t G) {
 inline int64_t attn_decode_blocks(int64_t items, int64_t KV, int64_t T, int64_t G) {
   return items * KV * attn_decode_row_blocks(T, G);
 }
-constexpr int kAttnParts = 512;  // stretches at most
 inline int64_t kv_store_threads(int64_t T, int64_t KV, int64_t D) { return (T * KV * (D / 8) + 255) / 256 * 256; }
 constexpr int kAssignTokens = 1024;  // new tokens of a workgroup
 inline int64_t kv_assign_blocks(int64_t T) { return T ? (T + kAssignTokens - 1) / kAssignTokens : 1; }
