@@ -155,15 +155,20 @@ kda_status check_decode(const kda_attn_decode_problem* p) {
   return KDA_OK;
 }
 
-// The stretches that the contexts are cut into where they are few, so that all
-// workgroups of the device have the same work; 0: a workgroup takes a whole context.
+// The stretches that contexts are cut into so that all workgroups of the device have the same
+// work; 0: a workgroup takes a whole context.  A cut costs a launch that joins and a search of
+// the lengths, some 10 us: contexts of 1024 positions are left whole (16 requests of up to 1000, 8
+// KV heads of 128, 20 us whole and 30 cut; of up to 2000, 31 and 32; one of 2000, 33 and 22), and
+// longer ones cut (256 of up to 8192 829 and 761; 1024 of up to 2048 932 and 818).  Of many rows, which
+// have more to join, they are cut as long as workgroups are few (64 requests of 16 tokens, up to
+// 8192, 4 heads a KV head, 350 and 289; 512 of 9, up to 4096, no difference).  Two workgroups
+// go on a CU, but for few contexts one has less to join (one of 131072 120 with 512, 111 with 256).
 int decode_parts(const kda_attn_decode_problem* p) {
   const int64_t KV = p->cache.num_kv_heads, G = p->num_heads / KV, T = p->tokens_per_seq;
   const int64_t per_item = kda::attn_decode_blocks(1, KV, T, G), blocks = p->num_seqs * per_item;
-  static const int64_t limit = getenv("KLIM") ? atoi(getenv("KLIM")) : 2048, fw = getenv("KFEW") ? atoi(getenv("KFEW")) : 512;
   const bool many = T * G > kda::kAttnFewRows;
-  if ((many && blocks >= limit) || (int64_t)p->table_width * p->cache.page_size <= 1024) return 0;
-  const int64_t parts = (many ? 512 : blocks <= 256 ? 256 : fw) / per_item;
+  if ((many && blocks >= 2048) || (int64_t)p->table_width * p->cache.page_size <= 1024) return 0;
+  const int64_t parts = (many || blocks > 256 ? 512 : 256) / per_item;
   return parts > 1 ? (int)parts : 0;
 }
 

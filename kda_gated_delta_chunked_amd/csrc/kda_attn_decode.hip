@@ -203,7 +203,7 @@ struct Place {
 };
 
 template <int D, bool E4M3>
-__global__ __launch_bounds__(THREADS, D == 64 ? 3 : 2) void kda_attn_decode_kernel(AttnDecodeArgs a) {
+__global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeArgs a) {
   using Copies = PageCopies<D, E4M3>;
   constexpr int TILE = Copies::TILE;
   constexpr int OUTPUTS = 32 * D * 4, WAVE_BYTES = 2 * TILE > OUTPUTS ? 2 * TILE : OUTPUTS;  // a tile of keys and one of values; at the end the wave's outputs
