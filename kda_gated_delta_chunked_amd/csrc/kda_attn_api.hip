@@ -167,7 +167,7 @@ int decode_parts(const kda_attn_decode_problem* p) {
   const int64_t KV = p->cache.num_kv_heads, G = p->num_heads / KV, T = p->tokens_per_seq;
   const int64_t per_item = kda::attn_decode_blocks(1, KV, T, G), blocks = p->num_seqs * per_item;
   const bool many = T * G > kda::kAttnFewRows;
-  if ((many && blocks >= 2048) || (int64_t)p->table_width * p->cache.page_size <= 1024) return 0;
+  if (blocks == 0 || (many && blocks >= 2048) || (int64_t)p->table_width * p->cache.page_size <= 1024) return 0;
   const int64_t parts = (many || blocks > 256 ? 512 : 256) / per_item;
   return parts > 1 ? (int)parts : 0;
 }
@@ -314,7 +314,7 @@ kda_status kda_kv_store_validate(const kda_kv_store_problem* p, const void* k, c
   if (st != KDA_OK) return st;
   const int64_t T = p->tokens, KV = c.num_kv_heads, row = KV * c.head_dim;
   if (T < 0 || !stride_ok(p->k_stride, row) || !stride_ok(p->v_stride, row)) return KDA_ERR_INVALID_ARG;
-  if (T > kInt32Max || kda::kv_store_threads(T, KV, c.head_dim) > kda::kMaxThreads) return KDA_ERR_TOO_LARGE;
+  if (T > kInt32Max || kda::kv_store_threads(T, KV, c.head_dim, c.dtype == KDA_CACHE_E4M3) > kda::kMaxThreads) return KDA_ERR_TOO_LARGE;
   const bool scaled = c.dtype == KDA_CACHE_E4M3;
   if (T > 0 && (!k || !v || !slots || !k_cache || !v_cache)) return KDA_ERR_INVALID_ARG;
   if (T > 0 && (scaled != (k_scale != nullptr) || scaled != (v_scale != nullptr))) return KDA_ERR_INVALID_ARG;

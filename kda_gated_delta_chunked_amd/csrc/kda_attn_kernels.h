@@ -93,8 +93,11 @@ inline int64_t attn_decode_row_blocks(int64_t T, int64_t G) {
 inline int64_t attn_decode_blocks(int64_t items, int64_t KV, int64_t T, int64_t G) {
   return items * KV * attn_decode_row_blocks(T, G);
 }
-inline int64_t kv_store_threads(int64_t T, int64_t KV, int64_t D) { return (T * KV * (D / 8) + 255) / 256 * 256; }
-constexpr int kAssignTokens = 1024;  // new tokens of a workgroup
+constexpr int kv_store_cols(bool e4m3) { return e4m3 ? 16 : 8; }  // of a thread
+inline int64_t kv_store_threads(int64_t T, int64_t KV, int64_t D, bool e4m3) {
+  return (T * KV * (D / kv_store_cols(e4m3)) + 255) / 256 * 256;
+}
+constexpr int kAssignTokens = 256;  // new tokens of a workgroup
 inline int64_t kv_assign_blocks(int64_t T) { return T ? (T + kAssignTokens - 1) / kAssignTokens : 1; }
 
 }  // namespace kda

@@ -119,12 +119,13 @@ def test_decode_checks(want, kw):
 
 
 def test_decode_workspace():
-    # few requests over long tables run in parts, with two numbers and a row of
-    # sums per part and row; many requests, or one short table, do not
+    # contexts over long tables are cut into stretches, with two numbers and a row of
+    # sums for each end of a stretch and row; many rows of many requests, or short tables, are not
     def size(n, T, H, W, **c):
         return A.decode_workspace_size(A.DecodeProblem(n, T, H, 0.1, n, W, 0, 0, 0, cache(**c)))
-    assert size(1024, 1, 32, 1024, KV=8) == 0
+    assert size(1024, 64, 32, 1024, KV=8) == 0
     assert size(1, 1, 4, 1) == 0
+    assert size(4096, 1, 32, 1024, KV=8) == size(512, 1, 32, 1024, KV=8)
     assert size(0, 1, 4, 1024) == 0
     got = size(1, 1, 8, 8192, KV=8, D=128)
     assert got > 0 and got % (8 * 130 * 4) == 0
