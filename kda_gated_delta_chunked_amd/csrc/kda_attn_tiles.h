@@ -201,16 +201,20 @@ __device__ __forceinline__ bf16x8 finite_only(const bf16x8& f) {
 // grown too far (or m is still that of no key).  Only then the scores' maximum is
 // looked for, and what has been summed is brought to it: a weight is at most kFar, which costs
 // no accuracy (sums are floating point), and most blocks need no maximum.
+//
+// c s - c m is one operation, c m rounded once.  Where it is so large (beyond kNear) that this rounding
+// would show, c (s - m) is taken, always from the maximum: `far` is less than any sum from then on.
 template <int D>
 struct AttnRows {
-  static constexpr float kFar = 4096.f;
+  static constexpr float kFar = 4096.f, kNear = 4096.f;
   bf16x8 q[D / 16];
   f32x16 o[D / 32];
-  float m, l;
+  float m, l, far;
 
   __device__ __forceinline__ void start() {
     m = kNone;
     l = 0.f;
+    far = kFar;
 #pragma unroll
     for (int b = 0; b < D / 32; ++b)
 #pragma unroll
@@ -239,11 +243,13 @@ struct AttnRows {
     return s;
   }
   // weights of scores from a maximum, as operands, and their sum
-  static __device__ __forceinline__ float weights(const f32x16& s, float c, float mc, bf16x8 (&p)[2]) {
+  template <bool NEAR>
+  static __device__ __forceinline__ float weights(const f32x16& s, float c, float m, bf16x8 (&p)[2]) {
+    const float mc = m * c;
     float e[16], sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], c, -mc));
+      e[i] = __builtin_amdgcn_exp2f(NEAR ? __builtin_fmaf(s[i], c, -mc) : (s[i] - m) * c);
       sum[i & 1] += e[i];
     }
 #pragma unroll
@@ -281,7 +287,7 @@ struct AttnRows {
     const float mc = m * c;
     float e = 0.f, part[2] = {0.f, 0.f};
     uint32_t pair[8];
-    bool far = false;
+    bool beyond = false;
 #pragma unroll
     for (int i = 0; i < 16; ++i) n[i] = 0.f;
 #pragma unroll
@@ -308,19 +314,19 @@ struct AttnRows {
       if (i % EVERY == 1 % EVERY && i / EVERY < Source::COUNT) source.put(i / EVERY);
       if (i == BUSY) {
         sum = part[0] + part[1];
-        far = __any(!(sum <= kFar));
+        beyond = __any(!(sum <= far));
       }
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k)
       next_p[k] = __builtin_bit_cast(bf16x8, make_uint4(pair[4 * k], pair[4 * k + 1], pair[4 * k + 2], pair[4 * k + 3]));
-    return far;
+    return beyond;
   }
   // Weights of the scores of 32 keys and their sum; whether one went too far.
   __device__ __forceinline__ bool try_weights(const f32x16& s, float c, bf16x8 (&p)[2], float& sum) const {
-    sum = weights(s, c, m * c, p);
-    return __any(!(sum <= kFar));
+    sum = weights<true>(s, c, m, p);
+    return __any(!(sum <= far));
   }
   // The same from the scores' maximum, to which the state is brought (FIRST: there is none yet).
   template <bool FIRST = false>
@@ -338,7 +344,13 @@ struct AttnRows {
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[b][i] *= keep;
     }
-    sum = weights(s, c, now == kNone ? 0.f : now * c, p);
+    const float from = now == kNone ? 0.f : now;
+    if (__builtin_expect(__any(fabsf(from) * c > kNear), 0)) {
+      far = -1.f;
+      sum = weights<false>(s, c, from, p);
+    } else {
+      sum = weights<true>(s, c, from, p);
+    }
   }
   // Scores of 32 keys become weights; the state takes them in.
   __device__ __forceinline__ void weigh(const f32x16& s, float c, bf16x8 (&p)[2]) {

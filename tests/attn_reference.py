@@ -31,7 +31,7 @@ def attend(q, k, v, seen, scale):
         s = scale * (k[at] @ q[i])
         terms[i] = (scale * (k[at].abs() @ q[i].abs())).max()
         lse[i] = torch.logsumexp(s, 0)
-        p = torch.exp(s - lse[i])
+        p = torch.softmax(s, 0)  # (exp(s - lse) would lose the sum where |s| is past 2^53)
         out[i], mag[i] = p @ v[at], p @ v[at].abs()
     return out, lse, mag, terms
 
