@@ -17,14 +17,13 @@ namespace {
 
 constexpr int WAVES = kAttnRows / 32;  // that share rows' keys
 constexpr int KEYS = 32;               // of a block
-constexpr int RING = 4;                // tiles of keys, and of values, in LDS
 
 // The keys and values of one head of a sequence, every SPLIT-th block of them from
 // block `side` on, for a wave of rows from `top` on.
 template <int D, int SPLIT>
 struct PromptSource {
-  using Places = TilePlaces<D, false>;
-  static constexpr int TILE = Places::BYTES;
+  using Places = TilePlaces<D, false, true>;
+  static constexpr int RING = 4, TILE = Places::BYTES;  // tiles of keys, and of values, in LDS
   static constexpr int PER_ROW = D / 8, ROWS = 64 / PER_ROW, PARTS = KEYS / ROWS;  // a copy's rows, a tile's copies
   static constexpr int COUNT = 2 * PARTS / WAVES;                                  // of a wave, keys and values
   static_assert(COUNT >= 1 && (PARTS <= WAVES || WAVES * ROWS == 16), "a lane's rows have one swizzle");
@@ -37,7 +36,7 @@ struct PromptSource {
 
   __device__ __forceinline__ PromptSource(const AttnArgs& a, int64_t token, int length_, int kv, int wave_, int side_, int top,
                                           uint8_t* tiles)
-      : ktiles(tiles), vtiles(tiles + RING * TILE), open(count(top / KEYS, side_)),
+      : ktiles(tiles), vtiles(tiles + RING * TILE), places(ktiles, vtiles), open(count(top / KEYS, side_)),
         kbase(reinterpret_cast<uint64_t>(a.k + (token + side_ * KEYS) * a.k_stride + kv * D)),
         vbase(reinterpret_cast<uint64_t>(a.v + (token + side_ * KEYS) * a.v_stride + kv * D)), kbytes((int)a.k_stride * 2),
         vbytes((int)a.v_stride * 2), length(length_ - side_ * KEYS), wave(wave_), side(side_) {
@@ -71,10 +70,7 @@ struct PromptSource {
     for (int i = 0; i < COUNT; ++i) put(i);
   }
   // Of the block of keys b, and of values b - 2: the b-th ones copied.
-  __device__ __forceinline__ Places place(int b) const {
-    const int at = (b & (RING - 1)) * TILE;
-    return Places(places, at, at);
-  }
+  __device__ __forceinline__ uint32_t at(int b) const { return (uint32_t)((b & (RING - 1)) * TILE); }
   template <int READS>
   __device__ __forceinline__ void turn() {
     memory_left<COUNT>();
@@ -107,7 +103,7 @@ __device__ __forceinline__ Span rows_of_slot(const Packing& p, int64_t slot) {
 template <int D, int SPLIT>
 __global__ __launch_bounds__(SPLIT * WAVES * 64, 2) void kda_attn_kernel(AttnArgs a) {
   using Source = PromptSource<D, SPLIT>;
-  __shared__ __attribute__((aligned(1024))) uint8_t tiles[SPLIT][2 * RING * Source::TILE];
+  __shared__ __attribute__((aligned(1024))) uint8_t tiles[SPLIT][2 * Source::RING * Source::TILE];
   // The heads of a slot side by side, a group's on one XCD where there are at least
   // as many groups as XCDs; a sequence's last, longest rows first.
   const int in = (int)(blockIdx.x % (unsigned)a.H), kv = in % a.KV, head = kv * (a.H / a.KV) + in / a.KV;

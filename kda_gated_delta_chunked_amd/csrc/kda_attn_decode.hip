@@ -232,7 +232,6 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
     asm volatile("" : "+v"(sees));  // there ahead of the copies
     const int32_t* table = a.table + (int64_t)req.row * a.table_width;
     const float c = a.scale * kLog2e * (E4M3 ? a.c.k_scale[kv] : 1.f);
-    const TilePlaces<D, E4M3> places;
     const Copies copies(a.c, kv);
     uint8_t* const ring = tiles[wave];
     const int first = begin + wave * KEYS, count = (end - first + STEP - 1) / STEP;  // the wave's tiles
@@ -255,10 +254,11 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
       fetch_values(0);
       r.settle();
     }
-    const TilePlaces<D, E4M3> at(places, 0, TILE);
+    const TilePlaces<D, E4M3, false> held(ring, ring + TILE);
     for (int tile = 0; tile < count; ++tile) {
       memory_left<Copies::PARTS>();
-      f32x16 s = r.scores(at, ring);
+      const auto places = held.fresh();
+      f32x16 s = r.scores(places, 0);
       reads_done();
       const bool all = first + tile * STEP + KEYS <= min(req.before, end) && half0 && half1;
       if (!all) mask_scores(s, seen_keys(first + tile * STEP, end, req.before, sees, half0, half1));
@@ -270,8 +270,8 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
       r.l += sum;
       if (more) memory_left<Copies::PARTS>();
       else memory_left<0>();
-      if (all) r.add(at, ring, p);
-      else not_finite = r.add_masked(at, ring, p) || not_finite;
+      if (all) r.add(places, 0, p);
+      else not_finite = r.add_masked(places, 0, p) || not_finite;
       reads_done();
       if (more) fetch_values(tile + 1);
     }
@@ -343,7 +343,7 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
 // The blocks of 32 positions of a part, for a wave of rows of a request.
 template <int D, bool E4M3>
 struct PagedSource {
-  using Places = TilePlaces<D, E4M3>;
+  using Places = TilePlaces<D, E4M3, false>;
   using Copies = PageCopies<D, E4M3>;
   static constexpr int RING = 4, TILE = Places::BYTES, COUNT = Copies::COUNT / WAVES;
   static_assert(COUNT >= 1 && Copies::PARTS % 2 == 0, "a copy for each wave at least");
@@ -359,12 +359,12 @@ struct PagedSource {
   uint64_t sees;  // the request's own tokens that the lane's row sees
   TileStarts<Copies::SIZE> starts;
   int copied = 0, slot = 0;  // blocks of keys so far (values are two behind), and the next one's place
-  int at = 0;                // the block of values that is copied next, in its group
+  int in_group = 0;           // the block of values that is copied next, in its group
   uint64_t there = 0;        // which halves have pages, two bits a block of keys, the last one lowest
 
   __device__ __forceinline__ PagedSource(const AttnDecodeArgs& a_, int kv, const int32_t* table_, int begin_, int end_,
                                          int before_, uint64_t sees_, int wave_, uint8_t* tiles)
-      : ktiles(tiles), vtiles(tiles + RING * TILE), open(max(min(before_, end_) - begin_, 0) / KEYS), copies(a_.c, kv), a(a_),
+      : ktiles(tiles), vtiles(tiles + RING * TILE), places(ktiles, vtiles), open(max(min(before_, end_) - begin_, 0) / KEYS), copies(a_.c, kv), a(a_),
         table(table_), begin(begin_), end(end_), before(before_), wave(wave_), from(copies.lane_from(wave_ % Copies::PARTS)),
         sees(sees_) {
     find();
@@ -375,13 +375,13 @@ struct PagedSource {
       starts.lo[0] = starts.lo[1];
       starts.hi[0] = starts.hi[1];
     }
-    at = 0;
+    in_group = 0;
   }
   // One of the COUNT copies of the next block of keys, and of the one of values two behind it
   // (of page 0 while there is none).
   __device__ __forceinline__ void put(int i) {
     if (i == 0) {
-      const bool h0 = starts.has(at + 2, 0), h1 = starts.has(at + 2, 1);
+      const bool h0 = starts.has(in_group + 2, 0), h1 = starts.has(in_group + 2, 1);
       there = there << 2 | (h0 ? 1u : 0u) | (h1 ? 2u : 0u);
       open = h0 && h1 ? open : min(open, copied);
     }
@@ -389,26 +389,23 @@ struct PagedSource {
     const bool key = COUNT == 1 ? u < Copies::PARTS : i < COUNT / 2;
     // (a wave's copies of a tile are 16 rows apart: their lanes' bytes are the same)
     static_assert(HALVES == 1 || WAVES * Copies::ROWS == 16, "a lane's rows have one swizzle");
-    copies.copy(key, part, starts.start(key ? at + 2 : at, i % HALVES), from,
+    copies.copy(key, part, starts.start(key ? in_group + 2 : in_group, i % HALVES), from,
                 lds_place(key ? ktiles : vtiles) + (uint32_t)slot);
     if (i < COUNT - 1) return;
     ++copied;
-    ++at;
+    ++in_group;
     slot = (slot + TILE) & (RING * TILE - 1);
   }
   __device__ __forceinline__ void put() {
 #pragma unroll
     for (int i = 0; i < COUNT; ++i) put(i);
   }
-  __device__ __forceinline__ Places place(int b) const {
-    const int at = (b & (RING - 1)) * TILE;
-    return Places(places, at, at);
-  }
+  __device__ __forceinline__ uint32_t at(int b) const { return (uint32_t)((b & (RING - 1)) * TILE); }
   template <int READS>
   __device__ __forceinline__ void turn() {
     memory_left<COUNT>();
     tiles_barrier<READS>();
-    if (at == GROUP) find();
+    if (in_group == GROUP) find();
   }
   __device__ __forceinline__ uint32_t seen(int j) const {
     const uint32_t halves = (uint32_t)(there >> (2 * (copied - 1 - j)));

@@ -67,53 +67,73 @@ __device__ __forceinline__ bf16x8 widen8(const uint2& u) {
 // group of 16 lanes, lane m of a transposed read of bf16 points to four columns of
 // row m / 4 of four, of codes to eight columns of row m / 2 of eight; lane i receives
 // column i of the 16.
-template <int D, bool E4M3>
+// where in LDS
+__device__ __forceinline__ uint32_t lds_place(const uint8_t* p) {
+  typedef __attribute__((address_space(3))) const uint8_t* lds_ptr;
+  return (uint32_t)(uintptr_t)(lds_ptr)p;
+}
+
+// HELD: the places of all operands are kept in registers, and those of the ring's other tiles are
+// a constant away; otherwise each is an exclusive or of one of two.
+template <int D, bool E4M3, bool HELD>
 struct TilePlaces {
   static constexpr int BYTES = 32 * D * (E4M3 ? 1 : 2);  // of a tile
   static constexpr int READS = E4M3 ? 2 : 3;             // of LDS for an operand of keys and one of values
-  int row, col;
-  __device__ __forceinline__ TilePlaces() {
+  static constexpr int STEP = E4M3 ? 16 : 32, KEYS = D / 16, VALUES = D / (E4M3 ? 32 : 16);  // of a lane's key, bytes; places
+  uint32_t k[HELD ? KEYS : 1], v[HELD ? VALUES : 1], keys_at, values_at;
+  __device__ __forceinline__ TilePlaces(const uint8_t* keys, const uint8_t* values) {
     const int lane = threadIdx.x & 63, h = lane >> 5, m = lane & 15, g = (lane >> 4) & 1;
-    if constexpr (E4M3) {
-      row = attn_tile_at<D, true>(lane & 31, 0) + h * 8;
-      col = attn_tile_at<D, true>(4 * h + ((m >> 1) & 3) + (m & 8), g) + (m & 1) * 8;
-    } else {
-      row = attn_tile_at<D, false>(lane & 31, h);
-      col = attn_tile_at<D, false>(4 * h + (m >> 2), 2 * g + ((m & 3) >> 1)) + (m & 1) * 8;
+    k[0] = attn_tile_at<D, E4M3>(lane & 31, E4M3 ? 0 : h) + (E4M3 ? h * 8 : 0);
+    v[0] = E4M3 ? attn_tile_at<D, true>(4 * h + ((m >> 1) & 3) + (m & 8), g) + (m & 1) * 8
+                : attn_tile_at<D, false>(4 * h + (m >> 2), 2 * g + ((m & 3) >> 1)) + (m & 1) * 8;
+    keys_at = lds_place(keys);
+    values_at = lds_place(values);
+    if constexpr (HELD) {
+      const uint32_t row = k[0], col = v[0];
+#pragma unroll
+      for (int i = 0; i < KEYS; ++i) k[i] = forget(keys_at + (row ^ (i * STEP)));
+#pragma unroll
+      for (int i = 0; i < VALUES; ++i) v[i] = forget(values_at + (col ^ (i * 32)));
     }
   }
-  // the tiles at `keys` and `values` bytes
-  __device__ __forceinline__ TilePlaces(const TilePlaces& at, int keys, int values)
-      : row(forget(at.row + keys)), col(forget(at.col + values)) {}
+  // The same, for a turn: nothing that is derived from it is kept across turns.
+  __device__ __forceinline__ TilePlaces fresh() const {
+    TilePlaces f = *this;
+    if constexpr (!HELD) {
+      f.k[0] = forget(k[0]);
+      f.v[0] = forget(v[0]);
+    }
+    return f;
+  }
+  __device__ __forceinline__ uint32_t key_place(int i) const { return HELD ? k[HELD ? i : 0] : (k[0] ^ (i * STEP)) + keys_at; }
+  __device__ __forceinline__ uint32_t value_place(int i) const {
+    return HELD ? v[HELD ? i : 0] : (v[0] ^ (i * 32)) + values_at;
+  }
   // an operand as it is read, and as it is used
   using Raw = std::conditional_t<E4M3, uint2, bf16x8>;
   static __device__ __forceinline__ bf16x8 use(const Raw& r) {
     if constexpr (E4M3) return widen8(r);
     else return r;
   }
-  // columns 16 step + 8 h .. + 7 of the lane's key
-  __device__ __forceinline__ Raw read_keys(const uint8_t* tiles, int step) const {
-    return *reinterpret_cast<const Raw*>(tiles + (row ^ (step * (E4M3 ? 16 : 32))));
+  // of the tile `at` bytes behind the first one: columns 16 step + 8 h .. + 7 of the lane's key
+  __device__ __forceinline__ Raw read_keys(uint32_t at, int step) const {
+    typedef __attribute__((address_space(3))) const std::conditional_t<E4M3, i32x2, bf16x8>* lds_ptr;
+    return __builtin_bit_cast(Raw, *(lds_ptr)(uintptr_t)(key_place(step) + at));
   }
   // column 32 block + lane % 32, keys 16 step + 4 h + (0..3) and 8 more
-  __device__ __forceinline__ Raw read_values(const uint8_t* tiles, int block, int step) const {
+  __device__ __forceinline__ Raw read_values(uint32_t at, int block, int step) const {
     if constexpr (E4M3) {
       typedef __attribute__((address_space(3))) i32x2* lds_ptr;
-      return __builtin_bit_cast(
-          uint2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_ptr)(tiles + step * 16 * D + (col ^ (block * 32)))));
+      return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_ptr)(uintptr_t)(value_place(block) + (at + step * 16 * D))));
     } else {
       typedef __attribute__((address_space(3))) s16x4* lds_ptr;
-      const int at = col ^ (block * 64);
-      const uint8_t* t = tiles + step * 32 * D;
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(t + at));
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(t + 16 * D + (at ^ 32)));
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(uintptr_t)(value_place(2 * block) + (at + step * 32 * D)));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(uintptr_t)(value_place(2 * block + 1) + (at + step * 32 * D + 16 * D)));
       return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
   }
-  __device__ __forceinline__ bf16x8 keys(const uint8_t* tiles, int step) const { return use(read_keys(tiles, step)); }
-  __device__ __forceinline__ bf16x8 values(const uint8_t* tiles, int block, int step) const {
-    return use(read_values(tiles, block, step));
-  }
+  __device__ __forceinline__ bf16x8 keys(uint32_t at, int step) const { return use(read_keys(at, step)); }
+  __device__ __forceinline__ bf16x8 values(uint32_t at, int block, int step) const { return use(read_values(at, block, step)); }
 };
 
 // Waits until at most `left` of the wave's memory accesses are under way.
@@ -129,10 +149,6 @@ __device__ __forceinline__ void memory_left() {
 // builtins the compiler would wait ahead of every transposed read of LDS until no copy is
 // under way.  memory_left waits for them; M0, which nothing else in these kernels uses, is
 // the place in LDS and takes effect one wait state later.
-__device__ __forceinline__ uint32_t lds_place(const uint8_t* p) {
-  typedef __attribute__((address_space(3))) const uint8_t* lds_ptr;
-  return (uint32_t)(uintptr_t)(lds_ptr)p;
-}
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 #if defined(__HIP_DEVICE_COMPILE__)
 __device__ __forceinline__ void copy_to_lds(uint32_t lds, uint64_t from, uint32_t offset) {
@@ -234,12 +250,12 @@ struct AttnRows {
   }
   // scores of a tile's 32 keys
   template <class Places>
-  __device__ __forceinline__ f32x16 scores(const Places& at, const uint8_t* tiles) const {
+  __device__ __forceinline__ f32x16 scores(const Places& places, uint32_t at) const {
     f32x16 s;
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[i] = 0.f;
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) s = mfma32(at.keys(tiles, k), q[k], s);
+    for (int k = 0; k < D / 16; ++k) s = mfma32(places.keys(at, k), q[k], s);
     return s;
   }
   // weights of scores from a maximum, as operands, and their sum
@@ -265,10 +281,9 @@ struct AttnRows {
   static constexpr int COUNT = D / 8, DEPTH = 2;
   static_assert(COUNT % DEPTH == 0, "operands of the next turn in the same places");
   template <class Places>
-  static __device__ __forceinline__ typename Places::Raw operand(const Places& at, const uint8_t* ktiles,
-                                                                 const uint8_t* vtiles, int i) {
-    if (i % 2) return at.read_values(vtiles, i / 2 % (D / 32), i / 2 / (D / 32));
-    return at.read_keys(ktiles, i / 2);
+  static __device__ __forceinline__ typename Places::Raw operand(const Places& places, uint32_t at, int i) {
+    if (i % 2) return places.read_values(at, i / 2 % (D / 32), i / 2 / (D / 32));
+    return places.read_keys(at, i / 2);
   }
   // scores(n), add(p) and try_weights(s, next_p) of three blocks in one, in an order in which
   // each covers the others: behind every product of matrices come the read of the operand
@@ -277,10 +292,10 @@ struct AttnRows {
   // nothing waits for them at the end.  (The compiler, left to itself, puts all products
   // ahead of all weights.)
   template <class Source, class Places = typename Source::Places>
-  __device__ __forceinline__ bool turn(Source& source, int j, typename Places::Raw (&f)[DEPTH], const f32x16& s, float c,
-                                       f32x16& n, const bf16x8 (&p)[2], bf16x8 (&next_p)[2], float& sum) {
-    const uint8_t *ktiles = source.ktiles, *vtiles = source.vtiles;
-    const Places at = source.place(j + 1), next = source.place(j + 2);
+  __device__ __forceinline__ bool turn(Source& source, uint32_t at, uint32_t next, typename Places::Raw (&f)[DEPTH],
+                                       const f32x16& s, float c, f32x16& n, const bf16x8 (&p)[2], bf16x8 (&next_p)[2],
+                                       float& sum) {
+    const Places places = source.places.fresh();
     constexpr int EVERY = (COUNT - 2) / Source::COUNT;  // products between copies
     static_assert(EVERY >= 1, "a copy behind a product");
     constexpr int BUSY = COUNT * 3 / 4;
@@ -296,7 +311,7 @@ struct AttnRows {
       if (i % 2) o[i / 2 % (D / 32)] = mfma32(v, p[i / 2 / (D / 32)], o[i / 2 % (D / 32)]);
       else n = mfma32(v, q[i / 2], n);
       const int ahead = i + DEPTH;
-      f[i % DEPTH] = ahead < COUNT ? operand(at, ktiles, vtiles, ahead) : operand(next, ktiles, vtiles, ahead - COUNT);
+      f[i % DEPTH] = ahead < COUNT ? operand(places, at, ahead) : operand(places, next, ahead - COUNT);
       if (i < BUSY) {
 #pragma unroll
         for (int w = 16 * i / BUSY; w < 16 * (i + 1) / BUSY; ++w) {
@@ -360,21 +375,21 @@ struct AttnRows {
   }
   // o += V^T P^T for a tile's 32 keys
   template <class Places>
-  __device__ __forceinline__ void add(const Places& at, const uint8_t* tiles, const bf16x8 (&p)[2]) {
+  __device__ __forceinline__ void add(const Places& places, uint32_t at, const bf16x8 (&p)[2]) {
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int b = 0; b < D / 32; ++b) o[b] = mfma32(at.values(tiles, b, k), p[k], o[b]);
+      for (int b = 0; b < D / 32; ++b) o[b] = mfma32(places.values(at, b, k), p[k], o[b]);
   }
   // The same where rows see different keys.  A weight of zero does not keep an
   // infinity or a NaN from a row, so where the tile holds any they are left out here:
   // the answer is true then, and add_not_finite has to bring them to the rows that see them.
   template <class Places>
-  __device__ __forceinline__ bool add_masked(const Places& at, const uint8_t* tiles, const bf16x8 (&p)[2]) {
+  __device__ __forceinline__ bool add_masked(const Places& places, uint32_t at, const bf16x8 (&p)[2]) {
     Exponents most;
     typename Places::Raw v[2 * (D / 32)];
 #pragma unroll
-    for (int i = 0; i < 2 * (D / 32); ++i) v[i] = at.read_values(tiles, i % (D / 32), i / (D / 32));
+    for (int i = 0; i < 2 * (D / 32); ++i) v[i] = places.read_values(at, i % (D / 32), i / (D / 32));
 #pragma unroll
     for (int i = 0; i < 2 * (D / 32); ++i) most.take(Places::use(v[i]));
     if (__builtin_expect(!__any(most.not_finite()), 1)) {
@@ -386,7 +401,7 @@ struct AttnRows {
     for (int k = 0; k < 2; ++k)
 #pragma unroll
       for (int b = 0; b < D / 32; ++b) {
-        o[b] = mfma32(finite_only(at.values(tiles, b, k)), p[k], o[b]);
+        o[b] = mfma32(finite_only(places.values(at, b, k)), p[k], o[b]);
         __builtin_amdgcn_sched_barrier(0);
       }
     return true;
@@ -448,14 +463,14 @@ template <int D, class Source>
 __device__ __forceinline__ bool attend(AttnRows<D>& r, Source& source, float c, int blocks, int mine) {
   using Rows = AttnRows<D>;
   using Places = typename Source::Places;
-  const uint8_t *kt = source.ktiles, *vt = source.vtiles;
+  const Places& places = source.places;
   bool left_out = false;
   float sum;
   bf16x8 p[2];
   // blocks 0 and 1: their keys are there with the first turn
   source.template turn<0>();
   source.put();
-  f32x16 s = r.scores(source.place(0), kt), n = r.scores(source.place(1), kt);
+  f32x16 s = r.scores(places, source.at(0)), n = r.scores(places, source.at(1));
   if (source.open < 1) mask_scores(s, source.seen(0));
   r.template weights_from_maximum<true>(s, c, p, sum);
   r.l += sum;
@@ -464,31 +479,52 @@ __device__ __forceinline__ bool attend(AttnRows<D>& r, Source& source, float c, 
   source.put();
   int j = 1;
   typename Places::Raw f[Rows::DEPTH];
-  auto read_ahead = [&]() {
-    const Places at = source.place(j + 1);
+  auto read_ahead = [&](uint32_t at) {
 #pragma unroll
-    for (int i = 0; i < Rows::DEPTH; ++i) f[i] = Rows::operand(at, kt, vt, i);
+    for (int i = 0; i < Rows::DEPTH; ++i) f[i] = Rows::operand(places, at, i);
   };
   bf16x8 next_p[2];
   if (j < source.open) {
+    // Four turns a pass: a turn's place in the ring is a constant, and the scores and weights of
+    // this block and of the next one change their registers' roles.
+    static_assert(Source::RING == 4, "turns of a pass");
     source.template turn<0>();
-    read_ahead();
-    for (;;) {
-      if (__builtin_expect(r.turn(source, j, f, s, c, n, p, next_p, sum), 0)) r.weights_from_maximum(s, c, next_p, sum);
+    read_ahead(source.at(2));
+    auto one = [&](auto place, f32x16& s, f32x16& n, bf16x8 (&p)[2], bf16x8 (&next_p)[2]) {
+      constexpr uint32_t AT = decltype(place)::value * Source::TILE, NEXT = (decltype(place)::value + 1) % 4 * Source::TILE;
+      if (__builtin_expect(r.turn(source, AT, NEXT, f, s, c, n, p, next_p, sum), 0)) r.weights_from_maximum(s, c, next_p, sum);
       r.l += sum;
+      return ++j >= source.open;
+    };
+    auto back = [&]() { source.template turn<Rows::DEPTH / 2 * Places::READS>(); };
+    bool odd;
+    for (;;) {
+      odd = true;
+      if (one(std::integral_constant<int, 2>(), s, n, p, next_p)) break;
+      back();
+      odd = false;
+      if (one(std::integral_constant<int, 3>(), n, s, next_p, p)) break;
+      back();
+      odd = true;
+      if (one(std::integral_constant<int, 0>(), s, n, p, next_p)) break;
+      back();
+      odd = false;
+      if (one(std::integral_constant<int, 1>(), n, s, next_p, p)) break;
+      back();
+    }
+    if (odd) {
       s = n;
       p[0] = next_p[0];
       p[1] = next_p[1];
-      if (++j >= source.open) break;
-      source.template turn<Rows::DEPTH / 2 * Places::READS>();
     }
   }
   if (j == source.open && j < mine) {
     // the first block with masked scores, behind one without
     source.template turn<0>();
-    read_ahead();
+    read_ahead(source.at(j + 1));
     mask_scores(s, source.seen(j));
-    if (__builtin_expect(r.turn(source, j, f, s, c, n, p, next_p, sum), 0)) r.weights_from_maximum(s, c, next_p, sum);
+    if (__builtin_expect(r.turn(source, source.at(j + 1), source.at(j + 2), f, s, c, n, p, next_p, sum), 0))
+      r.weights_from_maximum(s, c, next_p, sum);
     r.l += sum;
     s = n;
     p[0] = next_p[0];
@@ -498,16 +534,17 @@ __device__ __forceinline__ bool attend(AttnRows<D>& r, Source& source, float c, 
   for (; j <= blocks; ++j) {
     source.template turn<0>();
     source.put();
-    const Places at = source.place(j + 1);
+    const uint32_t at = source.at(j + 1);
+    const Places places = source.places.fresh();
     if (j <= mine) {
-      if (j - 1 < source.open) r.add(at, vt, p);
-      else left_out = r.add_masked(at, vt, p) || left_out;
+      if (j - 1 < source.open) r.add(places, at, p);
+      else left_out = r.add_masked(places, at, p) || left_out;
     }
     if (j < mine) {
       if (j >= source.open) mask_scores(s, source.seen(j));
       r.weigh(s, c, p);
     }
-    if (j + 1 < mine) s = r.scores(at, kt);
+    if (j + 1 < mine) s = r.scores(places, at);
   }
   memory_left<0>();  // no copy outlives the workgroup
   return left_out;
