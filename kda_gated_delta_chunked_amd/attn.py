@@ -101,6 +101,18 @@ def decode_workspace_size(problem: DecodeProblem) -> int:
     return int(n.value)
 
 
+def _rows(name: str, t, dtype, shape, dev):
+    """``_check_tensor`` of a tensor whose rows may be strided, with the usual
+    answer first: these calls take a good part of a small operator's time."""
+    if t.dtype is not dtype or t.shape != shape or t.device != dev:
+        _check_tensor(name, t, dtype, shape, dev, False)
+
+
+def _packed(name: str, t, dtype, shape, dev):
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        _check_tensor(name, t, dtype, shape, dev)
+
+
 def _scale(scale, D: int) -> float:
     return D ** -0.5 if scale is None else float(scale)
 
@@ -137,29 +149,30 @@ def prefill(q, k, v, *, cu_seqlens=None, scale=None, out=None, return_lse: bool 
     if k.dim() != lead + 2:
         raise ValueError("k and v must be q.shape[:-2] + (KV, D)")
     KV = k.shape[lead]
-    _check_tensor("q", q, bf, shape, dev, False)
-    _check_tensor("k", k, bf, shape[:lead] + (KV, D), dev, False)
-    _check_tensor("v", v, bf, k.shape, dev, False)
-    _check_tensor("out", out, bf, shape, dev, False)
+    _rows("q", q, bf, shape, dev)
+    _rows("k", k, bf, kv_shape := shape[:lead] + (KV, D), dev)
+    _rows("v", v, bf, kv_shape, dev)
     cu64 = _offsets(cu_seqlens, dev)
     mine = []
     if out is None:
         out = _like(q, stream)
         mine.append(out)
+    else:
+        _rows("out", out, bf, shape, dev)
     lse = _lse(lse, return_lse, q, shape[:-1], dev, stream, mine)
     p = PrefillProblem(N, T, H, KV, D, _scale(scale, D), cu64, _row_stride("q", q, lead), _row_stride("k", k, lead),
                        _row_stride("v", v, lead), _row_stride("out", out, lead))
     _launch("kda_attn_prefill", dev, stream, p,
-            [_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(out), _ptr(lse)], mine, call_raw)
+            [q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(cu_seqlens), out.data_ptr(), _ptr(lse)], mine, call_raw)
     return out, lse
 
 
-def _strides(name: str, c):
+def _strides(name: str, c, shape):
     """Elements between a cache's pages and between a page's tokens (0, 0: packed)."""
     if c.is_contiguous():
         return 0, 0
     page, token, head, one = c.stride()
-    P, size, KV, D = c.shape
+    P, size, KV, D = shape
     if (D > 1 and one != 1) or (KV > 1 and head != D):
         raise ValueError(f"{name}: the last 2 dimensions must be contiguous")
     if (P > 1 and page <= 0) or (size > 1 and token <= 0):
@@ -170,33 +183,37 @@ def _strides(name: str, c):
 def _cache(k_cache, v_cache, k_scale, v_scale, dev) -> KvCache:
     import torch
 
-    if k_cache.dim() != 4:
+    shape = k_cache.shape
+    if len(shape) != 4:
         raise ValueError("k_cache and v_cache must be [pages, page_size, KV, D]")
-    P, size, KV, D = k_cache.shape
+    P, size, KV, D = shape
     kind = k_cache.dtype
-    if kind not in (torch.bfloat16, torch.float8_e4m3fn):
+    e4m3 = kind is not torch.bfloat16
+    if e4m3 and kind is not torch.float8_e4m3fn:
         raise TypeError(f"k_cache must be bfloat16 or float8_e4m3fn, got {kind}")
-    _check_tensor("k_cache", k_cache, kind, k_cache.shape, dev, False)
-    _check_tensor("v_cache", v_cache, kind, k_cache.shape, dev, False)
-    e4m3 = kind != torch.bfloat16
+    _rows("k_cache", k_cache, kind, shape, dev)
+    _rows("v_cache", v_cache, kind, shape, dev)
     for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
         if e4m3 != (s is not None):
             raise ValueError(f"{name} is for a float8_e4m3fn cache" if s is not None else f"an 8-bit cache needs {name}")
-        _check_tensor(name, s, torch.float32, (KV,), dev)
-    strides = _strides("k_cache", k_cache)
-    if strides != _strides("v_cache", v_cache):
+        if e4m3:
+            _packed(name, s, torch.float32, (KV,), dev)
+    strides = _strides("k_cache", k_cache, shape)
+    if strides != _strides("v_cache", v_cache, shape):
         raise ValueError("k_cache and v_cache must have the same strides")
-    return KvCache(KV, D, int(e4m3), size, P, *strides)
+    return KvCache(KV, D, e4m3, size, P, *strides)
 
 
 def _table(table, rows, N, dev):
     import torch
 
-    if table.dim() != 2:
+    shape = table.shape
+    if len(shape) != 2:
         raise ValueError("table must be [rows, pages of a row]")
-    _check_tensor("table", table, torch.int32, table.shape, dev)
-    _check_tensor("rows", rows, torch.int32, (N,), dev)
-    return table.shape
+    _packed("table", table, torch.int32, shape, dev)
+    if rows is not None:
+        _packed("rows", rows, torch.int32, (N,), dev)
+    return shape
 
 
 def decode(q, k_cache, v_cache, table, lens, *, rows=None, tree=None, scale=None, k_scale=None, v_scale=None, out=None,
@@ -219,23 +236,24 @@ def decode(q, k_cache, v_cache, table, lens, *, rows=None, tree=None, scale=None
     import torch
 
     dev = _gpu(q, stream)
-    if q.dim() != 4:
-        raise ValueError("q must be [N, T, H, D]")
     shape = q.shape
+    if len(shape) != 4:
+        raise ValueError("q must be [N, T, H, D]")
     N, T, H, D = shape
-    _check_tensor("q", q, torch.bfloat16, shape, dev, False)
-    _check_tensor("out", out, torch.bfloat16, shape, dev, False)
+    _rows("q", q, torch.bfloat16, shape, dev)
     cache = _cache(k_cache, v_cache, k_scale, v_scale, dev)
     if cache.head_dim != D:
         raise ValueError(f"k_cache has heads of {cache.head_dim}, q of {D}")
     R, W = _table(table, rows, N, dev)
-    _check_tensor("lens", lens, torch.int32, (N,), dev)
+    _packed("lens", lens, torch.int32, (N,), dev)
     if tree is not None:
-        _check_tensor("tree", tree, torch.int64, (T,) if tree.dim() == 1 else (N, T), dev)
+        _packed("tree", tree, torch.int64, (T,) if tree.dim() == 1 else (N, T), dev)
     mine = []
     if out is None:
         out = _like(q, stream)
         mine.append(out)
+    else:
+        _rows("out", out, torch.bfloat16, shape, dev)
     lse = _lse(lse, return_lse, q, shape[:-1], dev, stream, mine)
     p = DecodeProblem(N, T, H, _scale(scale, D), R, W, int(tree is not None and tree.dim() == 2),
                       _row_stride("q", q, 2), _row_stride("out", out, 2), cache)
@@ -247,8 +265,8 @@ def decode(q, k_cache, v_cache, table, lens, *, rows=None, tree=None, scale=None
         raise ValueError(f"workspace must be contiguous on {dev}")
     size = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _launch("kda_attn_decode", dev, stream, p,
-            [_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(table), _ptr(rows), _ptr(lens), _ptr(tree), _ptr(k_scale),
-             _ptr(v_scale), _ptr(out), _ptr(lse), _ptr(workspace), size], mine, call_raw)
+            [q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), _ptr(rows), lens.data_ptr(), _ptr(tree),
+             _ptr(k_scale), _ptr(v_scale), out.data_ptr(), _ptr(lse), _ptr(workspace), size], mine, call_raw)
     return out, lse
 
 
@@ -262,16 +280,18 @@ def store(k, v, k_cache, v_cache, slots, *, k_scale=None, v_scale=None, stream=N
     import torch
 
     dev = _gpu(k, stream)
-    if k.dim() != 3:
+    shape = k.shape
+    if len(shape) != 3:
         raise ValueError("k and v must be [T, KV, D]")
-    T = k.shape[0]
+    T = shape[0]
     cache = _cache(k_cache, v_cache, k_scale, v_scale, dev)
-    _check_tensor("k", k, torch.bfloat16, (T, cache.num_kv_heads, cache.head_dim), dev, False)
-    _check_tensor("v", v, torch.bfloat16, k.shape, dev, False)
-    _check_tensor("slots", slots, torch.int64, (T,), dev)
+    _rows("k", k, torch.bfloat16, (T, cache.num_kv_heads, cache.head_dim), dev)
+    _rows("v", v, torch.bfloat16, shape, dev)
+    _packed("slots", slots, torch.int64, (T,), dev)
     p = StoreProblem(T, _row_stride("k", k, 1), _row_stride("v", v, 1), cache)
     _launch("kda_kv_store", dev, stream, p,
-            [_ptr(k), _ptr(v), _ptr(slots), _ptr(k_scale), _ptr(v_scale), _ptr(k_cache), _ptr(v_cache)], (), call_raw)
+            [k.data_ptr(), v.data_ptr(), slots.data_ptr(), _ptr(k_scale), _ptr(v_scale), k_cache.data_ptr(),
+             v_cache.data_ptr()], (), call_raw)
 
 
 def assign_pages(lens, table, free_pages, free_head, *, page_size: int, rows=None, cu_seqlens=None, total_tokens=None,
@@ -292,13 +312,15 @@ def assign_pages(lens, table, free_pages, free_head, *, page_size: int, rows=Non
 
     dev = _gpu(lens, stream)
     i32 = torch.int32
-    if lens.dim() != 1:
+    shape = lens.shape
+    if len(shape) != 1:
         raise ValueError("lens must be [N]")
-    N = lens.shape[0]
-    _check_tensor("lens", lens, i32, (N,), dev)
+    N = shape[0]
+    _packed("lens", lens, i32, shape, dev)
     R, W = _table(table, rows, N, dev)
-    _check_tensor("free_pages", free_pages, i32, (free_pages.numel(),), dev)
-    _check_tensor("free_head", free_head, i32, (1,), dev)
+    F = free_pages.numel()
+    _packed("free_pages", free_pages, i32, (F,), dev)
+    _packed("free_head", free_head, i32, (1,), dev)
     cu64 = _offsets(cu_seqlens, dev)
     if cu_seqlens is None:
         if total_tokens is not None or tokens_per_seq < 0:
@@ -313,18 +335,23 @@ def assign_pages(lens, table, free_pages, free_head, *, page_size: int, rows=Non
         T = slots.numel() if total_tokens is None else total_tokens
     mine = []
 
-    def result(name, t, shape, dtype):
-        if t is not None:
-            _check_tensor(name, t, dtype, shape, dev)
-            return t
-        mine.append(_new(lens, stream, shape, dtype))
-        return mine[-1]
-
-    slots = result("slots", slots, (T,), torch.int64)
-    lens_out = result("lens_out", lens_out, (N,), i32)
-    head_out = result("head_out", head_out, (1,), i32)
-    p = AssignProblem(N, T, page_size, W, R, free_pages.shape[0], cu64)
+    if slots is None:
+        slots = _new(lens, stream, (T,), torch.int64)
+        mine.append(slots)
+    else:
+        _packed("slots", slots, torch.int64, (T,), dev)
+    if lens_out is None:
+        lens_out = _like(lens, stream)
+        mine.append(lens_out)
+    else:
+        _packed("lens_out", lens_out, i32, shape, dev)
+    if head_out is None:
+        head_out = _like(free_head, stream)
+        mine.append(head_out)
+    else:
+        _packed("head_out", head_out, i32, (1,), dev)
+    p = AssignProblem(N, T, page_size, W, R, F, cu64)
     _launch("kda_kv_assign", dev, stream, p,
-            [_ptr(lens), _ptr(rows), _ptr(cu_seqlens), _ptr(table), _ptr(free_pages), _ptr(free_head), _ptr(slots),
-             _ptr(lens_out), _ptr(head_out)], mine, call_raw)
+            [lens.data_ptr(), _ptr(rows), _ptr(cu_seqlens), table.data_ptr(), free_pages.data_ptr(), free_head.data_ptr(),
+             slots.data_ptr(), lens_out.data_ptr(), head_out.data_ptr()], mine, call_raw)
     return slots, lens_out, head_out
