@@ -118,8 +118,11 @@ typedef struct {
  *   workspace       kda_attn_decode_workspace_size bytes: scratch that carries
  *                   nothing between calls and must not be used by two calls in
  *                   flight at once
- * Long contexts are cut into parts that run side by side and are joined by a second
- * launch; how many parts there may be follows from the sizes alone. */
+ * Contexts over tables with room for more than 1024 positions are laid end to end and
+ * cut into stretches of the same length, which run side by side; a second launch joins what
+ * a cut has parted.  The workspace's size follows from the problem's sizes alone; where the cuts
+ * are follows from the lengths too, so that a request's last bits can depend on the other requests'
+ * lengths (not on anything else: a call repeated gives the same bits). */
 typedef struct {
   int32_t num_seqs;          /* N >= 0 requests */
   int32_t tokens_per_seq;    /* T, 1..64; row n * T + t is token t of request n */
@@ -185,6 +188,8 @@ kda_status kda_kv_store(const kda_kv_store_problem* p, const uint16_t* k, const 
  * -1, its length is kept, nothing else happens.  Slots of rows behind the last
  * sequence are -1.  Lengths below zero count as zero; a table entry below zero names no page.  Rows must be
  * distinct (not checked on the device).
+ * Tokens can be given back by a smaller length (drafts that were not taken): positions from it on
+ * are assigned anew, and a page that only they had opened is the caller's to free.
  *
  *   lens, lens_out  int32 [N]
  *   rows            int32 [N] or NULL (request n has row n)

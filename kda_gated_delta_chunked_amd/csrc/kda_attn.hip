@@ -1,10 +1,21 @@
 // kda_attn.hip -- causal attention over prompts, for gfx950 (MI355X).
 //
-// A workgroup takes 128 tokens of a sequence for one head, 32 a wave, and runs
-// over the keys ahead of them 64 at a time: S^T = K Q^T on the matrix cores, the
-// softmax with a running maximum and sum, O^T += V^T P^T from the same registers.
-// Keys and values go straight from memory to two LDS buffers in turn, the next
-// tile while this one is worked on; rows behind the sequence's end read as zeros.
+// A workgroup takes 128 tokens of a sequence for one head, 32 a wave, and runs over the keys
+// ahead of them 32 at a time (kda_attn_tiles.h has a turn): S^T = K Q^T on the matrix cores, a lane a
+// row, so that the softmax needs nothing from another lane and its weights are, as they lie,
+// operands of O^T += V^T P^T.  Keys and values go straight from memory to LDS, four blocks
+// of each in a ring that the waves fill together; rows behind the sequence's end read as zeros.
+//
+// Bound.  With heads of 128 a turn of a wave is 16 products of 32 cycles, 59 vector and some 60
+// other instructions, two waves a SIMD.  8 sequences of 8192, 32 heads on 8: 3.83 ms, 1149 TFLOP/s, the
+// matrix cores 65% of the time at work at 1.66 GHz, to which the clock falls under this load (a
+// product of matrices of 16384 in a library: 1383).  With heads of 64 half as many
+// products meet the same 59 vector instructions, which bound it: 2.29 ms, 958 TFLOP/s.  Short prompts are
+// a chain of waits: the offsets, the first blocks, a turn for each 32 keys, the last, masked one
+// (6 prompts of 271 to 3063, 12 heads of 128 72 us; one of 37 8 us on the device).
+//
+// Tried and not kept: 64 rows a wave (spills), operands read four products ahead (no change:
+// LDS is not what a product waits for), keys 64 at a time (the same rate, twice the ring).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -165,7 +176,12 @@ __global__ __launch_bounds__(SPLIT * WAVES * 64, 2) void kda_attn_kernel(AttnArg
 template <int D>
 void launch(const AttnArgs& a, hipStream_t stream) {
   const int64_t blocks = attn_blocks(a.slots, a.H);
-  if (blocks <= 512) hipLaunchKernelGGL((kda_attn_kernel<D, 2>), dim3((unsigned)blocks), dim3(2 * WAVES * 64), 0, stream, a);
+  // Two sides of a workgroup share a row's keys where there are few workgroups and each has long
+  // rows (us with one side and with two, by blocks: 256 of 2048 tokens 41 and 36; 384 of 4096 82 and 67, of 2048
+  // 52 and 44; 512 of 8192 173 and 160, but of 2048 50 and 53; 768 of 8192 211 and 234).  Short
+  // prompts only pay for the join (32 blocks of 512 15.3 and 16.5; 16 prompts of up to 300 14.6 and 19.2).
+  const int64_t mean = a.pk.T_total / a.pk.N;
+  if (mean >= 1024 && blocks <= (mean >= 4096 ? 512 : 384)) hipLaunchKernelGGL((kda_attn_kernel<D, 2>), dim3((unsigned)blocks), dim3(2 * WAVES * 64), 0, stream, a);
   else hipLaunchKernelGGL((kda_attn_kernel<D, 1>), dim3((unsigned)blocks), dim3(WAVES * 64), 0, stream, a);
 }
 

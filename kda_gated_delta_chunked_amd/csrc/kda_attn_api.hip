@@ -167,7 +167,9 @@ int decode_parts(const kda_attn_decode_problem* p) {
   const int64_t KV = p->cache.num_kv_heads, G = p->num_heads / KV, T = p->tokens_per_seq;
   const int64_t per_item = kda::attn_decode_blocks(1, KV, T, G), blocks = p->num_seqs * per_item;
   const bool many = T * G > kda::kAttnFewRows;
-  if (blocks == 0 || (many && blocks >= 2048) || (int64_t)p->table_width * p->cache.page_size <= 1024) return 0;
+  const int64_t positions = (int64_t)p->table_width * p->cache.page_size;
+  if (blocks == 0 || (many && blocks >= 2048) || positions <= 1024) return 0;
+  if (p->num_seqs * ((positions + kda::kAttnUnit - 1) / kda::kAttnUnit) >= (int64_t)1 << 30) return 0;  // counted in 32 bits
   const int64_t parts = (many || blocks > 256 ? 512 : 256) / per_item;
   return parts > 1 ? (int)parts : 0;
 }

@@ -1,15 +1,24 @@
 // kda_attn_decode.hip -- attention of drafted tokens over a paged cache, for
 // gfx950 (MI355X).
 //
-// The rows of a request that read the same keys, its T tokens times the heads
-// of a group, go 32 to a workgroup.  The context is cut into parts, a workgroup each, and a
-// part's keys go to the four waves in turn, 32 at a time: every wave has a softmax of its own
-// over its keys and the waves are joined through LDS at the end, so no wave waits for
-// another one before that.  A second launch joins the parts.
+// The rows of a request that read the same keys are its T tokens times the heads of a
+// group.  What a single token reads it reads once: the cache's bytes bound it.
 //
-// Rows of keys and values pass registers on their way to the wave's own tile in
-// LDS: the next tile's loads are under way while one is worked on, 8-bit codes become
-// bf16 (exactly) there, and rows that hold no position of the context become zeros.
+// Up to 32 rows: one kernel, in which the four waves of a workgroup share the keys out, 32 at a
+// time each, with a softmax of their own, and are joined through LDS at the end, so that no
+// wave waits for another one before that.  A wave has a place in LDS for its tile of keys and one
+// for values, and fills each again as soon as it has read it; two workgroups on a CU keep
+// some 100 KiB on the way.  (Two places of each and one workgroup read long contexts as fast, and
+// 1024 requests of up to 128 tokens in 253 us for 133.)  256 requests of 1 .. 8192 tokens, 8 KV heads of
+// 128, bf16: 747 us, 5.6 TB/s; 64 of up to 16384 over e4m3 246 us, 4.7 TB/s.
+//
+// More rows: the four waves have 32 rows each, up to 128 a workgroup, and the keys together, with
+// the turns and the ring of the prompts' kernel.  32 trees of 32 drafts, 32 heads on 4, contexts of up to
+// 16384: 240 us over e4m3, 230 over bf16, 560 and 590 TFLOP/s while the device is warm, 190 after a
+// pause.  A turn takes as long as in prompts; the rest is the start of a stretch, the turns with a
+// request's own tokens, the younger workgroup of a CU, which gets less of it, and the join.
+//
+// Contexts are cut into stretches (see Stretch) where that fills the device better.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -24,6 +33,7 @@ namespace {
 constexpr int THREADS = 256, WAVES = 4;
 constexpr int KEYS = 32;            // of a wave's tile
 constexpr int STEP = KEYS * WAVES;  // keys of a workgroup's turn
+static_assert(STEP == kAttnUnit, "a unit is a turn");
 
 // Orders a wave's accesses of its own LDS (which execute in order).
 __device__ __forceinline__ void wave_order() {
@@ -144,45 +154,43 @@ struct Request {
 // stretch, the last units of a request, whole ones, the first of another.
 struct Stretch {
   struct Lds {
-    int64_t sums[WAVES];
-    int found[2];
+    int sums[WAVES], found[2];
   };
   int n, unit, left;  // the request, the unit in it, and the units of the stretch from there on
   int length;         // of a stretch
-  // stretch w, of the workgroup
+  // stretch w, of the workgroup (the host has seen that all units together are less than 2^30)
   __device__ __forceinline__ Stretch(const AttnDecodeArgs& a, int w, Lds& lds) {
-    const int each = (a.N + THREADS - 1) / THREADS, from = (int)threadIdx.x * each, to = min(from + each, a.N);
+    const int each = (a.N + THREADS - 1) / THREADS, from = min((int)threadIdx.x * each, a.N), to = min(from + each, a.N);
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    int64_t mine = 0;
+    int mine = 0;
     for (int i = from; i < to; ++i) mine += Request(a, i).units();
-    int64_t upto = mine;
+    int upto = mine;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-      const int64_t v = __shfl_up(upto, o, 64);
+      const int v = __shfl_up(upto, o, 64);
       if (lane >= o) upto += v;
     }
     if (lane == 63) lds.sums[wave] = upto;
     lds_barrier();
-    int64_t all = 0;
+    int all = 0;
     upto -= mine;
 #pragma unroll
     for (int i = 0; i < WAVES; ++i) {
       if (i < wave) upto += lds.sums[i];
       all += lds.sums[i];
     }
-    const int64_t each_of = (all + a.parts - 1) / a.parts, start = w * each_of;
+    length = __builtin_amdgcn_readfirstlane((all + a.parts - 1) / a.parts);
+    const int start = w * length;
+    left = __builtin_amdgcn_readfirstlane(min(length, all - start));  // (less than one: no stretch, nothing found)
     if (start >= upto && start < upto + mine) {
-      int i = from;
-      int64_t behind = start - upto;
+      int i = from, behind = start - upto;
       for (int units; behind >= (units = Request(a, i).units()); ++i) behind -= units;
       lds.found[0] = i;
-      lds.found[1] = (int)behind;
+      lds.found[1] = behind;
     }
     lds_barrier();
     n = __builtin_amdgcn_readfirstlane(lds.found[0]);
     unit = __builtin_amdgcn_readfirstlane(lds.found[1]);
-    length = __builtin_amdgcn_readfirstlane((int)min(each_of, (int64_t)0x7fffffff));
-    left = __builtin_amdgcn_readfirstlane((int)min(each_of, all - start));  // (less than one: no stretch, nothing found)
     lds_barrier();
   }
   // a request on its own

@@ -290,7 +290,7 @@ struct AttnRows {
   // DEPTH products ahead (f holds them; the last ones are those of the turn at `next`) and
   // weights that execute in its shadow.  The weights are done three quarters through, so that
   // nothing waits for them at the end.  (The compiler, left to itself, puts all products
-  // ahead of all weights.)
+  // ahead of all weights: 5.03 ms for 4.47 where this order came in.)
   template <class Source, class Places = typename Source::Places>
   __device__ __forceinline__ bool turn(Source& source, uint32_t at, uint32_t next, typename Places::Raw (&f)[DEPTH],
                                        const f32x16& s, float c, f32x16& n, const bf16x8 (&p)[2], bf16x8 (&next_p)[2],
@@ -454,7 +454,7 @@ __device__ __forceinline__ void mask_scores(f32x16& s, uint32_t seen) {
 // and the product of block j - 1's weights with its values, which do not
 // depend on each other.  The source, in turn<READS>(), waits for the keys up to block j + 2
 // and the values up to block j and lets all waves pass (READS of a wave's reads of these
-// tiles may be under way); then its COUNT further copies are started, put(i); place(j + 1) is where block j + 1's
+// tiles may be under way); then its COUNT further copies are started, put(i); at(j + 1) is where block j + 1's
 // keys and block j - 1's values are; seen(j) has the bits of the keys of block j that the lane's row sees.
 // `blocks`: of the workgroup; `mine`: of them, those that any of the wave's rows sees;
 // source.open: below it all rows see all keys (a put may lower it to the block of keys it copies).

