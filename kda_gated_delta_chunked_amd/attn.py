@@ -113,6 +113,19 @@ def _packed(name: str, t, dtype, shape, dev):
         _check_tensor(name, t, dtype, shape, dev)
 
 
+def _stride(name: str, t, lead: int, shape) -> int:
+    """``_row_stride``, the usual answers first."""
+    if t.is_contiguous():
+        return 0
+    st = t.stride()
+    if st[-1] == 1 and st[-2] == shape[-1] and shape[0] > 1:
+        if lead == 1 and st[0] > 0:
+            return st[0]
+        if lead == 2 and st[1] > 0 and st[0] == shape[1] * st[1]:
+            return st[1]
+    return _row_stride(name, t, lead)
+
+
 def _scale(scale, D: int) -> float:
     return D ** -0.5 if scale is None else float(scale)
 
@@ -160,8 +173,8 @@ def prefill(q, k, v, *, cu_seqlens=None, scale=None, out=None, return_lse: bool 
     else:
         _rows("out", out, bf, shape, dev)
     lse = _lse(lse, return_lse, q, shape[:-1], dev, stream, mine)
-    p = PrefillProblem(N, T, H, KV, D, _scale(scale, D), cu64, _row_stride("q", q, lead), _row_stride("k", k, lead),
-                       _row_stride("v", v, lead), _row_stride("out", out, lead))
+    p = PrefillProblem(N, T, H, KV, D, _scale(scale, D), cu64, _stride("q", q, lead, shape), _stride("k", k, lead, kv_shape),
+                       _stride("v", v, lead, kv_shape), _stride("out", out, lead, shape))
     _launch("kda_attn_prefill", dev, stream, p,
             [q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(cu_seqlens), out.data_ptr(), _ptr(lse)], mine, call_raw)
     return out, lse
@@ -169,8 +182,6 @@ def prefill(q, k, v, *, cu_seqlens=None, scale=None, out=None, return_lse: bool 
 
 def _strides(name: str, c, shape):
     """Elements between a cache's pages and between a page's tokens (0, 0: packed)."""
-    if c.is_contiguous():
-        return 0, 0
     page, token, head, one = c.stride()
     P, size, KV, D = shape
     if (D > 1 and one != 1) or (KV > 1 and head != D):
@@ -188,20 +199,25 @@ def _cache(k_cache, v_cache, k_scale, v_scale, dev) -> KvCache:
         raise ValueError("k_cache and v_cache must be [pages, page_size, KV, D]")
     P, size, KV, D = shape
     kind = k_cache.dtype
-    e4m3 = kind is not torch.bfloat16
-    if e4m3 and kind is not torch.float8_e4m3fn:
-        raise TypeError(f"k_cache must be bfloat16 or float8_e4m3fn, got {kind}")
-    _rows("k_cache", k_cache, kind, shape, dev)
-    _rows("v_cache", v_cache, kind, shape, dev)
-    for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if e4m3 != (s is not None):
-            raise ValueError(f"{name} is for a float8_e4m3fn cache" if s is not None else f"an 8-bit cache needs {name}")
-        if e4m3:
+    if kind is torch.bfloat16:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError(f"{'v_scale' if k_scale is None else 'k_scale'} is for a float8_e4m3fn cache")
+    elif kind is torch.float8_e4m3fn:
+        for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if s is None:
+                raise ValueError(f"an 8-bit cache needs {name}")
             _packed(name, s, torch.float32, (KV,), dev)
-    strides = _strides("k_cache", k_cache, shape)
-    if strides != _strides("v_cache", v_cache, shape):
-        raise ValueError("k_cache and v_cache must have the same strides")
-    return KvCache(KV, D, e4m3, size, P, *strides)
+    else:
+        raise TypeError(f"k_cache must be bfloat16 or float8_e4m3fn, got {kind}")
+    if k_cache.device != dev:
+        raise ValueError(f"k_cache is on {k_cache.device}, expected {dev}")
+    _rows("v_cache", v_cache, kind, shape, dev)
+    page = token = 0
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        page, token = _strides("k_cache", k_cache, shape)
+        if (page, token) != _strides("v_cache", v_cache, shape):
+            raise ValueError("k_cache and v_cache must have the same strides")
+    return KvCache(KV, D, kind is not torch.bfloat16, size, P, page, token)
 
 
 def _table(table, rows, N, dev):
@@ -256,7 +272,7 @@ def decode(q, k_cache, v_cache, table, lens, *, rows=None, tree=None, scale=None
         _rows("out", out, torch.bfloat16, shape, dev)
     lse = _lse(lse, return_lse, q, shape[:-1], dev, stream, mine)
     p = DecodeProblem(N, T, H, _scale(scale, D), R, W, int(tree is not None and tree.dim() == 2),
-                      _row_stride("q", q, 2), _row_stride("out", out, 2), cache)
+                      _stride("q", q, 2, shape), _stride("out", out, 2, shape), cache)
     if workspace is None:
         need = decode_workspace_size(p)
         if need:
@@ -288,7 +304,7 @@ def store(k, v, k_cache, v_cache, slots, *, k_scale=None, v_scale=None, stream=N
     _rows("k", k, torch.bfloat16, (T, cache.num_kv_heads, cache.head_dim), dev)
     _rows("v", v, torch.bfloat16, shape, dev)
     _packed("slots", slots, torch.int64, (T,), dev)
-    p = StoreProblem(T, _row_stride("k", k, 1), _row_stride("v", v, 1), cache)
+    p = StoreProblem(T, _stride("k", k, 1, shape), _stride("v", v, 1, shape), cache)
     _launch("kda_kv_store", dev, stream, p,
             [k.data_ptr(), v.data_ptr(), slots.data_ptr(), _ptr(k_scale), _ptr(v_scale), k_cache.data_ptr(),
              v_cache.data_ptr()], (), call_raw)
