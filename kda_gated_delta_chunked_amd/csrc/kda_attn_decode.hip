@@ -21,8 +21,8 @@
 // Contexts are cut into stretches (see Stretch) where that fills the device better.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
-#include <type_traits>
 
 #include "kda_attn_kernels.h"
 #include "kda_attn_tiles.h"
@@ -503,7 +503,7 @@ struct Joined {
 // The pieces of a context that stretches' ends have cut; the first of these ends has the
 // workgroups that join them.  D / 4 threads go over a row's pieces, eight at a time; as many of
 // them share a row as gives each some eight pieces.  A workgroup takes one row where
-// rows are few, and else as many as it has room for at once.
+// rows are few, and else so many that its search for the cut is not most of its work.
 template <int D>
 __global__ __launch_bounds__(THREADS) void kda_attn_join_kernel(AttnDecodeArgs a) {
   constexpr int LANES = D / 4, SIDES = THREADS / LANES, AHEAD = 8;
@@ -578,8 +578,9 @@ void launch(const AttnDecodeArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL(kernel, grid, dim3(THREADS), 0, stream, a);
   if (!a.part_out) return;
   AttnDecodeArgs join = a;
-  join.join_rows = (int64_t)a.parts * a.T * a.H <= 4096 ? 1 : THREADS / (D / 4);
-  const int64_t row_blocks = (a.T * G + join.join_rows - 1) / join.join_rows;
+  const int64_t side = THREADS / (D / 4), rows = a.T * G, groups = std::min<int64_t>(a.parts - 1, a.N) * a.c.KV * rows / side;
+  join.join_rows = (int64_t)a.parts * a.T * a.H <= 4096 ? 1 : (int)(side * std::max<int64_t>(1, groups / 2048));
+  const int64_t row_blocks = (rows + join.join_rows - 1) / join.join_rows;
   hipLaunchKernelGGL(kda_attn_join_kernel<D>, dim3((unsigned)((a.parts - 1) * a.c.KV * row_blocks)), dim3(THREADS), 0, stream, join);
 }
 

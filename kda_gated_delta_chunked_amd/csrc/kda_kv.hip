@@ -12,22 +12,31 @@ namespace {
 constexpr int THREADS = 256;
 constexpr float kE4m3Max = 448.f;
 
-// x / scale, within the codes' range; a NaN stays one
-__device__ __forceinline__ float code_of(float x, float scale) {
-  const float v = x / scale;
-  return v != v ? v : fminf(fmaxf(v, -kE4m3Max), kE4m3Max);
-}
-__device__ __forceinline__ uint32_t codes_of(const float* f, float scale) {
-  int codes = 0;
-  codes = __builtin_amdgcn_cvt_pk_fp8_f32(code_of(f[0], scale), code_of(f[1], scale), codes, false);
-  codes = __builtin_amdgcn_cvt_pk_fp8_f32(code_of(f[2], scale), code_of(f[3], scale), codes, true);
-  return (uint32_t)codes;
-}
-__device__ __forceinline__ uint4 codes16_of(const uint4* u, float scale) {
+// x / scale, within the codes' range; a NaN stays one.  The quotient is the rounded one of a
+// division: with y = 1 / scale rounded, x y is off by a unit at most, the remainder of it is exact, and
+// y times that rounds the sum correctly (Markstein).  A quotient past 1024 is one of 448 in any case: it is
+// kept where products and remainders stay finite.  (By division the store's instructions bound it.)
+struct Scale {
+  float scale, inverse;
+  bool plain;  // whether no step of the above leaves the normal numbers
+  __device__ __forceinline__ Scale(float s) : scale(s), inverse(1.f / s), plain(s >= 0x1p-60f && s <= 0x1p60f) {}
+  __device__ __forceinline__ float code(float x) const {
+    const float near = fminf(fmaxf(x * inverse, -1024.f), 1024.f);
+    const float v = plain ? __builtin_fmaf(__builtin_fmaf(-near, scale, x), inverse, near) : x / scale;
+    return v != v ? v : fminf(fmaxf(v, -kE4m3Max), kE4m3Max);
+  }
+  __device__ __forceinline__ uint32_t codes(const float* f) const {
+    int codes = 0;
+    codes = __builtin_amdgcn_cvt_pk_fp8_f32(code(f[0]), code(f[1]), codes, false);
+    codes = __builtin_amdgcn_cvt_pk_fp8_f32(code(f[2]), code(f[3]), codes, true);
+    return (uint32_t)codes;
+  }
+};
+__device__ __forceinline__ uint4 codes16_of(const uint4* u, const Scale& scale) {
   float f[16];
   bf16x8_f32(u[0], f);
   bf16x8_f32(u[1], f + 8);
-  return make_uint4(codes_of(f, scale), codes_of(f + 4, scale), codes_of(f + 8, scale), codes_of(f + 12, scale));
+  return make_uint4(scale.codes(f), scale.codes(f + 4), scale.codes(f + 8), scale.codes(f + 12));
 }
 
 // A thread takes 16 bytes of a token's keys in the cache, and of its values: the bytes bound it
@@ -51,8 +60,8 @@ __global__ __launch_bounds__(THREADS) void kda_kv_store_kernel(KvStoreArgs a) {
   const int64_t to = (page * a.c.page_stride + in * a.c.token_stride + col) * (E4M3 ? 1 : 2);
   if constexpr (E4M3) {
     const int head = col / a.c.D;
-    k[0] = codes16_of(k, a.c.k_scale[head]);
-    v[0] = codes16_of(v, a.c.v_scale[head]);
+    k[0] = codes16_of(k, Scale(a.c.k_scale[head]));
+    v[0] = codes16_of(v, Scale(a.c.v_scale[head]));
   }
   *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.c.k) + to) = k[0];
   *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.c.v) + to) = v[0];
