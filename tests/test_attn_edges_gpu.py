@@ -121,6 +121,49 @@ def test_a_batch_padded_with_short_sequences_and_one_long():
     R.assert_lse(lse, lse_ref, terms, 64)
 
 
+# Few workgroups of long rows: two sides of one share a row's keys.
+
+@dims
+@pytest.mark.parametrize("H,KV,lens", [(2, 1, [1024]), (3, 3, [1, 2047]), (2, 2, [1301, 0, 1900]), (1, 1, [4200])], ids=str)
+def test_long_rows(H, KV, lens, D):
+    q, k, v = prompts(lens, D, sum(lens), H=H, KV=KV, scale=1.4)
+    ref, lse_ref, mag, terms = R.prefill(q, k, v, lens)
+    out, lse = run_prompts(q, k, v, lens)
+    R.assert_out(out, ref, mag)
+    R.assert_lse(lse, lse_ref, terms, D)
+
+
+@dims
+@pytest.mark.parametrize("at", [0, 33, 1000, 1099])
+def test_long_rows_with_values_and_keys_that_are_no_numbers(at, D):
+    lens = [1100]
+    q, k, v = prompts(lens, D, at, H=2, KV=1)
+    ref, lse_ref, mag, terms = R.prefill(q, k, v, lens)
+    bad = v.clone()
+    bad[at, 0, 3], bad[at, 0, 7] = -INF, NAN
+    out, lse = run_prompts(q, k, bad, lens)
+    hit = torch.zeros(out.shape, dtype=torch.bool)
+    hit[at:, :, 3] = hit[at:, :, 7] = True
+    assert (out[at:, :, 3] == -INF).all() and torch.isnan(out[at:, :, 7].float()).all()
+    R.assert_out(out[~hit], ref[~hit], mag[~hit])
+    R.assert_lse(lse, lse_ref, terms, D)
+    k[at, 0, D - 1] = NAN
+    out, lse = run_prompts(q, k, v, lens)
+    assert torch.isnan(out[at:].float()).all() and torch.isnan(lse[at:]).all()
+    if at:
+        R.assert_out(out[:at], ref[:at], mag[:at])
+        R.assert_lse(lse[:at], lse_ref[:at], terms[:at], D)
+
+
+@dims
+def test_long_rows_with_scores_far_apart(D):
+    q, k, v = prompts([1200], D, 3, H=2, KV=1, scale=1e9)
+    ref, lse_ref, mag, terms = R.prefill(q, k, v, [1200])
+    out, lse = run_prompts(q, k, v, [1200])
+    R.assert_out(out, ref, mag)
+    R.assert_lse(lse, lse_ref, terms, D)
+
+
 # ---------------------------------------------------------------------------
 # the cache
 
@@ -191,6 +234,18 @@ def test_cut_contexts(lens, T, H, KV, D, e4m3):
     again = attn().decode(*to_gpu(q, kc, vc, table, i32(*lens)), rows=rows.cuda(), return_lse=True,
                           **({} if ks is None else dict(k_scale=ks.cuda(), v_scale=vs.cuda())))
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])  # (no sum in the order of arrival)
+
+
+@caches
+@dims
+@pytest.mark.parametrize("T,H,KV,lens", [(64, 12, 2, [0, 33]), (50, 9, 3, [100, 1, 64, 5]), (64, 4, 1, [2000, 100]), (2, 128, 1, [40, 300])],
+                         ids=str)
+def test_more_rows_than_a_workgroup_takes(T, H, KV, lens, D, e4m3):
+    g = torch.Generator().manual_seed(T * H)
+    table, rows, pages = pages_for(g, [x + T for x in lens], 32)
+    kc, vc, ks, vs = cache_of(g, pages, 32, KV, D, e4m3)
+    words = torch.randint(-2 ** 62, 2 ** 62, (len(lens), T), generator=g) if T > 2 else None
+    check_decode(rand(g, len(lens), T, H, D, scale=1.4), kc, vc, table, i32(*lens), rows, words, ks, vs)
 
 
 @caches
