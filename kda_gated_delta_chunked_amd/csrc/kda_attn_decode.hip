@@ -118,12 +118,22 @@ struct PageCopies {
   __device__ __forceinline__ void copy(bool keys, int part, int64_t start, int from, uint32_t lds) const {
     copy_to_lds(lds + part * 1024, (keys ? kbase : vbase) + start + part % (PARTS / 2) * ROWS * token, (uint32_t)from);
   }
+  // The lane's bytes of every copy: the swizzle, and with it they, repeat every 16 rows.
+  static constexpr int PERIOD = 16 / ROWS;
+  struct From {
+    uint32_t of[PERIOD];
+  };
+  __device__ __forceinline__ From from() const {
+    From f;
+#pragma unroll
+    for (int u = 0; u < PERIOD; ++u) f.of[u] = (uint32_t)forget(lane_from(u));
+    return f;
+  }
   // a tile of keys or of values
-  __device__ __forceinline__ void tile(bool keys, const TileStarts<SIZE>& starts, int tile, uint8_t* to) const {
-    const uint32_t lds = lds_place(to);
+  __device__ __forceinline__ void tile(bool keys, const TileStarts<SIZE>& starts, int tile, const From& from, uint32_t lds) const {
     const int64_t start[2] = {starts.start(tile, 0), starts.start(tile, 1)};
 #pragma unroll
-    for (int u = 0; u < PARTS; ++u) copy(keys, u, start[half(u)], lane_from(u), lds);
+    for (int u = 0; u < PARTS; ++u) copy(keys, u, start[half(u)], (int)from.of[u % PERIOD], lds);
   }
 };
 
@@ -197,16 +207,21 @@ struct Stretch {
   __device__ __forceinline__ Stretch(int n_) : n(n_), unit(0), left(1), length(1) {}
 };
 
-// A workgroup's place in the launch.  Row blocks of the same keys follow each other on the same
-// of the eight dies, whose cache they share.
+// A workgroup's place in the launch.  What reads the same cache lines follows each other on the same of
+// the eight dies, whose cache it shares: row blocks of the same keys, and two heads whose keys
+// are half a line each (codes of 64 columns).
+template <int D, bool E4M3>
 struct Place {
   int kv, block, item;  // item: request or stretch
   __device__ __forceinline__ Place(int KV, int row_blocks, int items) {
-    const uint32_t all = (uint32_t)items * KV, group = blockIdx.x / (8u * row_blocks) * 8u, in = blockIdx.x % (8u * row_blocks);
-    const uint32_t size = min(8u, all - group), unit = group + in % size;
-    block = (int)(in / size);
-    kv = (int)(unit % (uint32_t)KV);
-    item = (int)(unit / (uint32_t)KV);
+    const int pair = E4M3 && D == 64 && KV % 2 == 0 ? 2 : 1;
+    const uint32_t sets = (uint32_t)(KV / pair), each = (uint32_t)(row_blocks * pair), all = (uint32_t)items * sets;
+    const uint32_t group = blockIdx.x / (8u * each) * 8u, in = blockIdx.x % (8u * each), size = min(8u, all - group);
+    const uint32_t unit = group + in % size;
+    const int which = (int)(in / size);
+    block = which / pair;
+    kv = (int)(unit % sets) * pair + which % pair;
+    item = (int)(unit / sets);
   }
 };
 
@@ -214,11 +229,12 @@ template <int D, bool E4M3>
 __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeArgs a) {
   using Copies = PageCopies<D, E4M3>;
   constexpr int TILE = Copies::TILE;
-  constexpr int OUTPUTS = 32 * D * 4, WAVE_BYTES = 2 * TILE > OUTPUTS ? 2 * TILE : OUTPUTS;  // a tile of keys and one of values; at the end the wave's outputs
+  // a wave's tile of keys and one of values; at the end its outputs
+  constexpr int OUTPUTS = 32 * D * 4, WAVE_BYTES = 2 * TILE > OUTPUTS ? 2 * TILE : OUTPUTS, PARTS = Copies::PARTS;
   __shared__ __attribute__((aligned(1024))) uint8_t tiles[WAVES][WAVE_BYTES];
   __shared__ float stats[WAVES][2][32];
   const int KV = a.c.KV, G = a.H / KV, rows = a.T * G;
-  const Place at_place(KV, 1, a.part_out ? a.parts : a.N);
+  const Place<D, E4M3> at_place(KV, 1, a.part_out ? a.parts : a.N);
   const int kv = at_place.kv, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, h = lane >> 5;
   const int row = min(lane & 31, rows - 1);
   const int t = row / G;
@@ -247,41 +263,54 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
     // Keys' and values' places are filled again as soon as the wave has read them: keys while
     // their weights and products are worked out, values under the next tile's scores.
     TileStarts<Copies::SIZE> starts;
+    const typename Copies::From from = copies.from();
+    const TilePlaces<D, E4M3, false> held(ring, ring + TILE);
+    const uint32_t keys_at = lds_place(ring), values_at = keys_at + TILE;
     bool half0 = false, half1 = false;  // whether the halves of the last tile of keys have pages
     auto fetch_keys = [&](int tile) {
-      if ((tile & 63) == 0) starts.find(a, table, first + tile * STEP, STEP, begin, end);
       half0 = starts.has(tile & 63, 0);
       half1 = starts.has(tile & 63, 1);
-      copies.tile(true, starts, tile & 63, ring);
+      copies.tile(true, starts, tile & 63, from, keys_at);
     };
-    auto fetch_values = [&](int tile) { copies.tile(false, starts, tile & 63, ring + TILE); };
+    auto fetch_values = [&](int tile) { copies.tile(false, starts, tile & 63, from, values_at); };
     auto reads_done = [&]() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
     bool not_finite = false;  // left out of a tile with masked rows
     if (count > 0) {
+      starts.find(a, table, first, STEP, begin, end);
       fetch_keys(0);
       fetch_values(0);
       r.settle();
     }
-    const TilePlaces<D, E4M3, false> held(ring, ring + TILE);
-    for (int tile = 0; tile < count; ++tile) {
-      memory_left<Copies::PARTS>();
+    int tile = 0;
+    // A tile that all rows see, with another one behind it, or (SOME) any.
+    auto step = [&](auto some) {
+      constexpr bool SOME = decltype(some)::value;
       const auto places = held.fresh();
+      const bool more = !SOME || tile + 1 < count;
+      memory_left<PARTS>();
       f32x16 s = r.scores(places, 0);
       reads_done();
-      const bool all = first + tile * STEP + KEYS <= min(req.before, end) && half0 && half1;
-      if (!all) mask_scores(s, seen_keys(first + tile * STEP, end, req.before, sees, half0, half1));
-      const bool more = tile + 1 < count;
+      if (SOME) {
+        mask_scores(s, seen_keys(first + tile * STEP, end, req.before, sees, half0, half1));
+        if (more && ((tile + 1) & 63) == 0) starts.find(a, table, first + (tile + 1) * STEP, STEP, begin, end);
+      }
       if (more) fetch_keys(tile + 1);
       bf16x8 p[2];
       float sum;
       if (__builtin_expect(r.try_weights(s, c, p, sum), 0)) r.weights_from_maximum(s, c, p, sum);
       r.l += sum;
-      if (more) memory_left<Copies::PARTS>();
+      if (more) memory_left<PARTS>();
       else memory_left<0>();
-      if (all) r.add(places, 0, p);
-      else not_finite = r.add_masked(places, 0, p) || not_finite;
+      if (SOME) not_finite = r.add_masked(places, 0, p) || not_finite;
+      else r.add(places, 0, p);
       reads_done();
       if (more) fetch_values(tile + 1);
+      ++tile;
+    };
+    const int open = min(req.before, end) - KEYS - first;  // tiles up to there are seen whole, if they have pages
+    while (tile < count) {
+      while (tile * STEP <= open && half0 && half1 && tile + 1 < count && ((tile + 1) & 63)) step(std::false_type());
+      step(std::true_type());
     }
     if (__builtin_expect(not_finite, 0))
       for (int tile = 0; tile < count; ++tile)
@@ -426,7 +455,7 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_drafts_kernel(AttnDecodeA
   using Source = PagedSource<D, E4M3>;
   __shared__ __attribute__((aligned(1024))) uint8_t tiles[2 * Source::RING * Source::TILE];
   const int KV = a.c.KV, G = a.H / KV, rows = a.T * G, row_blocks = (rows + kAttnManyRows - 1) / kAttnManyRows;
-  const Place at_place(KV, row_blocks, a.part_out ? a.parts : a.N);
+  const Place<D, E4M3> at_place(KV, row_blocks, a.part_out ? a.parts : a.N);
   const int kv = at_place.kv, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int top = at_place.block * kAttnManyRows + wave * 32, row = top + (lane & 31), read = min(row, rows - 1);
   const int t = read / G;
