@@ -161,19 +161,18 @@ struct Request {
 
 // Contexts lie one behind another in units of STEP positions (one at least), and are cut into
 // a.parts stretches of the same length, whatever request they fall to: a workgroup has a
-// stretch, the last units of a request, whole ones, the first of another.
-struct Stretch {
+// stretch, the last units of a request, whole ones, the first of another.  Every workgroup searches the
+// lengths by itself, a thread a run of requests (the host has seen that all units together are
+// less than 2^30).
+struct Search {
   struct Lds {
-    int sums[WAVES], found[2];
+    int sums[WAVES], found[3];
   };
-  int n, unit, left;  // the request, the unit in it, and the units of the stretch from there on
-  int length;         // of a stretch
-  // stretch w, of the workgroup (the host has seen that all units together are less than 2^30)
-  __device__ __forceinline__ Stretch(const AttnDecodeArgs& a, int w, Lds& lds) {
-    const int each = (a.N + THREADS - 1) / THREADS, from = min((int)threadIdx.x * each, a.N), to = min(from + each, a.N);
+  int from, to, upto, mine;  // the thread's requests, the units ahead of them, and theirs
+  int all, length;     // units, and of a stretch
+  // the sum of the threads' values ahead of the thread's; `all`: of all
+  static __device__ __forceinline__ int ahead(int mine, int& all, Lds& lds) {
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    int mine = 0;
-    for (int i = from; i < to; ++i) mine += Request(a, i).units();
     int upto = mine;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -182,18 +181,34 @@ struct Stretch {
     }
     if (lane == 63) lds.sums[wave] = upto;
     lds_barrier();
-    int all = 0;
     upto -= mine;
+    all = 0;
 #pragma unroll
     for (int i = 0; i < WAVES; ++i) {
       if (i < wave) upto += lds.sums[i];
       all += lds.sums[i];
     }
+    return upto;
+  }
+  __device__ __forceinline__ Search(const AttnDecodeArgs& a, Lds& lds) {
+    const int each = (a.N + THREADS - 1) / THREADS;
+    from = min((int)threadIdx.x * each, a.N);
+    to = min(from + each, a.N);
+    mine = 0;
+    for (int i = from; i < to; ++i) mine += Request(a, i).units();
+    upto = ahead(mine, all, lds);
     length = __builtin_amdgcn_readfirstlane((all + a.parts - 1) / a.parts);
-    const int start = w * length;
-    left = __builtin_amdgcn_readfirstlane(min(length, all - start));  // (less than one: no stretch, nothing found)
-    if (start >= upto && start < upto + mine) {
-      int i = from, behind = start - upto;
+  }
+};
+struct Stretch {
+  int n, unit, left;  // the request, the unit in it, and the units of the stretch from there on
+  // stretch w
+  __device__ __forceinline__ Stretch(const AttnDecodeArgs& a, int w, Search::Lds& lds) {
+    const Search search(a, lds);
+    const int start = w * search.length;
+    left = __builtin_amdgcn_readfirstlane(min(search.length, search.all - start));  // (less than one: no stretch)
+    if (start >= search.upto && start < search.upto + search.mine) {
+      int i = search.from, behind = start - search.upto;
       for (int units; behind >= (units = Request(a, i).units()); ++i) behind -= units;
       lds.found[0] = i;
       lds.found[1] = behind;
@@ -204,7 +219,46 @@ struct Stretch {
     lds_barrier();
   }
   // a request on its own
-  __device__ __forceinline__ Stretch(int n_) : n(n_), unit(0), left(1), length(1) {}
+  __device__ __forceinline__ Stretch(int n_) : n(n_), unit(0), left(1) {}
+};
+// The index-th request that a stretch's end cuts, if there are so many: its pieces begin in
+// stretch `first`, as that one's second or (whole) only one.
+struct Cut {
+  int n, first, pieces;
+  bool second;
+  __device__ __forceinline__ Cut(const AttnDecodeArgs& a, int index, Search::Lds& lds) {
+    const Search search(a, lds);
+    // visits the thread's cut requests: stretch, units of it ahead of the request, the request's units
+    const uint32_t length = (uint32_t)search.length;
+    auto each = [&](auto visit) {
+      uint32_t in = (uint32_t)search.upto / length, at = (uint32_t)search.upto - in * length;
+      for (int i = search.from; i < search.to; ++i) {
+        const uint32_t units = (uint32_t)Request(a, i).units();
+        if (at + units > length) visit(i, in, at, units);
+        at += units;
+        if (at >= length) {
+          in += at / length;
+          at %= length;
+        }
+      }
+    };
+    int mine = 0, all;
+    each([&](int, uint32_t, uint32_t, uint32_t) { ++mine; });
+    lds_barrier();  // the sums are used again
+    int place = Search::ahead(mine, all, lds);
+    if (index >= place && index < place + mine)
+      each([&](int i, uint32_t in, uint32_t at, uint32_t units) {
+        if (place++ != index) return;
+        lds.found[0] = i;
+        lds.found[1] = (int)(in * 2 + (at > 0));
+        lds.found[2] = (int)((at + units - 1) / length + 1);
+      });
+    lds_barrier();
+    n = __builtin_amdgcn_readfirstlane(lds.found[0]);
+    first = __builtin_amdgcn_readfirstlane(lds.found[1]) >> 1;
+    second = __builtin_amdgcn_readfirstlane(lds.found[1]) & 1;
+    pieces = index < all ? __builtin_amdgcn_readfirstlane(lds.found[2]) : 0;
+  }
 };
 
 // A workgroup's place in the launch.  What reads the same cache lines follows each other on the same of
@@ -239,7 +293,7 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
   const int row = min(lane & 31, rows - 1);
   const int t = row / G;
   Stretch piece(at_place.item);
-  if (a.part_out) piece = Stretch(a, at_place.item, *reinterpret_cast<Stretch::Lds*>(tiles));
+  if (a.part_out) piece = Stretch(a, at_place.item, *reinterpret_cast<Search::Lds*>(tiles));
   for (int cut = 2 * at_place.item; piece.left > 0; ++piece.n, piece.unit = 0, cut |= 1) {
   const int n = piece.n;
   const Request req(a, n);
@@ -460,7 +514,7 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_drafts_kernel(AttnDecodeA
   const int top = at_place.block * kAttnManyRows + wave * 32, row = top + (lane & 31), read = min(row, rows - 1);
   const int t = read / G;
   Stretch piece(at_place.item);
-  if (a.part_out) piece = Stretch(a, at_place.item, *reinterpret_cast<Stretch::Lds*>(tiles));
+  if (a.part_out) piece = Stretch(a, at_place.item, *reinterpret_cast<Search::Lds*>(tiles));
   for (int cut = 2 * at_place.item; piece.left > 0; ++piece.n, piece.unit = 0, cut |= 1) {
   const int n = piece.n;
   const Request req(a, n);
@@ -529,24 +583,23 @@ struct Joined {
   }
 };
 
-// The pieces of a context that stretches' ends have cut; the first of these ends has the
-// workgroups that join them.  D / 4 threads go over a row's pieces, eight at a time; as many of
+// The pieces of a context that stretches' ends have cut.  D / 4 threads go over a row's pieces, eight at a time; as many of
 // them share a row as gives each some eight pieces.  A workgroup takes one row where
 // rows are few, and else so many that its search for the cut is not most of its work.
 template <int D>
 __global__ __launch_bounds__(THREADS) void kda_attn_join_kernel(AttnDecodeArgs a) {
   constexpr int LANES = D / 4, SIDES = THREADS / LANES, AHEAD = 8;
-  __shared__ Stretch::Lds lds;
+  __shared__ Search::Lds lds;
   __shared__ float4 sums[SIDES][LANES];
   __shared__ float2 stats[SIDES];
   const int KV = a.c.KV, G = a.H / KV, rows = a.T * G, row_blocks = (rows + a.join_rows - 1) / a.join_rows;
   const int block = (int)(blockIdx.x % (unsigned)row_blocks), at = (int)(blockIdx.x / (unsigned)row_blocks);
-  const int kv = at % KV, second = at / KV + 1;
-  const Stretch cut(a, second, lds);
-  if (cut.left <= 0 || cut.unit == 0 || cut.unit > cut.length) return;
-  const int n = cut.n, parts = 1 + (Request(a, n).units() - cut.unit + cut.length - 1) / cut.length;
+  const int kv = at % KV;
+  const Cut cut(a, at / KV, lds);
+  const int n = cut.n, parts = cut.pieces;
+  if (parts == 0) return;
   const int64_t step = (int64_t)KV * rows;  // of slots; a stretch has two
-  const int64_t first = 2 * (second - 1), head_slot = cut.unit < cut.length ? first + 1 : first;
+  const int64_t first = 2 * cut.first, head_slot = cut.second ? first + 1 : first;
   const float c = a.scale * kLog2e * (a.c.k_scale ? a.c.k_scale[kv] : 1.f);
   const int side = threadIdx.x / LANES, col = threadIdx.x % LANES;
   int share = a.join_rows == 1 ? SIDES : 1;  // sides of a row
@@ -607,10 +660,10 @@ void launch(const AttnDecodeArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL(kernel, grid, dim3(THREADS), 0, stream, a);
   if (!a.part_out) return;
   AttnDecodeArgs join = a;
-  const int64_t side = THREADS / (D / 4), rows = a.T * G, groups = std::min<int64_t>(a.parts - 1, a.N) * a.c.KV * rows / side;
-  join.join_rows = (int64_t)a.parts * a.T * a.H <= 4096 ? 1 : (int)(side * std::max<int64_t>(1, groups / 2048));
+  const int64_t side = THREADS / (D / 4), rows = a.T * G, cuts = std::min(a.parts - 1, a.N);
+  join.join_rows = cuts * a.c.KV * rows <= 1024 ? 1 : (int)(side * std::max<int64_t>(1, cuts * a.c.KV * rows / side / 2048));
   const int64_t row_blocks = (rows + join.join_rows - 1) / join.join_rows;
-  hipLaunchKernelGGL(kda_attn_join_kernel<D>, dim3((unsigned)((a.parts - 1) * a.c.KV * row_blocks)), dim3(THREADS), 0, stream, join);
+  hipLaunchKernelGGL(kda_attn_join_kernel<D>, dim3((unsigned)(cuts * a.c.KV * row_blocks)), dim3(THREADS), 0, stream, join);
 }
 
 }  // namespace
