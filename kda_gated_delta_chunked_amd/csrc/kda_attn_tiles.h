@@ -463,6 +463,14 @@ template <int D, class Source>
 __device__ __forceinline__ bool attend(AttnRows<D>& r, Source& source, float c, int blocks, int mine) {
   using Rows = AttnRows<D>;
   using Places = typename Source::Places;
+  if (mine == 0) {  // no rows, but a share of the copies: as many turns as the others have
+    for (int t = 0; t < blocks + 2; ++t) {
+      source.template turn<0>();
+      source.put();
+    }
+    memory_left<0>();
+    return false;
+  }
   const Places& places = source.places;
   bool left_out = false;
   float sum;
