@@ -434,7 +434,9 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
 // The blocks of 32 positions of a part, for a wave of rows of a request.
 template <int D, bool E4M3>
 struct PagedSource {
-  using Places = TilePlaces<D, E4M3, false>;
+  // (operands' places are held where registers allow: 32 trees over e4m3 234 us and 228 so; over bf16 with heads
+  // of 128, where it spills, 225 and 233)
+  using Places = TilePlaces<D, E4M3, E4M3 || D == 64>;
   using Copies = PageCopies<D, E4M3>;
   static constexpr int RING = 4, TILE = Places::BYTES, COUNT = Copies::COUNT / WAVES;
   static_assert(COUNT >= 1 && Copies::PARTS % 2 == 0, "a copy for each wave at least");
