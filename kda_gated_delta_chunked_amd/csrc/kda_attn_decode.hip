@@ -9,16 +9,17 @@
 // wave waits for another one before that.  A wave has a place in LDS for its tile of keys and one
 // for values, and fills each again as soon as it has read it; two workgroups on a CU keep
 // some 100 KiB on the way.  (Two places of each and one workgroup read long contexts as fast, and
-// 1024 requests of up to 128 tokens in 253 us for 133.)  256 requests of 1 .. 8192 tokens, 8 KV heads of
-// 128, bf16: 747 us, 5.6 TB/s; 64 of up to 16384 over e4m3 246 us, 4.7 TB/s.
+// 1024 requests of up to 128 tokens in 253 us for 131; places for two or four tiles of codes, no faster.)
+// 256 requests of 1 .. 8192 tokens, 8 KV heads of 128, bf16: 740 us, 5.7 TB/s; 64 of up to 16384 over e4m3 239 us, 4.8 TB/s.
 //
 // More rows: the four waves have 32 rows each, up to 128 a workgroup, and the keys together, with
 // the turns and the ring of the prompts' kernel.  32 trees of 32 drafts, 32 heads on 4, contexts of up to
-// 16384: 240 us over e4m3, 230 over bf16, 560 and 590 TFLOP/s while the device is warm, 190 after a
-// pause.  A turn takes as long as in prompts; the rest is the start of a stretch, the turns with a
-// request's own tokens, the younger workgroup of a CU, which gets less of it, and the join.
+// 16384: 230 us over e4m3, 227 over bf16, some 600 TFLOP/s while the device is warm, 185 after a
+// pause.  What bounds it: the instructions of a turn (some 190 for the prompts' 140: pages, and
+// conversions of codes or places that are not held), memory's latency (38 us of 228 over bf16), the start of a
+// piece and its turns with the request's own tokens, the join (19).
 //
-// Contexts are cut into stretches (see Stretch) where that fills the device better.
+// Contexts are cut into stretches (see Search) where that fills the device better.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -263,7 +264,8 @@ struct Cut {
 
 // A workgroup's place in the launch.  What reads the same cache lines follows each other on the same of
 // the eight dies, whose cache it shares: row blocks of the same keys, and two heads whose keys
-// are half a line each (codes of 64 columns).
+// are half a line each (codes of 64 columns: 512 requests of up to 4096 346 us with the heads apart, 255 so;
+// more than a line together gains nothing).
 template <int D, bool E4M3>
 struct Place {
   int kv, block, item;  // item: request or stretch
