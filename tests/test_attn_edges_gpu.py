@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import attn_reference as R
-from test_attn_gpu import BF, attn, cache_of, check_decode, offsets, pages_for, rand, to_gpu
+from test_attn_gpu import BF, assign_case, attn, cache_of, check_assign, check_decode, offsets, pages_for, rand, to_gpu
 
 pytestmark = pytest.mark.gpu
 NAN, INF = float("nan"), float("inf")
@@ -338,6 +338,61 @@ def test_a_cache_of_more_than_32_bits(T, e4m3):
             want = t[i] if s is None else (t[i].float() / s[:, None]).clamp(-448, 448).to(dtype)
             assert torch.equal(c[p, x].view(torch.uint8), want.view(torch.uint8))
     assert torch.equal(both[5].view(torch.uint8), before.view(torch.uint8))
+
+
+# ---------------------------------------------------------------------------
+# many of everything
+
+def test_thousands_of_prompts():
+    g = torch.Generator().manual_seed(4)
+    lens = torch.randint(0, 4, (3000,), generator=g).tolist()
+    lens[1234] = 150
+    q, k, v = prompts(lens, 64, 4, H=2, KV=1)
+    ref, lse_ref, mag, terms = R.prefill(q, k, v, lens)
+    out, lse = run_prompts(q, k, v, lens)
+    R.assert_out(out, ref, mag)
+    R.assert_lse(lse, lse_ref, terms, 64)
+
+
+@caches
+@pytest.mark.parametrize("T", [1, 40])
+def test_thousands_of_requests(T, e4m3):
+    g = torch.Generator().manual_seed(T)
+    N, size, W = 20000 if T == 1 else 900, 16, 70
+    lens = torch.randint(0, 5, (N,), generator=g).to(torch.int32)
+    some = [0, 1, 255, 256, 700, N // 2, N - 2, N - 1]
+    lens[some[3]], lens[some[5]], lens[N - 1] = 1000, 300, 900
+    kc, vc, ks, vs = cache_of(g, 200, size, 1, 64, e4m3)
+    table = torch.randint(0, 200, (N, W), generator=g).to(torch.int32)
+    q = rand(g, N, T, 2, 64, scale=1.4)
+    qd, kd, vd, td, ld, ksd, vsd = to_gpu(q, kc, vc, table, lens, ks, vs)
+    out, lse = attn().decode(qd, kd, vd, td, ld, k_scale=ksd, v_scale=vsd, return_lse=True)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    at = torch.tensor(some)
+    ref, lse_ref, mag, terms = R.decode(q[at], kc, vc, table[at].contiguous(), lens[at], k_scale=ks, v_scale=vs)
+    R.assert_out(out.cpu()[at], ref, mag)
+    R.assert_lse(lse.cpu()[at], lse_ref, terms, 64)
+    # and all of them against the same requests, a hundred at a time
+    for b in range(0, N, 4000):
+        part, _ = attn().decode(qd[b:b + 100], kd, vd, td[b:b + 100], ld[b:b + 100], k_scale=ksd, v_scale=vsd)
+        assert (out[b:b + 100].float() - part.float()).abs().max() <= 2 * R.STEP * 2 * vc.float().abs().max() * (1 if vs is None else vs.max())
+
+
+@caches
+@pytest.mark.parametrize("KV,size,length", [(128, 16, 1500), (2, 1024, 3000), (200, 64, 1200)])
+def test_many_heads_and_large_pages(KV, size, length, e4m3):
+    g = torch.Generator().manual_seed(KV)
+    lens = [length, 20]
+    table, rows, pages = pages_for(g, [x + 1 for x in lens], size)
+    kc, vc, ks, vs = cache_of(g, pages, size, KV, 64, e4m3)
+    check_decode(rand(g, 2, 1, KV, 64, scale=1.4), kc, vc, table, i32(*lens), rows, None, ks, vs)
+
+
+def test_thousands_of_requests_get_pages():
+    g = torch.Generator().manual_seed(6)
+    old, rows, cu, table, free = assign_case(g, 5000, 60, 5, 16)
+    rows[::7] = -1
+    check_assign(old, rows, cu, table, free, 0, 16, int(cu[-1]) + 300)
 
 
 # ---------------------------------------------------------------------------
