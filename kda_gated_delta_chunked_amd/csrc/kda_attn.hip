@@ -14,7 +14,8 @@
 // a chain of waits: the offsets, the first blocks, a turn for each 32 keys, the last, masked one
 // (6 prompts of 271 to 3063, 12 heads of 128 72 us; one of 37 8 us on the device).
 //
-// Tried and not kept: 64 rows a wave (spills), operands read four products ahead (no change:
+// Tried and not kept: 64 rows a wave, which halve the reads of LDS (heads of 128, one wave a SIMD, B8 T8192
+// 4.20 ms for 3.87; of 64, two waves, 2.29 for 2.31, but 32 ragged prompts 575 us for 519), operands read four products ahead (no change:
 // LDS is not what a product waits for), keys 64 at a time (the same rate, twice the ring).
 #include <hip/hip_runtime.h>
 
