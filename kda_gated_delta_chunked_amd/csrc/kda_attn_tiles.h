@@ -218,8 +218,8 @@ __device__ __forceinline__ bf16x8 finite_only(const bf16x8& f) {
 // looked for, and what has been summed is brought to it: a weight is at most kFar, which costs
 // no accuracy (sums are floating point), and most blocks need no maximum.
 //
-// c s - c m is one operation, c m rounded once.  Where it is so large (beyond kNear) that this rounding
-// would show, c (s - m) is taken, always from the maximum: `far` is less than any sum from then on.
+// c s - c m is one operation, of c m as it is rounded.  Where c m is so large (beyond kNear) that its
+// error would show, c (s - m) is taken, always from the maximum: `far` is less than any sum from then on.
 template <int D>
 struct AttnRows {
   static constexpr float kFar = 4096.f, kNear = 4096.f;
