@@ -162,7 +162,10 @@ kda_status check_decode(const kda_attn_decode_problem* p) {
 // longer ones cut (256 of up to 8192 829 and 761; 1024 of up to 2048 932 and 818).  Of many rows, which
 // have more to join, they are cut as long as workgroups are few (64 requests of 16 tokens, up to
 // 8192, 4 heads a KV head, 350 and 289; 512 of 9, up to 4096, no difference).  Two workgroups
-// go on a CU, but for few contexts one has less to join (one of 131072 120 with 512, 111 with 256).
+// go on a CU, but for few contexts one has less to join (one of 131072 120 with 512, 111 with 256), and
+// of up to 64 rows over bf16 with heads of 128 the bytes take longer than the work of one (64 requests of
+// 16 tokens up to 8192, 4 heads a KV head, 310 and 287; over e4m3 204 and 260, with heads of 64 145 and 173;
+// 32 of 32 tokens, 8 heads, 226 and 267).
 int decode_parts(const kda_attn_decode_problem* p) {
   const int64_t KV = p->cache.num_kv_heads, G = p->num_heads / KV, T = p->tokens_per_seq;
   const int64_t per_item = kda::attn_decode_blocks(1, KV, T, G), blocks = p->num_seqs * per_item;
@@ -170,7 +173,8 @@ int decode_parts(const kda_attn_decode_problem* p) {
   const int64_t positions = (int64_t)p->table_width * p->cache.page_size;
   if (blocks == 0 || (many && blocks >= 2048) || positions <= 1024) return 0;
   if (p->num_seqs * ((positions + kda::kAttnUnit - 1) / kda::kAttnUnit) >= (int64_t)1 << 30) return 0;  // counted in 32 bits
-  const int64_t parts = (many || blocks > 256 ? 512 : 256) / per_item;
+  const bool bytes_bound = many && T * G <= 64 && p->cache.head_dim * (p->cache.dtype == KDA_CACHE_BF16 ? 2 : 1) >= 256;
+  const int64_t parts = (bytes_bound || (!many && blocks <= 256) ? 256 : 512) / per_item;
   return parts > 1 ? (int)parts : 0;
 }
 
