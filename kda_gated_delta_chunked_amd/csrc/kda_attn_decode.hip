@@ -297,139 +297,139 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
   Stretch piece(at_place.item);
   if (a.part_out) piece = Stretch(a, at_place.item, *reinterpret_cast<Search::Lds*>(tiles));
   for (int cut = 2 * at_place.item; piece.left > 0; ++piece.n, piece.unit = 0, cut |= 1) {
-  const int n = piece.n;
-  const Request req(a, n);
-  const int units = req.units(), take = a.part_out ? min(units - piece.unit, piece.left) : units;
-  const bool whole = take == units;
-  const int begin = piece.unit * STEP, end = min(req.length, begin + take * STEP);
-  piece.left -= take;
-  const int64_t q_row = (int64_t)n * a.T + t;
-  AttnRows<D> r;
-  r.start();
-  if (begin < end) {
-    r.load(a.q + q_row * a.q_stride + (kv * G + row % G) * D);
-    uint64_t sees = own_seen(a, n, t);
-    asm volatile("" : "+v"(sees));  // there ahead of the copies
-    const int32_t* table = a.table + (int64_t)req.row * a.table_width;
-    const float c = a.scale * kLog2e * (E4M3 ? a.c.k_scale[kv] : 1.f);
-    const Copies copies(a.c, kv);
-    uint8_t* const ring = tiles[wave];
-    const int first = begin + wave * KEYS, count = (end - first + STEP - 1) / STEP;  // the wave's tiles
+    const int n = piece.n;
+    const Request req(a, n);
+    const int units = req.units(), take = a.part_out ? min(units - piece.unit, piece.left) : units;
+    const bool whole = take == units;
+    const int begin = piece.unit * STEP, end = min(req.length, begin + take * STEP);
+    piece.left -= take;
+    const int64_t q_row = (int64_t)n * a.T + t;
+    AttnRows<D> r;
+    r.start();
+    if (begin < end) {
+      r.load(a.q + q_row * a.q_stride + (kv * G + row % G) * D);
+      uint64_t sees = own_seen(a, n, t);
+      asm volatile("" : "+v"(sees));  // there ahead of the copies
+      const int32_t* table = a.table + (int64_t)req.row * a.table_width;
+      const float c = a.scale * kLog2e * (E4M3 ? a.c.k_scale[kv] : 1.f);
+      const Copies copies(a.c, kv);
+      uint8_t* const ring = tiles[wave];
+      const int first = begin + wave * KEYS, count = (end - first + STEP - 1) / STEP;  // the wave's tiles
 
-    // Keys' and values' places are filled again as soon as the wave has read them: keys while
-    // their weights and products are worked out, values under the next tile's scores.
-    TileStarts<Copies::SIZE> starts;
-    const typename Copies::From from = copies.from();
-    const TilePlaces<D, E4M3, false> held(ring, ring + TILE);
-    const uint32_t keys_at = lds_place(ring), values_at = keys_at + TILE;
-    bool half0 = false, half1 = false;  // whether the halves of the last tile of keys have pages
-    auto fetch_keys = [&](int tile) {
-      half0 = starts.has(tile & 63, 0);
-      half1 = starts.has(tile & 63, 1);
-      copies.tile(true, starts, tile & 63, from, keys_at);
-    };
-    auto fetch_values = [&](int tile) { copies.tile(false, starts, tile & 63, from, values_at); };
-    auto reads_done = [&]() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
-    bool not_finite = false;  // left out of a tile with masked rows
-    if (count > 0) {
-      starts.find(a, table, first, STEP, begin, end);
-      fetch_keys(0);
-      fetch_values(0);
-      r.settle();
-    }
-    int tile = 0;
-    // A tile that all rows see, with another one behind it, or (SOME) any.
-    auto step = [&](auto some) {
-      constexpr bool SOME = decltype(some)::value;
-      const auto places = held.fresh();
-      const bool more = !SOME || tile + 1 < count;
-      memory_left<PARTS>();
-      f32x16 s = r.scores(places, 0);
-      reads_done();
-      if (SOME) {
-        mask_scores(s, seen_keys(first + tile * STEP, end, req.before, sees, half0, half1));
-        if (more && ((tile + 1) & 63) == 0) starts.find(a, table, first + (tile + 1) * STEP, STEP, begin, end);
+      // Keys' and values' places are filled again as soon as the wave has read them: keys while
+      // their weights and products are worked out, values under the next tile's scores.
+      TileStarts<Copies::SIZE> starts;
+      const typename Copies::From from = copies.from();
+      const TilePlaces<D, E4M3, false> held(ring, ring + TILE);
+      const uint32_t keys_at = lds_place(ring), values_at = keys_at + TILE;
+      bool half0 = false, half1 = false;  // whether the halves of the last tile of keys have pages
+      auto fetch_keys = [&](int tile) {
+        half0 = starts.has(tile & 63, 0);
+        half1 = starts.has(tile & 63, 1);
+        copies.tile(true, starts, tile & 63, from, keys_at);
+      };
+      auto fetch_values = [&](int tile) { copies.tile(false, starts, tile & 63, from, values_at); };
+      auto reads_done = [&]() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
+      bool not_finite = false;  // left out of a tile with masked rows
+      if (count > 0) {
+        starts.find(a, table, first, STEP, begin, end);
+        fetch_keys(0);
+        fetch_values(0);
+        r.settle();
       }
-      if (more) fetch_keys(tile + 1);
-      bf16x8 p[2];
-      float sum;
-      if (__builtin_expect(r.try_weights(s, c, p, sum), 0)) r.weights_from_maximum(s, c, p, sum);
-      r.l += sum;
-      if (more) memory_left<PARTS>();
-      else memory_left<0>();
-      if (SOME) not_finite = r.add_masked(places, 0, p) || not_finite;
-      else r.add(places, 0, p);
-      reads_done();
-      if (more) fetch_values(tile + 1);
-      ++tile;
-    };
-    const int open = min(req.before, end) - KEYS - first;  // tiles up to there are seen whole, if they have pages
-    while (tile < count) {
-      while (tile * STEP <= open && half0 && half1 && tile + 1 < count && ((tile + 1) & 63)) step(std::false_type());
-      step(std::true_type());
-    }
-    if (__builtin_expect(not_finite, 0))
-      for (int tile = 0; tile < count; ++tile)
-        for (int pos = first + tile * STEP; pos < min(end, first + tile * STEP + KEYS); ++pos) {
-          const int page = page_of(a, table, pos, end), own = pos - req.before;
-          if (page < 0) continue;
-          r.add_not_finite(own < 0 || (sees >> (own & 63) & 1), [&](int d) { return value_at<E4M3>(a.c, kv, page, pos, d); });
+      int tile = 0;
+      // A tile that all rows see, with another one behind it, or (SOME) any.
+      auto step = [&](auto some) {
+        constexpr bool SOME = decltype(some)::value;
+        const auto places = held.fresh();
+        const bool more = !SOME || tile + 1 < count;
+        memory_left<PARTS>();
+        f32x16 s = r.scores(places, 0);
+        reads_done();
+        if (SOME) {
+          mask_scores(s, seen_keys(first + tile * STEP, end, req.before, sees, half0, half1));
+          if (more && ((tile + 1) & 63) == 0) starts.find(a, table, first + (tile + 1) * STEP, STEP, begin, end);
         }
-  }
+        if (more) fetch_keys(tile + 1);
+        bf16x8 p[2];
+        float sum;
+        if (__builtin_expect(r.try_weights(s, c, p, sum), 0)) r.weights_from_maximum(s, c, p, sum);
+        r.l += sum;
+        if (more) memory_left<PARTS>();
+        else memory_left<0>();
+        if (SOME) not_finite = r.add_masked(places, 0, p) || not_finite;
+        else r.add(places, 0, p);
+        reads_done();
+        if (more) fetch_values(tile + 1);
+        ++tile;
+      };
+      const int open = min(req.before, end) - KEYS - first;  // tiles up to there are seen whole, if they have pages
+      while (tile < count) {
+        while (tile * STEP <= open && half0 && half1 && tile + 1 < count && ((tile + 1) & 63)) step(std::false_type());
+        step(std::true_type());
+      }
+      if (__builtin_expect(not_finite, 0))
+        for (int tile = 0; tile < count; ++tile)
+          for (int pos = first + tile * STEP; pos < min(end, first + tile * STEP + KEYS); ++pos) {
+        const int page = page_of(a, table, pos, end), own = pos - req.before;
+        if (page < 0) continue;
+        r.add_not_finite(own < 0 || (sees >> (own & 63) & 1), [&](int d) { return value_at<E4M3>(a.c, kv, page, pos, d); });
+      }
+    }
 
-  // the waves' shares, joined through their tiles: O as [D][32 rows]
-  float* mine = reinterpret_cast<float*>(tiles[wave]);
-  wave_order();
+    // the waves' shares, joined through their tiles: O as [D][32 rows]
+    float* mine = reinterpret_cast<float*>(tiles[wave]);
+    wave_order();
 #pragma unroll
-  for (int b = 0; b < D / 32; ++b)
+    for (int b = 0; b < D / 32; ++b)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) mine[(32 * b + key_of(i, h)) * 32 + (lane & 31)] = r.o[b][i];
-  const float total = r.total();
-  if (h == 0) {
-    stats[wave][0][lane] = r.m;
-    stats[wave][1][lane] = total;
-  }
-  tiles_barrier<0>();
-  const int mine_row = threadIdx.x & 31, row_at = mine_row, cols = (threadIdx.x >> 5) * (D / 8);
-  if (row_at < rows) {
-  const float c = a.scale * kLog2e * (E4M3 && begin < end ? a.c.k_scale[kv] : 1.f);
-  float m = kNone;
+      for (int i = 0; i < 16; ++i) mine[(32 * b + key_of(i, h)) * 32 + (lane & 31)] = r.o[b][i];
+    const float total = r.total();
+    if (h == 0) {
+      stats[wave][0][lane] = r.m;
+      stats[wave][1][lane] = total;
+    }
+    tiles_barrier<0>();
+    const int mine_row = threadIdx.x & 31, row_at = mine_row, cols = (threadIdx.x >> 5) * (D / 8);
+    if (row_at < rows) {
+      const float c = a.scale * kLog2e * (E4M3 && begin < end ? a.c.k_scale[kv] : 1.f);
+      float m = kNone;
 #pragma unroll
-  for (int w = 0; w < WAVES; ++w) m = fmaxf(m, stats[w][0][mine_row]);
-  float weight[WAVES], sum = 0.f;
+      for (int w = 0; w < WAVES; ++w) m = fmaxf(m, stats[w][0][mine_row]);
+      float weight[WAVES], sum = 0.f;
 #pragma unroll
-  for (int w = 0; w < WAVES; ++w) {
-    weight[w] = stats[w][0][mine_row] == kNone ? 0.f : __builtin_amdgcn_exp2f((stats[w][0][mine_row] - m) * c);
-    // (a share whose scores are all NaN has no maximum, and a sum that is NaN)
-    sum += stats[w][1][mine_row] != stats[w][1][mine_row] ? stats[w][1][mine_row] : weight[w] * stats[w][1][mine_row];
-  }
-  float o[D / 8];
+      for (int w = 0; w < WAVES; ++w) {
+        weight[w] = stats[w][0][mine_row] == kNone ? 0.f : __builtin_amdgcn_exp2f((stats[w][0][mine_row] - m) * c);
+        // (a share whose scores are all NaN has no maximum, and a sum that is NaN)
+        sum += stats[w][1][mine_row] != stats[w][1][mine_row] ? stats[w][1][mine_row] : weight[w] * stats[w][1][mine_row];
+      }
+      float o[D / 8];
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
-    o[i] = 0.f;
+      for (int i = 0; i < D / 8; ++i) {
+        o[i] = 0.f;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w)
-      if (weight[w] != 0.f) o[i] += weight[w] * reinterpret_cast<const float*>(tiles[w])[(cols + i) * 32 + mine_row];
-  }
-  const int64_t out_row = (int64_t)n * a.T + row_at / G;
-  const int head = kv * G + row_at % G;
-  if (!whole) {
-    const int64_t slot = ((int64_t)cut * KV + kv) * rows + row_at;
-    float* to = a.part_out + slot * D + cols;
+        for (int w = 0; w < WAVES; ++w)
+          if (weight[w] != 0.f) o[i] += weight[w] * reinterpret_cast<const float*>(tiles[w])[(cols + i) * 32 + mine_row];
+      }
+      const int64_t out_row = (int64_t)n * a.T + row_at / G;
+      const int head = kv * G + row_at % G;
+      if (!whole) {
+        const int64_t slot = ((int64_t)cut * KV + kv) * rows + row_at;
+        float* to = a.part_out + slot * D + cols;
 #pragma unroll
-    for (int i = 0; i < D / 8; i += 4) *reinterpret_cast<float4*>(to + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-    if (cols == 0) *reinterpret_cast<float2*>(a.part_ml + slot * 2) = make_float2(m, sum);
-  } else {
-  const float inv = sum == 0.f ? 0.f : (E4M3 ? a.c.v_scale[kv] : 1.f) / sum;
-  uint16_t* to = a.out + out_row * a.out_stride + head * D + cols;
+        for (int i = 0; i < D / 8; i += 4) *reinterpret_cast<float4*>(to + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        if (cols == 0) *reinterpret_cast<float2*>(a.part_ml + slot * 2) = make_float2(m, sum);
+      } else {
+        const float inv = sum == 0.f ? 0.f : (E4M3 ? a.c.v_scale[kv] : 1.f) / sum;
+        uint16_t* to = a.out + out_row * a.out_stride + head * D + cols;
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) o[i] *= inv;
+        for (int i = 0; i < D / 8; ++i) o[i] *= inv;
 #pragma unroll
-  for (int i = 0; i < D / 8; i += 8) *reinterpret_cast<uint4*>(to + i) = f32_bf16x8(o + i);
-  if (a.lse && cols == 0) a.lse[out_row * a.H + head] = lse_of(m, c, sum);
-  }
-  }
-  if (piece.left > 0) tiles_barrier<0>();  // the tiles are copied to again
+        for (int i = 0; i < D / 8; i += 8) *reinterpret_cast<uint4*>(to + i) = f32_bf16x8(o + i);
+        if (a.lse && cols == 0) a.lse[out_row * a.H + head] = lse_of(m, c, sum);
+      }
+    }
+    if (piece.left > 0) tiles_barrier<0>();  // the tiles are copied to again
   }
 }
 
@@ -520,43 +520,43 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_drafts_kernel(AttnDecodeA
   Stretch piece(at_place.item);
   if (a.part_out) piece = Stretch(a, at_place.item, *reinterpret_cast<Search::Lds*>(tiles));
   for (int cut = 2 * at_place.item; piece.left > 0; ++piece.n, piece.unit = 0, cut |= 1) {
-  const int n = piece.n;
-  const Request req(a, n);
-  const int units = req.units(), take = a.part_out ? min(units - piece.unit, piece.left) : units;
-  const bool whole = take == units;
-  const int begin = piece.unit * STEP, end = min(req.length, begin + take * STEP);
-  piece.left -= take;
-  const int64_t q_row = (int64_t)n * a.T + t;
-  float c = 0.f;
-  AttnRows<D> r;
-  r.start();
-  if (begin < end) {
-    r.load(a.q + q_row * a.q_stride + (kv * G + read % G) * D);
-    uint64_t sees = own_seen(a, n, t);
-    asm volatile("" : "+v"(sees));  // there ahead of the copies
-    c = a.scale * kLog2e * (E4M3 ? a.c.k_scale[kv] : 1.f);
-    const int blocks = (end - begin + KEYS - 1) / KEYS;
-    Source source(a, kv, a.table + (int64_t)req.row * a.table_width, begin, end, req.before, sees, wave, tiles);
-    r.settle();
-    for (int i = 0; i < Source::RING - 1; ++i) source.put();
-    if (__builtin_expect(attend(r, source, c, blocks, top < rows ? blocks : 0), 0))
-      for (int pos = begin; pos < end; ++pos) {
+    const int n = piece.n;
+    const Request req(a, n);
+    const int units = req.units(), take = a.part_out ? min(units - piece.unit, piece.left) : units;
+    const bool whole = take == units;
+    const int begin = piece.unit * STEP, end = min(req.length, begin + take * STEP);
+    piece.left -= take;
+    const int64_t q_row = (int64_t)n * a.T + t;
+    float c = 0.f;
+    AttnRows<D> r;
+    r.start();
+    if (begin < end) {
+      r.load(a.q + q_row * a.q_stride + (kv * G + read % G) * D);
+      uint64_t sees = own_seen(a, n, t);
+      asm volatile("" : "+v"(sees));  // there ahead of the copies
+      c = a.scale * kLog2e * (E4M3 ? a.c.k_scale[kv] : 1.f);
+      const int blocks = (end - begin + KEYS - 1) / KEYS;
+      Source source(a, kv, a.table + (int64_t)req.row * a.table_width, begin, end, req.before, sees, wave, tiles);
+      r.settle();
+      for (int i = 0; i < Source::RING - 1; ++i) source.put();
+      if (__builtin_expect(attend(r, source, c, blocks, top < rows ? blocks : 0), 0))
+        for (int pos = begin; pos < end; ++pos) {
         const int page = page_of(a, source.table, pos, end), own = pos - req.before;
         if (page < 0) continue;
         r.add_not_finite(own < 0 || (sees >> (own & 63) & 1), [&](int d) { return value_at<E4M3>(a.c, kv, page, pos, d); });
       }
-  }
-  const float total = r.total();
-  if (row < rows && !whole) {
-    const int64_t slot = ((int64_t)cut * KV + kv) * rows + row;
-    r.store_sums(a.part_out + slot * D);
-    if (lane < 32) *reinterpret_cast<float2*>(a.part_ml + slot * 2) = make_float2(r.m, total);
-  } else if (row < rows) {
-    const int head = kv * G + row % G;
-    r.store(a.out + q_row * a.out_stride + head * D, total == 0.f ? 0.f : (E4M3 ? a.c.v_scale[kv] : 1.f) / total);
-    if (a.lse && lane < 32) a.lse[q_row * a.H + head] = lse_of(r.m, c, total);
-  }
-  if (piece.left > 0) tiles_barrier<0>();  // the tiles are copied to again
+    }
+    const float total = r.total();
+    if (row < rows && !whole) {
+      const int64_t slot = ((int64_t)cut * KV + kv) * rows + row;
+      r.store_sums(a.part_out + slot * D);
+      if (lane < 32) *reinterpret_cast<float2*>(a.part_ml + slot * 2) = make_float2(r.m, total);
+    } else if (row < rows) {
+      const int head = kv * G + row % G;
+      r.store(a.out + q_row * a.out_stride + head * D, total == 0.f ? 0.f : (E4M3 ? a.c.v_scale[kv] : 1.f) / total);
+      if (a.lse && lane < 32) a.lse[q_row * a.H + head] = lse_of(r.m, c, total);
+    }
+    if (piece.left > 0) tiles_barrier<0>();  // the tiles are copied to again
   }
 }
 
