@@ -27,7 +27,10 @@
  * Accuracy.  Scores, the softmax's maxima and sums and the outputs' sums are
  * fp32.  A weight exp(s - m) is rounded to bf16 ahead of the product with the
  * values (the sum that divides them is of the unrounded ones), an output once.
- * Range.  Scores have to be finite in fp32.  A row that sees an infinity or a NaN
+ * Range.  Scores have to be finite in fp32.  Values may be of any size up to 2^127 (of rows that see more
+ * than 2^23 positions, 2^150 over their number): no sum leaves fp32.  At its other end, with values
+ * in bf16, weights below 2^-94 of a row's largest count as zero, and what an output loses is 2^-94 times the
+ * positions at most.  A row that sees an infinity or a NaN
  * is infinite or NaN (which of them, and in which columns, is not specified where the
  * keys hold it; a value's stays in its column); rows that do not see it are
  * as if it were not there.

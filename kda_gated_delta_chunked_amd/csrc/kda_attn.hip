@@ -128,7 +128,7 @@ __global__ __launch_bounds__(SPLIT * WAVES * 64, 2) void kda_attn_kernel(AttnArg
 
   const int of_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = of_all % WAVES, side = of_all / WAVES;
   const int lane = threadIdx.x & 63, top = first + wave * 32, row = top + (lane & 31);  // the wave's first row, the lane's
-  AttnRows<D> r;
+  AttnRows<D, false> r;
   r.load(a.q + (span.begin + min(row, length - 1)) * a.q_stride + head * D);
   r.start();
   const float c = a.scale * kLog2e;
@@ -171,7 +171,7 @@ __global__ __launch_bounds__(SPLIT * WAVES * 64, 2) void kda_attn_kernel(AttnArg
   if (row >= length) return;
   const int64_t token = span.begin + row;
   r.store(a.out + token * a.out_stride + head * D, 1.f / total);
-  if (a.lse && lane < 32) a.lse[token * a.H + head] = lse_of(r.m, c, total);
+  if (a.lse && lane < 32) a.lse[token * a.H + head] = r.lse_of(r.m, c, total);
 }
 
 template <int D>

@@ -304,7 +304,7 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
     const int begin = piece.unit * STEP, end = min(req.length, begin + take * STEP);
     piece.left -= take;
     const int64_t q_row = (int64_t)n * a.T + t;
-    AttnRows<D> r;
+    AttnRows<D, E4M3> r;
     r.start();
     if (begin < end) {
       r.load(a.q + q_row * a.q_stride + (kv * G + row % G) * D);
@@ -430,7 +430,7 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
         for (int i = 0; i < D / 8; ++i) o[i] *= inv;
 #pragma unroll
         for (int i = 0; i < D / 8; i += 8) *reinterpret_cast<uint4*>(to + i) = f32_bf16x8(o + i);
-        if (a.lse && cols == 0) a.lse[out_row * a.H + head] = lse_of(m, c, sum);
+        if (a.lse && cols == 0) a.lse[out_row * a.H + head] = AttnRows<D, E4M3>::lse_of(m, c, sum);
       }
     }
     if (piece.left > 0) tiles_barrier<0>();  // the tiles are copied to again
@@ -532,7 +532,7 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_drafts_kernel(AttnDecodeA
     piece.left -= take;
     const int64_t q_row = (int64_t)n * a.T + t;
     float c = 0.f;
-    AttnRows<D> r;
+    AttnRows<D, E4M3> r;
     r.start();
     if (begin < end) {
       r.load(a.q + q_row * a.q_stride + (kv * G + read % G) * D);
@@ -558,7 +558,7 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_drafts_kernel(AttnDecodeA
     } else if (row < rows) {
       const int head = kv * G + row % G;
       r.store(a.out + q_row * a.out_stride + head * D, total == 0.f ? 0.f : (E4M3 ? a.c.v_scale[kv] : 1.f) / total);
-      if (a.lse && lane < 32) a.lse[q_row * a.H + head] = lse_of(r.m, c, total);
+      if (a.lse && lane < 32) a.lse[q_row * a.H + head] = r.lse_of(r.m, c, total);
     }
     if (piece.left > 0) tiles_barrier<0>();  // the tiles are copied to again
   }
@@ -657,7 +657,7 @@ __global__ __launch_bounds__(THREADS) void kda_attn_join_kernel(AttnDecodeArgs a
     const int head = kv * G + row % G;
     *reinterpret_cast<uint2*>(a.out + out_row * a.out_stride + head * D + col * 4) =
         make_uint2(bf16_pair(r.o.x * inv, r.o.y * inv), bf16_pair(r.o.z * inv, r.o.w * inv));
-    if (a.lse && col == 0) a.lse[out_row * a.H + head] = lse_of(r.m, c, r.l);
+    if (a.lse && col == 0) a.lse[out_row * a.H + head] = a.c.k_scale ? AttnRows<D, true>::lse_of(r.m, c, r.l) : AttnRows<D, false>::lse_of(r.m, c, r.l);
   }
 }
 

@@ -209,7 +209,7 @@ __device__ __forceinline__ bf16x8 finite_only(const bf16x8& f) {
 }
 
 // The softmax's state of a wave's 32 rows, and their outputs so far.  With c =
-// scale log2(e) > 0, weights are 2^(c (s - m)) for scores s = q . k; l is the sum of this half's,
+// scale log2(e) > 0, weights are 2^(c (s - m) - SHIFT) for scores s = q . k; l is the sum of this half's,
 // o that of the weighted values.
 //
 // m follows the maximum of a row's scores at a distance: weights are taken
@@ -218,11 +218,17 @@ __device__ __forceinline__ bf16x8 finite_only(const bf16x8& f) {
 // looked for, and what has been summed is brought to it: a weight is at most kFar, which costs
 // no accuracy (sums are floating point), and most blocks need no maximum.
 //
+// SHIFT keeps o within fp32's range for all finite values of bf16: weights of 32 keys sum to 2^(13 - SHIFT)
+// at most, those of L keys to L 2^(8 - SHIFT), which is 1/2 for 32 and 2^23 keys.  It divides out; what it costs is
+// at fp32's other end, weights below 2^-94 of the largest.  As a literal of c m + SHIFT it takes no
+// register and no instruction (as an argument for the context's length, 64 requests of 16 tokens took 317 us
+// for 286: a register more in a kernel that spills).  Codes, of 448 at most, need none.
+//
 // c s - c m is one operation, of c m as it is rounded.  Where c m is so large (beyond kNear) that its
 // error would show, c (s - m) is taken, always from the maximum: `far` is less than any sum from then on.
-template <int D>
+template <int D, bool E4M3>
 struct AttnRows {
-  static constexpr float kFar = 4096.f, kNear = 4096.f;
+  static constexpr float SHIFT = E4M3 ? 0.f : 32.f, kFar = E4M3 ? 0x1p12f : 0x1p-20f, kNear = 4096.f;
   bf16x8 q[D / 16];
   f32x16 o[D / 32];
   float m, l, far;
@@ -261,11 +267,11 @@ struct AttnRows {
   // weights of scores from a maximum, as operands, and their sum
   template <bool NEAR>
   static __device__ __forceinline__ float weights(const f32x16& s, float c, float m, bf16x8 (&p)[2]) {
-    const float mc = m * c;
+    const float mc = __builtin_fmaf(m, c, SHIFT);
     float e[16], sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      e[i] = __builtin_amdgcn_exp2f(NEAR ? __builtin_fmaf(s[i], c, -mc) : (s[i] - m) * c);
+      e[i] = __builtin_amdgcn_exp2f(NEAR ? __builtin_fmaf(s[i], c, -mc) : __builtin_fmaf(s[i] - m, c, -SHIFT));
       sum[i & 1] += e[i];
     }
 #pragma unroll
@@ -299,7 +305,7 @@ struct AttnRows {
     constexpr int EVERY = (COUNT - 2) / Source::COUNT;  // products between copies
     static_assert(EVERY >= 1, "a copy behind a product");
     constexpr int BUSY = COUNT * 3 / 4;
-    const float mc = m * c;
+    const float mc = __builtin_fmaf(m, c, SHIFT);
     float e = 0.f, part[2] = {0.f, 0.f};
     uint32_t pair[8];
     bool beyond = false;
@@ -419,6 +425,10 @@ struct AttnRows {
         o[b][i] += sees && !(fabsf(v) < __builtin_huge_valf()) ? v : 0.f;
       }
   }
+  // log sum exp(scale s) from a maximum of s, and the sum of weights from it
+  static __device__ __forceinline__ float lse_of(float m, float c, float total) {
+    return m == kNone && total == 0.f ? kNone : __builtin_fmaf(m, c, __builtin_amdgcn_logf(total * (E4M3 ? 1.f : 0x1p32f))) * kLn2;
+  }
   // the row's whole sum
   __device__ __forceinline__ float total() const { return l + other_half(l); }
   // the lane's part of a row of sums
@@ -459,9 +469,8 @@ __device__ __forceinline__ void mask_scores(f32x16& s, uint32_t seen) {
 // `blocks`: of the workgroup; `mine`: of them, those that any of the wave's rows sees;
 // source.open: below it all rows see all keys (a put may lower it to the block of keys it copies).
 // Whether infinities or NaNs were left out of masked blocks.
-template <int D, class Source>
-__device__ __forceinline__ bool attend(AttnRows<D>& r, Source& source, float c, int blocks, int mine) {
-  using Rows = AttnRows<D>;
+template <class Rows, class Source>
+__device__ __forceinline__ bool attend(Rows& r, Source& source, float c, int blocks, int mine) {
   using Places = typename Source::Places;
   if (mine == 0) {  // no rows, but a share of the copies: as many turns as the others have
     for (int t = 0; t < blocks + 2; ++t) {
@@ -556,11 +565,6 @@ __device__ __forceinline__ bool attend(AttnRows<D>& r, Source& source, float c, 
   }
   memory_left<0>();  // no copy outlives the workgroup
   return left_out;
-}
-
-// log sum exp(scale s) from a maximum of s, c = scale log2(e), and the sum
-__device__ __forceinline__ float lse_of(float m, float c, float total) {
-  return m == kNone && total == 0.f ? kNone : __builtin_fmaf(m, c, __builtin_amdgcn_logf(total)) * kLn2;
 }
 
 }  // namespace kda
