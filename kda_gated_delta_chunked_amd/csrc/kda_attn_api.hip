@@ -149,8 +149,8 @@ kda_status check_decode(const kda_attn_decode_problem* p) {
   const int64_t row = (int64_t)p->num_heads * p->cache.head_dim;
   if (!stride_ok(p->q_stride, row) || !stride_ok(p->out_stride, row)) return KDA_ERR_INVALID_ARG;
   const int64_t N = p->num_seqs, KV = p->cache.num_kv_heads, T = p->tokens_per_seq;
-  if (N * T > kInt32Max || N * T * p->num_heads * 256 > kda::kMaxThreads ||
-      kda::attn_decode_blocks(N, KV, T, p->num_heads / KV) * 256 > kda::kMaxThreads)
+  // (stretches take 512 workgroups at most, and the join of their pieces 5000)
+  if (N * T > kInt32Max || kda::attn_decode_blocks(N, KV, T, p->num_heads / KV) * 256 > kda::kMaxThreads)
     return KDA_ERR_TOO_LARGE;
   return KDA_OK;
 }
