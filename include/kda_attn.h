@@ -27,13 +27,13 @@
  * Accuracy.  Scores, the softmax's maxima and sums and the outputs' sums are
  * fp32.  A weight exp(s - m) is rounded to bf16 ahead of the product with the
  * values (the sum that divides them is of the unrounded ones), an output once.
- * Range.  Scores have to be finite in fp32.  Values may be of any size up to 2^127 (of rows that see more
- * than 2^23 positions, 2^150 over their number): no sum leaves fp32.  At its other end, with values
- * in bf16, weights below 2^-94 of a row's largest count as zero, and what an output loses is 2^-94 times the
- * positions at most.  A row that sees an infinity or a NaN
- * is infinite or NaN (which of them, and in which columns, is not specified where the
- * keys hold it; a value's stays in its column); rows that do not see it are
- * as if it were not there.
+ * Range.  Products q . k and scores have to be below 2^127 in magnitude.  Values may be of any size up to
+ * 2^127 (of rows that see more than 2^23 positions, 2^150 over their number): no sum leaves
+ * fp32.  At its other end, with values in bf16, weights below 2^-94 of a row's largest count as
+ * zero, and what an output loses is 2^-94 times the positions at most.
+ * A row that sees an infinity or a NaN is infinite or NaN (which of them, and in which columns,
+ * is not specified where the keys hold it; a value's stays in its column); rows that do not
+ * see it are as if it were not there.
  */
 #ifndef KDA_ATTN_H_
 #define KDA_ATTN_H_
@@ -62,7 +62,7 @@ typedef struct {
   int32_t num_heads;         /* H >= 1 */
   int32_t num_kv_heads;      /* >= 1, divides H */
   int32_t head_dim;          /* 64 or 128 */
-  float scale;               /* finite, > 0 */
+  float scale;               /* > 0 and at most 2^127 */
   int32_t cu_seqlens_int64;  /* 0: int32 offsets, 1: int64 */
   int64_t q_stride;          /* elements between rows, a multiple of 8, at least the row and below
                                 2^23; 0 = the row */
@@ -130,7 +130,7 @@ typedef struct {
   int32_t num_seqs;          /* N >= 0 requests */
   int32_t tokens_per_seq;    /* T, 1..64; row n * T + t is token t of request n */
   int32_t num_heads;         /* H >= 1, a multiple of cache.num_kv_heads */
-  float scale;               /* finite, > 0 */
+  float scale;               /* as for the prefill; times k_scale likewise, and at least 2^-126 */
   int64_t table_rows;        /* 0 .. 2^31 - 1 */
   int32_t table_width;       /* >= 1; table_width * page_size is at most 2^30 */
   int32_t tree_per_seq;      /* 1: tree is [N, T], 0: [T] */

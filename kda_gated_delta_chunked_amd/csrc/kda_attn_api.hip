@@ -64,7 +64,8 @@ kda::Packing packing(const void* cu, int cu64, int N, int64_t T) {
 
 kda_status check_heads(int32_t H, int32_t KV, int32_t D, float scale) {
   if (D != 64 && D != 128) return KDA_ERR_UNSUPPORTED;
-  if (H < 1 || KV < 1 || H % KV || !std::isfinite(scale) || scale <= 0.f) return KDA_ERR_INVALID_ARG;
+  // (the kernels take 2^(c s), c = scale log2 e)
+  if (H < 1 || KV < 1 || H % KV || !std::isfinite(scale * 1.44269504f) || scale <= 0.f) return KDA_ERR_INVALID_ARG;
   return (int64_t)H * D >= kRowElements ? KDA_ERR_TOO_LARGE : KDA_OK;
 }
 
