@@ -47,9 +47,8 @@ __device__ __forceinline__ int page_of(const AttnDecodeArgs& a, const int32_t* r
   const int p = pos < end ? row[pos >> a.c.page_shift] : -1;
   return p < a.c.pages ? p : -1;
 }
-// Elements from a cache's start to those of a position in `page`.
 __device__ __forceinline__ int64_t in_cache(const PagedCache& c, int page, int pos) {
-  return page * c.page_stride + (pos & ((1 << c.page_shift) - 1)) * c.token_stride;
+  return kda::in_cache(page, pos, c.page_shift, c.page_stride, c.token_stride);
 }
 
 // The request's own tokens that token t sees, a bit each.
@@ -100,27 +99,22 @@ struct TileStarts {
 // Tiles of KEYS rows of one head, keys or values, from the cache to LDS, asynchronously, 1 KiB
 // a copy in LDS order, the swizzle in the addresses.
 template <int D, bool E4M3>
-struct PageCopies {
-  static constexpr int SIZE = E4M3 ? 1 : 2, PER_ROW = D * SIZE / 16, ROWS = 64 / PER_ROW, PARTS = KEYS / ROWS;
+struct PageCopies : TileCopies<D, E4M3> {
+  using Tile = TileCopies<D, E4M3>;
+  static constexpr int SIZE = Tile::SIZE, PARTS = Tile::PARTS, PERIOD = Tile::PERIOD;
   static constexpr int COUNT = 2 * PARTS, TILE = KEYS * D * SIZE;  // of a tile's keys and values; bytes of either
-  static_assert(ROWS <= 16 && PARTS >= 2, "halves lie in one page each");
   uint64_t kbase, vbase;
   int token;  // bytes
   __device__ __forceinline__ PageCopies(const PagedCache& c, int kv)
       : kbase(reinterpret_cast<uint64_t>(c.k) + (int64_t)kv * D * SIZE),
         vbase(reinterpret_cast<uint64_t>(c.v) + (int64_t)kv * D * SIZE), token((int)c.token_stride * SIZE) {}
   // the lane's bytes of a copy's first row (rows are less than 2^24 bytes apart: 32 bits hold 16)
-  __device__ __forceinline__ int lane_from(int part) const {
-    const int lane = forget(threadIdx.x & 63), row = part * ROWS + lane / PER_ROW;
-    return lane / PER_ROW * token + (attn_tile_at<D, E4M3>(row, lane % PER_ROW) & (D * SIZE - 1));
-  }
-  static __device__ __forceinline__ int half(int part) { return part / (PARTS / 2); }
+  __device__ __forceinline__ int lane_from(int part) const { return Tile::lane_from(part, forget(threadIdx.x & 63), token); }
   // copy `part` of a tile of keys or values whose half starts at `start`
   __device__ __forceinline__ void copy(bool keys, int part, int64_t start, int from, uint32_t lds) const {
-    copy_to_lds(lds + part * 1024, (keys ? kbase : vbase) + start + part % (PARTS / 2) * ROWS * token, (uint32_t)from);
+    copy_to_lds(lds + part * 1024, (keys ? kbase : vbase) + start + Tile::part_from(part, token), (uint32_t)from);
   }
-  // The lane's bytes of every copy: the swizzle, and with it they, repeat every 16 rows.
-  static constexpr int PERIOD = 16 / ROWS;
+  // The lane's bytes of every copy.
   struct From {
     uint32_t of[PERIOD];
   };
@@ -134,7 +128,7 @@ struct PageCopies {
   __device__ __forceinline__ void tile(bool keys, const TileStarts<SIZE>& starts, int tile, const From& from, uint32_t lds) const {
     const int64_t start[2] = {starts.start(tile, 0), starts.start(tile, 1)};
 #pragma unroll
-    for (int u = 0; u < PARTS; ++u) copy(keys, u, start[half(u)], (int)from.of[u % PERIOD], lds);
+    for (int u = 0; u < PARTS; ++u) copy(keys, u, start[Tile::half(u)], (int)from.of[u % PERIOD], lds);
   }
 };
 
@@ -153,18 +147,16 @@ struct Request {
     row = a.rows ? a.rows[n] : n;
     if (row < 0 || row >= a.table_rows) row = -1;
     const int held = a.lens[n], before_ = held < 0 ? 0 : held;
-    const int64_t most = (int64_t)a.table_width << a.c.page_shift, all = (int64_t)before_ + a.T;
     before = before_;
+    const int64_t most = (int64_t)a.table_width << a.c.page_shift, all = (int64_t)before_ + a.T;
     length = row < 0 ? 0 : (int)(all < most ? all : most);
   }
-  __device__ __forceinline__ int units() const { return length > STEP ? (length + STEP - 1) / STEP : 1; }
+  __device__ __forceinline__ int units() const { return context_units(length); }
 };
 
-// Contexts lie one behind another in units of STEP positions (one at least), and are cut into
-// a.parts stretches of the same length, whatever request they fall to: a workgroup has a
-// stretch, the last units of a request, whole ones, the first of another.  Every workgroup searches the
-// lengths by itself, a thread a run of requests (the host has seen that all units together are
-// less than 2^30).
+// Contexts are cut into a.parts stretches (kda_stretches.h), of which a workgroup has one.  Every
+// workgroup searches the lengths by itself, a thread a run of requests (the host has seen that all
+// units together are less than 2^30).
 struct Search {
   struct Lds {
     int sums[WAVES], found[3];
@@ -198,7 +190,7 @@ struct Search {
     mine = 0;
     for (int i = from; i < to; ++i) mine += Request(a, i).units();
     upto = ahead(mine, all, lds);
-    length = __builtin_amdgcn_readfirstlane((all + a.parts - 1) / a.parts);
+    length = __builtin_amdgcn_readfirstlane(stretch_units(all, a.parts));
   }
 };
 struct Stretch {
@@ -209,10 +201,10 @@ struct Stretch {
     const int start = w * search.length;
     left = __builtin_amdgcn_readfirstlane(min(search.length, search.all - start));  // (less than one: no stretch)
     if (start >= search.upto && start < search.upto + search.mine) {
-      int i = search.from, behind = start - search.upto;
-      for (int units; behind >= (units = Request(a, i).units()); ++i) behind -= units;
+      int i, unit_;
+      find_unit(start, search.upto, search.from, [&](int i) { return Request(a, i).units(); }, i, unit_);
       lds.found[0] = i;
-      lds.found[1] = behind;
+      lds.found[1] = unit_;
     }
     lds_barrier();
     n = __builtin_amdgcn_readfirstlane(lds.found[0]);
@@ -229,19 +221,9 @@ struct Cut {
   bool second;
   __device__ __forceinline__ Cut(const AttnDecodeArgs& a, int index, Search::Lds& lds) {
     const Search search(a, lds);
-    // visits the thread's cut requests: stretch, units of it ahead of the request, the request's units
     const uint32_t length = (uint32_t)search.length;
     auto each = [&](auto visit) {
-      uint32_t in = (uint32_t)search.upto / length, at = (uint32_t)search.upto - in * length;
-      for (int i = search.from; i < search.to; ++i) {
-        const uint32_t units = (uint32_t)Request(a, i).units();
-        if (at + units > length) visit(i, in, at, units);
-        at += units;
-        if (at >= length) {
-          in += at / length;
-          at %= length;
-        }
-      }
+      each_cut(search.upto, search.from, search.to, length, [&](int i) { return Request(a, i).units(); }, visit);
     };
     int mine = 0, all;
     each([&](int, uint32_t, uint32_t, uint32_t) { ++mine; });
@@ -252,7 +234,7 @@ struct Cut {
         if (place++ != index) return;
         lds.found[0] = i;
         lds.found[1] = (int)(in * 2 + (at > 0));
-        lds.found[2] = (int)((at + units - 1) / length + 1);
+        lds.found[2] = cut_pieces(at, units, length);
       });
     lds_barrier();
     n = __builtin_amdgcn_readfirstlane(lds.found[0]);
@@ -299,7 +281,7 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
   for (int cut = 2 * at_place.item; piece.left > 0; ++piece.n, piece.unit = 0, cut |= 1) {
     const int n = piece.n;
     const Request req(a, n);
-    const int units = req.units(), take = a.part_out ? min(units - piece.unit, piece.left) : units;
+    const int units = req.units(), take = a.part_out ? take_units(units, piece.unit, piece.left) : units;
     const bool whole = take == units;
     const int begin = piece.unit * STEP, end = min(req.length, begin + take * STEP);
     piece.left -= take;
@@ -526,7 +508,7 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_drafts_kernel(AttnDecodeA
   for (int cut = 2 * at_place.item; piece.left > 0; ++piece.n, piece.unit = 0, cut |= 1) {
     const int n = piece.n;
     const Request req(a, n);
-    const int units = req.units(), take = a.part_out ? min(units - piece.unit, piece.left) : units;
+    const int units = req.units(), take = a.part_out ? take_units(units, piece.unit, piece.left) : units;
     const bool whole = take == units;
     const int begin = piece.unit * STEP, end = min(req.length, begin + take * STEP);
     piece.left -= take;
@@ -609,7 +591,6 @@ __global__ __launch_bounds__(THREADS) void kda_attn_join_kernel(AttnDecodeArgs a
   const int n = cut.n, parts = cut.pieces;
   if (parts == 0) return;
   const int64_t step = (int64_t)KV * rows;  // of slots; a stretch has two
-  const int64_t first = 2 * cut.first, head_slot = cut.second ? first + 1 : first;
   const float c = a.scale * kLog2e * (a.c.k_scale ? a.c.k_scale[kv] : 1.f);
   const int side = threadIdx.x / LANES, col = threadIdx.x % LANES;
   int share = a.join_rows == 1 ? SIDES : 1;  // sides of a row
@@ -626,7 +607,7 @@ __global__ __launch_bounds__(THREADS) void kda_attn_join_kernel(AttnDecodeArgs a
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) {
         const int piece = min(p + i * share, parts - 1);
-        const int64_t from = lane_slot + (piece ? first + 2 * piece : head_slot) * step;
+        const int64_t from = lane_slot + piece_slot(cut.first, cut.second, piece) * step;
         ml[i] = *reinterpret_cast<const float2*>(a.part_ml + from * 2);
         v[i] = *reinterpret_cast<const float4*>(a.part_out + from * D + col * 4);
       }

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "kda_ssm_kernels.h"
+#include "kda_stretches.h"
 
 namespace kda {
 
@@ -87,7 +88,6 @@ inline int64_t attn_blocks(int64_t slots, int64_t H) { return slots * H; }
 // Rows of a request that read the same keys, and those of a workgroup: up to 32 rows
 // its waves share the keys out, beyond they share the rows.
 constexpr int kAttnFewRows = 32, kAttnManyRows = 128;
-constexpr int kAttnUnit = 128;  // positions that a context is cut at multiples of
 inline int64_t attn_decode_row_blocks(int64_t T, int64_t G) {
   return T * G <= kAttnFewRows ? 1 : (T * G + kAttnManyRows - 1) / kAttnManyRows;
 }

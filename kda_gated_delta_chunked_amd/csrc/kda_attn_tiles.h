@@ -15,6 +15,7 @@
 #include <type_traits>
 
 #include "kda_ssm_kernels.h"
+#include "kda_stretches.h"
 
 namespace kda {
 
@@ -28,18 +29,6 @@ constexpr float kNone = -__builtin_huge_valf();  // a masked score, and the maxi
 
 __device__ __forceinline__ f32x16 mfma32(const bf16x8& a, const bf16x8& b, const f32x16& c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-}
-
-// Place of a 16-byte chunk of a tile's row, rows of D bf16 or of D codes: chunks are
-// swizzled within a row so that 32 rows' chunk c (a read with lane = row) and the chunks of
-// the rows of a transposed read are spread over the banks.  The swizzle
-// repeats every 16 rows and is an exclusive or.
-template <int D, bool E4M3>
-__device__ __forceinline__ int attn_tile_at(int row, int chunk) {
-  if constexpr (E4M3 && D == 128) return row * 128 + ((chunk ^ ((row >> 1) & 7)) << 4);
-  if constexpr (E4M3) return row * 64 + ((chunk ^ ((row >> 2) & 3)) << 4);
-  if constexpr (D == 128) return row * 256 + ((chunk ^ (((row & 3) << 2) | ((row >> 2) & 3))) << 4);
-  return row * 128 + ((chunk ^ ((((row >> 1) & 1) << 2) | ((row >> 2) & 3))) << 4);
 }
 
 // The key of register i in half h of the wave.
