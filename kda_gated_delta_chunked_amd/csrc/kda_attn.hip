@@ -88,6 +88,8 @@ struct PromptSource {
     memory_left<COUNT>();
     tiles_barrier<READS>();
   }
+  // (rows behind the sequence's end read as zeros)
+  static __device__ __forceinline__ void clear(int) {}
   __device__ __forceinline__ uint32_t seen(int j) const {
     const int n = row - (SPLIT * j + side) * KEYS;  // the last key that the row sees
     return n < 0 ? 0u : n >= 31 ? ~0u : (2u << n) - 1;

@@ -379,8 +379,10 @@ struct AttnRows {
   // The same where rows see different keys.  A weight of zero does not keep an
   // infinity or a NaN from a row, so where the tile holds any they are left out here:
   // the answer is true then, and add_not_finite has to bring them to the rows that see them.
-  template <class Places>
-  __device__ __forceinline__ bool add_masked(const Places& places, uint32_t at, const bf16x8 (&p)[2]) {
+  // (Not those of keys that no row can see, of which clear() makes zeros: the rest of a page holds anything, and
+  // add_not_finite takes as long as hundreds of keys.)
+  template <class Places, class Clear>
+  __device__ __forceinline__ bool add_masked(const Places& places, uint32_t at, const bf16x8 (&p)[2], Clear clear) {
     Exponents most;
     typename Places::Raw v[2 * (D / 32)];
 #pragma unroll
@@ -392,14 +394,18 @@ struct AttnRows {
       for (int i = 0; i < 2 * (D / 32); ++i) o[i % (D / 32)] = mfma32(Places::use(v[i]), p[i / (D / 32)], o[i % (D / 32)]);
       return false;
     }
+    clear();
+    Exponents left;
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
       for (int b = 0; b < D / 32; ++b) {
-        o[b] = mfma32(finite_only(places.values(at, b, k)), p[k], o[b]);
+        const bf16x8 f = places.values(at, b, k);
+        left.take(f);
+        o[b] = mfma32(finite_only(f), p[k], o[b]);
         __builtin_amdgcn_sched_barrier(0);
       }
-    return true;
+    return __any(left.not_finite());
   }
   // The infinities and NaNs of one key's values, column(d) of it, if the lane's row
   // sees the key.
@@ -456,7 +462,7 @@ __device__ __forceinline__ void mask_scores(f32x16& s, uint32_t seen) {
 // tiles may be under way); then its COUNT further copies are started, put(i); at(j + 1) is where block j + 1's
 // keys and block j - 1's values are; seen(j) has the bits of the keys of block j that the lane's row sees.
 // `blocks`: of the workgroup; `mine`: of them, those that any of the wave's rows sees;
-// source.open: below it all rows see all keys (a put may lower it to the block of keys it copies).
+// clear(j) makes zeros of the values of its keys that no row can see; source.open: below it all rows see all keys (a put may lower it to the block of keys it copies).
 // Whether infinities or NaNs were left out of masked blocks.
 template <class Rows, class Source>
 __device__ __forceinline__ bool attend(Rows& r, Source& source, float c, int blocks, int mine) {
@@ -544,7 +550,7 @@ __device__ __forceinline__ bool attend(Rows& r, Source& source, float c, int blo
     const Places places = source.places.fresh();
     if (j <= mine) {
       if (j - 1 < source.open) r.add(places, at, p);
-      else left_out = r.add_masked(places, at, p) || left_out;
+      else left_out = r.add_masked(places, at, p, [&]() { source.clear(j - 1); }) || left_out;
     }
     if (j < mine) {
       if (j >= source.open) mask_scores(s, source.seen(j));
