@@ -7,12 +7,12 @@
 // of each in a ring that the waves fill together; rows behind the sequence's end read as zeros.
 //
 // Bound.  With heads of 128 a turn of a wave is 16 products of 32 cycles, 59 vector and some 60
-// other instructions, two waves a SIMD.  8 sequences of 8192, 32 heads on 8: 3.83 ms, 1149 TFLOP/s, the
-// matrix cores 65% of the time at work at 1.66 GHz, to which the clock falls under this load (a
+// other instructions, two waves a SIMD.  8 sequences of 8192, 32 heads on 8: 3.9 to 4.1 ms, 1070 to 1130
+// TFLOP/s by the device, the matrix cores 65 to 69% of the time at work at 1.66 GHz, to which the clock falls under this load (a
 // product of matrices of 16384 in a library: 1383).  With heads of 64 half as many
-// products meet the same 59 vector instructions, which bound it: 2.29 ms, 958 TFLOP/s.  Short prompts are
+// products meet the same 59 vector instructions, which bound it: 2.28 to 2.35 ms, 935 to 965 TFLOP/s.  Short prompts are
 // a chain of waits: the offsets, the first blocks, a turn for each 32 keys, the last, masked one
-// (6 prompts of 271 to 3063, 12 heads of 128 72 us; one of 37 8 us on the device).
+// (6 prompts of 271 to 3063, 12 heads of 128 67 to 70 us; one of 37 5 us on the device).
 //
 // Tried and not kept: 64 rows a wave, which halve the reads of LDS (heads of 128, one wave a SIMD, B8 T8192
 // 4.20 ms for 3.87; of 64, two waves, 2.29 for 2.31, but 32 ragged prompts 575 us for 519), operands read four products ahead (no change:
@@ -183,6 +183,7 @@ void launch(const AttnArgs& a, hipStream_t stream) {
   // rows (us with one side and with two, by blocks: 256 of 2048 tokens 41 and 36; 384 of 4096 82 and 67, of 2048
   // 52 and 44; 512 of 8192 173 and 160, but of 2048 50 and 53; 768 of 8192 211 and 234).  Short
   // prompts only pay for the join (32 blocks of 512 15.3 and 16.5; 16 prompts of up to 300 14.6 and 19.2).
+  // The mean length, all that the host knows, hides one long prompt among short ones: it has one side.
   const int64_t mean = a.pk.T_total / a.pk.N;
   if (mean >= 1024 && blocks <= (mean >= 4096 ? 512 : 384)) hipLaunchKernelGGL((kda_attn_kernel<D, 2>), dim3((unsigned)blocks), dim3(2 * WAVES * 64), 0, stream, a);
   else hipLaunchKernelGGL((kda_attn_kernel<D, 1>), dim3((unsigned)blocks), dim3(WAVES * 64), 0, stream, a);

@@ -10,14 +10,15 @@
 // for values, and fills each again as soon as it has read it; two workgroups on a CU keep
 // some 100 KiB on the way.  (Two places of each and one workgroup read long contexts as fast, and
 // 1024 requests of up to 128 tokens in 253 us for 131; places for two or four tiles of codes, no faster.)
-// 256 requests of 1 .. 8192 tokens, 8 KV heads of 128, bf16: 740 us, 5.7 TB/s; 64 of up to 16384 over e4m3 239 us, 4.8 TB/s.
+// 256 requests of 1 .. 8192 tokens, 8 KV heads of 128, bf16: 717 us, 5.7 TB/s; 64 of up to 16384 over e4m3 242 us, 4.8 TB/s.
 //
 // More rows: the four waves have 32 rows each, up to 128 a workgroup, and the keys together, with
 // the turns and the ring of the prompts' kernel.  32 trees of 32 drafts, 32 heads on 4, contexts of up to
-// 16384: 230 us over e4m3, 227 over bf16, some 600 TFLOP/s while the device is warm, 185 after a
-// pause.  What bounds it: the instructions of a turn (some 190 for the prompts' 140: pages, and
-// conversions of codes or places that are not held), memory's latency (38 us of 228 over bf16), the start of a
-// piece and its turns with the request's own tokens, the join (19).
+// 16384: 185 to 195 us over e4m3, 208 to 213 over bf16.  What bounds it: the instructions of a turn (some 190 over
+// bf16, 210 to 225 over codes, for the prompts' 140: pages, and conversions of codes or places that are not held); over
+// codes, LDS, where a third of the cycles are bank conflicts; memory's latency (a sixth of the time over bf16); the
+// start of a piece and its turns with the request's own tokens, in which, with heads of 128, spilled registers are loaded
+// again behind copies under way and wait for them (the steady turns have none); the join (19).
 //
 // Contexts are cut into stretches (see Search) where that fills the device better.
 #include <hip/hip_runtime.h>
@@ -374,10 +375,10 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
       if (__builtin_expect(not_finite, 0))
         for (int tile = 0; tile < count; ++tile)
           for (int pos = first + tile * STEP; pos < min(end, first + tile * STEP + KEYS); ++pos) {
-        const int page = page_of(a, table, pos, end), own = pos - req.before;
-        if (page < 0) continue;
-        r.add_not_finite(own < 0 || (sees >> (own & 63) & 1), [&](int d) { return value_at<E4M3>(a.c, kv, page, pos, d); });
-      }
+            const int page = page_of(a, table, pos, end), own = pos - req.before;
+            if (page < 0) continue;
+            r.add_not_finite(own < 0 || (sees >> (own & 63) & 1), [&](int d) { return value_at<E4M3>(a.c, kv, page, pos, d); });
+          }
     }
 
     // the waves' shares, joined through their tiles: O as [D][32 rows]
@@ -550,10 +551,10 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_drafts_kernel(AttnDecodeA
       for (int i = 0; i < Source::RING - 1; ++i) source.put();
       if (__builtin_expect(attend(r, source, c, blocks, top < rows ? blocks : 0), 0))
         for (int pos = begin; pos < end; ++pos) {
-        const int page = page_of(a, source.table, pos, end), own = pos - req.before;
-        if (page < 0) continue;
-        r.add_not_finite(own < 0 || (sees >> (own & 63) & 1), [&](int d) { return value_at<E4M3>(a.c, kv, page, pos, d); });
-      }
+          const int page = page_of(a, source.table, pos, end), own = pos - req.before;
+          if (page < 0) continue;
+          r.add_not_finite(own < 0 || (sees >> (own & 63) & 1), [&](int d) { return value_at<E4M3>(a.c, kv, page, pos, d); });
+        }
     }
     const float total = r.total();
     if (row < rows && !whole) {

@@ -42,7 +42,7 @@ __device__ __forceinline__ uint4 codes16_of(const uint4* u, const Scale& scale) 
 }
 
 // A thread takes 16 bytes of a token's keys in the cache, and of its values: the bytes bound it
-// (65536 tokens of 8 heads of 128 to e4m3 83 us, 4.9 TB/s; 8 bytes of codes a thread 89).
+// (65536 tokens of 8 heads of 128 to e4m3 78 us, 5.2 TB/s; with 8 bytes of codes a thread, and divisions, 89 for 83).
 template <bool E4M3>
 __global__ __launch_bounds__(THREADS) void kda_kv_store_kernel(KvStoreArgs a) {
   constexpr int COLS = kv_store_cols(E4M3);
@@ -99,7 +99,7 @@ struct Share {
 // loaded together, their needs summed up, and where its tokens are among theirs, what these
 // have to know is put into LDS, in which a thread looks for its token's request.  What bounds
 // it is the chain of loads, lengths, then the page, and a few hundred cycles of the sums (1024 requests
-// of a token 7.1 us, 64 prompts of up to 8192 8.2; with the offsets searched in memory 20.6 and 12.8).
+// of a token 7.1 us, 64 prompts of up to 8192 8.2, now 6.1 and 7.3; with the offsets searched in memory 20.6 and 12.8).
 __global__ __launch_bounds__(THREADS) void kda_kv_assign_kernel(KvAssignArgs a) {
   constexpr int EACH = 4, GROUP = THREADS * EACH;
   static_assert(kAssignTokens == THREADS, "a token a thread");
