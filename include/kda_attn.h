@@ -31,9 +31,10 @@
  * 2^127 (of rows that see more than 2^23 positions, 2^150 over their number): no sum leaves
  * fp32.  At its other end, with values in bf16, weights below 2^-94 of a row's largest count as
  * zero, and what an output loses is 2^-94 times the positions at most.
- * A row that sees an infinity or a NaN is infinite or NaN (which of them, and in which columns,
- * is not specified where the keys hold it; a value's stays in its column); rows that do not
- * see it are as if it were not there.
+ * A score of minus infinity is a weight of zero.  A row of which no other score is left has an lse of minus
+ * infinity, and outputs that are NaN (over a cache zeros, as where it sees nothing).  A row that has a score of
+ * plus infinity or NaN is NaN, one that sees an infinity or a NaN among the values is infinite or NaN in
+ * that column; rows that do not see it are as if it were not there.
  */
 #ifndef KDA_ATTN_H_
 #define KDA_ATTN_H_

@@ -161,7 +161,8 @@ __global__ __launch_bounds__(SPLIT * WAVES * 64, 2) void kda_attn_kernel(AttnArg
     tiles_barrier<0>();
     if (side) return;
     const float m = mine_of[(D / 2) * 64], top_m = fmaxf(m, r.m);
-    const float here = __builtin_amdgcn_exp2f((r.m - top_m) * c), there = m == kNone ? 0.f : __builtin_amdgcn_exp2f((m - top_m) * c);
+    // (a side without a maximum has seen nothing, scores of minus infinity or NaNs, which its sum keeps)
+    const float here = r.m == kNone ? 0.f : __builtin_amdgcn_exp2f((r.m - top_m) * c), there = m == kNone ? 0.f : __builtin_amdgcn_exp2f((m - top_m) * c);
 #pragma unroll
     for (int b = 0; b < D / 32; ++b)
 #pragma unroll
