@@ -400,14 +400,12 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
       float m = kNone;
 #pragma unroll
       for (int w = 0; w < WAVES; ++w) m = fmaxf(m, stats[w][0][mine_row]);
-      // (a share that is so far below that its weight is zero is taken all the same: it may hold an
-      // infinity or a NaN that the row sees)
+      // (a share whose weight is zero is taken all the same: it may hold an infinity or a NaN that the row
+      // sees; one that has seen nothing is zeros)
       float weight[WAVES], sum = 0.f;
-      bool holds[WAVES];
 #pragma unroll
       for (int w = 0; w < WAVES; ++w) {
-        holds[w] = stats[w][0][mine_row] != kNone;
-        weight[w] = holds[w] ? __builtin_amdgcn_exp2f((stats[w][0][mine_row] - m) * c) : 0.f;
+        weight[w] = stats[w][0][mine_row] == kNone ? 0.f : __builtin_amdgcn_exp2f((stats[w][0][mine_row] - m) * c);
         // (a share whose scores are all NaN has no maximum, and a sum that is NaN)
         sum += stats[w][1][mine_row] != stats[w][1][mine_row] ? stats[w][1][mine_row] : weight[w] * stats[w][1][mine_row];
       }
@@ -416,8 +414,7 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
       for (int i = 0; i < D / 8; ++i) {
         o[i] = 0.f;
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w)
-          if (holds[w]) o[i] += weight[w] * reinterpret_cast<const float*>(tiles[w])[(cols + i) * 32 + mine_row];
+        for (int w = 0; w < WAVES; ++w) o[i] += weight[w] * reinterpret_cast<const float*>(tiles[w])[(cols + i) * 32 + mine_row];
       }
       const int64_t out_row = (int64_t)n * a.T + row_at / G;
       const int head = kv * G + row_at % G;
@@ -570,9 +567,8 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_drafts_kernel(AttnDecodeA
   }
 }
 
-// Pieces of a row's sums, joined: what they have is brought to the largest maximum.  Only a piece
-// without one, which has seen nothing, is left out: another's weight may be zero, but not
-// its infinities and NaNs, which the row sees.
+// Pieces of a row's sums, joined: what they have is brought to the largest maximum.  A piece whose weight is
+// zero is taken all the same: it may hold infinities and NaNs, which the row sees.
 struct Joined {
   float m = kNone, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -584,14 +580,13 @@ struct Joined {
   __device__ __forceinline__ void bring_to(float top, float c) {
     const float w = weight(m, top, c);
     l = times(w, l);
-    o = make_float4(w * o.x, w * o.y, w * o.z, w * o.w);  // (without a maximum, zeros)
+    o = make_float4(w * o.x, w * o.y, w * o.z, w * o.w);
     m = top;
   }
   // a piece whose maximum is not above m
   __device__ __forceinline__ void add(const float2& ml, const float4& v, float c) {
     const float w = weight(ml.x, m, c);
     l += times(w, ml.y);
-    if (ml.x == kNone) return;
     o.x += w * v.x;
     o.y += w * v.y;
     o.z += w * v.z;
@@ -637,7 +632,10 @@ __global__ __launch_bounds__(THREADS) void kda_attn_join_kernel(AttnDecodeArgs a
       }
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) {
-        if (p + i * share >= parts) ml[i] = make_float2(kNone, 0.f);
+        if (p + i * share >= parts) {
+          ml[i] = make_float2(kNone, 0.f);
+          v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
         top = fmaxf(top, ml[i].x);
       }
       r.bring_to(top, c);

@@ -78,3 +78,24 @@ def test_over_prompts(length, at, tops, D):
     keep[at:, :, 7] = keep[at:, :, 9] = False
     R.assert_out(out[keep], ref[keep], mag[keep])
     R.assert_lse(lse.cpu(), lse_ref, terms, D)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,length", [(1, 64), (4, 700), (1, 6000), (20, 6000), (1, 60000)])
+def test_behind_scores_of_minus_infinity(T, length, D):
+    # all weights of a share are zero, and it has no maximum
+    g = torch.Generator().manual_seed(length)
+    size = 64
+    pages = -(-(length + T) // size)
+    k, v, q = rand(g, pages * size, 1, D), rand(g, pages * size, 1, D), rand(g, 1, T, 4, D)
+    q[..., 0] = 1.0
+    k[..., 0] = 0.0
+    k[:32, :, 0] = k[length // 4:length // 2, :, 0] = -INF
+    at = 3 if length < 1000 else length // 3
+    v[at, 0, 7], v[at, 0, 9] = NAN, INF
+    table = torch.arange(pages, dtype=torch.int32)[None]
+    paged = lambda x: x.view(pages, size, 1, D).cuda()
+    out, _ = attn().decode(q.cuda(), paged(k), paged(v), table.cuda(), i32(length).cuda())
+    assert torch.isnan(out[..., 7]).all() and not torch.isfinite(out[..., 9]).any()
+    out[..., 7] = out[..., 9] = 0
+    assert torch.isfinite(out).all()
