@@ -34,7 +34,7 @@
  * A score of minus infinity is a weight of zero.  A row of which no other score is left has an lse of minus
  * infinity, and outputs that are NaN (over a cache zeros, as where it sees nothing).  A row that has a score of
  * plus infinity or NaN is NaN, one that sees an infinity or a NaN among the values is infinite or NaN in
- * that column; rows that do not see it are as if it were not there.
+ * that column; rows that do not see it are as if it were not there, but for their last bits.
  */
 #ifndef KDA_ATTN_H_
 #define KDA_ATTN_H_

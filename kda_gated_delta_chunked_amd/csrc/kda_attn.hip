@@ -138,11 +138,14 @@ __global__ __launch_bounds__(SPLIT * WAVES * 64, 2) void kda_attn_kernel(AttnArg
   const int mine = top < length ? min(blocks, top / KEYS + 1) : 0;        // any row of the wave
   Source source(a, span.begin, length, kv, wave, side, top, tiles[side]);
   r.settle();
-  if (__builtin_expect(attend(r, source, c, Source::count(blocks, 0), Source::count(mine, side)), 0))
-    for (int key = 0; key < min(mine * KEYS, length); ++key) {
-      if (key / KEYS % SPLIT != side) continue;
-      const uint16_t* v = a.v + (span.begin + key) * a.v_stride + kv * D;
-      r.add_not_finite(key <= row, [&](int d) { return bf16_f32(v[d]); });
+  const uint64_t left_out = attend(r, source, c, Source::count(blocks, 0), Source::count(mine, side));
+  if (__builtin_expect(left_out != 0, 0))
+    for (int block = side; block < mine; block += SPLIT) {
+      if (!(left_out & left_out_bit(block / SPLIT))) continue;
+      for (int key = block * KEYS; key < min((block + 1) * KEYS, length); ++key) {
+        const uint16_t* v = a.v + (span.begin + key) * a.v_stride + kv * D;
+        r.add_not_finite(key <= row, [&](int d) { return bf16_f32(v[d]); });
+      }
     }
   if constexpr (SPLIT == 2) {
     // the sides, joined lane by lane

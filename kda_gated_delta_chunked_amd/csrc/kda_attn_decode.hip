@@ -332,7 +332,7 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
       };
       auto fetch_values = [&](int tile) { copies.tile(false, starts, tile & 63, from, values_at); };
       auto reads_done = [&]() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
-      bool not_finite = false;  // left out of a tile with masked rows
+      uint64_t left_out = 0;  // the tiles out of which infinities or NaNs were left
       if (count > 0) {
         starts.find(a, table, first, STEP, begin, end);
         fetch_keys(0);
@@ -361,8 +361,8 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
         r.l += sum;
         if (more) memory_left<PARTS>();
         else memory_left<0>();
-        if (SOME) not_finite = r.add_masked(places, 0, p, [&]() { clear_rows<D, E4M3>(values_at, there); }) || not_finite;
-        else r.add(places, 0, p);
+        if (!SOME) r.add(places, 0, p);
+        else if (r.add_masked(places, 0, p, [&]() { clear_rows<D, E4M3>(values_at, there); })) left_out |= left_out_bit(tile);
         reads_done();
         if (more) fetch_values(tile + 1);
         ++tile;
@@ -372,13 +372,15 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_decode_kernel(AttnDecodeA
         while (tile * STEP <= open && half0 && half1 && tile + 1 < count && ((tile + 1) & 63)) step(std::false_type());
         step(std::true_type());
       }
-      if (__builtin_expect(not_finite, 0))
-        for (int tile = 0; tile < count; ++tile)
+      if (__builtin_expect(left_out != 0, 0))
+        for (int tile = 0; tile < count; ++tile) {
+          if (!(left_out & left_out_bit(tile))) continue;
           for (int pos = first + tile * STEP; pos < min(end, first + tile * STEP + KEYS); ++pos) {
             const int page = page_of(a, table, pos, end), own = pos - req.before;
             if (page < 0) continue;
             r.add_not_finite(own < 0 || (sees >> (own & 63) & 1), [&](int d) { return value_at<E4M3>(a.c, kv, page, pos, d); });
           }
+        }
     }
 
     // the waves' shares, joined through their tiles: O as [D][32 rows]
@@ -546,8 +548,10 @@ __global__ __launch_bounds__(THREADS, 2) void kda_attn_drafts_kernel(AttnDecodeA
       Source source(a, kv, a.table + (int64_t)req.row * a.table_width, begin, end, req.before, sees, wave, tiles);
       r.settle();
       for (int i = 0; i < Source::RING - 1; ++i) source.put();
-      if (__builtin_expect(attend(r, source, c, blocks, top < rows ? blocks : 0), 0))
+      const uint64_t left_out = attend(r, source, c, blocks, top < rows ? blocks : 0);
+      if (__builtin_expect(left_out != 0, 0))
         for (int pos = begin; pos < end; ++pos) {
+          if (!(left_out & left_out_bit((pos - begin) / KEYS))) continue;
           const int page = page_of(a, source.table, pos, end), own = pos - req.before;
           if (page < 0) continue;
           r.add_not_finite(own < 0 || (sees >> (own & 63) & 1), [&](int d) { return value_at<E4M3>(a.c, kv, page, pos, d); });

@@ -454,6 +454,10 @@ __device__ __forceinline__ void mask_scores(f32x16& s, uint32_t seen) {
   for (int i = 0; i < 16; ++i) s[i] = mine & 1u << key_of(i, 0) ? s[i] : kNone;
 }
 
+// The bit of a block or tile that infinities or NaNs were left out of.  Every 64th shares one: a block
+// may be looked over that was not left out, in which case what is added is there already and changes nothing.
+__device__ __forceinline__ uint64_t left_out_bit(int block) { return 1ull << (block & 63); }
+
 // A wave's rows over the blocks of 32 keys that the waves of a workgroup copy
 // together, in turns: turn j takes the scores of block j + 1, the weights of block j
 // and the product of block j - 1's weights with its values, which do not
@@ -463,9 +467,9 @@ __device__ __forceinline__ void mask_scores(f32x16& s, uint32_t seen) {
 // keys and block j - 1's values are; seen(j) has the bits of the keys of block j that the lane's row sees.
 // `blocks`: of the workgroup; `mine`: of them, those that any of the wave's rows sees;
 // clear(j) makes zeros of the values of its keys that no row can see; source.open: below it all rows see all keys (a put may lower it to the block of keys it copies).
-// Whether infinities or NaNs were left out of masked blocks.
+// The masked blocks out of which infinities or NaNs were left, a bit each (left_out_bit).
 template <class Rows, class Source>
-__device__ __forceinline__ bool attend(Rows& r, Source& source, float c, int blocks, int mine) {
+__device__ __forceinline__ uint64_t attend(Rows& r, Source& source, float c, int blocks, int mine) {
   using Places = typename Source::Places;
   if (mine == 0) {  // no rows, but a share of the copies: as many turns as the others have
     for (int t = 0; t < blocks + 2; ++t) {
@@ -473,10 +477,10 @@ __device__ __forceinline__ bool attend(Rows& r, Source& source, float c, int blo
       source.put();
     }
     memory_left<0>();
-    return false;
+    return 0;
   }
   const Places& places = source.places;
-  bool left_out = false;
+  uint64_t left_out = 0;
   float sum;
   bf16x8 p[2];
   // blocks 0 and 1: their keys are there with the first turn
@@ -550,7 +554,7 @@ __device__ __forceinline__ bool attend(Rows& r, Source& source, float c, int blo
     const Places places = source.places.fresh();
     if (j <= mine) {
       if (j - 1 < source.open) r.add(places, at, p);
-      else left_out = r.add_masked(places, at, p, [&]() { source.clear(j - 1); }) || left_out;
+      else if (r.add_masked(places, at, p, [&]() { source.clear(j - 1); })) left_out |= left_out_bit(j - 1);
     }
     if (j < mine) {
       if (j >= source.open) mask_scores(s, source.seen(j));
