@@ -10,7 +10,7 @@
 // other instructions, two waves a SIMD.  8 sequences of 8192, 32 heads on 8: 3.9 to 4.1 ms, 1070 to 1130
 // TFLOP/s by the device, the matrix cores 65 to 69% of the time at work at 1.66 GHz, to which the clock falls under this load (a
 // product of matrices of 16384 in a library: 1383).  With heads of 64 half as many
-// products meet the same 59 vector instructions, which bound it: 2.28 to 2.35 ms, 935 to 965 TFLOP/s.  Short prompts are
+// products meet the same 59 vector instructions, which bound it: 2.28 to 2.38 ms, 925 to 965 TFLOP/s.  Short prompts are
 // a chain of waits: the offsets, the first blocks, a turn for each 32 keys, the last, masked one
 // (6 prompts of 271 to 3063, 12 heads of 128 67 to 70 us; one of 37 5 us on the device).
 //

@@ -167,8 +167,8 @@ kda_status check_decode(const kda_attn_decode_problem* p) {
 // of up to 64 rows over bf16 with heads of 128 the bytes take longer than the work of one (64 requests of
 // 16 tokens up to 8192, 4 heads a KV head, 310 and 287; over e4m3 204 and 260, with heads of 64 145 and 173;
 // 32 of 32 tokens, 8 heads, 226 and 267).  The rule knows the table's room, not the lengths: with a table of 32768
-// positions short contexts are cut too (16 requests of up to 1000 15 us and 24, 9 of 4 drafts up to 600 11 and 16;
-// 256 of up to 1000 121 and 124, 1024 of up to 128 131 and 127).
+// positions short contexts are cut too (16 requests of up to 1000 14 us and 21, 9 of 4 drafts up to 600 12 and 16;
+// 256 of up to 1000 119 and 118, 1024 of up to 128 112 and 106).
 int decode_parts(const kda_attn_decode_problem* p) {
   const int64_t KV = p->cache.num_kv_heads, G = p->num_heads / KV, T = p->tokens_per_seq;
   const int64_t per_item = kda::attn_decode_blocks(1, KV, T, G), blocks = p->num_seqs * per_item;

@@ -9,12 +9,12 @@
 // wave waits for another one before that.  A wave has a place in LDS for its tile of keys and one
 // for values, and fills each again as soon as it has read it; two workgroups on a CU keep
 // some 100 KiB on the way.  (Two places of each and one workgroup read long contexts as fast, and
-// 1024 requests of up to 128 tokens in 253 us for 131; places for two or four tiles of codes, no faster.)
-// 256 requests of 1 .. 8192 tokens, 8 KV heads of 128, bf16: 717 us, 5.7 TB/s; 64 of up to 16384 over e4m3 242 us, 4.8 TB/s.
+// 1024 requests of up to 128 tokens in 253 us for 131, 113 by now; places for two or four tiles of codes, no faster.)
+// 256 requests of 1 .. 8192 tokens, 8 KV heads of 128, bf16: 713 us, 5.7 TB/s; 64 of up to 16384 over e4m3 237 us, 4.9 TB/s.
 //
 // More rows: the four waves have 32 rows each, up to 128 a workgroup, and the keys together, with
 // the turns and the ring of the prompts' kernel.  32 trees of 32 drafts, 32 heads on 4, contexts of up to
-// 16384: 185 to 195 us over e4m3, 208 to 213 over bf16.  What bounds it: the instructions of a turn (some 190 over
+// 16384: 185 to 195 us over e4m3, 208 to 214 over bf16.  What bounds it: the instructions of a turn (some 190 over
 // bf16, 210 to 225 over codes, for the prompts' 140: pages, and conversions of codes or places that are not held); over
 // codes, LDS, where a third of the cycles are bank conflicts; memory's latency (a sixth of the time over bf16); the
 // start of a piece and its turns with the request's own tokens, in which, with heads of 128, spilled registers are loaded

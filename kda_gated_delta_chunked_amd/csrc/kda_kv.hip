@@ -99,7 +99,7 @@ struct Share {
 // loaded together, their needs summed up, and where its tokens are among theirs, what these
 // have to know is put into LDS, in which a thread looks for its token's request.  What bounds
 // it is the chain of loads, lengths, then the page, and a few hundred cycles of the sums (1024 requests
-// of a token 7.1 us, 64 prompts of up to 8192 8.2, now 6.1 and 7.3; with the offsets searched in memory 20.6 and 12.8).
+// of a token 7.1 us, 64 prompts of up to 8192 8.2, now 6.2 and 7.6; with the offsets searched in memory 20.6 and 12.8).
 __global__ __launch_bounds__(THREADS) void kda_kv_assign_kernel(KvAssignArgs a) {
   constexpr int EACH = 4, GROUP = THREADS * EACH;
   static_assert(kAssignTokens == THREADS, "a token a thread");
