@@ -28,9 +28,9 @@
  * fp32.  A weight exp(s - m) is rounded to bf16 ahead of the product with the
  * values (the sum that divides them is of the unrounded ones), an output once.
  * Range.  Products q . k and scores have to be below 2^127 in magnitude.  Values may be of any size up to
- * 2^127 (of rows that see more than 2^23 positions, 2^150 over their number): no sum leaves
- * fp32.  At its other end, with values in bf16, weights below 2^-94 of a row's largest count as
- * zero, and what an output loses is 2^-94 times the positions at most.
+ * 2^127 (of rows that see more than 2^22 positions, 2^149 over their number): no sum leaves
+ * fp32.  At its other end, with values in bf16, weights below 2^-95 of a row's largest count as
+ * zero, and what an output loses is 2^-95 times the positions at most.
  * A score of minus infinity is a weight of zero.  A row of which no other score is left has an lse of minus
  * infinity, and outputs that are NaN (over a cache zeros, as where it sees nothing).  A row that has a score of
  * plus infinity or NaN is NaN, one that sees an infinity or a NaN among the values is infinite or NaN in

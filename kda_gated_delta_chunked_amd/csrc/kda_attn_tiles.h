@@ -208,16 +208,17 @@ __device__ __forceinline__ bf16x8 finite_only(const bf16x8& f) {
 // no accuracy (sums are floating point), and most blocks need no maximum.
 //
 // SHIFT keeps o within fp32's range for all finite values of bf16: weights of 32 keys sum to 2^(13 - SHIFT)
-// at most, those of L keys to L 2^(8 - SHIFT), which is 1/2 for 32 and 2^23 keys.  It divides out; what it costs is
-// at fp32's other end, weights below 2^-94 of the largest.  As a literal of c m + SHIFT it takes no
-// register and no instruction (as an argument for the context's length, 64 requests of 16 tokens took 317 us
+// at most, those of L keys to L 2^(8 - SHIFT), which is 1/2 for 31 and 2^22 keys.  It divides out; what it costs is
+// at fp32's other end, weights below 2^-95 of the largest, and that exponents of some -31 are rounded by 2^-20 (an
+// lse is 4e-7 to 5e-7 off in the mean for 3e-7; to bf16 weights are rounded by 2^-9).  As a literal of c m + SHIFT it
+// takes no register and no instruction (as an argument for the context's length, 64 requests of 16 tokens took 317 us
 // for 286: a register more in a kernel that spills).  Codes, of 448 at most, need none.
 //
 // c s - c m is one operation, of c m as it is rounded.  Where c m is so large (beyond kNear) that its
 // error would show, c (s - m) is taken, always from the maximum: `far` is less than any sum from then on.
 template <int D, bool E4M3>
 struct AttnRows {
-  static constexpr float SHIFT = E4M3 ? 0.f : 32.f, kFar = E4M3 ? 0x1p12f : 0x1p-20f, kNear = 4096.f;
+  static constexpr float SHIFT = E4M3 ? 0.f : 31.f, kFar = E4M3 ? 0x1p12f : 0x1p-19f, kNear = 4096.f;
   bf16x8 q[D / 16];
   f32x16 o[D / 32];
   float m, l, far;
@@ -420,9 +421,10 @@ struct AttnRows {
         o[b][i] += sees && !(fabsf(v) < __builtin_huge_valf()) ? v : 0.f;
       }
   }
-  // log sum exp(scale s) from a maximum of s, and the sum of weights from it
+  // log sum exp(scale s) from a maximum of s, and the sum of weights from it (from c m + SHIFT as it is rounded)
   static __device__ __forceinline__ float lse_of(float m, float c, float total) {
-    return m == kNone && total == 0.f ? kNone : __builtin_fmaf(m, c, __builtin_amdgcn_logf(total * (E4M3 ? 1.f : 0x1p32f))) * kLn2;
+    const float mc = __builtin_fmaf(m, c, SHIFT) - SHIFT;
+    return m == kNone && total == 0.f ? kNone : (mc + __builtin_amdgcn_logf(total * (E4M3 ? 1.f : 0x1p31f))) * kLn2;
   }
   // the row's whole sum
   __device__ __forceinline__ float total() const { return l + other_half(l); }
@@ -466,7 +468,8 @@ __device__ __forceinline__ uint64_t left_out_bit(int block) { return 1ull << (bl
 // tiles may be under way); then its COUNT further copies are started, put(i); at(j + 1) is where block j + 1's
 // keys and block j - 1's values are; seen(j) has the bits of the keys of block j that the lane's row sees.
 // `blocks`: of the workgroup; `mine`: of them, those that any of the wave's rows sees;
-// clear(j) makes zeros of the values of its keys that no row can see; source.open: below it all rows see all keys (a put may lower it to the block of keys it copies).
+// clear(j) makes zeros of the values of its keys that no row can see;
+// source.open: below it all rows see all keys (a put may lower it to the block of keys it copies).
 // The masked blocks out of which infinities or NaNs were left, a bit each (left_out_bit).
 template <class Rows, class Source>
 __device__ __forceinline__ uint64_t attend(Rows& r, Source& source, float c, int blocks, int mine) {

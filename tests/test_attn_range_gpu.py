@@ -2,8 +2,8 @@
 the way to them may not leave fp32's range where they do not.
 
 Bounds.  As tests/attn_reference.py, which counts the roundings relative to the values; at the
-lower end what falls below fp32's normal numbers (2^-126) may be lost.  Sums are held 2^-32 as
-large as weights of at most 1 make them, so that is an output's error of L 2^-94 at most over L
+lower end what falls below fp32's normal numbers (2^-126) may be lost.  Sums are held 2^-31 as
+large as weights of at most 1 make them, so that is an output's error of L 2^-95 at most over L
 positions."""
 import math
 
@@ -47,7 +47,7 @@ def check(out, lse, ref, floor):
 
 
 def floor_of(L):
-    return L * 2.0 ** -94
+    return L * 2.0 ** -95
 
 
 SIZES = [(2.0 ** 127, "rising"), (2.0 ** 127, "equal"), (2.0 ** 127, "random"), (2.0 ** 115, "rising"), (2.0 ** -60, "rising"),
